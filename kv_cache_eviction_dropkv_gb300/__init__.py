@@ -7,3 +7,4 @@ only marshals arguments; every step runs in the library's CUDA kernels.
 from ._binding import (DropKVError, dropkv_compact, dropkv_read_status, dropkv_score, dropkv_select,  # noqa: F401
                        dropkv_shape, dropkv_version, dropkv_workspace_size, make_shape)
 from .api import DropKV  # noqa: F401
+from .paged import PagedCache  # noqa: F401

@@ -1,4 +1,5 @@
-"""ctypes binding of libdropkv.so (include/dropkv.h), same names as the C ABI.
+"""ctypes binding of libdropkv.so (include/dropkv.h and include/kvcache.h), same
+names as the C ABI.
 
 Argument marshalling only: tensors are passed as device pointers and the
 current torch stream as the CUDA stream; every step runs in the library.  If
@@ -18,6 +19,7 @@ from . import _build
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "WORKSPACE", 3: "SINGULAR", 4: "NONFINITE", 5: "CUDA",
                 6: "UNSUPPORTED", 7: "DEVICE_ARG", 8: "TIMEOUT"}
 FLAG_SINGULAR, FLAG_NONFINITE, FLAG_BAD_LENGTH, FLAG_BAD_K, FLAG_OVERFLOW, FLAG_TIMEOUT = 1, 2, 4, 8, 16, 32
+FLAG_NO_PAGES, FLAG_BAD_SEQ, FLAG_BAD_PAGE = 0x1000, 0x2000, 0x4000
 
 
 class DropKVError(RuntimeError):
@@ -32,6 +34,17 @@ class dropkv_shape(ctypes.Structure):
 
     def astuple(self):
         return (self.B, self.Hq, self.Hkv, self.d, self.n_max, self.w)
+
+
+CACHE_CODES = {"e4m3": 0, "int8": 1}
+
+
+class kvcache_shape(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("layers", "Hkv", "d", "page", "pages", "seqs", "max_pages", "code")]
+
+
+class kvcache_buffers(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale", "refs", "table", "count", "length")]
 
 
 _lock = threading.Lock()
@@ -79,6 +92,20 @@ def _load(path):
     L.dropkv_read_status.restype = ctypes.c_int
     L.dropkv_version.argtypes = []
     L.dropkv_version.restype = ctypes.c_char_p
+    CS, CB = ctypes.POINTER(kvcache_shape), ctypes.POINTER(kvcache_buffers)
+    L.kvcache_workspace_size.argtypes = [CS, I32, I32]
+    L.kvcache_workspace_size.restype = SZ
+    for name, args in (
+            ("kvcache_reserve", [CS, CB, P, I32, P, P, SZ, P, P]),
+            ("kvcache_store", [CS, CB, I32, P, I32, P, P, I32, P, P, P]),
+            ("kvcache_attention", [CS, CB, I32, P, I32, P, I32, I32, I32, I32, P, P, SZ, P, P]),
+            ("kvcache_fork", [CS, CB, P, P, I32, I32, P, SZ, P, P]),
+            ("kvcache_compact", [CS, CB, P, I32, P, I32, P, P, SZ, P, P]),
+            ("kvcache_free", [CS, CB, P, I32, P, P]),
+            ("kvcache_window_attention", [I32, I32, I32, I32, I32, P, P, P, P, I32, I32, P, P, P]),
+            ("kvcache_read_status", [P, P, ctypes.POINTER(ctypes.c_uint32)])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = ctypes.c_int
     for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k"):
         if hasattr(L, hook):
             getattr(L, hook).argtypes = [I32, I32]
@@ -126,7 +153,7 @@ def declared_functions(header: str = None):
     header = header or os.path.join(_build.INCLUDE, "dropkv.h")
     text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(dropkv_[a-z0-9_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b((?:dropkv|kvcache)_[a-z0-9_]+)\s*\(", text)))
 
 
 def _ptr(t):
@@ -272,3 +299,55 @@ def dropkv_read_status(status, stream=None):
 
 def dropkv_version() -> str:
     return lib().dropkv_version().decode()
+
+
+# ------------------------------------------------------------------ include/kvcache.h
+# The cache's calls take the two structures (shape and buffers, built once per
+# cache), raw device addresses (0 or None: NULL) and a raw stream.
+def kvcache_workspace_size(shape, Hq, T) -> int:
+    return int(lib().kvcache_workspace_size(ctypes.byref(shape), int(Hq), int(T)))
+
+
+def kvcache_reserve(shape, cache, seqs, n, extra, workspace, workspace_bytes, status, stream):
+    _check(lib().kvcache_reserve(shape, cache, seqs, n, extra, workspace, workspace_bytes, status, stream),
+           "kvcache_reserve")
+
+
+def kvcache_store(shape, cache, layer, seqs, n, k, v, rows, counts, status, stream):
+    _check(lib().kvcache_store(shape, cache, layer, seqs, n, k, v, rows, counts, status, stream), "kvcache_store")
+
+
+def kvcache_attention(shape, cache, layer, seqs, n, q, Hq, T, window, sinks, out, workspace, workspace_bytes, status,
+                      stream):
+    _check(lib().kvcache_attention(shape, cache, layer, seqs, n, q, Hq, T, window, sinks, out, workspace,
+                                   workspace_bytes, status, stream), "kvcache_attention")
+
+
+def kvcache_fork(shape, cache, src, dst, n, share, workspace, workspace_bytes, status, stream):
+    _check(lib().kvcache_fork(shape, cache, src, dst, n, share, workspace, workspace_bytes, status, stream),
+           "kvcache_fork")
+
+
+def kvcache_compact(shape, cache, seqs, n, kept_idx, kept_stride, kept_len, workspace, workspace_bytes, status,
+                    stream):
+    _check(lib().kvcache_compact(shape, cache, seqs, n, kept_idx, kept_stride, kept_len, workspace, workspace_bytes,
+                                 status, stream), "kvcache_compact")
+
+
+def kvcache_free(shape, cache, seqs, n, status, stream):
+    _check(lib().kvcache_free(shape, cache, seqs, n, status, stream), "kvcache_free")
+
+
+def kvcache_window_attention(q, k, v, lengths, window, sinks, attn_out, status, stream=None):
+    """q, attn_out [B,Hq,n_max,d], k, v [B,Hkv,n_max,d] bf16, lengths [B] int32 or None."""
+    B, Hq, n_max, d = q.shape
+    _check(lib().kvcache_window_attention(B, Hq, k.shape[1], d, n_max, _ptr(q), _ptr(k), _ptr(v), _ptr(lengths),
+                                          int(window), int(sinks), _ptr(attn_out), _ptr(status), _stream(stream)),
+           "kvcache_window_attention")
+
+
+def kvcache_read_status(status, stream=None):
+    """Sync the stream and return (status code, raw flag word)."""
+    flags = ctypes.c_uint32(0)
+    code = lib().kvcache_read_status(_ptr(status), _stream(stream), ctypes.byref(flags))
+    return int(code), int(flags.value)

@@ -86,6 +86,22 @@ class DropKV:
         """The prompt's causal attention alone (dropkv_prefill_attention)."""
         B.dropkv_prefill_attention(self.shape, q, k, v, lengths, attn_out, self.workspace, self.status, stream)
 
+    def window_attention(self, q, k, v, lengths, attn_out, window: int, sinks: int = 0, stream=None):
+        """The prompt's causal attention over a sliding window with the first
+        tokens kept visible (kvcache_window_attention): row i sees keys j <= i
+        with j > i - window or j < sinks; window 0 is prefill_attention's mask.
+        The positional baseline next to the scored evictions."""
+        Bn, Hq, Hkv, d, n, _ = self.shape.astuple()
+        for t, heads in ((q, Hq), (k, Hkv), (v, Hkv), (attn_out, Hq)):
+            if t.dtype is not torch.bfloat16 or tuple(t.shape) != (Bn, heads, n, d) or t.device != self.status.device:
+                raise ValueError("expected bf16 [%d, %d, %d, %d] on %s, got %s %s on %s"
+                                 % (Bn, heads, n, d, self.device, t.dtype, tuple(t.shape), t.device))
+        if lengths is not None and (lengths.dtype is not torch.int32 or tuple(lengths.shape) != (Bn,)
+                                    or lengths.device != self.status.device):
+            raise ValueError("lengths: expected int32 [%d] on %s" % (Bn, self.device))
+        with torch.cuda.device(self.status.device):
+            B.kvcache_window_attention(q, k, v, lengths, window, sinks, attn_out, self.status, stream)
+
     def run_separate(self, q, k, v, lengths, evict_k, stream=None, keep_raw=True):
         """The same step as three library calls (score, select, compact)."""
         self.score(q, k, v, lengths, stream, keep_raw)

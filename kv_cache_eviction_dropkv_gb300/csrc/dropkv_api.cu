@@ -26,21 +26,6 @@ int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
 
 int nr_for(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : -1; }
 
-// SM count of the current device (cached per device ordinal).
-int current_sms(int* dev_out) {
-  static std::mutex mu;
-  static int cache[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
-  if (dev_out) *dev_out = dev;
-  std::lock_guard<std::mutex> lk(mu);
-  if (dev < 64 && cache[dev] > 0) return cache[dev];
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
-  if (dev < 64) cache[dev] = sms;
-  return sms;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -57,13 +42,36 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 // K or V viewed as a 3-D tensor (d, n_max, B*Hkv) of bf16, loaded as boxes of
 // 64 columns x 128 rows with 128-byte swizzle; reads past d or n_max fill zero.
+bool encode_rows_map(CUtensorMap* map, const void* base, const Geom& g, int depth) {
+  return encode_rows(map, base, g.d, g.n_max, depth);
+}
+
+bool encode_kv_map(CUtensorMap* map, const void* base, const Geom& g) { return encode_rows_map(map, base, g, g.U); }
+
+}  // namespace
+
+// SM count of the current device (cached per device ordinal).
+int current_sms(int* dev_out) {
+  static std::mutex mu;
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
+  if (dev_out) *dev_out = dev;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 64 && cache[dev] > 0) return cache[dev];
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (dev < 64) cache[dev] = sms;
+  return sms;
+}
+
 // A [depth][n_max][d] bf16 tensor (K or V: depth = B * Hkv; every query row:
 // depth = B * Hq) as boxes of 64 columns x 128 rows, 128-byte swizzled.
-bool encode_rows_map(CUtensorMap* map, const void* base, const Geom& g, int depth) {
+bool encode_rows(CUtensorMap* map, const void* base, int d, int n_max, int depth) {
   auto enc = encoder();
   if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)g.d, (cuuint64_t)g.n_max, (cuuint64_t)depth};
-  cuuint64_t strides[2] = {(cuuint64_t)g.d * 2, (cuuint64_t)g.d * 2 * (cuuint64_t)g.n_max};
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n_max, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * (cuuint64_t)n_max};
   cuuint32_t box[3] = {64, (cuuint32_t)kTile, 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
@@ -72,14 +80,10 @@ bool encode_rows_map(CUtensorMap* map, const void* base, const Geom& g, int dept
   return r == CUDA_SUCCESS;
 }
 
-bool encode_kv_map(CUtensorMap* map, const void* base, const Geom& g) { return encode_rows_map(map, base, g, g.U); }
-
 bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
-
-}  // namespace
 
 bool make_geom(const dropkv_shape* s, int num_sms, Geom* g) {
   if (!s || !g || num_sms <= 0) return false;

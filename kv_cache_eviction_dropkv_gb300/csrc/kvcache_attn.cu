@@ -1,0 +1,782 @@
+// Attention of a few query rows per sequence over the paged 8-bit cache.
+//
+//   x_rj = q_r . (ck_j s_k(page of j)) / sqrt(d),  o_r = sum_j p_rj cv_j s_v / sum_j p_rj,
+//   p_rj = exp(x_rj - m_r) over the tokens row r sees.
+//
+// The call reads each visible code once and computes 4 R operations per code
+// pair for the R = g T query rows of a KV head: it is bound by memory, and
+// the kernel's work is to keep copies in flight and to turn bytes into fp16
+// operands cheaply.
+//
+// Work is cut into tiles of 32 tokens of one KV head (a tile lies inside a
+// page, so it has one K and one V scale).  The tiles of the whole call,
+// counted on the device from the lengths and the window, are dealt out to the
+// warps of one resident wave in equal contiguous runs, so ragged batches
+// leave no tail.  A warp is on its own: it copies its tiles with cp.async
+// into its own ring of kStages tiles (no block barrier anywhere), and keeps
+// its rows' softmax state and outputs in registers.  A run that holds a whole
+// (sequence, head, row group) writes the output; the pieces of one that is
+// cut by run borders go to the workspace and a second kernel joins them in
+// run order (no atomics: results do not depend on timing).
+//
+// Per tile, on mma.m16n8k16 with the tokens on the M side, so that 8 query
+// rows fill the N side (a decode step has g = 1 to 8 rows per KV head; the
+// 128-row tcgen05 tile would be 94 % padding and wants its operands as 16-bit
+// tiles in shared memory, which is four times the traffic of these bytes):
+//   S^T[32 tokens x 8 rows] = K . Q^T,  then O^T[d x 8 rows] += V^T . P.
+// The index of a contraction may be permuted freely if both operands agree:
+// a lane takes 16 contiguous bytes of a K row as its k elements of four MMAs
+// (one 128-bit shared load), and 16 contiguous channels of a V row as its row
+// indices of eight MMAs.  P goes from S^T's accumulator layout to the B
+// operand with one movmatrix per 8 x 8 block.  Rows of 128 bytes are staged
+// with their 16-byte chunks XOR-ed by the token's low bits: both kinds of
+// read then touch all banks.
+#include <algorithm>
+#include <cmath>
+
+#include "kvcache_internal.cuh"
+#include "sm103_ptx.cuh"
+
+namespace kvcache {
+namespace {
+
+using dropkv::cp_async_cg16;
+using dropkv::ex2_approx;
+using dropkv::grid_dep_launch;
+using dropkv::grid_dep_wait;
+using dropkv::launch_pdl;
+
+constexpr int kTok = 32;                    // tokens of a tile
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kPitch = 128;                 // bytes of a staged row
+constexpr int kStageBytes = 2 * kTok * kPitch;   // K rows, then V rows
+constexpr int kSmem = kWarps * kStages * kStageBytes;
+constexpr int kMergeThreads = 256;
+// A row's reference moves only when a tile's maximum is this far above it
+// (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
+constexpr float kMoveLog2 = 8.0f;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 16 bytes into shared memory, zeros when !take.
+__device__ __forceinline__ void cp16(uint32_t dst, const uint8_t* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const uint8_t* src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(take ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four codes (bytes 0..3 of w) as two fp16 pairs (0, 1) and (2, 3).
+template <int CODE>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  if constexpr (CODE == KVCACHE_E4M3) {
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(h01), "=r"(h23)
+        : "r"(w));
+  } else {
+    // bytes as the low bits of fp16 1024 + (code + 128), minus 1152: exact
+    const uint32_t x = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h01) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h23) : "r"(b), "r"(0x64806480u));
+  }
+}
+
+// What a sequence's length, T and the window leave to read: tiles [0, ns) and
+// [s2, s2 + rest).
+struct Span {
+  int ns, s2, tiles;
+  int lo;                                   // first token some row's window reaches
+};
+__device__ __forceinline__ Span span_of(int len, int T, int window, int sinks) {
+  Span s;
+  const int end = (len + kTok - 1) / kTok;
+  s.lo = window > 0 ? max(0, max(0, len - T) - window + 1) : 0;
+  s.ns = window > 0 ? (min(sinks, s.lo) + kTok - 1) / kTok : 0;
+  s.s2 = max(s.lo / kTok, s.ns);
+  s.tiles = s.ns + end - s.s2;
+  if (len <= 0) s.ns = s.s2 = s.tiles = 0;
+  return s;
+}
+
+// Length of entry i's sequence; 0 (and a flag, once) when it cannot be served.
+__device__ __forceinline__ int entry_len(const AttnCall& p, int i, bool report) {
+  const int s = p.seqs ? p.seqs[i] : i;
+  if (s < 0 || s >= p.c.S) {
+    if (report) flag(p.c.status, KVCACHE_FLAG_BAD_SEQ);
+    return 0;
+  }
+  const int len = p.c.length[s], held = p.c.count[s];
+  if (len < 0 || held < 0 || held > p.c.M || (long long)len > ((long long)held << p.c.page_log2)) {
+    if (report) flag(p.c.status, DROPKV_FLAG_BAD_LENGTH);
+    return 0;
+  }
+  return len;
+}
+
+// Where the tiles of the call lie, as one warp sees it.
+struct Deal {
+  long long total;                          // tiles of the call
+  long long share, more;                    // the first `more` runs have share + 1 tiles, the others share
+};
+__device__ __forceinline__ long long warp_total(const AttnCall& p, int lane, int upb, bool report) {
+  long long sum = 0;
+  for (int b = lane; b < p.n; b += 32) sum += span_of(entry_len(p, b, report), p.T, p.window, p.sinks).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * upb;
+}
+__device__ __forceinline__ Deal deal_of(long long total, int workers) {
+  Deal d;
+  d.total = total;
+  d.share = total / workers;
+  d.more = total - d.share * workers;
+  return d;
+}
+__device__ __forceinline__ long long run_start(const Deal& d, long long w) { return w * d.share + min(w, d.more); }
+// The run that holds tile x.
+__device__ __forceinline__ int run_of(const Deal& d, long long x) {
+  const long long cut = d.more * (d.share + 1);
+  return (int)(x < cut ? x / (d.share + 1) : d.more + (x - cut) / d.share);
+}
+// The entry whose units hold position x of the running sum of tiles * upb (by
+// tile), or of upb (by unit); *cum gets the tiles before it.
+__device__ __forceinline__ int find_entry(const AttnCall& p, int lane, int upb, long long x, long long* cum) {
+  long long before = 0;
+  for (int base = 0; base < p.n; base += 32) {
+    const int b = base + lane;
+    long long t = b < p.n ? (long long)span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles * upb : 0;
+    long long inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + inc > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      *cum = before + __shfl_sync(0xffffffffu, inc - t, l);
+      return base + l;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  *cum = before;
+  return p.n;
+}
+
+template <int CODE, int DP, int NR>
+__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p) {
+  constexpr int KS = DP / 16;               // MMAs along d for S, and row blocks of O
+  constexpr int KB = DP / 4, VB = DP / 8;   // bytes a lane takes of a K row, of a V row
+  constexpr int RB = 8 * NR;
+  extern __shared__ uint8_t smem[];
+  grid_dep_wait();
+  grid_dep_launch();
+  const Cache& c = p.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g8 = lane >> 2, c4 = lane & 3;
+  const int worker = blockIdx.x * kWarps + warp;
+  const int upb = c.Hkv * p.RG;             // units (head, row group) per sequence
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring_s = dropkv::smem_addr(ring);
+  if (worker >= p.workers) return;
+
+  // rows of sequences with nothing to read
+  for (int b = worker; b < p.n; b += p.workers) {
+    if (span_of(entry_len(p, b, true), p.T, p.window, p.sinks).tiles > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * p.T * c.d);
+    for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
+  }
+
+  // this warp's run [x0, x1)
+  const Deal deal = deal_of(warp_total(p, lane, upb, false), p.workers);
+  long long x0, x1;
+  int b0;
+  long long cum0;
+  if (p.whole) {
+    // runs of whole units: unit ua .. ub - 1
+    const long long units = (long long)p.n * upb;
+    const long long ua = units * worker / p.workers, ub = units * (worker + 1) / p.workers;
+    long long cum[2];
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const long long u = e ? ub : ua;
+      const int b = (int)(u / upb);
+      long long before = 0;
+      for (int i = lane; i < b; i += 32) before += span_of(entry_len(p, i, false), p.T, p.window, p.sinks).tiles;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+      const int t = b < p.n ? span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles : 0;
+      cum[e] = before * upb + (u - (long long)b * upb) * t;
+    }
+    x0 = cum[0];
+    x1 = cum[1];
+  } else {
+    x0 = run_start(deal, worker);
+    x1 = run_start(deal, worker + 1);
+  }
+  if (x0 >= x1) return;
+  b0 = find_entry(p, lane, upb, x0, &cum0);
+  // the run begins inside a unit
+  const bool cut = (int)(x0 - cum0) % span_of(entry_len(p, b0, false), p.T, p.window, p.sinks).tiles != 0;
+
+  // columns past d stay zero in every stage (copies never touch them)
+  if (c.d < kPitch)
+    for (int u = lane; u < kStages * kStageBytes / 16; u += 32)
+      reinterpret_cast<uint4*>(ring)[u] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+
+  // -------------------------------------------------- tile descriptions
+  // Lane l describes tile x0 + 32 k + l of the run: its unit, first token,
+  // cache row and scales; the warp broadcasts them when the tile comes up.
+  struct Tile {
+    int unit, tok;                          // b * upb + u;  first token, -1: unreadable page
+    long long row;                          // first cache row
+    float ks, lv;                           // K scale, log2 of the V scale
+    int len;
+  };
+  int wb = b0;                              // entry the lane's cursor stands at
+  long long wcum = cum0;
+  auto describe = [&](long long x) {
+    Tile t;
+    t.unit = -1; t.tok = 0; t.row = 0; t.ks = 0.f; t.lv = 0.f; t.len = 0;
+    if (x >= x1) return t;
+    int len = entry_len(p, wb, false);
+    Span s = span_of(len, p.T, p.window, p.sinks);
+    while (x >= wcum + (long long)s.tiles * upb) {
+      wcum += (long long)s.tiles * upb;
+      ++wb;
+      len = entry_len(p, wb, false);
+      s = span_of(len, p.T, p.window, p.sinks);
+    }
+    const int y = (int)(x - wcum), u = y / s.tiles, k = y - u * s.tiles;
+    const int tile = k < s.ns ? k : s.s2 + (k - s.ns);
+    const int sq = p.seqs ? p.seqs[wb] : wb;
+    t.unit = wb * upb + u;
+    t.tok = tile * kTok;
+    t.len = len;
+    const int pg = c.table[(size_t)sq * c.M + (t.tok >> c.page_log2)];
+    if (pg < 0 || pg >= c.P) {
+      flag(c.status, KVCACHE_FLAG_BAD_PAGE);
+      t.tok = -1;
+    } else {
+      const size_t ur = (size_t)pg * c.Hkv + u / p.RG;
+      t.row = (long long)(ur * c.page + (t.tok & (c.page - 1)));
+      t.ks = c.ks[ur];
+      t.lv = __log2f(fmaxf(c.vs[ur], 0x1p-126f));
+    }
+    return t;
+  };
+
+  // -------------------------------------------------- copies
+  const int units16 = (c.d + 15) >> 4;      // 16-byte pieces of a row (the last may be 8 bytes)
+  const bool odd8 = (c.d & 15) != 0;
+  auto copy_tile = [&](int stage, int tok, long long row, int len) {
+    // slots some row sees: [lo, len) and the first tokens
+    int v0 = 0, v1 = kTok, v2 = 0;          // rows [v0, v1) and [0, v2)
+    if (tok < 0) {
+      v1 = 0;
+    } else {
+      v1 = min(kTok, len - tok);
+      if (p.window > 0) {
+        const int lo = max(0, max(0, len - p.T) - p.window + 1);
+        v0 = max(0, lo - tok);
+        v2 = min(min(kTok, len - tok), p.sinks - tok);
+      }
+    }
+    const uint8_t* kp = c.k + (tok < 0 ? 0 : row * c.d);
+    const uint8_t* vp = c.v + (tok < 0 ? 0 : row * c.d);
+    const uint32_t base = ring_s + stage * kStageBytes;
+    if (!odd8) {
+      // 8 lanes take a row's 16-byte pieces, 4 rows at a time
+      const int piece = lane & 7, r0 = lane >> 3;
+      if (piece < units16) {
+#pragma unroll
+        for (int u = 0; u < kTok / 4; ++u) {
+          const int r = r0 + 4 * u;
+          const bool take = (r >= v0 && r < v1) || r < v2;
+          const uint32_t at = base + r * kPitch + ((piece ^ (r & 7)) << 4);
+          const size_t off = take ? (size_t)r * c.d + piece * 16 : 0;
+          cp16(at, kp + off, take);
+          cp16(at + kTok * kPitch, vp + off, take);
+        }
+      }
+    } else {
+      const int piece = lane & 15, r0 = lane >> 4;   // 8-byte pieces, 2 rows at a time
+      if (piece * 8 < c.d) {
+#pragma unroll 4
+        for (int u = 0; u < kTok / 2; ++u) {
+          const int r = r0 + 2 * u;
+          const bool take = (r >= v0 && r < v1) || r < v2;
+          const uint32_t at = base + r * kPitch + (((piece >> 1) ^ (r & 7)) << 4) + (piece & 1) * 8;
+          const size_t off = take ? (size_t)r * c.d + piece * 8 : 0;
+          cp8(at, kp + off, take);
+          cp8(at + kTok * kPitch, vp + off, take);
+        }
+      }
+    }
+  };
+
+  // -------------------------------------------------- state of the current unit
+  uint32_t qf[NR][KS][2];                   // query rows as the B operand
+  float fq[NR][2];                          // rows 2 c4, 2 c4 + 1: logit factor (base-2)
+  int pos[NR][2];                           // their positions (-1: no such row)
+  float o[NR][KS][4];
+  float m[NR][2], M[NR][2], l[NR][2];
+  int unit = -1, len = 0;
+  int unit_first = 0;                       // tile of the run the unit's part starts at
+
+  auto load_unit = [&](int un, int ln) {
+    unit = un;
+    len = ln;
+    const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
+    const __nv_bfloat16* q = p.q + ((size_t)b * p.Hq + (size_t)h * p.g) * p.T * c.d;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = rg * RB + nr * 8 + g8;
+      float x[KB];
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < KB; e += 8) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < p.R && c4 * KB + e < c.d) w = *reinterpret_cast<const uint4*>(q + (size_t)r * c.d + c4 * KB + e);
+        const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[e + 2 * i] = __uint_as_float(w4[i] << 16);
+          x[e + 2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
+          amax = fmaxf(amax, fmaxf(fabsf(x[e + 2 * i]), fabsf(x[e + 2 * i + 1])));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // a power of two that brings the row's largest element to [2^14, 2^15)
+      const int e = min(126, max(-113, 14 - ((int)(__float_as_uint(amax) >> 23) - 127)));
+      const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qf[nr][s][0] = pack_half2(x[4 * s] * up, x[4 * s + 1] * up);
+        qf[nr][s][1] = pack_half2(x[4 * s + 2] * up, x[4 * s + 3] * up);
+      }
+      // lane (g8, c4) needs the factors of rows 2 c4 and 2 c4 + 1 (held by lanes with that g8)
+      const float f = down * p.scale_log2;
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        fq[nr][e2] = __shfl_sync(0xffffffffu, f, (2 * c4 + e2) * 4);
+        const int rr = rg * RB + nr * 8 + 2 * c4 + e2;
+        pos[nr][e2] = rr < p.R ? ln - p.T + rr % p.T : -1;
+        m[nr][e2] = M[nr][e2] = -INFINITY;
+        l[nr][e2] = 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nr][s][i] = 0.f;
+    }
+  };
+
+  // The unit's part ends: the output, or this run's piece of it.
+  auto store_unit = [&](bool whole, int slot) {
+    const int b = unit / upb, u = unit - b * upb, h = u / p.RG, rg = u - h * p.RG;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], s);
+        const int rl = nr * 8 + 2 * c4 + e, r = rg * RB + rl;
+        if (r >= p.R) continue;
+        if (whole) {
+          // o stands for o 2^(M - m); a row that saw nothing has l = 0
+          const float f = l[nr][e] == 0.f ? 0.f : ex2_approx(M[nr][e] - m[nr][e]) / l[nr][e];
+          __nv_bfloat16* dst = p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + g8 * VB;
+#pragma unroll
+          for (int s = 0; s < KS; s += 4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[nr][s + i][e] * f, o[nr][s + i][2 + e] * f);
+              w[i] = l[nr][e] == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            if (g8 * VB + 2 * s < c.d) *reinterpret_cast<uint4*>(dst + 2 * s) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          const size_t row = ((size_t)worker * 2 + slot) * RB + rl;
+          float* dst = p.part_o + row * c.d + g8 * VB;
+#pragma unroll
+          for (int s = 0; s < KS; s += 2)
+            if (g8 * VB + 2 * s < c.d)
+              *reinterpret_cast<float4*>(dst + 2 * s) =
+                  make_float4(o[nr][s][e], o[nr][s][2 + e], o[nr][s + 1][e], o[nr][s + 1][2 + e]);
+          if (g8 == 0) p.part_s[row] = make_float4(m[nr][e], l[nr][e], M[nr][e], 0.f);
+        }
+      }
+  };
+
+  // -------------------------------------------------- the run
+  const int T_run = (int)(x1 - x0);
+  Tile cur = describe(x0 + lane), nxt;
+  nxt.unit = -1; nxt.tok = 0; nxt.row = 0; nxt.ks = 0.f; nxt.lv = 0.f; nxt.len = 0;
+  if (T_run > 32) nxt = describe(x0 + 32 + lane);
+  // stage the copy of run tile i (described by cur, or by nxt when ahead of it)
+  auto issue = [&](int i, int batch) {
+    if (i < T_run) {
+      const int src = i & 31;
+      const bool ahead = (i >> 5) != batch;
+      const int tok = __shfl_sync(0xffffffffu, ahead ? nxt.tok : cur.tok, src);
+      const int ln = __shfl_sync(0xffffffffu, ahead ? nxt.len : cur.len, src);
+      const long long row = __shfl_sync(0xffffffffu, ahead ? nxt.row : cur.row, src);
+      copy_tile(i % kStages, tok, row, ln);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i, 0);
+
+  int batch = 0;
+#pragma unroll 1
+  for (int i = 0; i < T_run; ++i) {
+    if ((i >> 5) != batch) {
+      batch = i >> 5;
+      cur = nxt;
+      if (x0 + (batch + 1) * 32 < x1) nxt = describe(x0 + (batch + 1) * 32 + lane);
+    }
+    __syncwarp();                           // tile i - 1 has been read by every lane
+    issue(i + kStages - 1, batch);
+    const int un = __shfl_sync(0xffffffffu, cur.unit, i & 31);
+    const int ln = __shfl_sync(0xffffffffu, cur.len, i & 31);
+    const int tok = __shfl_sync(0xffffffffu, cur.tok, i & 31);
+    const float ks = __shfl_sync(0xffffffffu, cur.ks, i & 31);
+    const float lv = __shfl_sync(0xffffffffu, cur.lv, i & 31);
+    if (un != unit) {
+      if (unit >= 0) {
+        // the part before ends with its unit; it is whole when the unit began in this run
+        const Span s = span_of(len, p.T, p.window, p.sinks);
+        store_unit(i - unit_first >= s.tiles, 0);
+      }
+      load_unit(un, ln);
+      unit_first = i;
+    }
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    const uint8_t* sk = ring + (i % kStages) * kStageBytes;
+    const uint8_t* sv = sk + kTok * kPitch;
+
+    // S^T: tokens mt * 16 + g8 (+ 8) against rows 2 c4 (+ 1)
+    float s[NR][2][4];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nr][mt][e] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int ch = 0; ch < KB / 16; ++ch) {
+        const int t0 = mt * 16 + g8;        // t0 & 7 == (t0 + 8) & 7
+        const int at = (((c4 * (KB / 16) + ch) ^ (t0 & 7)) << 4);
+        const uint4 wa = *reinterpret_cast<const uint4*>(sk + t0 * kPitch + at);
+        const uint4 wb4 = *reinterpret_cast<const uint4*>(sk + (t0 + 8) * kPitch + at);
+        const uint32_t a4[4] = {wa.x, wa.y, wa.z, wa.w}, b4[4] = {wb4.x, wb4.y, wb4.z, wb4.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[4];
+          codes_to_half<CODE>(a4[q], a[0], a[2]);
+          codes_to_half<CODE>(b4[q], a[1], a[3]);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr][mt], a, qf[nr][ch * 4 + q][0], qf[nr][ch * 4 + q][1]);
+        }
+      }
+    }
+
+    // masks: only where some row does not see some token of the tile
+    const bool masked = tok < 0 || tok + kTok > ln - p.T + 1 ||
+                        (p.window > 0 && tok < ln - p.window && tok + kTok > p.sinks);
+    if (masked) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = tok + mt * 16 + g8 + (e >> 1) * 8, i_pos = pos[nr][e & 1];
+            const bool sees = tok >= 0 && j <= i_pos && (p.window == 0 || j > i_pos - p.window || j < p.sinks);
+            if (!sees) s[nr][mt][e] = -INFINITY;
+          }
+    }
+
+    // softmax of the tile: references m (sums) and M (outputs, which carry the V scale)
+    uint32_t pb[NR][2][2];                  // P as the B operand
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      float f[2], mt2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f[e] = fmaxf(fq[nr][e] * ks, 0x1p-126f);   // never 0: a masked logit stays -inf
+        float t = fmaxf(fmaxf(s[nr][0][e], s[nr][0][2 + e]), fmaxf(s[nr][1][e], s[nr][1][2 + e]));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        mt2[e] = t == -INFINITY ? -INFINITY : t * f[e];
+      }
+      const bool move = mt2[0] > m[nr][0] + kMoveLog2 || mt2[1] > m[nr][1] + kMoveLog2 ||
+                        mt2[0] + lv > M[nr][0] + kMoveLog2 || mt2[1] + lv > M[nr][1] + kMoveLog2;
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = mt2[e] > m[nr][e] + kMoveLog2 ? mt2[e] : m[nr][e];
+          const float Mn = mt2[e] + lv > M[nr][e] + kMoveLog2 ? mt2[e] + lv : M[nr][e];
+          const float fl = m[nr][e] == mn ? 1.f : ex2_approx(m[nr][e] - mn);   // 0 from an empty state
+          const float fo = M[nr][e] == Mn ? 1.f : ex2_approx(M[nr][e] - Mn);
+          m[nr][e] = mn;
+          M[nr][e] = Mn;
+          l[nr][e] *= fl;
+#pragma unroll
+          for (int q = 0; q < KS; ++q) {
+            o[nr][q][e] *= fo;
+            o[nr][q][2 + e] *= fo;
+          }
+        }
+      }
+      float w[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
+        // P enters the product as p 2^(lv + m - M) <= 2^8; the cap keeps 0 times it finite
+        const float cv = ex2_approx(fminf(lv + ref - M[nr][e], 100.f));
+        float sum = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const float pr = ex2_approx(fmaf(s[nr][mt][2 * e2 + e], f[e], -ref));
+            sum += pr;
+            w[mt][2 * e2 + e] = pr * cv;
+          }
+        l[nr][e] += sum;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        pb[nr][mt][0] = movmatrix(pack_half2(w[mt][0], w[mt][1]));
+        pb[nr][mt][1] = movmatrix(pack_half2(w[mt][2], w[mt][3]));
+      }
+    }
+
+    // O^T += V^T P: k index (2 c4, 2 c4 + 1, +8, +9) = tokens, rows = the lane's channels
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t vw[4][VB / 4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int tk = mt * 16 + 2 * c4 + (t & 1) + (t >> 1) * 8;
+        if constexpr (VB == 16) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sv + tk * kPitch + ((g8 ^ (tk & 7)) << 4));
+          vw[t][0] = w.x; vw[t][1] = w.y; vw[t][2] = w.z; vw[t][3] = w.w;
+        } else {
+          const uint2 w =
+              *reinterpret_cast<const uint2*>(sv + tk * kPitch + (((g8 >> 1) ^ (tk & 7)) << 4) + (g8 & 1) * 8);
+          vw[t][0] = w.x; vw[t][1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < VB / 4; ++j) {
+        uint32_t a0[4], a1[4];              // row blocks 2 j (channels 4 j, 4 j + 1) and 2 j + 1
+        codes_to_half<CODE>(__byte_perm(vw[0][j], vw[1][j], 0x5140), a0[0], a0[1]);
+        codes_to_half<CODE>(__byte_perm(vw[0][j], vw[1][j], 0x7362), a1[0], a1[1]);
+        codes_to_half<CODE>(__byte_perm(vw[2][j], vw[3][j], 0x5140), a0[2], a0[3]);
+        codes_to_half<CODE>(__byte_perm(vw[2][j], vw[3][j], 0x7362), a1[2], a1[3]);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          mma_f16(o[nr][2 * j], a0, pb[nr][mt][0], pb[nr][mt][1]);
+          mma_f16(o[nr][2 * j + 1], a1, pb[nr][mt][0], pb[nr][mt][1]);
+        }
+      }
+    }
+  }
+  // the last part: whole when all tiles of its unit lie in this run; else its
+  // piece goes to slot 0 if the unit began before the run, slot 1 if it began inside
+  const int tiles = span_of(len, p.T, p.window, p.sinks).tiles;
+  store_unit(T_run - unit_first >= tiles, unit_first == 0 && cut ? 0 : 1);
+}
+
+// Joins the pieces of the units that run borders cut: one warp group per
+// row, the pieces shared out over its warps, all loads in flight at once.
+template <int DP>
+__global__ void __launch_bounds__(kMergeThreads) join_kernel(const AttnCall p) {
+  constexpr int kW = kMergeThreads / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ float4 s_o[kW][32];
+  __shared__ float s_l[kW], s_m[kW], s_M[kW];
+  const Cache& c = p.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int upb = c.Hkv * p.RG;
+  const int groups = (p.RB + p.merge_rows - 1) / p.merge_rows;
+  const int un = blockIdx.x / groups, rg0 = (blockIdx.x - un * groups) * p.merge_rows;
+  const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
+  const Deal deal = deal_of(warp_total(p, lane, upb, false), p.workers);
+  const int tiles = span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles;
+  if (tiles == 0) return;
+  long long before = 0;
+  for (int i = lane; i < b; i += 32) before += span_of(entry_len(p, i, false), p.T, p.window, p.sinks).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  const long long u0 = before * upb + (long long)u * tiles, u1 = u0 + tiles;
+  const int w0 = run_of(deal, u0), w1 = run_of(deal, u1 - 1);
+  if (w0 == w1) return;                     // whole in one run
+  // the unit begins in run w0 (its slot 1) and before every later one (slot 0)
+  for (int rl = rg0; rl < min(rg0 + p.merge_rows, p.RB); ++rl) {
+    const int r = rg * p.RB + rl;
+    if (r >= p.R) break;
+    float m = -INFINITY, M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = w0 + warp; base <= w1; base += kW * 8) {
+      float4 st[8], ov[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int w = base + k * kW;
+        st[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w <= w1) {
+          const size_t row = ((size_t)w * 2 + (w == w0 ? 1 : 0)) * p.RB + rl;
+          st[k] = p.part_s[row];
+          if (lane * 4 < c.d) ov[k] = *reinterpret_cast<const float4*>(p.part_o + row * c.d + lane * 4);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float mn = fmaxf(m, st[k].x), Mn = fmaxf(M, st[k].z);
+        const float a = m == mn ? 1.f : ex2_approx(m - mn), bb = st[k].x == mn ? 1.f : ex2_approx(st[k].x - mn);
+        const float A = M == Mn ? 1.f : ex2_approx(M - Mn), B = st[k].z == Mn ? 1.f : ex2_approx(st[k].z - Mn);
+        l = l * a + st[k].y * bb;
+        acc.x = acc.x * A + ov[k].x * B;
+        acc.y = acc.y * A + ov[k].y * B;
+        acc.z = acc.z * A + ov[k].z * B;
+        acc.w = acc.w * A + ov[k].w * B;
+        m = mn;
+        M = Mn;
+      }
+    }
+    s_o[warp][lane] = acc;
+    if (lane == 0) {
+      s_l[warp] = l;
+      s_m[warp] = m;
+      s_M[warp] = M;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float mt = s_m[0], Mt = s_M[0];
+#pragma unroll
+      for (int k = 1; k < kW; ++k) {
+        mt = fmaxf(mt, s_m[k]);
+        Mt = fmaxf(Mt, s_M[k]);
+      }
+      float lt = 0.f;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kW; ++k) {
+        const float a = s_m[k] == mt ? 1.f : ex2_approx(s_m[k] - mt);
+        const float A = s_M[k] == Mt ? 1.f : ex2_approx(s_M[k] - Mt);
+        lt += s_l[k] * a;
+        const float4 x = s_o[k][lane];
+        t.x += x.x * A;
+        t.y += x.y * A;
+        t.z += x.z * A;
+        t.w += x.w * A;
+      }
+      if (lane * 4 < c.d) {
+        const float f = lt == 0.f ? 0.f : ex2_approx(Mt - mt) / lt;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(t.x * f, t.y * f), h1 = __floats2bfloat162_rn(t.z * f, t.w * f);
+        uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        if (lt == 0.f) w = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + lane * 4) = w;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int CODE, int DP, int NR>
+cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
+  auto kern = attention_kernel<CODE, DP, NR>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
+  if (e != cudaSuccess || p.whole) return e;
+  const int groups = (p.RB + p.merge_rows - 1) / p.merge_rows;
+  const unsigned grid = (unsigned)((long long)p.n * p.c.Hkv * p.RG * groups);
+  return launch_pdl(join_kernel<DP>, dim3(grid), dim3(kMergeThreads), 0, st, p);
+}
+
+template <int CODE>
+cudaError_t launch_code(const AttnCall& p, cudaStream_t st) {
+  const bool small = p.c.d <= 64;
+  switch (p.RB) {
+    case 8: return small ? launch_t<CODE, 64, 1>(p, st) : launch_t<CODE, 128, 1>(p, st);
+    case 16: return small ? launch_t<CODE, 64, 2>(p, st) : launch_t<CODE, 128, 2>(p, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+namespace {
+int rows_per_warp(int R) { return R <= 8 ? 8 : 16; }
+// One wave: two CTAs of kWarps warps per SM.
+long long wave_of(int sms) { return (long long)sms * 2 * kWarps; }
+size_t piece_bytes(long long workers, int RB, int d) {
+  return ((size_t)workers * 2 * RB * d * 4 + 255) / 256 * 256 + (size_t)workers * 2 * RB * 16;
+}
+}  // namespace
+
+bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, int sinks, int sms, AttnPlan* a) {
+  const long long R = (long long)Hq / s.Hkv * T;
+  a->RB = rows_per_warp((int)R);
+  a->RG = (int)((R + a->RB - 1) / a->RB);
+  // most tiles a unit can have
+  long long cap = ((long long)s.max_pages * s.page + kTok - 1) / kTok;
+  const long long upb = (long long)s.Hkv * a->RG, units = n * upb;
+  if (cap * upb >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
+  if (window > 0)
+    cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
+  // Units of at most 4 tiles are never cut: joining costs more than the 3
+  // tiles a warp would be spared.
+  a->whole = cap <= 4 ? 1 : 0;
+  a->workers = (int)std::min(wave_of(sms), a->whole ? units : units * cap);
+  const long long rows = units * a->RB;
+  a->merge_rows = (int)std::min<long long>(a->RB, std::max<long long>(1, rows / ((long long)sms * 8)));
+  a->part_s = ((size_t)a->workers * 2 * a->RB * s.d * 4 + 255) / 256 * 256;
+  a->total = piece_bytes(a->workers, a->RB, s.d);
+  return true;
+}
+
+size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms) {
+  return piece_bytes(wave_of(sms), rows_per_warp((int)std::min<long long>(1 << 20, (long long)Hq / s.Hkv * T)), s.d);
+}
+
+cudaError_t launch_attention(const AttnCall& p, cudaStream_t st) {
+  return p.c.code == KVCACHE_INT8 ? launch_code<KVCACHE_INT8>(p, st) : launch_code<KVCACHE_E4M3>(p, st);
+}
+
+}  // namespace kvcache

@@ -1,0 +1,153 @@
+// Internal declarations of the paged 8-bit KV cache: parameter blocks, the
+// workspace plan and launchers.
+#pragma once
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+#include <type_traits>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/kvcache.h"
+#include "dropkv_internal.cuh"
+
+namespace kvcache {
+
+constexpr float kScaleMin = 0x1p-120f;      // smallest scale of a page
+constexpr int kMaxHeads = 4096;
+constexpr int kMaxPages = 1 << 24;
+
+// The cache as the kernels see it.
+struct Cache {
+  uint8_t *k, *v;                // [layers][P][Hkv][page][d]
+  float *ks, *vs;                // [layers][P][Hkv]
+  int32_t *refs, *table, *count, *length;
+  int layers, Hkv, d, page, P, S, M;
+  int page_log2;
+  int code;
+  uint32_t* status;
+};
+
+// Workspace of the page calls (int32 arrays).
+struct PagePlan {
+  size_t claim;                  // [S] lowest call index that names the sequence
+  size_t mark;                   // [S] 1: the sequence is a source of this fork
+  size_t offs;                   // [S + 1] pages taken by entries before i
+  size_t entry;                  // [S][4] per entry: what the second kernel needs
+  size_t list;                   // [P] pages taken, in order
+  size_t total;                  // bytes
+};
+PagePlan make_page_plan(int S, int P);
+
+struct PageCall {
+  Cache c;
+  const int32_t *seqs, *other;   // sequences (fork: src and dst)
+  int n;
+  const int32_t* extra;          // reserve
+  const int32_t *kept_idx, *kept_len;
+  int kept_stride, share;
+  int32_t *claim, *mark, *offs, *list;
+  int4* entry;
+};
+
+cudaError_t launch_free(const PageCall& p, cudaStream_t st);
+cudaError_t launch_reserve(const PageCall& p, cudaStream_t st);
+cudaError_t launch_fork(const PageCall& p, int sms, cudaStream_t st);
+cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st);
+
+struct StoreCall {
+  Cache c;                       // k, v, ks, vs at the layer
+  const int32_t* seqs;
+  int n, rows;
+  const __nv_bfloat16 *k, *v;
+  const int32_t* counts;
+};
+cudaError_t launch_store(const StoreCall& p, cudaStream_t st);
+
+struct AttnCall {
+  Cache c;                       // k, v, ks, vs at the layer
+  const int32_t* seqs;
+  int n, Hq, T, g, R;            // R = g * T query rows per KV head
+  int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
+  int window, sinks;
+  int workers;                   // warps of the grid
+  int whole;                     // 1: every unit belongs to one warp
+  int merge_rows;                // rows a merge CTA handles
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* part_o;                 // [workers][2][RB][d]
+  float4* part_s;                // [workers][2][RB] (m, l, M, unused)
+  float scale_log2;
+};
+struct AttnPlan {
+  int RB, RG, workers, whole, merge_rows;
+  size_t part_s, total;          // byte offsets
+};
+// false: more tiles than a 32-bit count holds.
+bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, int sinks, int sms, AttnPlan* a);
+// Workspace bytes that hold for every attention call of at most T rows on the cache.
+size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms);
+cudaError_t launch_attention(const AttnCall& p, cudaStream_t st);
+
+struct WindowCall {
+  const __nv_bfloat16* q;        // [B][Hq][n_max][d]
+  __nv_bfloat16* out;
+  const int32_t* lengths;
+  int B, Hq, Hkv, g, d, n_max, window, sinks;
+  float scale_log2;
+  uint32_t* status;
+};
+cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          cudaStream_t st);
+
+// ---------------------------------------------------------------- device helpers
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t bits) { atomicOr(status, bits); }
+
+// The page scale of values whose largest magnitude is amax (finite, >= 0).
+__device__ __forceinline__ float page_scale(float amax, int code) {
+  if (code == KVCACHE_INT8) return fmaxf(__fdiv_rn(amax, 127.f), kScaleMin);
+  // amax = f 2^E with 1 <= f < 2: 448 = 1.75 * 2^8, so the exponent is E - 8
+  // when f <= 1.75, else E - 7 (amax is a bf16 number: below 2^-112 the floor rules)
+  const uint32_t b = __float_as_uint(amax);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = max(e, -120);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two values already divided by their scale, as two e4m3 codes (round to
+// nearest even, saturating; lo in the low byte).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t codes) {
+  uint32_t r;
+  asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t int8_code(float x) {   // x divided by its scale; not-a-number gives 0
+  return (uint32_t)min(127, max(-127, __float2int_rn(x))) & 0xFFu;
+}
+
+// Four codes of scale `from` rounded again at scale `to` >= from.  e4m3
+// scales are powers of two: their ratio is exact.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float from, float to, float ratio, int code) {
+  if (code == KVCACHE_INT8) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = (float)(int8_t)(w >> (8 * i));
+      r |= int8_code(__fdiv_rn(__fmul_rn(c, from), to)) << (8 * i);
+    }
+    return r;
+  }
+  const uint32_t h0 = e4m3x2_to_half2(w & 0xFFFFu), h1 = e4m3x2_to_half2(w >> 16);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+  return e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(b.x * ratio, b.y * ratio) << 16);
+}
+
+}  // namespace kvcache

@@ -1,0 +1,367 @@
+// A prompt's causal attention over a sliding window with the first tokens
+// kept visible: row i sees keys j <= i with j > i - W or j < S.
+//
+//   o_i = sum_j exp(x_ij - m_i) v_j / sum_j exp(x_ij - m_i),  x_ij = q_i . k_j / sqrt(d)
+//
+// 4 d operations for each visible (row, key): for windows of a few hundred
+// tokens and more it is bound by the tensor cores (and, one step behind, by
+// the exponentials: 128 x 128 of them against 2 x 128^3 multiply-adds per
+// tile), so the tiles go through tcgen05 with TMEM accumulators.
+//
+// A CTA holds two 128-row query tiles of one head, t and t + 1, one per
+// softmax group of four warps; thread r of a group owns TMEM lane r, the
+// whole of its row, so a row's maximum and sum need no exchange between
+// threads.  Both walk one list of 128-key tiles: those with first tokens,
+// then those the two windows reach.  Per key tile and group: S = Q K^T into
+// the group's TMEM columns; P = 2^(x - ref), with a reference that moves only
+// when it must, written back over S as bf16 pairs; O += P V with P read from
+// tensor memory.  The MMA warp alternates between the groups, so one group's
+// products run under the other's softmax; two K and two V tiles are in flight.
+// A group skips tiles outside its own window; only tiles that cut the
+// diagonal or a window's edge are masked element by element.
+#include "kvcache_internal.cuh"
+#include "sm103_ptx.cuh"
+
+namespace kvcache {
+namespace {
+
+using namespace dropkv;
+
+constexpr int kQT = 128;                          // rows of a query tile, keys of a key tile
+constexpr int kTileB = kQT * kDPad * 2;           // 32 KB: two SW128 blocks of 64 columns
+constexpr int kHalfB = kTileB / 2;
+constexpr int kProducerK = 8, kIssuer = 9, kProducerV = 10, kWinThreads = 32 * 12;   // warp 11 idle
+constexpr int kOffQ = 0, kOffK = 2 * kTileB, kOffV = 4 * kTileB, kOffSmall = 6 * kTileB;
+constexpr uint32_t kCols = 512;                   // group g: S / P at [128 g, +128), O at [256 + 128 g, +128)
+constexpr float kMove = 24.0f;                    // base-2 logarithm by which a maximum may pass its reference
+constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
+
+struct Small {
+  uint64_t qbar, kfull[2], kempty[2], vfull[2], vempty[2];
+  uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
+  uint64_t pfull[2];   // group g: its P written by the group's four warps
+  uint64_t odone[2];   // group g: its last P V complete
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kWinSmem = kOffSmall + (int)sizeof(Small) + 1024;
+static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
+
+// The key tiles of a CTA: list entry i is key tile tile(i); group g takes the
+// entries with takes(g, i).
+struct List {
+  int t[2];                                       // query tiles of the groups (-1: none)
+  int lo[2];                                      // first key tile their windows reach
+  int sink_tiles;                                 // tiles that hold first tokens
+  int ns, s2, n;                                  // tiles [0, ns), then s2, s2 + 1, ...: n entries
+  __device__ __forceinline__ int tile(int i) const { return i < ns ? i : s2 + (i - ns); }
+  __device__ __forceinline__ bool takes(int g, int i) const {
+    const int k = tile(i);
+    return i < n && k <= t[g] && (k < sink_tiles || k >= lo[g]);
+  }
+};
+__device__ __forceinline__ List make_list(const WindowCall& p, int t0, int t1) {
+  List l;
+  l.t[0] = t0;
+  l.t[1] = t1;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) l.lo[g] = p.window > 0 ? max(0, l.t[g] * kQT - p.window + 1) / kQT : 0;
+  const int lo = t0 >= 0 ? l.lo[0] : l.lo[1];
+  l.sink_tiles = p.window > 0 ? (min(p.sinks, p.n_max) + kQT - 1) / kQT : 0;
+  l.ns = min(l.sink_tiles, lo);                   // those before both windows
+  l.s2 = lo;
+  l.n = l.ns + (t1 + 1 - l.s2);
+  return l;
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(bar, parity); ++it)
+    if (global_timer_ns() - t0 > kDrain) break;
+}
+
+__device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem,
+                                              const List& list, int warp, int lane, int b, int hq, int nb) {
+  const int g = warp >> 2, quarter = warp & 3;
+  const int tg = list.t[g];
+  const int row = quarter * 32 + lane, pos = tg * kQT + row;
+  const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+  const uint32_t tS = tmem + lane_base + 128 * g, tO = tmem + lane_base + 256 + 128 * g;
+  const float scale = p.scale_log2;
+  float ref = -INFINITY, l = 0.f;
+  bool bad = tg < 0;
+  auto give_up = [&]() {
+    bad = true;
+    if (lane == 0) {
+      S.abort = 1;
+      atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
+    }
+  };
+  int seen = 0;                                   // tiles of this group so far
+  for (int i = 0; !bad && i < list.n; ++i) {
+    if (!list.takes(g, i)) continue;
+    const int kt = list.tile(i);
+    if (!__all_sync(0xffffffffu, mbar_wait(&S.sfull[g], seen & 1, &S.abort))) { give_up(); break; }
+    tc_fence_after();
+    float x[128];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
+    tmem_wait_ld();
+    const int j0 = kt * kQT;
+    // the last row of the tile reaches back to tg 128 + 127 - W + 1
+    const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
+    if (kt == tg || edge) {
+      const int lo = p.window > 0 ? pos - p.window : -1;   // keys above it are in the window
+#pragma unroll
+      for (int u = 0; u < 128; ++u) {
+        const int j = j0 + u;
+        if (!(j <= pos && (j > lo || j < p.sinks))) x[u] = -INFINITY;
+      }
+    }
+    float m8[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m8[u] = x[u];
+#pragma unroll
+    for (int u = 8; u < 128; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
+    const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale;
+    const bool need = mt > ref + kMove;
+    float factor = 1.f;
+    if (need) {
+      factor = ref == -INFINITY ? 0.f : ex2_approx(ref - mt);
+      ref = mt;
+      l *= factor;
+    }
+    // a row that has seen nothing yet keeps P = 0
+    const float r0 = ref == -INFINITY ? 0.f : ref;
+    const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-r0, -r0);
+#pragma unroll
+    for (int u = 0; u < 128; u += 2) {
+      const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
+      x[u] = ex2_approx(f2_lo(y));
+      x[u + 1] = ex2_approx(f2_hi(y));
+    }
+    uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int u = 0; u < 128; u += 2) ls2[(u >> 1) & 3] = f2_add(ls2[(u >> 1) & 3], f2_pack(x[u], x[u + 1]));
+    const uint64_t lsum = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
+    l += f2_lo(lsum) + f2_hi(lsum);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float hw[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[32 * c + 2 * q], x[32 * c + 2 * q + 1]);
+        hw[q] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+      }
+      tmem_st16(tS + 16 * c, hw);
+    }
+    // the group's P V of its tile before is complete (the commit its S
+    // signalled came after it): O follows the reference
+    if (seen > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        float o[16];
+        tmem_ld16(tO + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] *= factor;
+        tmem_st16(tO + 16 * c, o);
+      }
+    }
+    if (j0 + kQT > nb) {
+      // the sequence's last key tile (group 1's alone): rows past the end may
+      // hold anything; zero them so that 0 * NaN never reaches O
+      if (!__all_sync(0xffffffffu, mbar_wait(&S.vfull[i & 1], (i >> 1) & 1, &S.abort))) { give_up(); break; }
+      if (j0 + row >= nb) {
+        uint8_t* vrow = sm + kOffV + (i & 1) * kTileB + row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vrow + kHalfB + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.pfull[g]);
+    ++seen;
+  }
+  if (tg < 0) return;
+  const bool ok = !bad && __all_sync(0xffffffffu, mbar_wait(&S.odone[g], 0, &S.abort));
+  if (!bad && !ok) give_up();
+  if (!ok) return;
+  tc_fence_after();
+  const float inv_l = 1.0f / l;                   // a row sees itself at least
+  __nv_bfloat16* orow = p.out + (((size_t)b * p.Hq + hq) * p.n_max + pos) * p.d;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    float o[16];
+    tmem_ld16(tO + 16 * c, o);
+    tmem_wait_ld();
+    const int c0 = 16 * c;
+    if (pos < nb && c0 < p.d) {
+      uint32_t w8[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * u] * inv_l, o[2 * u + 1] * inv_l);
+        w8[u] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      *reinterpret_cast<uint4*>(orow + c0) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+      if (c0 + 8 < p.d) *reinterpret_cast<uint4*>(orow + c0 + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kWinThreads, 1)
+    window_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv, const WindowCall p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Small& S = *reinterpret_cast<Small*>(sm + kOffSmall);
+  grid_dep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.z, hq = blockIdx.y;
+  const int nb = p.lengths ? p.lengths[b] : p.n_max;
+  if (nb < 0 || nb > p.n_max) {
+    if (tid == 0 && blockIdx.x == 0 && hq == 0) atomicOr(p.status, DROPKV_FLAG_BAD_LENGTH);
+    return;
+  }
+  // pairs of query tiles from the sequence's end: the last tile is group 1's
+  const int t1 = (nb + kQT - 1) / kQT - 1 - 2 * (int)blockIdx.x, t0 = t1 - 1;
+  if (t1 < 0) return;
+  const List list = make_list(p, t0, t1);
+  const int unit = b * p.Hkv + hq / p.g;
+
+  if (tid == 0) {
+    mbar_init(&S.qbar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.kfull[i], 1); mbar_init(&S.kempty[i], 1);
+      mbar_init(&S.vfull[i], 1); mbar_init(&S.vempty[i], 1);
+      mbar_init(&S.sfull[i], 1); mbar_init(&S.pfull[i], 4);
+      mbar_init(&S.odone[i], 1);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kIssuer) tmem_alloc(&S.tmem_base, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  grid_dep_launch();
+
+  if (warp == kProducerK || warp == kProducerV) {
+    if (lane == 0) {
+      const bool is_k = warp == kProducerK;       // Q, then the K ring; or the V ring
+      if (is_k) {
+        const int zq = b * p.Hq + hq;
+        mbar_arrive_expect_tx(&S.qbar, (t0 >= 0 ? 2 : 1) * kTileB);
+        if (t0 >= 0) {
+          tma_load_3d(sm + kOffQ, &tmq, &S.qbar, 0, t0 * kQT, zq);
+          tma_load_3d(sm + kOffQ + kHalfB, &tmq, &S.qbar, 64, t0 * kQT, zq);
+        }
+        tma_load_3d(sm + kOffQ + kTileB, &tmq, &S.qbar, 0, t1 * kQT, zq);
+        tma_load_3d(sm + kOffQ + kTileB + kHalfB, &tmq, &S.qbar, 64, t1 * kQT, zq);
+      }
+      uint64_t *full = is_k ? S.kfull : S.vfull, *empty = is_k ? S.kempty : S.vempty;
+      uint8_t* ring = sm + (is_k ? kOffK : kOffV);
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; i < list.n; ++i) {
+        if (i >= 2 && !mbar_wait(&empty[i & 1], ((i >> 1) + 1) & 1, &S.abort)) { ok = false; break; }
+        uint8_t* dst = ring + (i & 1) * kTileB;
+        mbar_arrive_expect_tx(&full[i & 1], kTileB);
+        tma_load_3d(dst, map, &full[i & 1], 0, list.tile(i) * kQT, unit);
+        tma_load_3d(dst + kHalfB, map, &full[i & 1], 64, list.tile(i) * kQT, unit);
+        ++issued;
+      }
+      if (!ok) {
+        S.abort = 1;
+        atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
+      }
+      // every copy has landed before the CTA can leave
+      for (int i = max(0, issued - 2); i < issued; ++i) drain_wait(&full[i & 1], (i >> 1) & 1);
+      if (is_k) drain_wait(&S.qbar, 0);
+    }
+    __syncwarp();
+  } else if (warp == kIssuer) {
+    if (lane == 0) {
+      const uint32_t idS = umma_idesc_bf16(128, 128, 0, 0);
+      const uint32_t idO = umma_idesc_bf16(128, 128, 0, 1);
+      int seen[2] = {0, 0};
+      auto issue_S = [&](int g, int i) {          // K entry i has landed
+        const uint32_t qa = smem_addr(sm + kOffQ + g * kTileB);
+        const uint32_t kb = smem_addr(sm + kOffK + (i & 1) * kTileB);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          umma_bf16(tmem + 128 * g, desc_kmajor_sw128(qa, kQT, s), desc_kmajor_sw128(kb, kQT, s), idS, s > 0);
+        umma_commit(&S.sfull[g]);
+      };
+      bool ok = mbar_wait(&S.qbar, 0, &S.abort) && mbar_wait(&S.kfull[0], 0, &S.abort);
+      if (ok) {
+        tc_fence_after();
+        for (int g = 0; g < 2; ++g)
+          if (list.takes(g, 0)) issue_S(g, 0);
+        umma_commit(&S.kempty[0]);
+      }
+      for (int i = 0; ok && i < list.n; ++i) {
+        const bool more = i + 1 < list.n;
+        if (!(ok = mbar_wait(&S.vfull[i & 1], (i >> 1) & 1, &S.abort))) break;
+        if (more && !(ok = mbar_wait(&S.kfull[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) break;
+        const uint32_t vb = smem_addr(sm + kOffV + (i & 1) * kTileB);
+        for (int g = 0; g < 2; ++g) {
+          if (list.takes(g, i)) {
+            if (!(ok = mbar_wait(&S.pfull[g], seen[g] & 1, &S.abort))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              umma_bf16_tmem_a(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, desc_mnmajor_sw128(vb, kQT, s), idO,
+                               seen[g] > 0 || s > 0);
+            ++seen[g];
+            if (list.tile(i) == list.t[g]) umma_commit(&S.odone[g]);
+          }
+          if (list.takes(g, i + 1)) issue_S(g, i + 1);   // over P, which P V issued before it has read
+        }
+        if (!ok) break;
+        if (more) umma_commit(&S.kempty[(i + 1) & 1]);
+        umma_commit(&S.vempty[i & 1]);
+      }
+      if (!ok) {
+        S.abort = 1;
+        atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
+      }
+      // no MMA may still be writing TMEM when it is released
+      umma_commit(&S.drain);
+      drain_wait(&S.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    softmax_group(p, S, sm, tmem, list, warp, lane, b, hq, nb);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          cudaStream_t st) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(window_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWinSmem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.n_max + kQT - 1) / kQT;
+  return launch_pdl(window_prefill_kernel, dim3((tiles + 1) / 2, p.Hq, p.B), dim3(kWinThreads), kWinSmem, st, tq, tk,
+                    tv, p);
+}
+
+}  // namespace kvcache

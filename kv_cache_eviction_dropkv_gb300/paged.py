@@ -1,0 +1,186 @@
+"""A paged KV cache in 8 bits: where an eviction's kept rows go, and what
+decoding reads.
+
+Every computation runs in libdropkv.so (include/kvcache.h); this module owns
+the buffers and checks arguments.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _binding as B
+
+DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+class PagedCache:
+    """Pages of keys and values for up to `seqs` sequences on one device.
+
+    A step of a serving loop is reserve() (make room for the new tokens), then
+    per layer store() (their keys and values) and attention() (their queries).
+    fork(), copy(), compact() and free() work on whole sequences, all layers at
+    once.  Calls run on the current stream of the cache's device (or `stream`)
+    in the order they are made; calls on one cache, or on one workspace, that
+    would overlap on the GPU are the caller's to order.  Problems found on the
+    device (a sequence that does not exist, too few free pages, ...) are
+    reported by check().
+
+    Buffers (device tensors, free to read): k, v [layers, pages, Hkv, page, d]
+    codes, k_scale, v_scale [layers, pages, Hkv], refs [pages], table
+    [seqs, max_pages], count and length [seqs]."""
+
+    def __init__(self, seqs: int, Hkv: int, d: int, pages: int, page: int = 64, max_pages: Optional[int] = None,
+                 layers: int = 1, code: str = "e4m3", Hq: Optional[int] = None, T: int = 1, device=None):
+        """pages: pages in the pool; page: tokens per page (32, 64 or 128);
+        max_pages: most pages of one sequence (default: all); code: "e4m3" or
+        "int8"; Hq, T: query heads (default: Hkv) and most query rows per
+        sequence of an attention() call (they size the workspace)."""
+        if code not in B.CACHE_CODES:
+            raise ValueError("code must be one of %s" % sorted(B.CACHE_CODES))
+        max_pages = pages if max_pages is None else max_pages
+        self.layers, self.Hkv, self.d, self.page, self.pages = int(layers), int(Hkv), int(d), int(page), int(pages)
+        self.seqs, self.max_pages, self.code = int(seqs), int(max_pages), code
+        self.Hq, self.T = int(Hkv if Hq is None else Hq), int(T)
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
+        self.shape = B.kvcache_shape(self.layers, self.Hkv, self.d, self.page, self.pages, self.seqs, self.max_pages,
+                                     B.CACHE_CODES[code])
+        with torch.cuda.device(self.device):
+            self.device = torch.device("cuda", torch.cuda.current_device())
+            ws = B.kvcache_workspace_size(self.shape, self.Hq, self.T)
+            if ws == 0:
+                raise B.DropKVError(6, "kvcache_workspace_size")
+            dev = self.device
+            self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+            self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+            pool, scales = (self.layers, self.pages, self.Hkv, self.page, self.d), (self.layers, self.pages, self.Hkv)
+            self.k = torch.zeros(pool, dtype=DTYPES[code], device=dev)
+            self.v = torch.zeros(pool, dtype=DTYPES[code], device=dev)
+            self.k_scale = torch.zeros(scales, dtype=torch.float32, device=dev)
+            self.v_scale = torch.zeros(scales, dtype=torch.float32, device=dev)
+            self.refs = torch.zeros(self.pages, dtype=torch.int32, device=dev)
+            self.table = torch.full((self.seqs, self.max_pages), -1, dtype=torch.int32, device=dev)
+            self.count = torch.zeros(self.seqs, dtype=torch.int32, device=dev)
+            self.length = torch.zeros(self.seqs, dtype=torch.int32, device=dev)
+        self._buffers = B.kvcache_buffers(*(t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.refs,
+                                                                    self.table, self.count, self.length)))
+        self._shape_ref, self._buffers_ref = ctypes.byref(self.shape), ctypes.byref(self._buffers)
+        self._status, self._ws, self._ws_bytes = self.status.data_ptr(), self.workspace.data_ptr(), ws
+
+    # -------------------------------------------------------------- arguments
+    def _ints(self, name, t, *shape):
+        """Address of an int32 device tensor of `shape`."""
+        if t.dtype is not torch.int32 or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous int32 %s tensor on %s, got %s %s on %s"
+                             % (name, list(shape), self.device, t.dtype, list(t.shape), t.device))
+        return t.data_ptr()
+
+    def _rows(self, name, t, *shape):
+        """Address of a bf16 device tensor of `shape`."""
+        if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous bf16 %s tensor on %s, got %s %s on %s"
+                             % (name, list(shape), self.device, t.dtype, list(t.shape), t.device))
+        return t.data_ptr()
+
+    def _entries(self, seqs, n):
+        """Address of the sequence numbers of a call with n entries (None: 0 .. n - 1)."""
+        if n > self.seqs:
+            raise ValueError("%d entries, but the cache has %d sequences" % (n, self.seqs))
+        return None if seqs is None else self._ints("seqs", seqs, n)
+
+    def _layer(self, layer):
+        if not 0 <= layer < self.layers:
+            raise ValueError("layer %d of a cache with %d" % (layer, self.layers))
+        return layer
+
+    def _run(self, stream, call, *args):
+        """call(*args, raw stream) with the cache's device current."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if torch.cuda.current_device() == self.device.index:
+            call(*args, raw)
+        else:
+            with torch.cuda.device(self.device):
+                call(*args, raw)
+
+    # -------------------------------------------------------------- a step
+    def reserve(self, extra, seqs=None, stream=None):
+        """Room for extra[i] more tokens of sequence seqs[i] (int32 [n]); their
+        lengths grow.  All or nothing when pages run out."""
+        n = extra.shape[0]
+        self._run(stream, B.kvcache_reserve, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n,
+                  self._ints("extra", extra, n), self._ws, self._ws_bytes, self._status)
+
+    def store(self, layer, k, v, counts=None, seqs=None, stream=None):
+        """Rows 0 .. counts[i] - 1 (default: all) of k, v [n, Hkv, rows, d] bf16
+        become the last counts[i] tokens of sequence seqs[i] in `layer`."""
+        n, _, rows, _ = k.shape
+        want = (n, self.Hkv, rows, self.d)
+        self._run(stream, B.kvcache_store, self._shape_ref, self._buffers_ref, self._layer(layer),
+                  self._entries(seqs, n), n, self._rows("k", k, *want), self._rows("v", v, *want), rows,
+                  None if counts is None else self._ints("counts", counts, n), self._status)
+
+    def attention(self, layer, q, out, window: int = 0, sinks: int = 0, seqs=None, stream=None):
+        """Attention of the last T tokens of each sequence, q [n, Hq, T, d] bf16,
+        into out (same shape): row t stands at position length - T + t and sees
+        the tokens up to it; with a window only the last `window` of them and
+        the first `sinks` tokens of the sequence."""
+        n, Hq, T, _ = q.shape
+        if T > self.T or Hq != self.Hq:
+            raise ValueError("the workspace is sized for %d query heads and at most %d rows, got %d and %d"
+                             % (self.Hq, self.T, Hq, T))
+        if T == 0 or n == 0:
+            return
+        want = (n, Hq, T, self.d)
+        self._run(stream, B.kvcache_attention, self._shape_ref, self._buffers_ref, self._layer(layer),
+                  self._entries(seqs, n), n, self._rows("q", q, *want), Hq, T, int(window), int(sinks),
+                  self._rows("out", out, *want), self._ws, self._ws_bytes, self._status)
+
+    # -------------------------------------------------------------- whole sequences
+    def fork(self, src, dst, stream=None):
+        """Empty sequences dst[i] become branches of src[i] (int32 [n]): full
+        pages are shared, the partly filled last one is copied."""
+        n = src.shape[0]
+        self._run(stream, B.kvcache_fork, self._shape_ref, self._buffers_ref, self._ints("src", src, n),
+                  self._ints("dst", dst, n), self._checked(n), 1, self._ws, self._ws_bytes, self._status)
+
+    def copy(self, src, dst, stream=None):
+        """Empty sequences dst[i] become copies of src[i] that share no page."""
+        n = src.shape[0]
+        self._run(stream, B.kvcache_fork, self._shape_ref, self._buffers_ref, self._ints("src", src, n),
+                  self._ints("dst", dst, n), self._checked(n), 0, self._ws, self._ws_bytes, self._status)
+
+    def _checked(self, n):
+        self._entries(None, n)
+        return n
+
+    def compact(self, kept_idx, kept_len, seqs=None, stream=None):
+        """Evict: sequence seqs[i] keeps the kept_len[i] tokens at positions
+        kept_idx[layer, i, head, :kept_len[i]] (int32 [layers, n, Hkv, any])."""
+        n = kept_len.shape[0]
+        stride = kept_idx.shape[-1]
+        self._run(stream, B.kvcache_compact, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n,
+                  self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride), stride,
+                  self._ints("kept_len", kept_len, n), self._ws, self._ws_bytes, self._status)
+
+    def free(self, seqs, stream=None):
+        """Release every page of sequences seqs (int32 [n])."""
+        n = seqs.shape[0]
+        self._run(stream, B.kvcache_free, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n, self._status)
+
+    # -------------------------------------------------------------- status
+    def check(self, stream=None):
+        """Sync and raise if the device status word reports an error."""
+        with torch.cuda.device(self.device):
+            code, flags = B.kvcache_read_status(self.status, stream)
+        if code != 0:
+            raise B.DropKVError(code, "device status 0x%x" % flags)
+        return flags
+
+    def reset_status(self):
+        self.status.zero_()

@@ -1,0 +1,114 @@
+"""The windowed prompt attention against the plain reference in 64 bits.
+
+Bound per element: the output is rounded to bf16 (2^-8 |o|), each probability
+enters the product as bf16 (2^-8 of itself: at most 2^-8 V after the division
+by the sum, V the largest |v| the row sees); 2^-6 of that covers the fp32
+arguments and sums (below 2^-14 relative at these sizes)."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_eviction_dropkv_gb300 import DropKV, DropKVError, _binding as B
+from tests import _paged as R
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0) if torch.cuda.is_available() else None
+
+
+def _inputs(B_, Hq, Hkv, d, n, lengths, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn(B_, h, n, d, generator=g).bfloat16() for h in (Hq, Hkv, Hkv))
+    for b, L in enumerate(lengths):
+        q[b, :, L:] = float("nan")
+        k[b, :, L:] = float("nan")
+        v[b, :, L:] = float("inf")
+    return q, k, v
+
+
+def _check(op, q, k, v, lengths, window, sinks):
+    out = torch.full(q.shape, -7.25, dtype=torch.bfloat16, device=DEV)
+    op.window_attention(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(lengths, dtype=torch.int32, device=DEV), out,
+                        window, sinks)
+    ref, vmax = R.window_attention(q.float().numpy(), k.float().numpy(), v.float().numpy(), lengths, window, sinks)
+    got = out.cpu().double().numpy()
+    for b, L in enumerate(lengths):
+        assert np.all(got[b, :, L:] == -7.25)               # rows behind the sequence are left as they were
+        bound = (1 + 2.0 ** -6) * 2.0 ** -8 * (np.abs(ref[b, :, :L]) + vmax[b, :, :L, None])
+        err = np.abs(got[b, :, :L] - ref[b, :, :L])
+        assert np.all(err <= bound), float((err / bound).max())
+    return out
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 64), (3, 3, 96), (4, 2, 128), (2, 2, 8), (7, 1, 72)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 1), (5, 0), (100, 4), (127, 0), (128, 128), (129, 3),
+                                          (256, 300), (333, 7), (2000, 4)])
+def test_window_matches_reference(Hq, Hkv, d, window, sinks):
+    lengths = [700, 0, 1, 129, 384, 641]
+    op = DropKV(6, Hq, Hkv, d, 700, 1, out_rows=1, device=DEV)
+    _check(op, *_inputs(6, Hq, Hkv, d, 700, lengths, seed=d), lengths, window, sinks)
+    assert op.check() == 0
+
+
+@pytest.mark.parametrize("n", [1, 2, 127, 128, 129, 255, 256, 257])
+def test_window_short_prompts(n):
+    op = DropKV(1, 2, 1, 64, n, 1, out_rows=1, device=DEV)
+    for window, sinks in ((0, 0), (1, 0), (3, 2), (128, 1), (n, 0), (2 ** 31 - 1, 2 ** 31 - 1)):
+        _check(op, *_inputs(1, 2, 1, 64, n, [n], seed=n), [n], window, sinks)
+
+
+def test_without_a_window_it_is_the_prefill_attention():
+    op = DropKV(2, 4, 2, 128, 900, 1, out_rows=1, device=DEV)
+    q, k, v = (t.to(DEV) for t in _inputs(2, 4, 2, 128, 900, [900, 900]))
+    a, b, c = (torch.zeros_like(q) for _ in range(3))
+    op.prefill_attention(q, k, v, None, a)
+    op.window_attention(q, k, v, None, b, 0)
+    op.window_attention(q, k, v, None, c, 900, 5)
+    assert torch.equal(b, c)
+    assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -7 * float(v.float().abs().max())
+
+
+def test_first_tokens_far_from_the_window():
+    """Large first keys (an attention sink) that every row keeps, and the rows'
+    own window far behind them."""
+    op = DropKV(1, 2, 1, 128, 2100, 1, out_rows=1, device=DEV)
+    q, k, v = _inputs(1, 2, 1, 128, 2100, [2100])
+    k[0, 0, 0] = q[0, 0, :2000].float().mean(0).bfloat16() * 40
+    v[0, 0, 0] = 3.0
+    _check(op, q, k, v, [2100], 64, 1)
+    _check(op, q, k, v, [2100], 64, 0)
+
+
+def test_refusals_and_flags():
+    op = DropKV(2, 4, 2, 64, 256, 1, out_rows=1, device=DEV)
+    q, k, v = (t.to(DEV) for t in _inputs(2, 4, 2, 64, 256, [256, 256]))
+    out = torch.zeros_like(q)
+    for args in ((q, k, v, None, q, 5, 0), (q, k, v, None, out, -1, 0), (q, k, v, None, out, 5, -1)):
+        with pytest.raises(DropKVError) as e:
+            op.window_attention(*args)
+        assert e.value.code == 1
+    for args in ((q.float(), k, v, None, out, 5), (q[:1], k, v, None, out, 5), (q, k.cpu(), v, None, out, 5),
+                 (q, k, v, torch.zeros(2, dtype=torch.int64, device=DEV), out, 5)):
+        with pytest.raises(ValueError):
+            op.window_attention(*args)
+    op.window_attention(q, k, v, torch.tensor([257, -1], dtype=torch.int32, device=DEV), out, 5)
+    assert B.kvcache_read_status(op.status) == (7, B.FLAG_BAD_LENGTH)
+    assert torch.all(out == 0)
+
+
+def test_window_on_another_stream_and_in_a_graph():
+    op = DropKV(1, 4, 2, 128, 1000, 1, out_rows=1, device=DEV)
+    q, k, v = (t.to(DEV) for t in _inputs(1, 4, 2, 128, 1000, [1000]))
+    want, out = torch.zeros_like(q), torch.zeros_like(q)
+    op.window_attention(q, k, v, None, want, 300, 4)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    op.window_attention(q, k, v, None, out, 300, 4, stream=st)
+    st.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.window_attention(q, k, v, None, out, 300, 4)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
