@@ -16,7 +16,8 @@
  *                 448); the scale is the smallest power of two 2^e with
  *                 max|x| / 2^e <= 448, so that a change of scale moves no
  *                 mantissa bit of a normal code
- *   KVCACHE_INT8  code = integer in [-127, 127]; the scale is max|x| / 127
+ *   KVCACHE_INT8  code = integer in [-127, 127]; the scale is max|x| times the
+ *                 32-bit reciprocal of 127
  * and never below 2^-120.  Sequence s holds count[s] pages, table[s][0 ..
  * count[s]), length[s] tokens, and count[s] = ceil(length[s] / page).
  * refs[p] counts the sequences that hold page p; 0 means free.  A partly

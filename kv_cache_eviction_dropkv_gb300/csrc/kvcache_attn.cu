@@ -40,7 +40,6 @@
 namespace kvcache {
 namespace {
 
-using dropkv::cp_async_cg16;
 using dropkv::ex2_approx;
 using dropkv::grid_dep_launch;
 using dropkv::grid_dep_wait;
@@ -53,6 +52,7 @@ constexpr int kPitch = 128;                 // bytes of a staged row
 constexpr int kStageBytes = 2 * kTok * kPitch;   // K rows, then V rows
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 constexpr int kMergeThreads = 256;
+constexpr int kUnitCost = 2;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
 constexpr float kMoveLog2 = 8.0f;
@@ -62,6 +62,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same from a zero accumulator.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -76,6 +83,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // 16 bytes into shared memory, zeros when !take.
 __device__ __forceinline__ void cp16(uint32_t dst, const uint8_t* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_cg(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp8(uint32_t dst, const uint8_t* src, bool take) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(take ? 8 : 0) : "memory");
@@ -134,57 +144,89 @@ __device__ __forceinline__ int entry_len(const AttnCall& p, int i, bool report) 
   return len;
 }
 
-// Where the tiles of the call lie, as one warp sees it.
+// The tiles of the call lie in a row: sequence by sequence, unit by unit.  For
+// the deal each unit is kUnitCost tiles longer than it is (its query rows are
+// loaded and its output written), and the runs are equal parts of that.
 struct Deal {
-  long long total;                          // tiles of the call
-  long long share, more;                    // the first `more` runs have share + 1 tiles, the others share
+  long long share, more;                    // the first `more` runs have share + 1, the others share
 };
-__device__ __forceinline__ long long warp_total(const AttnCall& p, int lane, int upb, bool report) {
-  long long sum = 0;
-  for (int b = lane; b < p.n; b += 32) sum += span_of(entry_len(p, b, report), p.T, p.window, p.sinks).tiles;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * upb;
+__device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+__device__ __forceinline__ int entry_tiles(const AttnCall& p, int b) {
+  return span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles;
 }
-__device__ __forceinline__ Deal deal_of(long long total, int workers) {
+// Sum over entries [0, n) of tiles (and cost) per unit, over the warp's lanes.
+__device__ __forceinline__ void sum_entries(const AttnCall& p, int lane, int n, long long* tiles, long long* cost) {
+  long long a = 0, c = 0;
+  for (int b = lane; b < n; b += 32) {
+    const int t = entry_tiles(p, b);
+    a += t;
+    c += cost_of(t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    c += __shfl_xor_sync(0xffffffffu, c, o);
+  }
+  *tiles = a;
+  *cost = c;
+}
+__device__ __forceinline__ Deal make_deal(long long cost, int workers) {
   Deal d;
-  d.total = total;
-  d.share = total / workers;
-  d.more = total - d.share * workers;
+  d.share = cost / workers;
+  d.more = cost - d.share * workers;
   return d;
 }
 __device__ __forceinline__ long long run_start(const Deal& d, long long w) { return w * d.share + min(w, d.more); }
-// The run that holds tile x.
+// The run that holds cost position x.
 __device__ __forceinline__ int run_of(const Deal& d, long long x) {
   const long long cut = d.more * (d.share + 1);
   return (int)(x < cut ? x / (d.share + 1) : d.more + (x - cut) / d.share);
 }
-// The entry whose units hold position x of the running sum of tiles * upb (by
-// tile), or of upb (by unit); *cum gets the tiles before it.
-__device__ __forceinline__ int find_entry(const AttnCall& p, int lane, int upb, long long x, long long* cum) {
-  long long before = 0;
+// Cost position x as a place among the tiles: entry b, `first` tiles before
+// it, and the tile of the call that x stands at.
+struct Place {
+  int b, tiles;                             // entry and its tiles per unit (0: past the end)
+  long long first, tile;
+};
+__device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb, long long x) {
+  Place r;
+  long long cost0 = 0, tiles0 = 0;          // before this batch of entries
   for (int base = 0; base < p.n; base += 32) {
     const int b = base + lane;
-    long long t = b < p.n ? (long long)span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles * upb : 0;
-    long long inc = t;
+    const int t = b < p.n ? entry_tiles(p, b) : 0;
+    long long cost = (long long)cost_of(t) * upb, tiles = (long long)t * upb;
+    const long long own_cost = cost, own_tiles = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      const long long y = __shfl_up_sync(0xffffffffu, cost, o), z = __shfl_up_sync(0xffffffffu, tiles, o);
+      if (lane >= o) {
+        cost += y;
+        tiles += z;
+      }
     }
-    const unsigned past = __ballot_sync(0xffffffffu, before + inc > x);
+    const unsigned past = __ballot_sync(0xffffffffu, cost0 + cost > x);
     if (past) {
       const int l = __ffs(past) - 1;
-      *cum = before + __shfl_sync(0xffffffffu, inc - t, l);
-      return base + l;
+      r.b = base + l;
+      r.tiles = __shfl_sync(0xffffffffu, t, l);
+      r.first = tiles0 + __shfl_sync(0xffffffffu, tiles - own_tiles, l);
+      const long long in = x - (cost0 + __shfl_sync(0xffffffffu, cost - own_cost, l));   // < upb (tiles + kUnitCost)
+      const int per = cost_of(r.tiles);
+      const int u = (int)((unsigned)in / (unsigned)per), k = (int)in - u * per - kUnitCost;
+      r.tile = r.first + (long long)u * r.tiles + max(k, 0);
+      return r;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    cost0 += __shfl_sync(0xffffffffu, cost, 31);
+    tiles0 += __shfl_sync(0xffffffffu, tiles, 31);
   }
-  *cum = before;
-  return p.n;
+  r.b = p.n;
+  r.tiles = 0;
+  r.first = r.tile = tiles0;
+  return r;
 }
 
-template <int CODE, int DP, int NR>
+// EXACT: d == DP, so that a tile's row offsets are constants.
+template <int CODE, int DP, int NR, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p) {
   constexpr int KS = DP / 16;               // MMAs along d for S, and row blocks of O
   constexpr int KB = DP / 4, VB = DP / 8;   // bytes a lane takes of a K row, of a V row
@@ -208,37 +250,32 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
   }
 
-  // this warp's run [x0, x1)
-  const Deal deal = deal_of(warp_total(p, lane, upb, false), p.workers);
-  long long x0, x1;
+  // this warp's run: tiles [x0, x1) of the call; entry b0 holds x0 and begins at tile cum0
+  long long x0, x1, cum0;
   int b0;
-  long long cum0;
+  bool cut = false;                         // the run begins inside a unit
   if (p.whole) {
-    // runs of whole units: unit ua .. ub - 1
+    // whole units ua .. ub - 1; tiles are counted from entry b0 on
     const long long units = (long long)p.n * upb;
     const long long ua = units * worker / p.workers, ub = units * (worker + 1) / p.workers;
-    long long cum[2];
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-      const long long u = e ? ub : ua;
-      const int b = (int)(u / upb);
-      long long before = 0;
-      for (int i = lane; i < b; i += 32) before += span_of(entry_len(p, i, false), p.T, p.window, p.sinks).tiles;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-      const int t = b < p.n ? span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles : 0;
-      cum[e] = before * upb + (u - (long long)b * upb) * t;
-    }
-    x0 = cum[0];
-    x1 = cum[1];
+    b0 = (int)(ua / upb);
+    cum0 = 0;
+    x0 = (ua - (long long)b0 * upb) * entry_tiles(p, b0);
+    x1 = 0;
+    for (int b = b0; b < p.n && (long long)b * upb < ub; ++b)
+      x1 += min((long long)upb, ub - (long long)b * upb) * entry_tiles(p, b);
   } else {
-    x0 = run_start(deal, worker);
-    x1 = run_start(deal, worker + 1);
+    long long tiles, cost;
+    sum_entries(p, lane, p.n, &tiles, &cost);
+    const Deal deal = make_deal(cost * upb, p.workers);
+    const Place from = find_place(p, lane, upb, run_start(deal, worker));
+    x0 = from.tile;
+    x1 = find_place(p, lane, upb, run_start(deal, worker + 1)).tile;
+    b0 = from.b;
+    cum0 = from.first;
+    cut = from.tiles > 0 && (int)(x0 - cum0) % from.tiles != 0;
   }
   if (x0 >= x1) return;
-  b0 = find_entry(p, lane, upb, x0, &cum0);
-  // the run begins inside a unit
-  const bool cut = (int)(x0 - cum0) % span_of(entry_len(p, b0, false), p.T, p.window, p.sinks).tiles != 0;
 
   // columns past d stay zero in every stage (copies never touch them)
   if (c.d < kPitch)
@@ -307,7 +344,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     const uint8_t* kp = c.k + (tok < 0 ? 0 : row * c.d);
     const uint8_t* vp = c.v + (tok < 0 ? 0 : row * c.d);
     const uint32_t base = ring_s + stage * kStageBytes;
-    if (!odd8) {
+    if (!odd8 && v0 == 0 && v1 == kTok) {
+      // the whole tile: 8 lanes take a row's 16-byte pieces, 4 rows at a time
+      // (rows r and r + 8 share a swizzle)
+      const int piece = lane & 7, r0 = lane >> 3;
+      if (piece < units16) {
+        const uint32_t even = base + r0 * kPitch + ((piece ^ r0) << 4);
+        const uint32_t odd = base + (r0 + 4) * kPitch + ((piece ^ (r0 + 4)) << 4);
+        kp += r0 * c.d + piece * 16;
+        vp += r0 * c.d + piece * 16;
+        const int step = EXACT ? 4 * DP : 4 * c.d;
+#pragma unroll
+        for (int u = 0; u < kTok / 4; ++u) {
+          const uint32_t at = (u & 1 ? odd : even) + (u >> 1) * 8 * kPitch;
+          cp_async_cg(at, kp + u * step);
+          cp_async_cg(at + kTok * kPitch, vp + u * step);
+        }
+      }
+    } else if (!odd8) {
       // 8 lanes take a row's 16-byte pieces, 4 rows at a time
       const int piece = lane & 7, r0 = lane >> 3;
       if (piece < units16) {
@@ -485,12 +539,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     // S^T: tokens mt * 16 + g8 (+ 8) against rows 2 c4 (+ 1)
     float s[NR][2][4];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nr][mt][e] = 0.f;
-#pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
       for (int ch = 0; ch < KB / 16; ++ch) {
@@ -505,7 +553,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
           codes_to_half<CODE>(a4[q], a[0], a[2]);
           codes_to_half<CODE>(b4[q], a[1], a[3]);
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr][mt], a, qf[nr][ch * 4 + q][0], qf[nr][ch * 4 + q][1]);
+          for (int nr = 0; nr < NR; ++nr) {
+            if (ch == 0 && q == 0) mma_f16_first(s[nr][mt], a, qf[nr][0][0], qf[nr][0][1]);
+            else mma_f16(s[nr][mt], a, qf[nr][ch * 4 + q][0], qf[nr][ch * 4 + q][1]);
+          }
         }
       }
     }
@@ -635,15 +686,15 @@ __global__ void __launch_bounds__(kMergeThreads) join_kernel(const AttnCall p) {
   const int groups = (p.RB + p.merge_rows - 1) / p.merge_rows;
   const int un = blockIdx.x / groups, rg0 = (blockIdx.x - un * groups) * p.merge_rows;
   const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
-  const Deal deal = deal_of(warp_total(p, lane, upb, false), p.workers);
-  const int tiles = span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles;
+  const int tiles = entry_tiles(p, b);
   if (tiles == 0) return;
-  long long before = 0;
-  for (int i = lane; i < b; i += 32) before += span_of(entry_len(p, i, false), p.T, p.window, p.sinks).tiles;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const long long u0 = before * upb + (long long)u * tiles, u1 = u0 + tiles;
-  const int w0 = run_of(deal, u0), w1 = run_of(deal, u1 - 1);
+  long long all_tiles, all_cost, tiles0, cost0;
+  sum_entries(p, lane, p.n, &all_tiles, &all_cost);
+  sum_entries(p, lane, b, &tiles0, &cost0);
+  const Deal deal = make_deal(all_cost * upb, p.workers);
+  // cost positions of the unit's first and last tile
+  const long long u0 = cost0 * upb + (long long)u * cost_of(tiles) + kUnitCost;
+  const int w0 = run_of(deal, u0), w1 = run_of(deal, u0 + tiles - 1);
   if (w0 == w1) return;                     // whole in one run
   // the unit begins in run w0 (its slot 1) and before every later one (slot 0)
   for (int rl = rg0; rl < min(rg0 + p.merge_rows, p.RB); ++rl) {
@@ -717,10 +768,10 @@ __global__ void __launch_bounds__(kMergeThreads) join_kernel(const AttnCall p) {
   }
 }
 
-template <int CODE, int DP, int NR>
+template <int CODE, int DP, int NR, bool EXACT>
 cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
-  auto kern = attention_kernel<CODE, DP, NR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  auto kern = attention_kernel<CODE, DP, NR, EXACT>;
+  cudaError_t e = allow_smem<attention_kernel<CODE, DP, NR, EXACT>>(kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
   if (e != cudaSuccess || p.whole) return e;
@@ -731,17 +782,13 @@ cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
 
 template <int CODE>
 cudaError_t launch_code(const AttnCall& p, cudaStream_t st) {
-  const bool small = p.c.d <= 64;
-  switch (p.RB) {
-    case 8: return small ? launch_t<CODE, 64, 1>(p, st) : launch_t<CODE, 128, 1>(p, st);
-    case 16: return small ? launch_t<CODE, 64, 2>(p, st) : launch_t<CODE, 128, 2>(p, st);
-    default: return cudaErrorInvalidValue;
-  }
+  const int NR = p.RB / 8;
+  if (p.c.d == 128) return NR == 1 ? launch_t<CODE, 128, 1, true>(p, st) : launch_t<CODE, 128, 2, true>(p, st);
+  if (p.c.d == 64) return NR == 1 ? launch_t<CODE, 64, 1, true>(p, st) : launch_t<CODE, 64, 2, true>(p, st);
+  if (p.c.d > 64) return NR == 1 ? launch_t<CODE, 128, 1, false>(p, st) : launch_t<CODE, 128, 2, false>(p, st);
+  return NR == 1 ? launch_t<CODE, 64, 1, false>(p, st) : launch_t<CODE, 64, 2, false>(p, st);
 }
 
-}  // namespace
-
-namespace {
 int rows_per_warp(int R) { return R <= 8 ? 8 : 16; }
 // One wave: two CTAs of kWarps warps per SM.
 long long wave_of(int sms) { return (long long)sms * 2 * kWarps; }

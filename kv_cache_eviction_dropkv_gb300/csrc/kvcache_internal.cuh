@@ -2,6 +2,7 @@
 // workspace plan and launchers.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <type_traits>
@@ -102,12 +103,27 @@ struct WindowCall {
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t st);
 
+// Allow a kernel its dynamic shared memory on the current device, once per
+// device (the setting stays; making it at every launch costs host time).
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};     // devices 0 .. 63
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // ---------------------------------------------------------------- device helpers
 __device__ __forceinline__ void flag(uint32_t* status, uint32_t bits) { atomicOr(status, bits); }
 
 // The page scale of values whose largest magnitude is amax (finite, >= 0).
 __device__ __forceinline__ float page_scale(float amax, int code) {
-  if (code == KVCACHE_INT8) return fmaxf(__fdiv_rn(amax, 127.f), kScaleMin);
+  if (code == KVCACHE_INT8) return fmaxf(__fmul_rn(amax, 1.0f / 127.0f), kScaleMin);
   // amax = f 2^E with 1 <= f < 2: 448 = 1.75 * 2^8, so the exponent is E - 8
   // when f <= 1.75, else E - 7 (amax is a bf16 number: below 2^-112 the floor rules)
   const uint32_t b = __float_as_uint(amax);

@@ -356,8 +356,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t st) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(window_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWinSmem);
+  const cudaError_t e = allow_smem<window_prefill_kernel>(kWinSmem);
   if (e != cudaSuccess) return e;
   const int tiles = (p.n_max + kQT - 1) / kQT;
   return launch_pdl(window_prefill_kernel, dim3((tiles + 1) / 2, p.Hq, p.B), dim3(kWinThreads), kWinSmem, st, tq, tk,

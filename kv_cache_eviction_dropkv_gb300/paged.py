@@ -13,6 +13,11 @@ import torch
 
 from . import _binding as B
 
+# Plain lookups of the current stream's handle and the current device: a small
+# call (one new token) costs a few microseconds, and building a Stream object
+# would add two.
+_current_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
 DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
 
 
@@ -66,31 +71,28 @@ class PagedCache:
             self.table = torch.full((self.seqs, self.max_pages), -1, dtype=torch.int32, device=dev)
             self.count = torch.zeros(self.seqs, dtype=torch.int32, device=dev)
             self.length = torch.zeros(self.seqs, dtype=torch.int32, device=dev)
+        self._index = self.device.index
         self._buffers = B.kvcache_buffers(*(t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.refs,
                                                                     self.table, self.count, self.length)))
         self._shape_ref, self._buffers_ref = ctypes.byref(self.shape), ctypes.byref(self._buffers)
         self._status, self._ws, self._ws_bytes = self.status.data_ptr(), self.workspace.data_ptr(), ws
 
     # -------------------------------------------------------------- arguments
-    def _ints(self, name, t, *shape):
-        """Address of an int32 device tensor of `shape`."""
-        if t.dtype is not torch.int32 or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            raise ValueError("%s: expected a contiguous int32 %s tensor on %s, got %s %s on %s"
-                             % (name, list(shape), self.device, t.dtype, list(t.shape), t.device))
+    def _tensor(self, name, t, dtype, shape):
+        """Address of a contiguous device tensor of that type and shape."""
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous %s %s tensor on %s, got %s %s on %s"
+                             % (name, dtype, list(shape), self.device, t.dtype, list(t.shape), t.device))
         return t.data_ptr()
 
-    def _rows(self, name, t, *shape):
-        """Address of a bf16 device tensor of `shape`."""
-        if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            raise ValueError("%s: expected a contiguous bf16 %s tensor on %s, got %s %s on %s"
-                             % (name, list(shape), self.device, t.dtype, list(t.shape), t.device))
-        return t.data_ptr()
+    def _ints(self, name, t, *shape):
+        return self._tensor(name, t, torch.int32, shape)
 
     def _entries(self, seqs, n):
         """Address of the sequence numbers of a call with n entries (None: 0 .. n - 1)."""
         if n > self.seqs:
             raise ValueError("%d entries, but the cache has %d sequences" % (n, self.seqs))
-        return None if seqs is None else self._ints("seqs", seqs, n)
+        return None if seqs is None else self._tensor("seqs", seqs, torch.int32, (n,))
 
     def _layer(self, layer):
         if not 0 <= layer < self.layers:
@@ -100,9 +102,10 @@ class PagedCache:
     def _run(self, stream, call, *args):
         """call(*args, raw stream) with the cache's device current."""
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if torch.cuda.current_device() == self.device.index:
+            raw = _current_raw_stream(self._index)
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if _current_device() == self._index:
             call(*args, raw)
         else:
             with torch.cuda.device(self.device):
@@ -120,9 +123,9 @@ class PagedCache:
         """Rows 0 .. counts[i] - 1 (default: all) of k, v [n, Hkv, rows, d] bf16
         become the last counts[i] tokens of sequence seqs[i] in `layer`."""
         n, _, rows, _ = k.shape
-        want = (n, self.Hkv, rows, self.d)
+        want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
         self._run(stream, B.kvcache_store, self._shape_ref, self._buffers_ref, self._layer(layer),
-                  self._entries(seqs, n), n, self._rows("k", k, *want), self._rows("v", v, *want), rows,
+                  self._entries(seqs, n), n, self._tensor("k", k, bf16, want), self._tensor("v", v, bf16, want), rows,
                   None if counts is None else self._ints("counts", counts, n), self._status)
 
     def attention(self, layer, q, out, window: int = 0, sinks: int = 0, seqs=None, stream=None):
@@ -136,10 +139,10 @@ class PagedCache:
                              % (self.Hq, self.T, Hq, T))
         if T == 0 or n == 0:
             return
-        want = (n, Hq, T, self.d)
+        want, bf16 = (n, Hq, T, self.d), torch.bfloat16
         self._run(stream, B.kvcache_attention, self._shape_ref, self._buffers_ref, self._layer(layer),
-                  self._entries(seqs, n), n, self._rows("q", q, *want), Hq, T, int(window), int(sinks),
-                  self._rows("out", out, *want), self._ws, self._ws_bytes, self._status)
+                  self._entries(seqs, n), n, self._tensor("q", q, bf16, want), Hq, T, window, sinks,
+                  self._tensor("out", out, bf16, want), self._ws, self._ws_bytes, self._status)
 
     # -------------------------------------------------------------- whole sequences
     def fork(self, src, dst, stream=None):

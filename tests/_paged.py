@@ -12,7 +12,7 @@ FLAG = dict(NONFINITE=0x2, BAD_LENGTH=0x4, BAD_K=0x8, OVERFLOW=0x10, NO_PAGES=0x
 
 def page_scale(amax, code):
     if code == "int8":
-        return max(float(np.float32(amax) / np.float32(127)), SCALE_MIN)
+        return max(float(np.float32(amax) * (np.float32(1) / np.float32(127))), SCALE_MIN)
     if amax == 0:
         return SCALE_MIN
     e = math.ceil(math.log2(amax / 448.0))
