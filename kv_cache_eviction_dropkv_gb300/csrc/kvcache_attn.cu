@@ -41,16 +41,35 @@ namespace kvcache {
 namespace {
 
 using dropkv::ex2_approx;
+using dropkv::f2_add;
+using dropkv::f2_fma;
+using dropkv::f2_hi;
+using dropkv::f2_lo;
+using dropkv::f2_mul;
+using dropkv::f2_pack;
 using dropkv::grid_dep_launch;
 using dropkv::grid_dep_wait;
 using dropkv::launch_pdl;
 
 constexpr int kTok = 32;                    // tokens of a tile
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kPitch = 128;                 // bytes of a staged row
 constexpr int kStageBytes = 2 * kTok * kPitch;   // K rows, then V rows
-constexpr int kSmem = kWarps * kStages * kStageBytes;
+constexpr int kMeta = 64;                   // tile descriptions a warp holds (two batches of 32)
+struct alignas(16) Tile {
+  long long at;                             // byte offset of its first row in the layer's K or V
+  int tok;                                  // first token
+  int len;                                  // tokens of its sequence
+  int unit;                                 // entry * (Hkv * RG) + head * RG + row group
+  float ks, lv;                             // K scale, log2 of the V scale
+  int how;                                  // kPartial, kMasked, kUnreadable
+};
+constexpr int kPartial = 1;                 // some of its slots are seen by no row
+constexpr int kMasked = 2;                  // some row does not see some of its tokens
+constexpr int kUnreadable = 4;              // its table entry is no page
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kMergeThreads = 256;
 constexpr int kUnitCost = 2;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
@@ -284,20 +303,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   __syncwarp();
 
   // -------------------------------------------------- tile descriptions
-  // Lane l describes tile x0 + 32 k + l of the run: its unit, first token,
-  // cache row and scales; the warp broadcasts them when the tile comes up.
-  struct Tile {
-    int unit, tok;                          // b * upb + u;  first token, -1: unreadable page
-    long long row;                          // first cache row
-    float ks, lv;                           // K scale, log2 of the V scale
-    int len;
-  };
+  // Lane l describes tile x0 + 32 k + l of the run (table entry and scales:
+  // two dependent loads, 32 tiles ahead of their use).
+  Tile* meta = reinterpret_cast<Tile*>(smem + kRingBytes) + warp * kMeta;
   int wb = b0;                              // entry the lane's cursor stands at
   long long wcum = cum0;
-  auto describe = [&](long long x) {
-    Tile t;
-    t.unit = -1; t.tok = 0; t.row = 0; t.ks = 0.f; t.lv = 0.f; t.len = 0;
-    if (x >= x1) return t;
+  auto describe = [&](long long x, Tile* to) {
+    if (x >= x1) return;
     int len = entry_len(p, wb, false);
     Span s = span_of(len, p.T, p.window, p.sinks);
     while (x >= wcum + (long long)s.tiles * upb) {
@@ -307,44 +319,51 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
       s = span_of(len, p.T, p.window, p.sinks);
     }
     const int y = (int)(x - wcum), u = y / s.tiles, k = y - u * s.tiles;
-    const int tile = k < s.ns ? k : s.s2 + (k - s.ns);
+    const int tok = (k < s.ns ? k : s.s2 + (k - s.ns)) * kTok;
     const int sq = p.seqs ? p.seqs[wb] : wb;
-    t.unit = wb * upb + u;
-    t.tok = tile * kTok;
+    const int pg = c.table[(size_t)sq * c.M + (tok >> c.page_log2)];
+    Tile t;
+    t.tok = tok;
     t.len = len;
-    const int pg = c.table[(size_t)sq * c.M + (t.tok >> c.page_log2)];
+    t.unit = wb * upb + u;
+    // slots [lo, len) and the first tokens are seen by some row, every row
+    // sees up to len - T and (with a window) from len - window on
+    const bool first = tok + kTok <= p.sinks;
+    t.how = (tok + kTok > len || (tok < s.lo && !first) ? kPartial : 0) |
+            (tok + kTok > len - p.T + 1 || (p.window > 0 && tok < len - p.window && !first) ? kMasked : 0);
     if (pg < 0 || pg >= c.P) {
       flag(c.status, KVCACHE_FLAG_BAD_PAGE);
-      t.tok = -1;
+      t.at = 0;
+      t.ks = 0.f;
+      t.lv = 0.f;
+      t.how = kPartial | kMasked | kUnreadable;
     } else {
       const size_t ur = (size_t)pg * c.Hkv + u / p.RG;
-      t.row = (long long)(ur * c.page + (t.tok & (c.page - 1)));
+      t.at = (long long)(ur * c.page + (tok & (c.page - 1))) * c.d;
       t.ks = c.ks[ur];
       t.lv = __log2f(fmaxf(c.vs[ur], 0x1p-126f));
     }
-    return t;
+    *to = t;
   };
 
   // -------------------------------------------------- copies
   const int units16 = (c.d + 15) >> 4;      // 16-byte pieces of a row (the last may be 8 bytes)
   const bool odd8 = (c.d & 15) != 0;
-  auto copy_tile = [&](int stage, int tok, long long row, int len) {
-    // slots some row sees: [lo, len) and the first tokens
-    int v0 = 0, v1 = kTok, v2 = 0;          // rows [v0, v1) and [0, v2)
-    if (tok < 0) {
-      v1 = 0;
-    } else {
-      v1 = min(kTok, len - tok);
-      if (p.window > 0) {
-        const int lo = max(0, max(0, len - p.T) - p.window + 1);
-        v0 = max(0, lo - tok);
-        v2 = min(min(kTok, len - tok), p.sinks - tok);
+  auto copy_tile = [&](int stage, const Tile* from) {
+    const long long at0 = from->at;
+    const int tok = from->tok, len = from->len, how = from->how;
+    const uint8_t* kp = c.k + at0;
+    const uint8_t* vp = c.v + at0;
+    const uint32_t base = ring_s + stage * kStageBytes;
+    int v0 = 0, v1 = kTok, v2 = 0;          // rows [v0, v1) and [0, v2) are seen by some row
+    if (how & kPartial) {
+      v1 = how & kUnreadable ? 0 : min(kTok, len - tok);
+      if (p.window > 0 && !(how & kUnreadable)) {
+        v0 = max(0, span_of(len, p.T, p.window, p.sinks).lo - tok);
+        v2 = min(v1, p.sinks - tok);
       }
     }
-    const uint8_t* kp = c.k + (tok < 0 ? 0 : row * c.d);
-    const uint8_t* vp = c.v + (tok < 0 ? 0 : row * c.d);
-    const uint32_t base = ring_s + stage * kStageBytes;
-    if (!odd8 && v0 == 0 && v1 == kTok) {
+    if (!odd8 && !(how & kPartial)) {
       // the whole tile: 8 lanes take a row's 16-byte pieces, 4 rows at a time
       // (rows r and r + 8 share a swizzle)
       const int piece = lane & 7, r0 = lane >> 3;
@@ -489,39 +508,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 
   // -------------------------------------------------- the run
   const int T_run = (int)(x1 - x0);
-  Tile cur = describe(x0 + lane), nxt;
-  nxt.unit = -1; nxt.tok = 0; nxt.row = 0; nxt.ks = 0.f; nxt.lv = 0.f; nxt.len = 0;
-  if (T_run > 32) nxt = describe(x0 + 32 + lane);
-  // stage the copy of run tile i (described by cur, or by nxt when ahead of it)
-  auto issue = [&](int i, int batch) {
-    if (i < T_run) {
-      const int src = i & 31;
-      const bool ahead = (i >> 5) != batch;
-      const int tok = __shfl_sync(0xffffffffu, ahead ? nxt.tok : cur.tok, src);
-      const int ln = __shfl_sync(0xffffffffu, ahead ? nxt.len : cur.len, src);
-      const long long row = __shfl_sync(0xffffffffu, ahead ? nxt.row : cur.row, src);
-      copy_tile(i % kStages, tok, row, ln);
-    }
+  describe(x0 + lane, meta + lane);
+  __syncwarp();
+  auto issue = [&](int i) {                 // stage the copy of run tile i
+    if (i < T_run) copy_tile(i % kStages, meta + (i & (kMeta - 1)));
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i, 0);
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-  int batch = 0;
 #pragma unroll 1
   for (int i = 0; i < T_run; ++i) {
-    if ((i >> 5) != batch) {
-      batch = i >> 5;
-      cur = nxt;
-      if (x0 + (batch + 1) * 32 < x1) nxt = describe(x0 + (batch + 1) * 32 + lane);
-    }
+    // the batch after this one takes the place of the one before
+    if ((i & 31) == 0) describe(x0 + i + 32 + lane, meta + ((i + 32) & (kMeta - 1)) + lane);
     __syncwarp();                           // tile i - 1 has been read by every lane
-    issue(i + kStages - 1, batch);
-    const int un = __shfl_sync(0xffffffffu, cur.unit, i & 31);
-    const int ln = __shfl_sync(0xffffffffu, cur.len, i & 31);
-    const int tok = __shfl_sync(0xffffffffu, cur.tok, i & 31);
-    const float ks = __shfl_sync(0xffffffffu, cur.ks, i & 31);
-    const float lv = __shfl_sync(0xffffffffu, cur.lv, i & 31);
+    issue(i + kStages - 1);
+    const Tile* now = meta + (i & (kMeta - 1));
+    const int un = now->unit, tok = now->tok, ln = now->len, how = now->how;
+    const float ks = now->ks, lv = now->lv;
     if (un != unit) {
       if (unit >= 0) {
         // the part before ends with its unit; it is whole when the unit began in this run
@@ -562,9 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     }
 
     // masks: only where some row does not see some token of the tile
-    const bool masked = tok < 0 || tok + kTok > ln - p.T + 1 ||
-                        (p.window > 0 && tok < ln - p.window && tok + kTok > p.sinks);
-    if (masked) {
+    if (how & kMasked) {
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = tok + mt * 16 + g8 + (e >> 1) * 8, i_pos = pos[nr][e & 1];
-            const bool sees = tok >= 0 && j <= i_pos && (p.window == 0 || j > i_pos - p.window || j < p.sinks);
+            const bool sees = !(how & kUnreadable) && j <= i_pos && (p.window == 0 || j > i_pos - p.window || j < p.sinks);
             if (!sees) s[nr][mt][e] = -INFINITY;
           }
     }
@@ -610,28 +612,25 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
           }
         }
       }
-      float w[2][4];
+      // rows 2 c4 and 2 c4 + 1 side by side in packed pairs
+      const float r0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0], r1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
+      const uint64_t f2 = f2_pack(f[0], f[1]), n2 = f2_pack(-r0, -r1);
+      // P enters the product as p 2^(lv + m - M) <= 2^8; the cap keeps 0 times it finite
+      const uint64_t cv2 = f2_pack(ex2_approx(fminf(lv + r0 - M[nr][0], 100.f)),
+                                   ex2_approx(fminf(lv + r1 - M[nr][1], 100.f)));
+      uint64_t sum2 = 0ull;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ref = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
-        // P enters the product as p 2^(lv + m - M) <= 2^8; the cap keeps 0 times it finite
-        const float cv = ex2_approx(fminf(lv + ref - M[nr][e], 100.f));
-        float sum = 0.f;
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const float pr = ex2_approx(fmaf(s[nr][mt][2 * e2 + e], f[e], -ref));
-            sum += pr;
-            w[mt][2 * e2 + e] = pr * cv;
-          }
-        l[nr][e] += sum;
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        pb[nr][mt][0] = movmatrix(pack_half2(w[mt][0], w[mt][1]));
-        pb[nr][mt][1] = movmatrix(pack_half2(w[mt][2], w[mt][3]));
-      }
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const uint64_t x2 = f2_fma(f2_pack(s[nr][mt][2 * e2], s[nr][mt][2 * e2 + 1]), f2, n2);
+          const uint64_t p2 = f2_pack(ex2_approx(f2_lo(x2)), ex2_approx(f2_hi(x2)));
+          sum2 = f2_add(sum2, p2);
+          const uint64_t w2 = f2_mul(p2, cv2);
+          pb[nr][mt][e2] = movmatrix(pack_half2(f2_lo(w2), f2_hi(w2)));
+        }
+      l[nr][0] += f2_lo(sum2);
+      l[nr][1] += f2_hi(sum2);
     }
 
     // O^T += V^T P: k index (2 c4, 2 c4 + 1, +8, +9) = tokens, rows = the lane's channels
