@@ -133,13 +133,14 @@ dropkv_status kvcache_attention(const kvcache_shape* shape, const kvcache_buffer
   p.n = n; p.Hq = Hq; p.T = T;
   p.g = Hq / shape->Hkv;
   p.R = p.g * T;
-  p.RB = a.RB; p.RG = a.RG; p.workers = a.workers; p.whole = a.whole; p.merge_rows = a.merge_rows;
+  p.RB = a.RB; p.RG = a.RG; p.workers = a.workers; p.whole = a.whole; p.by_unit = a.by_unit; p.rowwise = a.rowwise;
   p.window = window;
   p.sinks = sinks;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_s = reinterpret_cast<float4*>(ws + a.part_s);
+  p.cuts = reinterpret_cast<int2*>(ws + a.cuts);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape->d));
   return launched(launch_attention(p, stream));
 }

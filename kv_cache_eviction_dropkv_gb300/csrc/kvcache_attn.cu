@@ -70,7 +70,7 @@ constexpr int kMasked = 2;                  // some row does not see some of its
 constexpr int kUnreadable = 4;              // its table entry is no page
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
-constexpr int kMergeThreads = 256;
+constexpr int kJoinThreads = 128, kJoinWide = 512;
 constexpr int kUnitCost = 2;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
@@ -206,6 +206,7 @@ __device__ __forceinline__ int run_of(const Deal& d, long long x) {
 struct Place {
   int b, tiles;                             // entry and its tiles per unit (0: past the end)
   long long first, tile;
+  long long last;                           // cost position of the last tile of x's unit
 };
 __device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb, long long x) {
   Place r;
@@ -233,6 +234,7 @@ __device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb
       const int per = cost_of(r.tiles);
       const int u = (int)((unsigned)in / (unsigned)per), k = (int)in - u * per - kUnitCost;
       r.tile = r.first + (long long)u * r.tiles + max(k, 0);
+      r.last = x - (k + kUnitCost) + per - 1;
       return r;
     }
     cost0 += __shfl_sync(0xffffffffu, cost, 31);
@@ -241,6 +243,7 @@ __device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb
   r.b = p.n;
   r.tiles = 0;
   r.first = r.tile = tiles0;
+  r.last = x;
   return r;
 }
 
@@ -265,6 +268,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   // rows of sequences with nothing to read
   for (int b = worker; b < p.n; b += p.workers) {
     if (span_of(entry_len(p, b, true), p.T, p.window, p.sinks).tiles > 0) continue;
+    if (!p.whole && p.by_unit)
+      for (int u = lane; u < upb; u += 32) p.cuts[b * upb + u] = make_int2(-1, 0);
     uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * p.T * c.d);
     for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
   }
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   long long x0, x1, cum0;
   int b0;
   bool cut = false;                         // the run begins inside a unit
+  int run_last = 0;                         // last run of the unit the next run begins inside
   if (p.whole) {
     // whole units ua .. ub - 1; tiles are counted from entry b0 on
     const long long units = (long long)p.n * upb;
@@ -289,11 +295,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     const Deal deal = make_deal(cost * upb, p.workers);
     const Place from = find_place(p, lane, upb, run_start(deal, worker));
     x0 = from.tile;
-    x1 = find_place(p, lane, upb, run_start(deal, worker + 1)).tile;
+    const Place to = find_place(p, lane, upb, run_start(deal, worker + 1));
+    x1 = to.tile;
+    if (to.tiles > 0) run_last = run_of(deal, to.last);
     b0 = from.b;
     cum0 = from.first;
     cut = from.tiles > 0 && (int)(x0 - cum0) % from.tiles != 0;
   }
+  if (!p.whole && !p.by_unit && lane == 0) p.cuts[worker] = make_int2(-1, 0);
   if (x0 >= x1) return;
 
   // columns past d stay zero in every stage (copies never touch them)
@@ -470,6 +479,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 
   // The unit's part ends: the output, or this run's piece of it.
   auto store_unit = [&](bool whole, int slot) {
+    if (!p.whole && lane == 0) {
+      // who joins it: the run it begins in says so
+      if (p.by_unit) {
+        if (whole) p.cuts[unit] = make_int2(-1, 0);
+        else if (slot == 1) p.cuts[unit] = make_int2(worker, run_last);
+      } else if (slot == 1 && !whole) {
+        p.cuts[worker] = make_int2(unit, run_last);
+      }
+    }
     const int b = unit / upb, u = unit - b * upb, h = u / p.RG, rg = u - h * p.RG;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
@@ -670,100 +688,96 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   store_unit(T_run - unit_first >= tiles, unit_first == 0 && cut ? 0 : 1);
 }
 
-// Joins the pieces of the units that run borders cut: one warp group per
-// row, the pieces shared out over its warps, all loads in flight at once.
-template <int DP>
-__global__ void __launch_bounds__(kMergeThreads) join_kernel(const AttnCall p) {
-  constexpr int kW = kMergeThreads / 32;
+// Joins the pieces of the units that run borders cut, in run order.  Each
+// unit's first run has left word of its last one (per unit, or per run where
+// there are more units than runs), so nothing is searched for here.
+// ROWWISE: a CTA joins one row of a unit, its warps sharing out the pieces
+// with all loads in flight at once (few units, up to hundreds of pieces
+// each); else each warp joins rows of the unit on its own (few pieces each).
+struct Joined {
+  float m, M, l;
+  float4 o;
+};
+__device__ __forceinline__ void join_in(Joined& a, float m, float l, float M, const float4& o) {
+  const float mn = fmaxf(a.m, m), Mn = fmaxf(a.M, M);
+  const float fa = a.m == mn ? 1.f : ex2_approx(a.m - mn), fb = m == mn ? 1.f : ex2_approx(m - mn);
+  const float Fa = a.M == Mn ? 1.f : ex2_approx(a.M - Mn), Fb = M == Mn ? 1.f : ex2_approx(M - Mn);
+  a.l = a.l * fa + l * fb;
+  a.o.x = a.o.x * Fa + o.x * Fb;
+  a.o.y = a.o.y * Fa + o.y * Fb;
+  a.o.z = a.o.z * Fa + o.z * Fb;
+  a.o.w = a.o.w * Fa + o.w * Fb;
+  a.m = mn;
+  a.M = Mn;
+}
+
+template <bool ROWWISE>
+__global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kernel(const AttnCall p) {
+  constexpr int kW = (ROWWISE ? kJoinWide : kJoinThreads) / 32, kBatch = ROWWISE ? 10 : 4;
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float4 s_o[kW][32];
   __shared__ float s_l[kW], s_m[kW], s_M[kW];
   const Cache& c = p.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int2 cut = p.cuts[blockIdx.x];
+  if (cut.x < 0) return;
+  const int un = p.by_unit ? (int)blockIdx.x : cut.x, w0 = p.by_unit ? cut.x : (int)blockIdx.x, w1 = cut.y;
   const int upb = c.Hkv * p.RG;
-  const int groups = (p.RB + p.merge_rows - 1) / p.merge_rows;
-  const int un = blockIdx.x / groups, rg0 = (blockIdx.x - un * groups) * p.merge_rows;
   const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
-  const int tiles = entry_tiles(p, b);
-  if (tiles == 0) return;
-  long long all_tiles, all_cost, tiles0, cost0;
-  sum_entries(p, lane, p.n, &all_tiles, &all_cost);
-  sum_entries(p, lane, b, &tiles0, &cost0);
-  const Deal deal = make_deal(all_cost * upb, p.workers);
-  // cost positions of the unit's first and last tile
-  const long long u0 = cost0 * upb + (long long)u * cost_of(tiles) + kUnitCost;
-  const int w0 = run_of(deal, u0), w1 = run_of(deal, u0 + tiles - 1);
-  if (w0 == w1) return;                     // whole in one run
-  // the unit begins in run w0 (its slot 1) and before every later one (slot 0)
-  for (int rl = rg0; rl < min(rg0 + p.merge_rows, p.RB); ++rl) {
-    const int r = rg * p.RB + rl;
-    if (r >= p.R) break;
-    float m = -INFINITY, M = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int base = w0 + warp; base <= w1; base += kW * 8) {
-      float4 st[8], ov[8];
+  const int rows = min(p.RB, p.R - rg * p.RB);
+  const bool cols = lane * 4 < c.d;
+  // pieces w0 + first, w0 + first + step, ... of row rl; the unit begins in
+  // run w0 (its slot 1) and before every later one (slot 0)
+  auto take = [&](int rl, int first, int step) {
+    Joined a;
+    a.m = a.M = -INFINITY;
+    a.l = 0.f;
+    a.o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = w0 + first; base <= w1; base += step * kBatch) {
+      float4 st[kBatch], ov[kBatch];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int w = base + k * kW;
+      for (int k = 0; k < kBatch; ++k) {
+        const int w = base + k * step;
         st[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
         ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (w <= w1) {
           const size_t row = ((size_t)w * 2 + (w == w0 ? 1 : 0)) * p.RB + rl;
           st[k] = p.part_s[row];
-          if (lane * 4 < c.d) ov[k] = *reinterpret_cast<const float4*>(p.part_o + row * c.d + lane * 4);
+          if (cols) ov[k] = *reinterpret_cast<const float4*>(p.part_o + row * c.d + lane * 4);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float mn = fmaxf(m, st[k].x), Mn = fmaxf(M, st[k].z);
-        const float a = m == mn ? 1.f : ex2_approx(m - mn), bb = st[k].x == mn ? 1.f : ex2_approx(st[k].x - mn);
-        const float A = M == Mn ? 1.f : ex2_approx(M - Mn), B = st[k].z == Mn ? 1.f : ex2_approx(st[k].z - Mn);
-        l = l * a + st[k].y * bb;
-        acc.x = acc.x * A + ov[k].x * B;
-        acc.y = acc.y * A + ov[k].y * B;
-        acc.z = acc.z * A + ov[k].z * B;
-        acc.w = acc.w * A + ov[k].w * B;
-        m = mn;
-        M = Mn;
-      }
+      for (int k = 0; k < kBatch; ++k) join_in(a, st[k].x, st[k].y, st[k].z, ov[k]);
     }
-    s_o[warp][lane] = acc;
+    return a;
+  };
+  auto write = [&](int rl, const Joined& a) {
+    if (!cols) return;
+    const float f = a.l == 0.f ? 0.f : ex2_approx(a.M - a.m) / a.l;
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.o.x * f, a.o.y * f), h1 = __floats2bfloat162_rn(a.o.z * f, a.o.w * f);
+    uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    if (a.l == 0.f) w = make_uint2(0u, 0u);
+    const int r = rg * p.RB + rl;
+    *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + lane * 4) = w;
+  };
+  if constexpr (ROWWISE) {
+    const int rl = blockIdx.y;
+    if (rl >= rows) return;
+    Joined a = take(rl, warp, kW);
+    s_o[warp][lane] = a.o;
     if (lane == 0) {
-      s_l[warp] = l;
-      s_m[warp] = m;
-      s_M[warp] = M;
+      s_l[warp] = a.l;
+      s_m[warp] = a.m;
+      s_M[warp] = a.M;
     }
     __syncthreads();
-    if (warp == 0) {
-      float mt = s_m[0], Mt = s_M[0];
+    if (warp > 0) return;
 #pragma unroll
-      for (int k = 1; k < kW; ++k) {
-        mt = fmaxf(mt, s_m[k]);
-        Mt = fmaxf(Mt, s_M[k]);
-      }
-      float lt = 0.f;
-      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        const float a = s_m[k] == mt ? 1.f : ex2_approx(s_m[k] - mt);
-        const float A = s_M[k] == Mt ? 1.f : ex2_approx(s_M[k] - Mt);
-        lt += s_l[k] * a;
-        const float4 x = s_o[k][lane];
-        t.x += x.x * A;
-        t.y += x.y * A;
-        t.z += x.z * A;
-        t.w += x.w * A;
-      }
-      if (lane * 4 < c.d) {
-        const float f = lt == 0.f ? 0.f : ex2_approx(Mt - mt) / lt;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(t.x * f, t.y * f), h1 = __floats2bfloat162_rn(t.z * f, t.w * f);
-        uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-        if (lt == 0.f) w = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + lane * 4) = w;
-      }
-    }
-    __syncthreads();
+    for (int k = 1; k < kW; ++k) join_in(a, s_m[k], s_l[k], s_M[k], s_o[k][lane]);
+    write(rl, a);
+  } else {
+    for (int rl = warp; rl < rows; rl += kW) write(rl, take(rl, 0, 1));
   }
 }
 
@@ -774,9 +788,9 @@ cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
   if (e != cudaSuccess || p.whole) return e;
-  const int groups = (p.RB + p.merge_rows - 1) / p.merge_rows;
-  const unsigned grid = (unsigned)((long long)p.n * p.c.Hkv * p.RG * groups);
-  return launch_pdl(join_kernel<DP>, dim3(grid), dim3(kMergeThreads), 0, st, p);
+  const unsigned units = (unsigned)(p.n * p.c.Hkv * p.RG);
+  if (p.rowwise) return launch_pdl(join_kernel<true>, dim3(units, std::min(p.RB, p.R)), dim3(kJoinWide), 0, st, p);
+  return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers), dim3(kJoinThreads), 0, st, p);
 }
 
 template <int CODE>
@@ -788,12 +802,14 @@ cudaError_t launch_code(const AttnCall& p, cudaStream_t st) {
   return NR == 1 ? launch_t<CODE, 64, 1, false>(p, st) : launch_t<CODE, 64, 2, false>(p, st);
 }
 
+// Query rows a warp holds (one or two MMA column blocks).
 int rows_per_warp(int R) { return R <= 8 ? 8 : 16; }
 // One wave: two CTAs of kWarps warps per SM.
 long long wave_of(int sms) { return (long long)sms * 2 * kWarps; }
-size_t piece_bytes(long long workers, int RB, int d) {
-  return ((size_t)workers * 2 * RB * d * 4 + 255) / 256 * 256 + (size_t)workers * 2 * RB * 16;
-}
+// The workspace: outputs of the pieces, their softmax states, who joins what.
+size_t pieces_o(long long workers, int RB, int d) { return ((size_t)workers * 2 * RB * d * 4 + 255) / 256 * 256; }
+size_t pieces_s(long long workers, int RB) { return ((size_t)workers * 2 * RB * 16 + 255) / 256 * 256; }
+
 }  // namespace
 
 bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, int sinks, int sms, AttnPlan* a) {
@@ -810,15 +826,19 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   // tiles a warp would be spared.
   a->whole = cap <= 4 ? 1 : 0;
   a->workers = (int)std::min(wave_of(sms), a->whole ? units : units * cap);
-  const long long rows = units * a->RB;
-  a->merge_rows = (int)std::min<long long>(a->RB, std::max<long long>(1, rows / ((long long)sms * 8)));
-  a->part_s = ((size_t)a->workers * 2 * a->RB * s.d * 4 + 255) / 256 * 256;
-  a->total = piece_bytes(a->workers, a->RB, s.d);
+  // Joins: by row where the rows are fewer than the CTAs they can fill
+  a->by_unit = units <= a->workers ? 1 : 0;
+  a->rowwise = a->by_unit && units * std::min<long long>(R, a->RB) <= 4LL * sms ? 1 : 0;
+  a->part_s = pieces_o(a->workers, a->RB, s.d);
+  a->cuts = a->part_s + pieces_s(a->workers, a->RB);
+  a->total = a->cuts + (size_t)a->workers * 8;
   return true;
 }
 
 size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms) {
-  return piece_bytes(wave_of(sms), rows_per_warp((int)std::min<long long>(1 << 20, (long long)Hq / s.Hkv * T)), s.d);
+  const int RB = rows_per_warp((int)std::min<long long>(1 << 20, (long long)Hq / s.Hkv * T));
+  const long long w = wave_of(sms);
+  return pieces_o(w, RB, s.d) + pieces_s(w, RB) + (size_t)w * 8;
 }
 
 cudaError_t launch_attention(const AttnCall& p, cudaStream_t st) {

@@ -75,16 +75,18 @@ struct AttnCall {
   int window, sinks;
   int workers;                   // warps of the grid
   int whole;                     // 1: every unit belongs to one warp
-  int merge_rows;                // rows a merge CTA handles
+  int by_unit;                   // 1: cuts is per unit, 0: per run
+  int rowwise;                   // 1: a join CTA takes one row
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   float* part_o;                 // [workers][2][RB][d]
   float4* part_s;                // [workers][2][RB] (m, l, M, unused)
+  int2* cuts;                    // by_unit: [units] (first run or -1, last run); else [workers] (unit or -1, last run)
   float scale_log2;
 };
 struct AttnPlan {
-  int RB, RG, workers, whole, merge_rows;
-  size_t part_s, total;          // byte offsets
+  int RB, RG, workers, whole, by_unit, rowwise;
+  size_t part_s, cuts, total;    // byte offsets
 };
 // false: more tiles than a 32-bit count holds.
 bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, int sinks, int sms, AttnPlan* a);
