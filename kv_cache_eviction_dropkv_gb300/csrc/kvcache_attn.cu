@@ -71,7 +71,8 @@ constexpr int kUnreadable = 4;              // its table entry is no page
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kJoinThreads = 128, kJoinWide = 512;
-constexpr int kUnitCost = 2;                // tiles that taking up a unit is worth
+constexpr int kTeamTiles = 16;              // most tiles of a unit that one CTA takes
+constexpr int kUnitCost = 3;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
 constexpr float kMoveLog2 = 8.0f;
@@ -173,21 +174,14 @@ __device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + k
 __device__ __forceinline__ int entry_tiles(const AttnCall& p, int b) {
   return span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles;
 }
-// Sum over entries [0, n) of tiles (and cost) per unit, over the warp's lanes.
-__device__ __forceinline__ void sum_entries(const AttnCall& p, int lane, int n, long long* tiles, long long* cost) {
-  long long a = 0, c = 0;
-  for (int b = lane; b < n; b += 32) {
-    const int t = entry_tiles(p, b);
-    a += t;
-    c += cost_of(t);
-  }
+// Cost per head and row group of all entries, over the warp's lanes (mine:
+// the tiles of entry `lane`, which every scan starts with).
+__device__ __forceinline__ long long sum_cost(const AttnCall& p, int lane, int mine) {
+  long long c = cost_of(mine);
+  for (int b = lane + 32; b < p.n; b += 32) c += cost_of(entry_tiles(p, b));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    c += __shfl_xor_sync(0xffffffffu, c, o);
-  }
-  *tiles = a;
-  *cost = c;
+  for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  return c;
 }
 __device__ __forceinline__ Deal make_deal(long long cost, int workers) {
   Deal d;
@@ -208,12 +202,12 @@ struct Place {
   long long first, tile;
   long long last;                           // cost position of the last tile of x's unit
 };
-__device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb, long long x) {
+__device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int mine, int upb, long long x) {
   Place r;
   long long cost0 = 0, tiles0 = 0;          // before this batch of entries
   for (int base = 0; base < p.n; base += 32) {
     const int b = base + lane;
-    const int t = b < p.n ? entry_tiles(p, b) : 0;
+    const int t = base == 0 ? mine : b < p.n ? entry_tiles(p, b) : 0;
     long long cost = (long long)cost_of(t) * upb, tiles = (long long)t * upb;
     const long long own_cost = cost, own_tiles = tiles;
 #pragma unroll
@@ -247,6 +241,41 @@ __device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int upb
   return r;
 }
 
+// Pieces of a row: softmax references m (sums) and M (outputs), the sum l
+// and four output channels.
+struct Joined {
+  float m, M, l;
+  float4 o;
+};
+__device__ __forceinline__ void join_in(Joined& a, float m, float l, float M, const float4& o) {
+  const float mn = fmaxf(a.m, m), Mn = fmaxf(a.M, M);
+  const float fa = a.m == mn ? 1.f : ex2_approx(a.m - mn), fb = m == mn ? 1.f : ex2_approx(m - mn);
+  const float Fa = a.M == Mn ? 1.f : ex2_approx(a.M - Mn), Fb = M == Mn ? 1.f : ex2_approx(M - Mn);
+  a.l = a.l * fa + l * fb;
+  a.o.x = a.o.x * Fa + o.x * Fb;
+  a.o.y = a.o.y * Fa + o.y * Fb;
+  a.o.z = a.o.z * Fa + o.z * Fb;
+  a.o.w = a.o.w * Fa + o.w * Fb;
+  a.m = mn;
+  a.M = Mn;
+}
+__device__ __forceinline__ Joined nothing_joined() {
+  Joined a;
+  a.m = a.M = -INFINITY;
+  a.l = 0.f;
+  a.o = make_float4(0.f, 0.f, 0.f, 0.f);
+  return a;
+}
+// Row r of head h of entry b: channels 4 lane .. 4 lane + 3; 0 where nothing was seen.
+__device__ __forceinline__ void write_row(const AttnCall& p, int b, int h, int r, int lane, const Joined& a) {
+  if (lane * 4 >= p.c.d) return;
+  const float f = a.l == 0.f ? 0.f : ex2_approx(a.M - a.m) / a.l;
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.o.x * f, a.o.y * f), h1 = __floats2bfloat162_rn(a.o.z * f, a.o.w * f);
+  uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+  if (a.l == 0.f) w = make_uint2(0u, 0u);
+  *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * p.c.d + lane * 4) = w;
+}
+
 // EXACT: d == DP, so that a tile's row offsets are constants.
 template <int CODE, int DP, int NR, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p) {
@@ -263,47 +292,42 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   const int upb = c.Hkv * p.RG;             // units (head, row group) per sequence
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_s = dropkv::smem_addr(ring);
-  if (worker >= p.workers) return;
-
-  // rows of sequences with nothing to read
-  for (int b = worker; b < p.n; b += p.workers) {
-    if (span_of(entry_len(p, b, true), p.T, p.window, p.sinks).tiles > 0) continue;
-    if (!p.whole && p.by_unit)
-      for (int u = lane; u < upb; u += 32) p.cuts[b * upb + u] = make_int2(-1, 0);
-    uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * p.T * c.d);
-    for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
-  }
-
-  // this warp's run: tiles [x0, x1) of the call; entry b0 holds x0 and begins at tile cum0
-  long long x0, x1, cum0;
-  int b0;
+  // this warp's run: tiles x0, x0 + stride, ... below x1 of the call; entry b0
+  // holds x0 and begins at tile cum0
+  long long x0, x1, cum0 = 0;
+  int b0, stride = 1;
   bool cut = false;                         // the run begins inside a unit
   int run_last = 0;                         // last run of the unit the next run begins inside
-  if (p.whole) {
-    // whole units ua .. ub - 1; tiles are counted from entry b0 on
-    const long long units = (long long)p.n * upb;
-    const long long ua = units * worker / p.workers, ub = units * (worker + 1) / p.workers;
-    b0 = (int)(ua / upb);
-    cum0 = 0;
-    x0 = (ua - (long long)b0 * upb) * entry_tiles(p, b0);
-    x1 = 0;
-    for (int b = b0; b < p.n && (long long)b * upb < ub; ++b)
-      x1 += min((long long)upb, ub - (long long)b * upb) * entry_tiles(p, b);
+  if (p.team) {
+    // the CTA's unit, dealt to its warps tile by tile; tiles are counted from its entry on
+    b0 = blockIdx.x / upb;
+    const int tiles = span_of(entry_len(p, b0, true), p.T, p.window, p.sinks).tiles;
+    x1 = (long long)(blockIdx.x - b0 * upb + 1) * tiles;
+    x0 = x1 - tiles + warp;
+    stride = kWarps;
   } else {
-    long long tiles, cost;
-    sum_entries(p, lane, p.n, &tiles, &cost);
-    const Deal deal = make_deal(cost * upb, p.workers);
-    const Place from = find_place(p, lane, upb, run_start(deal, worker));
+    if (worker >= p.workers) return;
+    // rows of sequences with nothing to read
+    for (int b = worker; b < p.n; b += p.workers) {
+      if (span_of(entry_len(p, b, true), p.T, p.window, p.sinks).tiles > 0) continue;
+      if (p.by_unit)
+        for (int u = lane; u < upb; u += 32) p.cuts[b * upb + u] = make_int2(-1, 0);
+      uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * p.T * c.d);
+      for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
+    }
+    const int mine = lane < p.n ? entry_tiles(p, lane) : 0;
+    const Deal deal = make_deal(sum_cost(p, lane, mine) * upb, p.workers);
+    const Place from = find_place(p, lane, mine, upb, run_start(deal, worker));
+    const Place to = find_place(p, lane, mine, upb, run_start(deal, worker + 1));
     x0 = from.tile;
-    const Place to = find_place(p, lane, upb, run_start(deal, worker + 1));
     x1 = to.tile;
     if (to.tiles > 0) run_last = run_of(deal, to.last);
     b0 = from.b;
     cum0 = from.first;
     cut = from.tiles > 0 && (int)(x0 - cum0) % from.tiles != 0;
+    if (!p.by_unit && lane == 0) p.cuts[worker] = make_int2(-1, 0);
+    if (x0 >= x1) return;
   }
-  if (!p.whole && !p.by_unit && lane == 0) p.cuts[worker] = make_int2(-1, 0);
-  if (x0 >= x1) return;
 
   // columns past d stay zero in every stage (copies never touch them)
   if (c.d < kPitch)
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   __syncwarp();
 
   // -------------------------------------------------- tile descriptions
-  // Lane l describes tile x0 + 32 k + l of the run (table entry and scales:
+  // Lane l describes tile 32 k + l of the run (table entry and scales:
   // two dependent loads, 32 tiles ahead of their use).
   Tile* meta = reinterpret_cast<Tile*>(smem + kRingBytes) + warp * kMeta;
   int wb = b0;                              // entry the lane's cursor stands at
@@ -479,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 
   // The unit's part ends: the output, or this run's piece of it.
   auto store_unit = [&](bool whole, int slot) {
-    if (!p.whole && lane == 0) {
+    if (lane == 0) {
       // who joins it: the run it begins in says so
       if (p.by_unit) {
         if (whole) p.cuts[unit] = make_int2(-1, 0);
@@ -525,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   };
 
   // -------------------------------------------------- the run
-  const int T_run = (int)(x1 - x0);
-  describe(x0 + lane, meta + lane);
+  const int T_run = x0 < x1 ? (int)(x1 - x0 + stride - 1) / stride : 0;
+  describe(x0 + lane * stride, meta + lane);
   __syncwarp();
   auto issue = [&](int i) {                 // stage the copy of run tile i
     if (i < T_run) copy_tile(i % kStages, meta + (i & (kMeta - 1)));
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 #pragma unroll 1
   for (int i = 0; i < T_run; ++i) {
     // the batch after this one takes the place of the one before
-    if ((i & 31) == 0) describe(x0 + i + 32 + lane, meta + ((i + 32) & (kMeta - 1)) + lane);
+    if ((i & 31) == 0) describe(x0 + (i + 32 + lane) * stride, meta + ((i + 32) & (kMeta - 1)) + lane);
     __syncwarp();                           // tile i - 1 has been read by every lane
     issue(i + kStages - 1);
     const Tile* now = meta + (i & (kMeta - 1));
@@ -682,6 +706,40 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
       }
     }
   }
+  if (p.team) {
+    // the warps' pieces of the unit, through shared memory (each warp's ring)
+    float* po = reinterpret_cast<float*>(ring);
+    float4* ps = reinterpret_cast<float4*>(meta);
+    __syncwarp();
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rl = nr * 8 + 2 * c4 + e;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], x);
+#pragma unroll
+        for (int s = 0; s < KS; s += 2)
+          *reinterpret_cast<float4*>(po + rl * DP + g8 * VB + 2 * s) =
+              T_run > 0 ? make_float4(o[nr][s][e], o[nr][s][2 + e], o[nr][s + 1][e], o[nr][s + 1][2 + e])
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g8 == 0)
+          ps[rl] = T_run > 0 ? make_float4(m[nr][e], l[nr][e], M[nr][e], 0.f) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      }
+    __syncthreads();
+    const int h = (blockIdx.x % upb) / p.RG, rg = (blockIdx.x % upb) % p.RG;
+    for (int rl = warp; rl < min(RB, p.R - rg * RB); rl += kWarps) {
+      Joined a = nothing_joined();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 st = reinterpret_cast<const float4*>(smem + kRingBytes + w * kMeta * sizeof(Tile))[rl];
+        const float* ow = reinterpret_cast<const float*>(smem + w * kStages * kStageBytes) + rl * DP;
+        join_in(a, st.x, st.y, st.z, lane * 4 < DP ? *reinterpret_cast<const float4*>(ow + lane * 4) : a.o);
+      }
+      write_row(p, b0, h, rg * RB + rl, lane, a);
+    }
+    return;
+  }
   // the last part: whole when all tiles of its unit lie in this run; else its
   // piece goes to slot 0 if the unit began before the run, slot 1 if it began inside
   const int tiles = span_of(len, p.T, p.window, p.sinks).tiles;
@@ -694,23 +752,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 // ROWWISE: a CTA joins one row of a unit, its warps sharing out the pieces
 // with all loads in flight at once (few units, up to hundreds of pieces
 // each); else each warp joins rows of the unit on its own (few pieces each).
-struct Joined {
-  float m, M, l;
-  float4 o;
-};
-__device__ __forceinline__ void join_in(Joined& a, float m, float l, float M, const float4& o) {
-  const float mn = fmaxf(a.m, m), Mn = fmaxf(a.M, M);
-  const float fa = a.m == mn ? 1.f : ex2_approx(a.m - mn), fb = m == mn ? 1.f : ex2_approx(m - mn);
-  const float Fa = a.M == Mn ? 1.f : ex2_approx(a.M - Mn), Fb = M == Mn ? 1.f : ex2_approx(M - Mn);
-  a.l = a.l * fa + l * fb;
-  a.o.x = a.o.x * Fa + o.x * Fb;
-  a.o.y = a.o.y * Fa + o.y * Fb;
-  a.o.z = a.o.z * Fa + o.z * Fb;
-  a.o.w = a.o.w * Fa + o.w * Fb;
-  a.m = mn;
-  a.M = Mn;
-}
-
 template <bool ROWWISE>
 __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kernel(const AttnCall p) {
   constexpr int kW = (ROWWISE ? kJoinWide : kJoinThreads) / 32, kBatch = ROWWISE ? 10 : 4;
@@ -730,10 +771,7 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
   // pieces w0 + first, w0 + first + step, ... of row rl; the unit begins in
   // run w0 (its slot 1) and before every later one (slot 0)
   auto take = [&](int rl, int first, int step) {
-    Joined a;
-    a.m = a.M = -INFINITY;
-    a.l = 0.f;
-    a.o = make_float4(0.f, 0.f, 0.f, 0.f);
+    Joined a = nothing_joined();
     for (int base = w0 + first; base <= w1; base += step * kBatch) {
       float4 st[kBatch], ov[kBatch];
 #pragma unroll
@@ -752,15 +790,6 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
     }
     return a;
   };
-  auto write = [&](int rl, const Joined& a) {
-    if (!cols) return;
-    const float f = a.l == 0.f ? 0.f : ex2_approx(a.M - a.m) / a.l;
-    const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.o.x * f, a.o.y * f), h1 = __floats2bfloat162_rn(a.o.z * f, a.o.w * f);
-    uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-    if (a.l == 0.f) w = make_uint2(0u, 0u);
-    const int r = rg * p.RB + rl;
-    *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + lane * 4) = w;
-  };
   if constexpr (ROWWISE) {
     const int rl = blockIdx.y;
     if (rl >= rows) return;
@@ -775,9 +804,9 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
     if (warp > 0) return;
 #pragma unroll
     for (int k = 1; k < kW; ++k) join_in(a, s_m[k], s_l[k], s_M[k], s_o[k][lane]);
-    write(rl, a);
+    write_row(p, b, h, rg * p.RB + rl, lane, a);
   } else {
-    for (int rl = warp; rl < rows; rl += kW) write(rl, take(rl, 0, 1));
+    for (int rl = warp; rl < rows; rl += kW) write_row(p, b, h, rg * p.RB + rl, lane, take(rl, 0, 1));
   }
 }
 
@@ -786,9 +815,9 @@ cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
   auto kern = attention_kernel<CODE, DP, NR, EXACT>;
   cudaError_t e = allow_smem<attention_kernel<CODE, DP, NR, EXACT>>(kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
-  if (e != cudaSuccess || p.whole) return e;
   const unsigned units = (unsigned)(p.n * p.c.Hkv * p.RG);
+  e = launch_pdl(kern, dim3(p.team ? units : (p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
+  if (e != cudaSuccess || p.team) return e;
   if (p.rowwise) return launch_pdl(join_kernel<true>, dim3(units, std::min(p.RB, p.R)), dim3(kJoinWide), 0, st, p);
   return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers), dim3(kJoinThreads), 0, st, p);
 }
@@ -822,10 +851,9 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   if (cap * upb >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
   if (window > 0)
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
-  // Units of at most 4 tiles are never cut: joining costs more than the 3
-  // tiles a warp would be spared.
-  a->whole = cap <= 4 ? 1 : 0;
-  a->workers = (int)std::min(wave_of(sms), a->whole ? units : units * cap);
+  // Few short units: a CTA each, its warps join in shared memory, no second kernel.
+  a->team = units <= 2LL * sms && cap <= kTeamTiles ? 1 : 0;
+  a->workers = (int)std::min(wave_of(sms), units * cap);
   // Joins: by row where the rows are fewer than the CTAs they can fill
   a->by_unit = units <= a->workers ? 1 : 0;
   a->rowwise = a->by_unit && units * std::min<long long>(R, a->RB) <= 4LL * sms ? 1 : 0;

@@ -74,7 +74,7 @@ struct AttnCall {
   int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
   int window, sinks;
   int workers;                   // warps of the grid
-  int whole;                     // 1: every unit belongs to one warp
+  int team;                      // 1: a CTA per unit, joined in shared memory
   int by_unit;                   // 1: cuts is per unit, 0: per run
   int rowwise;                   // 1: a join CTA takes one row
   const __nv_bfloat16* q;
@@ -85,7 +85,7 @@ struct AttnCall {
   float scale_log2;
 };
 struct AttnPlan {
-  int RB, RG, workers, whole, by_unit, rowwise;
+  int RB, RG, workers, team, by_unit, rowwise;
   size_t part_s, cuts, total;    // byte offsets
 };
 // false: more tiles than a 32-bit count holds.

@@ -305,13 +305,15 @@ def test_damaged_tables_are_flagged():
     (4, 2, 64, 32, 1), (8, 1, 128, 64, 1), (7, 1, 96, 32, 2), (2, 2, 40, 32, 5), (32, 2, 16, 64, 1), (6, 3, 72, 128, 3),
     (3, 1, 8, 32, 9), (4, 4, 128, 128, 1), (5, 1, 112, 64, 8)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (37, 3), (64, 70), (500, 4)])
-def test_attention_matches_reference(code, Hq, Hkv, d, page, T, window, sinks):
+@pytest.mark.parametrize("room", [1, 8])
+def test_attention_matches_reference(code, Hq, Hkv, d, page, T, window, sinks, room):
     """Sequences of 0, 1, a few and a few hundred tokens in one call; rows that
     see nothing; random bytes (not-a-number codes among them) in every slot
-    that holds no token."""
+    that holds no token.  room: how many times longer the sequences could be
+    (short units go to a CTA each, others are cut over the GPU)."""
     lengths = [0, 1, 3, page, page + 1, 211, 300]
     M = -(-300 // page)
-    c, r = pair(seqs=7, Hkv=Hkv, d=d, pages=7 * M, page=page, max_pages=M, code=code, Hq=Hq, T=T, seed=d + T)
+    c, r = pair(seqs=7, Hkv=Hkv, d=d, pages=7 * M, page=page, max_pages=room * M, code=code, Hq=Hq, T=T, seed=d + T)
     fill(c, r, lengths, seed=T)
     q = draw_rows(7, Hq, T, d, 77, spread=0.3)
     check_attention(c, r, q, window=window, sinks=sinks)
