@@ -16,9 +16,14 @@
 // the group's TMEM columns; P = 2^(x - ref), with a reference that moves only
 // when it must, written back over S as bf16 pairs; O += P V with P read from
 // tensor memory.  The MMA warp alternates between the groups, so one group's
-// products run under the other's softmax; two K and two V tiles are in flight.
-// A group skips tiles outside its own window; only tiles that cut the
-// diagonal or a window's edge are masked element by element.
+// products run under the other's softmax.  Its issuing thread is what bounds
+// the kernel (an MMA of 128 x 128 x 16 is issued about as fast as it runs, and
+// S = Q K^T reads both operands from shared memory at its full rate), so it is
+// spared everything else: K tile i and V tile i - 1 come as one pair on one
+// barrier, and the softmax groups release a pair when S(i) is complete, which
+// every product issued before it then is too.  A group skips tiles outside
+// its own window; only tiles that cut the diagonal or a window's edge are
+// masked element by element.
 #include "kvcache_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -30,14 +35,15 @@ using namespace dropkv;
 constexpr int kQT = 128;                          // rows of a query tile, keys of a key tile
 constexpr int kTileB = kQT * kDPad * 2;           // 32 KB: two SW128 blocks of 64 columns
 constexpr int kHalfB = kTileB / 2;
-constexpr int kProducerK = 8, kIssuer = 9, kProducerV = 10, kWinThreads = 32 * 12;   // warp 11 idle
+constexpr int kProducer = 8, kIssuer = 9, kWinThreads = 32 * 12;   // warps 10, 11 idle (register shares)
 constexpr int kOffQ = 0, kOffK = 2 * kTileB, kOffV = 4 * kTileB, kOffSmall = 6 * kTileB;
 constexpr uint32_t kCols = 512;                   // group g: S / P at [128 g, +128), O at [256 + 128 g, +128)
 constexpr float kMove = 24.0f;                    // base-2 logarithm by which a maximum may pass its reference
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
 
 struct Small {
-  uint64_t qbar, kfull[2], kempty[2], vfull[2], vempty[2];
+  uint64_t qbar, full[2];
+  uint64_t empty[2];   // pairs released by the groups (one arrival each)
   uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
   uint64_t pfull[2];   // group g: its P written by the group's four warps
   uint64_t odone[2];   // group g: its last P V complete
@@ -48,30 +54,31 @@ struct Small {
 constexpr int kWinSmem = kOffSmall + (int)sizeof(Small) + 1024;
 static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
 
-// The key tiles of a CTA: list entry i is key tile tile(i); group g takes the
-// entries with takes(g, i).
+// The key tiles of a CTA: list entry i is key tile tile(i).  Group 0 (query
+// tile t[0], -1: none) takes all entries but the last, group 1 (t[1] = t[0] +
+// 1) all but `skip`, the one tile that only group 0's window may reach.
+// Pair j of the rings is K of entry j with V of entry j - 1.
 struct List {
-  int t[2];                                       // query tiles of the groups (-1: none)
-  int lo[2];                                      // first key tile their windows reach
-  int sink_tiles;                                 // tiles that hold first tokens
+  int t[2];
   int ns, s2, n;                                  // tiles [0, ns), then s2, s2 + 1, ...: n entries
+  int skip;
   __device__ __forceinline__ int tile(int i) const { return i < ns ? i : s2 + (i - ns); }
   __device__ __forceinline__ bool takes(int g, int i) const {
-    const int k = tile(i);
-    return i < n && k <= t[g] && (k < sink_tiles || k >= lo[g]);
+    return g ? i < n && i != skip : t[0] >= 0 && i < n - 1;
   }
 };
 __device__ __forceinline__ List make_list(const WindowCall& p, int t0, int t1) {
   List l;
   l.t[0] = t0;
   l.t[1] = t1;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) l.lo[g] = p.window > 0 ? max(0, l.t[g] * kQT - p.window + 1) / kQT : 0;
-  const int lo = t0 >= 0 ? l.lo[0] : l.lo[1];
-  l.sink_tiles = p.window > 0 ? (min(p.sinks, p.n_max) + kQT - 1) / kQT : 0;
-  l.ns = min(l.sink_tiles, lo);                   // those before both windows
+  // first key tiles the groups' windows reach, and the tiles that hold first tokens
+  const int lo1 = p.window > 0 ? max(0, t1 * kQT - p.window + 1) / kQT : 0;
+  const int lo = t0 >= 0 && p.window > 0 ? max(0, t0 * kQT - p.window + 1) / kQT : lo1;
+  const int sink_tiles = p.window > 0 ? (min(p.sinks, p.n_max) + kQT - 1) / kQT : 0;
+  l.ns = min(sink_tiles, lo);                     // those before both windows
   l.s2 = lo;
   l.n = l.ns + (t1 + 1 - l.s2);
+  l.skip = lo < lo1 && lo >= sink_tiles ? l.ns : -1;
   return l;
 }
 
@@ -98,12 +105,18 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
       atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
     }
   };
+  // Pair i is needed no more by this group (waited for when pair i + 2 takes its place).
+  auto release = [&](int i) {
+    if (quarter == 0 && lane == 0 && i + 2 <= list.n) mbar_arrive(&S.empty[i & 1]);
+  };
   int seen = 0;                                   // tiles of this group so far
   for (int i = 0; !bad && i < list.n; ++i) {
     if (!list.takes(g, i)) continue;
     const int kt = list.tile(i);
     if (!__all_sync(0xffffffffu, mbar_wait(&S.sfull[g], seen & 1, &S.abort))) { give_up(); break; }
     tc_fence_after();
+    if (g == 1 && list.skip >= 0 && i == list.skip + 1) release(list.skip);
+    release(i);                                   // S is complete, and the P V issued before it
     float x[128];
 #pragma unroll
     for (int c = 0; c < 8; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
@@ -135,28 +148,33 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     }
     // a row that has seen nothing yet keeps P = 0
     const float r0 = ref == -INFINITY ? 0.f : ref;
+    // P = 2^(x scale - ref), 16 columns at a time: while the exponentials of
+    // one block run, the block before is summed, packed and stored
     const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-r0, -r0);
-#pragma unroll
-    for (int u = 0; u < 128; u += 2) {
-      const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
-      x[u] = ex2_approx(f2_lo(y));
-      x[u + 1] = ex2_approx(f2_hi(y));
-    }
     uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+    float hw[16];
 #pragma unroll
-    for (int u = 0; u < 128; u += 2) ls2[(u >> 1) & 3] = f2_add(ls2[(u >> 1) & 3], f2_pack(x[u], x[u + 1]));
+    for (int c = 0; c <= 8; ++c) {
+      if (c < 8) {
+#pragma unroll
+        for (int u = 16 * c; u < 16 * c + 16; u += 2) {
+          const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
+          x[u] = ex2_approx(f2_lo(y));
+          x[u + 1] = ex2_approx(f2_hi(y));
+        }
+      }
+      if (c > 0) {
+#pragma unroll
+        for (int u = 16 * c - 16; u < 16 * c; u += 2) {
+          ls2[(u >> 1) & 3] = f2_add(ls2[(u >> 1) & 3], f2_pack(x[u], x[u + 1]));
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[u], x[u + 1]);
+          hw[(u >> 1) & 15] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+        }
+        if (c % 2 == 0) tmem_st16(tS + 16 * (c / 2 - 1), hw);
+      }
+    }
     const uint64_t lsum = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
     l += f2_lo(lsum) + f2_hi(lsum);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float hw[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[32 * c + 2 * q], x[32 * c + 2 * q + 1]);
-        hw[q] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
-      }
-      tmem_st16(tS + 16 * c, hw);
-    }
     // the group's P V of its tile before is complete (the commit its S
     // signalled came after it): O follows the reference
     if (seen > 0 && __any_sync(0xffffffffu, need)) {
@@ -173,9 +191,9 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     if (j0 + kQT > nb) {
       // the sequence's last key tile (group 1's alone): rows past the end may
       // hold anything; zero them so that 0 * NaN never reaches O
-      if (!__all_sync(0xffffffffu, mbar_wait(&S.vfull[i & 1], (i >> 1) & 1, &S.abort))) { give_up(); break; }
+      if (!__all_sync(0xffffffffu, mbar_wait(&S.full[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) { give_up(); break; }
       if (j0 + row >= nb) {
-        uint8_t* vrow = sm + kOffV + (i & 1) * kTileB + row * 128;
+        uint8_t* vrow = sm + kOffV + ((i + 1) & 1) * kTileB + row * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0, 0, 0, 0);
@@ -237,14 +255,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const int unit = b * p.Hkv + hq / p.g;
 
   if (tid == 0) {
+    const int groups = t0 >= 0 ? 2 : 1;
     mbar_init(&S.qbar, 1);
+    mbar_init(&S.drain, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.kfull[i], 1); mbar_init(&S.kempty[i], 1);
-      mbar_init(&S.vfull[i], 1); mbar_init(&S.vempty[i], 1);
+      mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], groups);
       mbar_init(&S.sfull[i], 1); mbar_init(&S.pfull[i], 4);
       mbar_init(&S.odone[i], 1);
     }
-    mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
   }
@@ -255,30 +273,30 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   const uint32_t tmem = S.tmem_base;
   grid_dep_launch();
 
-  if (warp == kProducerK || warp == kProducerV) {
+  if (warp == kProducer) {
     if (lane == 0) {
-      const bool is_k = warp == kProducerK;       // Q, then the K ring; or the V ring
-      if (is_k) {
-        const int zq = b * p.Hq + hq;
-        mbar_arrive_expect_tx(&S.qbar, (t0 >= 0 ? 2 : 1) * kTileB);
-        if (t0 >= 0) {
-          tma_load_3d(sm + kOffQ, &tmq, &S.qbar, 0, t0 * kQT, zq);
-          tma_load_3d(sm + kOffQ + kHalfB, &tmq, &S.qbar, 64, t0 * kQT, zq);
-        }
-        tma_load_3d(sm + kOffQ + kTileB, &tmq, &S.qbar, 0, t1 * kQT, zq);
-        tma_load_3d(sm + kOffQ + kTileB + kHalfB, &tmq, &S.qbar, 64, t1 * kQT, zq);
+      const int zq = b * p.Hq + hq;
+      mbar_arrive_expect_tx(&S.qbar, (t0 >= 0 ? 2 : 1) * kTileB);
+      for (int g = t0 >= 0 ? 0 : 1; g < 2; ++g) {
+        tma_load_3d(sm + kOffQ + g * kTileB, &tmq, &S.qbar, 0, list.t[g] * kQT, zq);
+        tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qbar, 64, list.t[g] * kQT, zq);
       }
-      uint64_t *full = is_k ? S.kfull : S.vfull, *empty = is_k ? S.kempty : S.vempty;
-      uint8_t* ring = sm + (is_k ? kOffK : kOffV);
-      const CUtensorMap* map = is_k ? &tmk : &tmv;
       int issued = 0;
       bool ok = true;
-      for (int i = 0; i < list.n; ++i) {
-        if (i >= 2 && !mbar_wait(&empty[i & 1], ((i >> 1) + 1) & 1, &S.abort)) { ok = false; break; }
-        uint8_t* dst = ring + (i & 1) * kTileB;
-        mbar_arrive_expect_tx(&full[i & 1], kTileB);
-        tma_load_3d(dst, map, &full[i & 1], 0, list.tile(i) * kQT, unit);
-        tma_load_3d(dst + kHalfB, map, &full[i & 1], 64, list.tile(i) * kQT, unit);
+      for (int j = 0; j <= list.n; ++j) {
+        uint64_t* full = &S.full[j & 1];
+        if (j >= 2 && !mbar_wait(&S.empty[j & 1], ((j >> 1) + 1) & 1, &S.abort)) { ok = false; break; }
+        mbar_arrive_expect_tx(full, (j < list.n ? kTileB : 0) + (j > 0 ? kTileB : 0));
+        if (j > 0) {                              // needed first
+          uint8_t* dst = sm + kOffV + (j & 1) * kTileB;
+          tma_load_3d(dst, &tmv, full, 0, list.tile(j - 1) * kQT, unit);
+          tma_load_3d(dst + kHalfB, &tmv, full, 64, list.tile(j - 1) * kQT, unit);
+        }
+        if (j < list.n) {
+          uint8_t* dst = sm + kOffK + (j & 1) * kTileB;
+          tma_load_3d(dst, &tmk, full, 0, list.tile(j) * kQT, unit);
+          tma_load_3d(dst + kHalfB, &tmk, full, 64, list.tile(j) * kQT, unit);
+        }
         ++issued;
       }
       if (!ok) {
@@ -286,51 +304,50 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
       }
       // every copy has landed before the CTA can leave
-      for (int i = max(0, issued - 2); i < issued; ++i) drain_wait(&full[i & 1], (i >> 1) & 1);
-      if (is_k) drain_wait(&S.qbar, 0);
+      for (int j = max(0, issued - 2); j < issued; ++j) drain_wait(&S.full[j & 1], (j >> 1) & 1);
+      drain_wait(&S.qbar, 0);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
     if (lane == 0) {
       const uint32_t idS = umma_idesc_bf16(128, 128, 0, 0);
       const uint32_t idO = umma_idesc_bf16(128, 128, 0, 1);
+      const uint64_t qd = desc_kmajor_sw128(smem_addr(sm + kOffQ), kQT, 0);
+      const uint64_t kd = desc_kmajor_sw128(smem_addr(sm + kOffK), kQT, 0);
+      const uint64_t vd = desc_mnmajor_sw128(smem_addr(sm + kOffV), kQT, 0);
       int seen[2] = {0, 0};
       auto issue_S = [&](int g, int i) {          // K entry i has landed
-        const uint32_t qa = smem_addr(sm + kOffQ + g * kTileB);
-        const uint32_t kb = smem_addr(sm + kOffK + (i & 1) * kTileB);
+        const uint64_t qg = qd + ((g * kTileB) >> 4), kg = kd + (((i & 1) * kTileB) >> 4);
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          umma_bf16(tmem + 128 * g, desc_kmajor_sw128(qa, kQT, s), desc_kmajor_sw128(kb, kQT, s), idS, s > 0);
+        for (int s = 0; s < 8; ++s) {
+          const uint64_t at = ((s >> 2) * kHalfB + (s & 3) * 32) >> 4;   // as desc_kmajor_sw128 steps
+          umma_bf16(tmem + 128 * g, qg + at, kg + at, idS, s > 0);
+        }
         umma_commit(&S.sfull[g]);
       };
-      bool ok = mbar_wait(&S.qbar, 0, &S.abort) && mbar_wait(&S.kfull[0], 0, &S.abort);
+      bool ok = mbar_wait(&S.qbar, 0, &S.abort) && mbar_wait(&S.full[0], 0, &S.abort);
       if (ok) {
         tc_fence_after();
         for (int g = 0; g < 2; ++g)
           if (list.takes(g, 0)) issue_S(g, 0);
-        umma_commit(&S.kempty[0]);
       }
       for (int i = 0; ok && i < list.n; ++i) {
-        const bool more = i + 1 < list.n;
-        if (!(ok = mbar_wait(&S.vfull[i & 1], (i >> 1) & 1, &S.abort))) break;
-        if (more && !(ok = mbar_wait(&S.kfull[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) break;
-        const uint32_t vb = smem_addr(sm + kOffV + (i & 1) * kTileB);
+        if (!(ok = mbar_wait(&S.full[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) break;   // V(i), K(i + 1)
+        const uint64_t vg = vd + ((((i + 1) & 1) * kTileB) >> 4);
+#pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (list.takes(g, i)) {
             if (!(ok = mbar_wait(&S.pfull[g], seen[g] & 1, &S.abort))) break;
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              umma_bf16_tmem_a(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, desc_mnmajor_sw128(vb, kQT, s), idO,
+              umma_bf16_tmem_a(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, vg + ((s * 16 * 128) >> 4), idO,
                                seen[g] > 0 || s > 0);
             ++seen[g];
             if (list.tile(i) == list.t[g]) umma_commit(&S.odone[g]);
           }
           if (list.takes(g, i + 1)) issue_S(g, i + 1);   // over P, which P V issued before it has read
         }
-        if (!ok) break;
-        if (more) umma_commit(&S.kempty[(i + 1) & 1]);
-        umma_commit(&S.vempty[i & 1]);
       }
       if (!ok) {
         S.abort = 1;
