@@ -23,7 +23,8 @@
 // barrier, and the softmax groups release a pair when S(i) is complete, which
 // every product issued before it then is too.  A group skips tiles outside
 // its own window; only tiles that cut the diagonal or a window's edge are
-// masked element by element.
+// masked element by element, and a tile of which only the first kNarrow keys
+// are first tokens is taken kNarrow keys wide.
 #include "kvcache_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -40,6 +41,8 @@ constexpr int kOffQ = 0, kOffK = 2 * kTileB, kOffV = 4 * kTileB, kOffSmall = 6 *
 constexpr uint32_t kCols = 512;                   // group g: S / P at [128 g, +128), O at [256 + 128 g, +128)
 constexpr float kMove = 24.0f;                    // base-2 logarithm by which a maximum may pass its reference
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
+
+constexpr int kNarrow = 32;
 
 struct Small {
   uint64_t qbar, full[2];
@@ -62,6 +65,7 @@ struct List {
   int t[2];
   int ns, s2, n;                                  // tiles [0, ns), then s2, s2 + 1, ...: n entries
   int skip;
+  int narrow;                                     // entry that is taken kNarrow keys wide (-1: none)
   __device__ __forceinline__ int tile(int i) const { return i < ns ? i : s2 + (i - ns); }
   __device__ __forceinline__ bool takes(int g, int i) const {
     return g ? i < n && i != skip : t[0] >= 0 && i < n - 1;
@@ -79,13 +83,85 @@ __device__ __forceinline__ List make_list(const WindowCall& p, int t0, int t1) {
   l.s2 = lo;
   l.n = l.ns + (t1 + 1 - l.s2);
   l.skip = lo < lo1 && lo >= sink_tiles ? l.ns : -1;
+  l.narrow = l.ns > 0 && l.ns == sink_tiles && p.sinks - (l.ns - 1) * kQT <= kNarrow ? l.ns - 1 : -1;
   return l;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(bar, parity); ++it)
     if (global_timer_ns() - t0 > kDrain) break;
+}
+
+// One row against the first NC columns of its S: moves the reference, turns S
+// into P in place.  Returns the factor O (and l, already done) follows by.
+template <int NC>
+__device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, int j0, int pos, bool mask, float& ref,
+                                              float& l, bool& need) {
+  const float scale = p.scale_log2;
+  float x[NC];
+#pragma unroll
+  for (int c = 0; c < NC / 16; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
+  tmem_wait_ld();
+  if (mask) {
+    const int lo = p.window > 0 ? pos - p.window : -1;   // keys above it are in the window
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+      const int j = j0 + u;
+      if (!(j <= pos && (j > lo || j < p.sinks))) x[u] = -INFINITY;
+    }
+  }
+  float m8[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) m8[u] = x[u];
+#pragma unroll
+  for (int u = 8; u < NC; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
+  const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                         fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale;
+  need = mt > ref + kMove;
+  float factor = 1.f;
+  if (need) {
+    factor = ref == -INFINITY ? 0.f : ex2_approx(ref - mt);
+    ref = mt;
+    l *= factor;
+  }
+  // a row that has seen nothing yet keeps P = 0
+  const float r0 = ref == -INFINITY ? 0.f : ref;
+  // P = 2^(x scale - ref), 16 columns at a time: while the exponentials of
+  // one block run, the block before is summed, packed and stored
+  const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-r0, -r0);
+  uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+  float hw[16];
+#pragma unroll
+  for (int c = 0; c <= NC / 16; ++c) {
+    if (c < NC / 16) {
+#pragma unroll
+      for (int u = 16 * c; u < 16 * c + 16; u += 2) {
+        const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
+        x[u] = ex2_approx(f2_lo(y));
+        x[u + 1] = ex2_approx(f2_hi(y));
+      }
+    }
+    if (c > 0) {
+#pragma unroll
+      for (int u = 16 * c - 16; u < 16 * c; u += 2) {
+        ls2[(u >> 1) & 3] = f2_add(ls2[(u >> 1) & 3], f2_pack(x[u], x[u + 1]));
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[u], x[u + 1]);
+        hw[(u >> 1) & 15] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+      }
+      if (c % 2 == 0) tmem_st16(tS + 16 * (c / 2 - 1), hw);
+    }
+  }
+  const uint64_t lsum = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
+  l += f2_lo(lsum) + f2_hi(lsum);
+  return factor;
 }
 
 __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem,
@@ -95,7 +171,6 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   const int row = quarter * 32 + lane, pos = tg * kQT + row;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   const uint32_t tS = tmem + lane_base + 128 * g, tO = tmem + lane_base + 256 + 128 * g;
-  const float scale = p.scale_log2;
   float ref = -INFINITY, l = 0.f;
   bool bad = tg < 0;
   auto give_up = [&]() {
@@ -117,64 +192,12 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     tc_fence_after();
     if (g == 1 && list.skip >= 0 && i == list.skip + 1) release(list.skip);
     release(i);                                   // S is complete, and the P V issued before it
-    float x[128];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
-    tmem_wait_ld();
     const int j0 = kt * kQT;
     // the last row of the tile reaches back to tg 128 + 127 - W + 1
     const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
-    if (kt == tg || edge) {
-      const int lo = p.window > 0 ? pos - p.window : -1;   // keys above it are in the window
-#pragma unroll
-      for (int u = 0; u < 128; ++u) {
-        const int j = j0 + u;
-        if (!(j <= pos && (j > lo || j < p.sinks))) x[u] = -INFINITY;
-      }
-    }
-    float m8[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) m8[u] = x[u];
-#pragma unroll
-    for (int u = 8; u < 128; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
-    const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale;
-    const bool need = mt > ref + kMove;
-    float factor = 1.f;
-    if (need) {
-      factor = ref == -INFINITY ? 0.f : ex2_approx(ref - mt);
-      ref = mt;
-      l *= factor;
-    }
-    // a row that has seen nothing yet keeps P = 0
-    const float r0 = ref == -INFINITY ? 0.f : ref;
-    // P = 2^(x scale - ref), 16 columns at a time: while the exponentials of
-    // one block run, the block before is summed, packed and stored
-    const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-r0, -r0);
-    uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-    float hw[16];
-#pragma unroll
-    for (int c = 0; c <= 8; ++c) {
-      if (c < 8) {
-#pragma unroll
-        for (int u = 16 * c; u < 16 * c + 16; u += 2) {
-          const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
-          x[u] = ex2_approx(f2_lo(y));
-          x[u + 1] = ex2_approx(f2_hi(y));
-        }
-      }
-      if (c > 0) {
-#pragma unroll
-        for (int u = 16 * c - 16; u < 16 * c; u += 2) {
-          ls2[(u >> 1) & 3] = f2_add(ls2[(u >> 1) & 3], f2_pack(x[u], x[u + 1]));
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[u], x[u + 1]);
-          hw[(u >> 1) & 15] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
-        }
-        if (c % 2 == 0) tmem_st16(tS + 16 * (c / 2 - 1), hw);
-      }
-    }
-    const uint64_t lsum = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
-    l += f2_lo(lsum) + f2_hi(lsum);
+    bool need;
+    const float factor = i == list.narrow ? softmax_tile<kNarrow>(p, tS, j0, pos, true, ref, l, need)
+                                          : softmax_tile<kQT>(p, tS, j0, pos, kt == tg || edge, ref, l, need);
     // the group's P V of its tile before is complete (the commit its S
     // signalled came after it): O follows the reference
     if (seen > 0 && __any_sync(0xffffffffu, need)) {
@@ -309,51 +332,74 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     }
     __syncwarp();
   } else if (warp == kIssuer) {
-    if (lane == 0) {
-      const uint32_t idS = umma_idesc_bf16(128, 128, 0, 0);
-      const uint32_t idO = umma_idesc_bf16(128, 128, 0, 1);
-      const uint64_t qd = desc_kmajor_sw128(smem_addr(sm + kOffQ), kQT, 0);
-      const uint64_t kd = desc_kmajor_sw128(smem_addr(sm + kOffK), kQT, 0);
-      const uint64_t vd = desc_mnmajor_sw128(smem_addr(sm + kOffV), kQT, 0);
-      int seen[2] = {0, 0};
-      auto issue_S = [&](int g, int i) {          // K entry i has landed
-        const uint64_t qg = qd + ((g * kTileB) >> 4), kg = kd + (((i & 1) * kTileB) >> 4);
+    // The whole warp walks the list, one elected lane issues: descriptors and
+    // tensor-memory addresses then stay in uniform registers, where the MMA
+    // instruction takes them from.  (All 512 columns are the CTA's: they
+    // start at 0.)
+    const bool leader = elect_one();
+    const uint64_t qd = desc_kmajor_sw128(smem_addr(sm + kOffQ), kQT, 0);
+    const uint64_t kd = desc_kmajor_sw128(smem_addr(sm + kOffK), kQT, 0);
+    const uint64_t vd = desc_mnmajor_sw128(smem_addr(sm + kOffV), kQT, 0);
+    constexpr uint32_t idO = umma_idesc_bf16(128, 128, 0, 1);
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort)) != 0;
+    };
+    // S of group g from the K tile in slot `slot`
+    auto issue_S = [&](int g, int slot, uint32_t id) {
+      const uint64_t qg = qd + ((g * kTileB) >> 4), kg = kd + ((slot * kTileB) >> 4);
+      if (leader) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const uint64_t at = ((s >> 2) * kHalfB + (s & 3) * 32) >> 4;   // as desc_kmajor_sw128 steps
-          umma_bf16(tmem + 128 * g, qg + at, kg + at, idS, s > 0);
+          umma_bf16(128 * g, qg + at, kg + at, id, s > 0);
         }
         umma_commit(&S.sfull[g]);
-      };
-      bool ok = mbar_wait(&S.qbar, 0, &S.abort) && mbar_wait(&S.full[0], 0, &S.abort);
-      if (ok) {
-        tc_fence_after();
-        for (int g = 0; g < 2; ++g)
-          if (list.takes(g, 0)) issue_S(g, 0);
       }
-      for (int i = 0; ok && i < list.n; ++i) {
-        if (!(ok = mbar_wait(&S.full[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) break;   // V(i), K(i + 1)
-        const uint64_t vg = vd + ((((i + 1) & 1) * kTileB) >> 4);
+      __syncwarp();
+    };
+    auto issue_PV = [&](int g, int slot, auto steps, bool first) {
+      const uint64_t vg = vd + ((slot * kTileB) >> 4);
+      if (leader) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (list.takes(g, i)) {
-            if (!(ok = mbar_wait(&S.pfull[g], seen[g] & 1, &S.abort))) break;
-            tc_fence_after();
+        for (int s = 0; s < decltype(steps)::value; ++s)
+          umma_bf16_tmem_a(256 + 128 * g, 128 * g + 8 * s, vg + ((s * 16 * 128) >> 4), idO, !first || s > 0);
+      }
+      __syncwarp();
+    };
+    auto next_S = [&](int g, int i) {
+      if (i == list.narrow) issue_S(g, i & 1, umma_idesc_bf16(128, kNarrow, 0, 0));
+      else issue_S(g, i & 1, umma_idesc_bf16(128, 128, 0, 0));
+    };
+    int seen0 = 0, seen1 = 0;
+    bool ok = wait(&S.qbar, 0) && wait(&S.full[0], 0);
+    if (ok) {
+      tc_fence_after();
+      if (list.takes(0, 0)) next_S(0, 0);
+      if (list.takes(1, 0)) next_S(1, 0);
+    }
+    for (int i = 0; ok && i < list.n; ++i) {
+      const int slot = (i + 1) & 1;               // V(i), K(i + 1)
+      if (!(ok = wait(&S.full[slot], (i + 1) >> 1))) break;
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              umma_bf16_tmem_a(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, vg + ((s * 16 * 128) >> 4), idO,
-                               seen[g] > 0 || s > 0);
-            ++seen[g];
-            if (list.tile(i) == list.t[g]) umma_commit(&S.odone[g]);
-          }
-          if (list.takes(g, i + 1)) issue_S(g, i + 1);   // over P, which P V issued before it has read
+      for (int g = 0; g < 2; ++g) {
+        int& seen = g ? seen1 : seen0;
+        if (list.takes(g, i)) {
+          if (!(ok = wait(&S.pfull[g], seen))) break;
+          tc_fence_after();
+          if (i == list.narrow) issue_PV(g, slot, std::integral_constant<int, kNarrow / 16>{}, seen == 0);
+          else issue_PV(g, slot, std::integral_constant<int, 8>{}, seen == 0);
+          ++seen;
+          if (list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
         }
+        if (list.takes(g, i + 1)) next_S(g, i + 1);   // over P, which P V issued before it has read
       }
-      if (!ok) {
-        S.abort = 1;
-        atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
-      }
-      // no MMA may still be writing TMEM when it is released
+    }
+    if (!ok && leader) {
+      S.abort = 1;
+      atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
+    }
+    // no MMA may still be writing TMEM when it is released
+    if (leader) {
       umma_commit(&S.drain);
       drain_wait(&S.drain, 0);
     }
