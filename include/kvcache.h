@@ -173,7 +173,8 @@ DROPKV_API dropkv_status kvcache_free(const kvcache_shape* shape, const kvcache_
  *   lengths      device int32 [B], 0 <= n_b <= n_max, or NULL for n_max
  * Values and keys of live rows must be finite (a key tile of 128 tokens
  * enters the tensor cores whole, and 0 times an infinity is not 0).
- * Supported: Hq % Hkv == 0; d a multiple of 8 in [8, 128]; B, Hq <= 65535. */
+ * Supported: Hq % Hkv == 0; d a multiple of 8 in [8, 128]; B, Hq <= 65535;
+ * n_max <= 2^30; Hq * ceil(n_max / 256) < 2^31. */
 DROPKV_API dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t n_max,
                                                   const void* q, const void* k, const void* v,
                                                   const int32_t* lengths, int32_t window, int32_t sinks,

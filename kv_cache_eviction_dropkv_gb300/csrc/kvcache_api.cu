@@ -191,7 +191,7 @@ dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32
   if (B < 1 || Hq < 1 || Hkv < 1 || d < 1 || n_max < 1 || Hq % Hkv != 0 || window < 0 || sinks < 0)
     return DROPKV_ERR_INVALID_ARG;
   if (d % 8 != 0 || d > dropkv::kDPad || B > 65535 || Hq > 65535 || n_max > (1 << 30) ||
-      (long long)B * Hq >= (1LL << 31))
+      (long long)B * Hq >= (1LL << 31) || ((long long)n_max + 255) / 256 * Hq >= (1LL << 31))
     return DROPKV_ERR_UNSUPPORTED;
   if (!q || !k || !v || !attn_out || !status || !aligned(q) || !aligned(k) || !aligned(v) || !aligned(attn_out) ||
       !aligned(status, 4))
@@ -200,6 +200,8 @@ dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32
   if (ranges_overlap(attn_out, q_bytes, q, q_bytes) || ranges_overlap(attn_out, q_bytes, k, kv_bytes) ||
       ranges_overlap(attn_out, q_bytes, v, kv_bytes))
     return DROPKV_ERR_INVALID_ARG;
+  const int sms = current_sms(nullptr);
+  if (sms <= 0) return DROPKV_ERR_CUDA;
   CUtensorMap tq, tk, tv;
   if (!dropkv::encode_rows(&tq, q, d, n_max, B * Hq) || !dropkv::encode_rows(&tk, k, d, n_max, B * Hkv) ||
       !dropkv::encode_rows(&tv, v, d, n_max, B * Hkv))
@@ -213,7 +215,7 @@ dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32
   p.sinks = sinks;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
   p.status = status;
-  return launched(launch_window(p, tq, tk, tv, stream));
+  return launched(launch_window(p, tq, tk, tv, sms, stream));
 }
 
 dropkv_status kvcache_read_status(const uint32_t* status, cudaStream_t stream, uint32_t* flags_out) {

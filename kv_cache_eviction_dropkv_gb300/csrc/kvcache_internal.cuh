@@ -103,7 +103,7 @@ struct WindowCall {
   uint32_t* status;
 };
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          cudaStream_t st);
+                          int sms, cudaStream_t st);
 
 // Allow a kernel its dynamic shared memory on the current device, once per
 // device (the setting stays; making it at every launch costs host time).

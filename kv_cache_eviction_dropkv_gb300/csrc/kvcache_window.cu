@@ -8,23 +8,25 @@
 // the exponentials: 128 x 128 of them against 2 x 128^3 multiply-adds per
 // tile), so the tiles go through tcgen05 with TMEM accumulators.
 //
-// A CTA holds two 128-row query tiles of one head, t and t + 1, one per
-// softmax group of four warps; thread r of a group owns TMEM lane r, the
-// whole of its row, so a row's maximum and sum need no exchange between
-// threads.  Both walk one list of 128-key tiles: those with first tokens,
-// then those the two windows reach.  Per key tile and group: S = Q K^T into
-// the group's TMEM columns; P = 2^(x - ref), with a reference that moves only
-// when it must, written back over S as bf16 pairs; O += P V with P read from
-// tensor memory.  The MMA warp alternates between the groups, so one group's
-// products run under the other's softmax.  Its issuing thread is what bounds
-// the kernel (an MMA of 128 x 128 x 16 is issued about as fast as it runs, and
-// S = Q K^T reads both operands from shared memory at its full rate), so it is
-// spared everything else: K tile i and V tile i - 1 come as one pair on one
-// barrier, and the softmax groups release a pair when S(i) is complete, which
-// every product issued before it then is too.  A group skips tiles outside
-// its own window; only tiles that cut the diagonal or a window's edge are
-// masked element by element, and a tile of which only the first kNarrow keys
-// are first tokens is taken kNarrow keys wide.
+// One CTA per SM works through items: two 128-row query tiles of one head, t
+// and t + 1, one per softmax group of four warps; thread r of a group owns
+// TMEM lane r, the whole of its row, so a row's maximum and sum need no
+// exchange between threads.  Both walk one list of 128-key tiles: those with
+// first tokens, then those the two windows reach.  Per key tile and group:
+// S = Q K^T into the group's TMEM columns; P = 2^(x - ref), with a reference
+// that moves only when it must, written back over S as bf16 pairs; O += P V
+// with P read from tensor memory.  The MMA warp alternates between the groups,
+// so one group's products run under the other's softmax.  Issuing is what
+// bounds the kernel (an MMA of 128 x 128 x 16 is issued about as fast as it
+// runs, and S = Q K^T reads both operands from shared memory at its full
+// rate), so the MMA warp is spared everything else: K tile i and V tile i - 1
+// come as one pair on one barrier, and the softmax groups release a pair when
+// S(i) is complete, which every product issued before it then is too.  The
+// rings run on from item to item: the next item's Q, K and first S come in
+// under the last one's softmax and output.  A group skips tiles outside its
+// own window; only tiles that cut the diagonal or a window's edge are masked
+// element by element, and a tile of which only the first kNarrow keys are
+// first tokens is taken kNarrow keys wide.
 #include "kvcache_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -45,11 +47,11 @@ constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after
 constexpr int kNarrow = 32;
 
 struct Small {
-  uint64_t qbar, full[2];
-  uint64_t empty[2];   // pairs released by the groups (one arrival each)
+  uint64_t qfull[2], qempty[2];   // group g's Q: landed; its last S of the item complete
+  uint64_t full[2], empty[2];     // K and V pairs: landed; released by the groups (one arrival each)
   uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
   uint64_t pfull[2];   // group g: its P written by the group's four warps
-  uint64_t odone[2];   // group g: its last P V complete
+  uint64_t odone[2];   // group g: its last P V of the item complete
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -57,7 +59,7 @@ struct Small {
 constexpr int kWinSmem = kOffSmall + (int)sizeof(Small) + 1024;
 static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
 
-// The key tiles of a CTA: list entry i is key tile tile(i).  Group 0 (query
+// The key tiles of an item: list entry i is key tile tile(i).  Group 0 (query
 // tile t[0], -1: none) takes all entries but the last, group 1 (t[1] = t[0] +
 // 1) all but `skip`, the one tile that only group 0's window may reach.
 // Pair j of the rings is K of entry j with V of entry j - 1.
@@ -85,6 +87,39 @@ __device__ __forceinline__ List make_list(const WindowCall& p, int t0, int t1) {
   l.skip = lo < lo1 && lo >= sink_tiles ? l.ns : -1;
   l.narrow = l.ns > 0 && l.ns == sink_tiles && p.sinks - (l.ns - 1) * kQT <= kNarrow ? l.ns - 1 : -1;
   return l;
+}
+
+// The items of the call in order: sequence by sequence, pairs of query tiles
+// from the sequence's end (the last tile is group 1's), heads innermost.  A
+// CTA takes every gridDim.x-th; each role walks the same cursor.
+struct Cursor {
+  int b = -1, pairs = 0;                          // sequence, its pairs of query tiles
+  int nb = 0;
+  long long first = 0;                            // items before it
+};
+__device__ __forceinline__ int length_of(const WindowCall& p, int b) {
+  const int nb = p.lengths ? p.lengths[b] : p.n_max;
+  return nb < 0 || nb > p.n_max ? 0 : nb;
+}
+struct Item {
+  int b, hq, nb;
+  List list;
+};
+// Item `it`, if there is one.
+__device__ __forceinline__ bool item_at(const WindowCall& p, Cursor& c, long long it, Item* w) {
+  while (c.b < 0 || it >= c.first + (long long)c.pairs * p.Hq) {
+    c.first += (long long)c.pairs * p.Hq;
+    if (++c.b >= p.B) return false;
+    c.nb = length_of(p, c.b);
+    c.pairs = (c.nb + 2 * kQT - 1) / (2 * kQT);
+  }
+  const int y = (int)(it - c.first), x = y / p.Hq;
+  w->b = c.b;
+  w->nb = c.nb;
+  w->hq = y - x * p.Hq;
+  const int t1 = (c.nb + kQT - 1) / kQT - 1 - 2 * x;
+  w->list = make_list(p, t1 - 1, t1);
+  return true;
 }
 
 // One lane of a converged warp.
@@ -164,95 +199,126 @@ __device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, 
   return factor;
 }
 
-__device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem,
-                                              const List& list, int warp, int lane, int b, int hq, int nb) {
+__device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem, int warp,
+                                              int lane) {
   const int g = warp >> 2, quarter = warp & 3;
-  const int tg = list.t[g];
-  const int row = quarter * 32 + lane, pos = tg * kQT + row;
+  const int row = quarter * 32 + lane;
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   const uint32_t tS = tmem + lane_base + 128 * g, tO = tmem + lane_base + 256 + 128 * g;
-  float ref = -INFINITY, l = 0.f;
-  bool bad = tg < 0;
+  const bool speaks = quarter == 0 && lane == 0;
+  uint32_t pair0 = 0, seen = 0, done = 0;         // pairs, the group's tiles and items so far
+  // A wait this warp gave up on raises the timeout flag and the CTA's abort
+  // flag, which ends every other wait of the CTA; the warp stops.
   auto give_up = [&]() {
-    bad = true;
     if (lane == 0) {
       S.abort = 1;
       atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
     }
   };
-  // Pair i is needed no more by this group (waited for when pair i + 2 takes its place).
-  auto release = [&](int i) {
-    if (quarter == 0 && lane == 0 && i + 2 <= list.n) mbar_arrive(&S.empty[i & 1]);
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort));
   };
-  int seen = 0;                                   // tiles of this group so far
-  for (int i = 0; !bad && i < list.n; ++i) {
-    if (!list.takes(g, i)) continue;
-    const int kt = list.tile(i);
-    if (!__all_sync(0xffffffffu, mbar_wait(&S.sfull[g], seen & 1, &S.abort))) { give_up(); break; }
-    tc_fence_after();
-    if (g == 1 && list.skip >= 0 && i == list.skip + 1) release(list.skip);
-    release(i);                                   // S is complete, and the P V issued before it
-    const int j0 = kt * kQT;
-    // the last row of the tile reaches back to tg 128 + 127 - W + 1
-    const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
-    bool need;
-    const float factor = i == list.narrow ? softmax_tile<kNarrow>(p, tS, j0, pos, true, ref, l, need)
-                                          : softmax_tile<kQT>(p, tS, j0, pos, kt == tg || edge, ref, l, need);
-    // the group's P V of its tile before is complete (the commit its S
-    // signalled came after it): O follows the reference
-    if (seen > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        float o[16];
-        tmem_ld16(tO + 16 * c, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] *= factor;
-        tmem_st16(tO + 16 * c, o);
-      }
+  // Pair j of the item is needed no more by this group.
+  auto release = [&](int j) {
+    if (speaks) mbar_arrive(&S.empty[(pair0 + j) & 1]);
+  };
+  // The same for a pair this group never touched: only once it has landed, so
+  // that the release counts for it and not for the pair before in its slot.
+  auto pass = [&](int j) {
+    if (!wait(&S.full[(pair0 + j) & 1], (pair0 + j) >> 1)) return false;
+    release(j);
+    return true;
+  };
+  Cursor at;
+  Item w;
+  for (long long it = blockIdx.x; item_at(p, at, it, &w); it += gridDim.x) {
+    const List& list = w.list;
+    const int n = list.n, tg = list.t[g], pos = tg * kQT + row;
+    if (tg < 0) {
+      for (int j = 0; j <= n; ++j)
+        if (!pass(j)) { give_up(); return; }
+      pair0 += n + 1;
+      continue;
     }
-    if (j0 + kQT > nb) {
-      // the sequence's last key tile (group 1's alone): rows past the end may
-      // hold anything; zero them so that 0 * NaN never reaches O
-      if (!__all_sync(0xffffffffu, mbar_wait(&S.full[(i + 1) & 1], ((i + 1) >> 1) & 1, &S.abort))) { give_up(); break; }
-      if (j0 + row >= nb) {
-        uint8_t* vrow = sm + kOffV + ((i + 1) & 1) * kTileB + row * 128;
-#pragma unroll
+    float ref = -INFINITY, l = 0.f;
+    bool first = true;
+    for (int i = 0; i < n; ++i) {
+      if (!list.takes(g, i)) continue;
+      const int kt = list.tile(i), j0 = kt * kQT;
+      if (!wait(&S.sfull[g], seen)) { give_up(); return; }
+      tc_fence_after();
+      if (g == 1 && list.skip >= 0 && i == list.skip + 1) release(list.skip);
+      release(i);                                 // S is complete, and the P V issued before it
+      if (speaks && kt == tg) mbar_arrive(&S.qempty[g]);
+      // the last row of the tile reaches back to tg 128 + 127 - W + 1
+      const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
+      bool need;
+      const float factor = i == list.narrow ? softmax_tile<kNarrow>(p, tS, j0, pos, true, ref, l, need)
+                                            : softmax_tile<kQT>(p, tS, j0, pos, kt == tg || edge, ref, l, need);
+      // the group's P V of its tile before is complete (the commit its S
+      // signalled came after it): O follows the reference
+      if (!first && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
         for (int c = 0; c < 8; ++c) {
-          *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vrow + kHalfB + c * 16) = make_uint4(0, 0, 0, 0);
+          float o[16];
+          tmem_ld16(tO + 16 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o[u] *= factor;
+          tmem_st16(tO + 16 * c, o);
         }
       }
-      fence_proxy_async_smem();
-    }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.pfull[g]);
-    ++seen;
-  }
-  if (tg < 0) return;
-  const bool ok = !bad && __all_sync(0xffffffffu, mbar_wait(&S.odone[g], 0, &S.abort));
-  if (!bad && !ok) give_up();
-  if (!ok) return;
-  tc_fence_after();
-  const float inv_l = 1.0f / l;                   // a row sees itself at least
-  __nv_bfloat16* orow = p.out + (((size_t)b * p.Hq + hq) * p.n_max + pos) * p.d;
-#pragma unroll 1
-  for (int c = 0; c < 8; ++c) {
-    float o[16];
-    tmem_ld16(tO + 16 * c, o);
-    tmem_wait_ld();
-    const int c0 = 16 * c;
-    if (pos < nb && c0 < p.d) {
-      uint32_t w8[8];
+      first = false;
+      if (j0 + kQT > w.nb) {
+        // the sequence's last key tile (group 1's alone): rows past the end may
+        // hold anything; zero them so that 0 * NaN never reaches O
+        const uint32_t pr = pair0 + i + 1;
+        if (!wait(&S.full[pr & 1], pr >> 1)) { give_up(); return; }
+        if (j0 + row >= w.nb) {
+          uint8_t* vrow = sm + kOffV + (pr & 1) * kTileB + row * 128;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * u] * inv_l, o[2 * u + 1] * inv_l);
-        w8[u] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int c = 0; c < 8; ++c) {
+            *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(vrow + kHalfB + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
       }
-      *reinterpret_cast<uint4*>(orow + c0) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-      if (c0 + 8 < p.d) *reinterpret_cast<uint4*>(orow + c0 + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.pfull[g]);
+      ++seen;
+    }
+    if (!wait(&S.odone[g], done)) { give_up(); return; }
+    ++done;
+    tc_fence_after();
+    // group 0: pair n - 1 (its last V) and the one it never touched; group 1: its last V
+    if (g == 0) {
+      release(n - 1);
+      if (!pass(n)) { give_up(); return; }
+    } else {
+      release(n);
+    }
+    pair0 += n + 1;
+    const float inv_l = 1.0f / l;                 // a row sees itself at least
+    __nv_bfloat16* orow = p.out + (((size_t)w.b * p.Hq + w.hq) * p.n_max + pos) * p.d;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      float o[16];
+      tmem_ld16(tO + 16 * c, o);
+      tmem_wait_ld();
+      const int c0 = 16 * c;
+      if (pos < w.nb && c0 < p.d) {
+        uint32_t w8[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * u] * inv_l, o[2 * u + 1] * inv_l);
+          w8[u] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        *reinterpret_cast<uint4*>(orow + c0) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+        if (c0 + 8 < p.d) *reinterpret_cast<uint4*>(orow + c0 + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+      }
     }
   }
 }
@@ -263,29 +329,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Small& S = *reinterpret_cast<Small*>(sm + kOffSmall);
-  grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.z, hq = blockIdx.y;
-  const int nb = p.lengths ? p.lengths[b] : p.n_max;
-  if (nb < 0 || nb > p.n_max) {
-    if (tid == 0 && blockIdx.x == 0 && hq == 0) atomicOr(p.status, DROPKV_FLAG_BAD_LENGTH);
-    return;
-  }
-  // pairs of query tiles from the sequence's end: the last tile is group 1's
-  const int t1 = (nb + kQT - 1) / kQT - 1 - 2 * (int)blockIdx.x, t0 = t1 - 1;
-  if (t1 < 0) return;
-  const List list = make_list(p, t0, t1);
-  const int unit = b * p.Hkv + hq / p.g;
-
   if (tid == 0) {
-    const int groups = t0 >= 0 ? 2 : 1;
-    mbar_init(&S.qbar, 1);
-    mbar_init(&S.drain, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], groups);
+      mbar_init(&S.qfull[i], 1); mbar_init(&S.qempty[i], 1);
+      mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 2);
       mbar_init(&S.sfull[i], 1); mbar_init(&S.pfull[i], 4);
       mbar_init(&S.odone[i], 1);
     }
+    mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
   }
@@ -294,41 +346,54 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
+  grid_dep_wait();
   grid_dep_launch();
+  if (blockIdx.x == 0)                            // lengths that cannot be served are left out
+    for (int b = tid; b < p.B; b += kWinThreads)
+      if (p.lengths && (p.lengths[b] < 0 || p.lengths[b] > p.n_max)) atomicOr(p.status, DROPKV_FLAG_BAD_LENGTH);
 
   if (warp == kProducer) {
     if (lane == 0) {
-      const int zq = b * p.Hq + hq;
-      mbar_arrive_expect_tx(&S.qbar, (t0 >= 0 ? 2 : 1) * kTileB);
-      for (int g = t0 >= 0 ? 0 : 1; g < 2; ++g) {
-        tma_load_3d(sm + kOffQ + g * kTileB, &tmq, &S.qbar, 0, list.t[g] * kQT, zq);
-        tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qbar, 64, list.t[g] * kQT, zq);
-      }
-      int issued = 0;
+      uint32_t pair = 0, used[2] = {0, 0};        // pairs issued, items of group g
       bool ok = true;
-      for (int j = 0; j <= list.n; ++j) {
-        uint64_t* full = &S.full[j & 1];
-        if (j >= 2 && !mbar_wait(&S.empty[j & 1], ((j >> 1) + 1) & 1, &S.abort)) { ok = false; break; }
-        mbar_arrive_expect_tx(full, (j < list.n ? kTileB : 0) + (j > 0 ? kTileB : 0));
-        if (j > 0) {                              // needed first
-          uint8_t* dst = sm + kOffV + (j & 1) * kTileB;
-          tma_load_3d(dst, &tmv, full, 0, list.tile(j - 1) * kQT, unit);
-          tma_load_3d(dst + kHalfB, &tmv, full, 64, list.tile(j - 1) * kQT, unit);
+      Cursor at;
+      Item w;
+      for (long long it = blockIdx.x; ok && item_at(p, at, it, &w); it += gridDim.x) {
+        const List& list = w.list;
+        const int zq = w.b * p.Hq + w.hq, unit = w.b * p.Hkv + w.hq / p.g;
+        for (int g = 0; ok && g < 2; ++g) {
+          if (list.t[g] < 0) continue;
+          if (used[g] > 0 && !(ok = mbar_wait(&S.qempty[g], (used[g] - 1) & 1, &S.abort))) break;
+          mbar_arrive_expect_tx(&S.qfull[g], kTileB);
+          tma_load_3d(sm + kOffQ + g * kTileB, &tmq, &S.qfull[g], 0, list.t[g] * kQT, zq);
+          tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qfull[g], 64, list.t[g] * kQT, zq);
+          ++used[g];
         }
-        if (j < list.n) {
-          uint8_t* dst = sm + kOffK + (j & 1) * kTileB;
-          tma_load_3d(dst, &tmk, full, 0, list.tile(j) * kQT, unit);
-          tma_load_3d(dst + kHalfB, &tmk, full, 64, list.tile(j) * kQT, unit);
+        for (int j = 0; ok && j <= list.n; ++j) {
+          const uint32_t slot = pair & 1;
+          if (pair >= 2 && !(ok = mbar_wait(&S.empty[slot], ((pair >> 1) + 1) & 1, &S.abort))) break;
+          mbar_arrive_expect_tx(&S.full[slot], (j < list.n ? kTileB : 0) + (j > 0 ? kTileB : 0));
+          if (j > 0) {                            // needed first
+            uint8_t* dst = sm + kOffV + slot * kTileB;
+            tma_load_3d(dst, &tmv, &S.full[slot], 0, list.tile(j - 1) * kQT, unit);
+            tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, list.tile(j - 1) * kQT, unit);
+          }
+          if (j < list.n) {
+            uint8_t* dst = sm + kOffK + slot * kTileB;
+            tma_load_3d(dst, &tmk, &S.full[slot], 0, list.tile(j) * kQT, unit);
+            tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, list.tile(j) * kQT, unit);
+          }
+          ++pair;
         }
-        ++issued;
       }
       if (!ok) {
         S.abort = 1;
         atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
       }
       // every copy has landed before the CTA can leave
-      for (int j = max(0, issued - 2); j < issued; ++j) drain_wait(&S.full[j & 1], (j >> 1) & 1);
-      drain_wait(&S.qbar, 0);
+      for (uint32_t j = pair > 2 ? pair - 2 : 0; j < pair; ++j) drain_wait(&S.full[j & 1], (j >> 1) & 1);
+      for (int g = 0; g < 2; ++g)
+        if (used[g] > 0) drain_wait(&S.qfull[g], (used[g] - 1) & 1);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
@@ -366,33 +431,44 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
       __syncwarp();
     };
-    auto next_S = [&](int g, int i) {
-      if (i == list.narrow) issue_S(g, i & 1, umma_idesc_bf16(128, kNarrow, 0, 0));
-      else issue_S(g, i & 1, umma_idesc_bf16(128, 128, 0, 0));
-    };
-    int seen0 = 0, seen1 = 0;
-    bool ok = wait(&S.qbar, 0) && wait(&S.full[0], 0);
-    if (ok) {
+    uint32_t pair0 = 0, seen0 = 0, seen1 = 0, used0 = 0, used1 = 0;   // pairs, tiles and items of the groups so far
+    bool ok = true;
+    Cursor at;
+    Item w;
+    for (long long it = blockIdx.x; ok && item_at(p, at, it, &w); it += gridDim.x) {
+      const List& list = w.list;
+      auto next_S = [&](int g, int i) {
+        const int slot = (pair0 + i) & 1;
+        if (i == list.narrow) issue_S(g, slot, umma_idesc_bf16(128, kNarrow, 0, 0));
+        else issue_S(g, slot, umma_idesc_bf16(128, 128, 0, 0));
+      };
+      const bool two = list.t[0] >= 0;
+      ok = (!two || wait(&S.qfull[0], used0++)) && wait(&S.qfull[1], used1++) && wait(&S.full[pair0 & 1], pair0 >> 1);
+      if (!ok) break;
       tc_fence_after();
       if (list.takes(0, 0)) next_S(0, 0);
       if (list.takes(1, 0)) next_S(1, 0);
-    }
-    for (int i = 0; ok && i < list.n; ++i) {
-      const int slot = (i + 1) & 1;               // V(i), K(i + 1)
-      if (!(ok = wait(&S.full[slot], (i + 1) >> 1))) break;
+      bool first0 = true, first1 = true;
+      for (int i = 0; ok && i < list.n; ++i) {
+        const uint32_t pr = pair0 + i + 1;        // V(i), K(i + 1)
+        if (!(ok = wait(&S.full[pr & 1], pr >> 1))) break;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        int& seen = g ? seen1 : seen0;
-        if (list.takes(g, i)) {
-          if (!(ok = wait(&S.pfull[g], seen))) break;
-          tc_fence_after();
-          if (i == list.narrow) issue_PV(g, slot, std::integral_constant<int, kNarrow / 16>{}, seen == 0);
-          else issue_PV(g, slot, std::integral_constant<int, 8>{}, seen == 0);
-          ++seen;
-          if (list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t& seen = g ? seen1 : seen0;
+          bool& first = g ? first1 : first0;
+          if (list.takes(g, i)) {
+            if (!(ok = wait(&S.pfull[g], seen))) break;
+            tc_fence_after();
+            if (i == list.narrow) issue_PV(g, pr & 1, std::integral_constant<int, kNarrow / 16>{}, first);
+            else issue_PV(g, pr & 1, std::integral_constant<int, 8>{}, first);
+            first = false;
+            ++seen;
+            if (list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
+          }
+          if (list.takes(g, i + 1)) next_S(g, i + 1);   // over P, which P V issued before it has read
         }
-        if (list.takes(g, i + 1)) next_S(g, i + 1);   // over P, which P V issued before it has read
       }
+      pair0 += list.n + 1;
     }
     if (!ok && leader) {
       S.abort = 1;
@@ -405,7 +481,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    softmax_group(p, S, sm, tmem, list, warp, lane, b, hq, nb);
+    softmax_group(p, S, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -418,11 +494,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 }  // namespace
 
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          cudaStream_t st) {
+                          int sms, cudaStream_t st) {
   const cudaError_t e = allow_smem<window_prefill_kernel>(kWinSmem);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.n_max + kQT - 1) / kQT;
-  return launch_pdl(window_prefill_kernel, dim3((tiles + 1) / 2, p.Hq, p.B), dim3(kWinThreads), kWinSmem, st, tq, tk,
+  const long long most = (long long)((p.n_max + 2 * kQT - 1) / (2 * kQT)) * p.Hq * p.B;
+  return launch_pdl(window_prefill_kernel, dim3((unsigned)std::min<long long>(most, sms)), dim3(kWinThreads), kWinSmem, st, tq, tk,
                     tv, p);
 }
 
