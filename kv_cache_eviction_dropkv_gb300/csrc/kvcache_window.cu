@@ -135,29 +135,34 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kDrain) break;
 }
 
-// One row against the first NC columns of its S: moves the reference, turns S
-// into P in place.  Returns the factor O (and l, already done) follows by.
-template <int NC>
-__device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, int j0, int pos, bool mask, float& ref,
-                                              float& l, bool& need) {
+// One row against its 128 columns of S: moves the reference, turns S into P in
+// place.  Returns the factor O follows by (l has followed).  Columns [from,
+// to) and [0, first) are seen.  The masked path is kept short: this code runs
+// four warps wide from a small instruction cache, and a cold branch of a few
+// hundred instructions costs more than the exponentials.
+__device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, bool mask, int from, int to, int first,
+                                              float& ref, float& l, bool& need) {
   const float scale = p.scale_log2;
-  float x[NC];
+  float x[kQT];
 #pragma unroll
-  for (int c = 0; c < NC / 16; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
+  for (int c = 0; c < 8; ++c) tmem_ld16(tS + 16 * c, x + 16 * c);
   tmem_wait_ld();
   if (mask) {
-    const int lo = p.window > 0 ? pos - p.window : -1;   // keys above it are in the window
+    auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };   // bits [0, n)
 #pragma unroll
-    for (int u = 0; u < NC; ++u) {
-      const int j = j0 + u;
-      if (!(j <= pos && (j > lo || j < p.sinks))) x[u] = -INFINITY;
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t seen = (below(to - 32 * c) & ~below(from - 32 * c)) | below(first - 32 * c);
+      if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+#pragma unroll
+      for (int u = 0; u < 32; ++u)
+        if (!(seen & (1u << u))) x[32 * c + u] = -INFINITY;
     }
   }
   float m8[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) m8[u] = x[u];
 #pragma unroll
-  for (int u = 8; u < NC; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
+  for (int u = 8; u < kQT; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
   const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale;
   need = mt > ref + kMove;
@@ -175,8 +180,8 @@ __device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, 
   uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
   float hw[16];
 #pragma unroll
-  for (int c = 0; c <= NC / 16; ++c) {
-    if (c < NC / 16) {
+  for (int c = 0; c <= 8; ++c) {
+    if (c < 8) {
 #pragma unroll
       for (int u = 16 * c; u < 16 * c + 16; u += 2) {
         const uint64_t y = f2_fma(f2_pack(x[u], x[u + 1]), sc2, nr2);
@@ -253,8 +258,11 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
       // the last row of the tile reaches back to tg 128 + 127 - W + 1
       const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
       bool need;
-      const float factor = i == list.narrow ? softmax_tile<kNarrow>(p, tS, j0, pos, true, ref, l, need)
-                                            : softmax_tile<kQT>(p, tS, j0, pos, kt == tg || edge, ref, l, need);
+      // keys j <= pos with j > pos - window or j < sinks; past a narrow tile's
+      // kNarrow columns S holds anything
+      const float factor = softmax_tile(p, tS, kt == tg || edge || i == list.narrow,
+                                        p.window > 0 ? pos - p.window + 1 - j0 : 0, pos + 1 - j0,
+                                        p.window > 0 ? min(p.sinks, pos + 1) - j0 : 0, ref, l, need);
       // the group's P V of its tile before is complete (the commit its S
       // signalled came after it): O follows the reference
       if (!first && __any_sync(0xffffffffu, need)) {
