@@ -211,8 +211,8 @@ dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32
   p.out = static_cast<__nv_bfloat16*>(attn_out);
   p.lengths = lengths;
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.d = d; p.n_max = n_max;
-  p.window = window;
-  p.sinks = sinks;
+  p.window = std::min(window, n_max);      // the same rows, and positions stay in 32 bits
+  p.sinks = std::min(sinks, n_max);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
   p.status = status;
   return launched(launch_window(p, tq, tk, tv, sms, stream));

@@ -19,14 +19,14 @@
 // so one group's products run under the other's softmax.  Issuing is what
 // bounds the kernel (an MMA of 128 x 128 x 16 is issued about as fast as it
 // runs, and S = Q K^T reads both operands from shared memory at its full
-// rate), so the MMA warp is spared everything else: K tile i and V tile i - 1
-// come as one pair on one barrier, and the softmax groups release a pair when
-// S(i) is complete, which every product issued before it then is too.  The
-// rings run on from item to item: the next item's Q, K and first S come in
-// under the last one's softmax and output.  A group skips tiles outside its
-// own window; only tiles that cut the diagonal or a window's edge are masked
-// element by element, and a tile of which only the first kNarrow keys are
-// first tokens is taken kNarrow keys wide.
+// rate), so the MMA warp is spared everything else: the items' lists
+// follow one another as one row of entries, K of an entry comes with V of the
+// entry before as one pair on one barrier, and the softmax groups release a
+// pair when their S of it is complete, which every product issued before it
+// then is too.  The next item's Q, K and first S so come in under the last
+// one's softmax and output.  A group skips tiles outside its own window; only
+// tiles that cut the diagonal or a window's edge are masked, and a tile of
+// which only the first kNarrow keys are first tokens is taken kNarrow keys wide.
 #include "kvcache_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -62,7 +62,6 @@ static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
 // The key tiles of an item: list entry i is key tile tile(i).  Group 0 (query
 // tile t[0], -1: none) takes all entries but the last, group 1 (t[1] = t[0] +
 // 1) all but `skip`, the one tile that only group 0's window may reach.
-// Pair j of the rings is K of entry j with V of entry j - 1.
 struct List {
   int t[2];
   int ns, s2, n;                                  // tiles [0, ns), then s2, s2 + 1, ...: n entries
@@ -211,7 +210,7 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
   const uint32_t tS = tmem + lane_base + 128 * g, tO = tmem + lane_base + 256 + 128 * g;
   const bool speaks = quarter == 0 && lane == 0;
-  uint32_t pair0 = 0, seen = 0, done = 0;         // pairs, the group's tiles and items so far
+  uint32_t pair0 = 0, seen = 0, done = 0;         // entries, the group's tiles and items so far
   // A wait this warp gave up on raises the timeout flag and the CTA's abort
   // flag, which ends every other wait of the CTA; the warp stops.
   auto give_up = [&]() {
@@ -223,12 +222,13 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   auto wait = [&](uint64_t* bar, uint32_t phase) {
     return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort));
   };
-  // Pair j of the item is needed no more by this group.
+  // The pair of the item's entry j (with V of the entry before) is needed no
+  // more by this group.
   auto release = [&](int j) {
     if (speaks) mbar_arrive(&S.empty[(pair0 + j) & 1]);
   };
-  // The same for a pair this group never touched: only once it has landed, so
-  // that the release counts for it and not for the pair before in its slot.
+  // The same for an entry this group does not take: only once it has landed,
+  // so that the release counts for it and not for the pair before in its slot.
   auto pass = [&](int j) {
     if (!wait(&S.full[(pair0 + j) & 1], (pair0 + j) >> 1)) return false;
     release(j);
@@ -240,9 +240,9 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     const List& list = w.list;
     const int n = list.n, tg = list.t[g], pos = tg * kQT + row;
     if (tg < 0) {
-      for (int j = 0; j <= n; ++j)
+      for (int j = 0; j < n; ++j)
         if (!pass(j)) { give_up(); return; }
-      pair0 += n + 1;
+      pair0 += n;
       continue;
     }
     float ref = -INFINITY, l = 0.f;
@@ -301,31 +301,29 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     if (!wait(&S.odone[g], done)) { give_up(); return; }
     ++done;
     tc_fence_after();
-    // group 0: pair n - 1 (its last V) and the one it never touched; group 1: its last V
-    if (g == 0) {
-      release(n - 1);
-      if (!pass(n)) { give_up(); return; }
-    } else {
-      release(n);
-    }
-    pair0 += n + 1;
+    // group 0 does not take the last entry, but its last V came with it
+    if (g == 0 && !pass(n - 1)) { give_up(); return; }
+    pair0 += n;
     const float inv_l = 1.0f / l;                 // a row sees itself at least
     __nv_bfloat16* orow = p.out + (((size_t)w.b * p.Hq + w.hq) * p.n_max + pos) * p.d;
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-      float o[16];
-      tmem_ld16(tO + 16 * c, o);
+    for (int c0 = 0; c0 < p.d; c0 += 32) {
+      float o[32];
+      tmem_ld16(tO + c0, o);
+      tmem_ld16(tO + c0 + 16, o + 16);
       tmem_wait_ld();
-      const int c0 = 16 * c;
-      if (pos < w.nb && c0 < p.d) {
-        uint32_t w8[8];
+      if (pos < w.nb) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * u] * inv_l, o[2 * u + 1] * inv_l);
-          w8[u] = *reinterpret_cast<const uint32_t*>(&h2);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[8 * q + 2 * u] * inv_l, o[8 * q + 2 * u + 1] * inv_l);
+            w4[u] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          if (c0 + 8 * q < p.d)
+            *reinterpret_cast<uint4*>(orow + c0 + 8 * q) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
-        *reinterpret_cast<uint4*>(orow + c0) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-        if (c0 + 8 < p.d) *reinterpret_cast<uint4*>(orow + c0 + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
       }
     }
   }
@@ -363,12 +361,33 @@ __global__ void __launch_bounds__(kWinThreads, 1)
   if (warp == kProducer) {
     if (lane == 0) {
       uint32_t pair = 0, used[2] = {0, 0};        // pairs issued, items of group g
+      int v_tile = -1, v_unit = 0;                // the entry before: its V comes with this one's K
+      auto put = [&](int k_tile, int k_unit) {    // k_tile -1: the last V alone
+        const uint32_t slot = pair & 1;
+        if (pair >= 2 && !mbar_wait(&S.empty[slot], ((pair >> 1) + 1) & 1, &S.abort)) return false;
+        mbar_arrive_expect_tx(&S.full[slot], (k_tile >= 0 ? kTileB : 0) + (v_tile >= 0 ? kTileB : 0));
+        if (v_tile >= 0) {                        // needed first
+          uint8_t* dst = sm + kOffV + slot * kTileB;
+          tma_load_3d(dst, &tmv, &S.full[slot], 0, v_tile * kQT, v_unit);
+          tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, v_tile * kQT, v_unit);
+        }
+        if (k_tile >= 0) {
+          uint8_t* dst = sm + kOffK + slot * kTileB;
+          tma_load_3d(dst, &tmk, &S.full[slot], 0, k_tile * kQT, k_unit);
+          tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, k_tile * kQT, k_unit);
+        }
+        v_tile = k_tile;
+        v_unit = k_unit;
+        ++pair;
+        return true;
+      };
       bool ok = true;
       Cursor at;
       Item w;
       for (long long it = blockIdx.x; ok && item_at(p, at, it, &w); it += gridDim.x) {
         const List& list = w.list;
         const int zq = w.b * p.Hq + w.hq, unit = w.b * p.Hkv + w.hq / p.g;
+        if (!(ok = put(list.tile(0), unit))) break;   // with the last item's last V: before the waits for Q
         for (int g = 0; ok && g < 2; ++g) {
           if (list.t[g] < 0) continue;
           if (used[g] > 0 && !(ok = mbar_wait(&S.qempty[g], (used[g] - 1) & 1, &S.abort))) break;
@@ -377,23 +396,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qfull[g], 64, list.t[g] * kQT, zq);
           ++used[g];
         }
-        for (int j = 0; ok && j <= list.n; ++j) {
-          const uint32_t slot = pair & 1;
-          if (pair >= 2 && !(ok = mbar_wait(&S.empty[slot], ((pair >> 1) + 1) & 1, &S.abort))) break;
-          mbar_arrive_expect_tx(&S.full[slot], (j < list.n ? kTileB : 0) + (j > 0 ? kTileB : 0));
-          if (j > 0) {                            // needed first
-            uint8_t* dst = sm + kOffV + slot * kTileB;
-            tma_load_3d(dst, &tmv, &S.full[slot], 0, list.tile(j - 1) * kQT, unit);
-            tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, list.tile(j - 1) * kQT, unit);
-          }
-          if (j < list.n) {
-            uint8_t* dst = sm + kOffK + slot * kTileB;
-            tma_load_3d(dst, &tmk, &S.full[slot], 0, list.tile(j) * kQT, unit);
-            tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, list.tile(j) * kQT, unit);
-          }
-          ++pair;
-        }
+        for (int j = 1; ok && j < list.n; ++j) ok = put(list.tile(j), unit);
       }
+      if (ok && v_tile >= 0) ok = put(-1, 0);
       if (!ok) {
         S.abort = 1;
         atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
@@ -439,44 +444,71 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
       __syncwarp();
     };
-    uint32_t pair0 = 0, seen0 = 0, seen1 = 0, used0 = 0, used1 = 0;   // pairs, tiles and items of the groups so far
-    bool ok = true;
+    uint32_t pair0 = 0, seen0 = 0, seen1 = 0, used0 = 0, used1 = 0;   // entries, tiles and items of the groups so far
     Cursor at;
-    Item w;
-    for (long long it = blockIdx.x; ok && item_at(p, at, it, &w); it += gridDim.x) {
-      const List& list = w.list;
-      auto next_S = [&](int g, int i) {
-        const int slot = (pair0 + i) & 1;
-        if (i == list.narrow) issue_S(g, slot, umma_idesc_bf16(128, kNarrow, 0, 0));
-        else issue_S(g, slot, umma_idesc_bf16(128, 128, 0, 0));
-      };
-      const bool two = list.t[0] >= 0;
-      ok = (!two || wait(&S.qfull[0], used0++)) && wait(&S.qfull[1], used1++) && wait(&S.full[pair0 & 1], pair0 >> 1);
-      if (!ok) break;
+    Item w, w2;                                   // the item, the one after
+    long long it = blockIdx.x;
+    bool have = item_at(p, at, it, &w), ok = true;
+    // the first S of group g in an item that begins with pair pr
+    auto first_S = [&](int g, const Item& x, uint32_t pr) {
+      if (!wait(&S.qfull[g], g ? used1++ : used0++)) return false;
       tc_fence_after();
-      if (list.takes(0, 0)) next_S(0, 0);
-      if (list.takes(1, 0)) next_S(1, 0);
+      if (x.list.narrow == 0) issue_S(g, pr & 1, umma_idesc_bf16(128, kNarrow, 0, 0));
+      else issue_S(g, pr & 1, umma_idesc_bf16(128, 128, 0, 0));
+      return true;
+    };
+    if (have) {
+      ok = wait(&S.full[0], 0);
+      if (ok && w.list.takes(0, 0)) ok = first_S(0, w, 0);
+      if (ok && w.list.takes(1, 0)) ok = first_S(1, w, 0);
+    }
+    while (ok && have) {
+      it += gridDim.x;
+      const bool more = item_at(p, at, it, &w2);
+      const List& list = w.list;
       bool first0 = true, first1 = true;
-      for (int i = 0; ok && i < list.n; ++i) {
-        const uint32_t pr = pair0 + i + 1;        // V(i), K(i + 1)
-        if (!(ok = wait(&S.full[pr & 1], pr >> 1))) break;
+      // Entry i: P V of it and S of the entry after it, group 0, then group 1.
+      // plain: neither is narrow, skipped or the item's last.
+      auto entry = [&](int i, auto plain) {
+        constexpr bool kPlain = decltype(plain)::value;
+        const uint32_t pr = pair0 + i + 1;        // V(i), K of the entry after it
+        if (!wait(&S.full[pr & 1], pr >> 1)) return false;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           uint32_t& seen = g ? seen1 : seen0;
           bool& first = g ? first1 : first0;
-          if (list.takes(g, i)) {
-            if (!(ok = wait(&S.pfull[g], seen))) break;
+          if (kPlain || list.takes(g, i)) {
+            if (!wait(&S.pfull[g], seen)) return false;
             tc_fence_after();
-            if (i == list.narrow) issue_PV(g, pr & 1, std::integral_constant<int, kNarrow / 16>{}, first);
-            else issue_PV(g, pr & 1, std::integral_constant<int, 8>{}, first);
+            if (!kPlain && i == list.narrow) issue_PV(g, pr & 1, std::integral_constant<int, kNarrow / 16>{}, first);
+            else issue_PV(g, pr & 1, std::integral_constant<int, 8>{}, !kPlain && first);
             first = false;
             ++seen;
-            if (list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
+            if (!kPlain && list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
           }
-          if (list.takes(g, i + 1)) next_S(g, i + 1);   // over P, which P V issued before it has read
+          // the group's next S, over P, which P V issued before it has read
+          if (kPlain) {
+            issue_S(g, pr & 1, umma_idesc_bf16(128, 128, 0, 0));
+          } else if (i + 1 < list.n) {
+            if (list.takes(g, i + 1)) {
+              // (a group that passes over entry 0 meets its Q here)
+              if (g == 1 && list.skip == 0 && i == 0 && !wait(&S.qfull[1], used1++)) return false;
+              if (i + 1 == list.narrow) issue_S(g, pr & 1, umma_idesc_bf16(128, kNarrow, 0, 0));
+              else issue_S(g, pr & 1, umma_idesc_bf16(128, 128, 0, 0));
+            }
+          } else if (more && w2.list.takes(g, 0)) {
+            if (!first_S(g, w2, pr)) return false;
+          }
         }
-      }
-      pair0 += list.n + 1;
+        return true;
+      };
+      int i = 0;
+      for (; ok && i < min(list.ns + 2, list.n); ++i) ok = entry(i, std::false_type{});
+      for (; ok && i < list.n - 2; ++i) ok = entry(i, std::true_type{});
+      for (; ok && i < list.n; ++i) ok = entry(i, std::false_type{});
+      pair0 += list.n;
+      w = w2;
+      have = more;
     }
     if (!ok && leader) {
       S.abort = 1;
