@@ -63,6 +63,7 @@ dropkv_status open_pages(const kvcache_shape* s, const kvcache_buffers* b, int32
   p->offs = reinterpret_cast<int32_t*>(ws + w.offs);
   p->entry = reinterpret_cast<int4*>(ws + w.entry);
   p->list = reinterpret_cast<int32_t*>(ws + w.list);
+  p->rows = reinterpret_cast<int32_t*>(ws + w.rows);
   return DROPKV_OK;
 }
 
@@ -171,6 +172,7 @@ dropkv_status kvcache_compact(const kvcache_shape* shape, const kvcache_buffers*
   p.kept_idx = kept_idx;
   p.kept_stride = kept_stride;
   p.kept_len = kept_len;
+  p.early = (long long)n * shape->max_pages <= kEarlyRows ? 1 : 0;
   return launched(launch_compact_pages(p, current_sms(nullptr), stream));
 }
 

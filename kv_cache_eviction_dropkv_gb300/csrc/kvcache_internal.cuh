@@ -38,8 +38,10 @@ struct PagePlan {
   size_t offs;                   // [S + 1] pages taken by entries before i
   size_t entry;                  // [S][4] per entry: what the second kernel needs
   size_t list;                   // [P] pages taken, in order
+  size_t rows;                   // [kEarlyRows] old table rows of a compaction
   size_t total;                  // bytes
 };
+constexpr int kEarlyRows = 8192;            // table entries one CTA rewrites by itself
 PagePlan make_page_plan(int S, int P);
 
 struct PageCall {
@@ -49,8 +51,9 @@ struct PageCall {
   const int32_t* extra;          // reserve
   const int32_t *kept_idx, *kept_len;
   int kept_stride, share;
-  int32_t *claim, *mark, *offs, *list;
+  int32_t *claim, *mark, *offs, *list, *rows;
   int4* entry;
+  int early;                     // compact: the bookkeeping rewrites the tables
 };
 
 cudaError_t launch_free(const PageCall& p, cudaStream_t st);

@@ -5,10 +5,12 @@
 // taken in order: there is no free list whose order would depend on the order
 // of atomics, and results depend on the state alone.  The integer bookkeeping
 // of a call (who wants how many pages, which pages those are) is one CTA's
-// work: block scans over the call's entries and over the reference counts,
-// 16 counts a thread at a time.  What grows with the cache (page bytes, table
-// rows, reference counts of shared pages) is a second kernel's, spread over
-// the GPU and launched with programmatic dependent launch.
+// work: block scans over the call's entries and over the reference counts, 16
+// counts a thread at a time, loaded before anything that waits for them.
+// What grows with the cache (page bytes, table rows, reference counts of
+// shared pages) is a second kernel's, spread over the GPU and launched with
+// programmatic dependent launch.  (One cluster of 16 CTAs doing both in one
+// launch was slower even for a few hundred kilobytes: 16 against 10 us.)
 #include "kvcache_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -27,9 +29,11 @@ __device__ __forceinline__ int pages_for(const Cache& c, int tokens) {
   return (int)(((unsigned)tokens + (unsigned)c.page - 1u) >> c.page_log2);
 }
 
-// Exclusive sum over the block's threads; *total gets the sum of all.
-__device__ __forceinline__ int block_scan(int x, int* total) {
-  __shared__ int warp_sum[kBookWarps];
+// Exclusive sum over the block's threads; *total gets the sum of all.  `turn`
+// counts the calls (it picks one of two buffers, so a call needs one barrier).
+__device__ __forceinline__ int block_scan(int x, int* total, int& turn) {
+  __shared__ int warp_sum[2][kBookWarps];
+  int* sums = warp_sum[turn++ & 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = x;
 #pragma unroll
@@ -37,61 +41,88 @@ __device__ __forceinline__ int block_scan(int x, int* total) {
     const int y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __syncthreads();                         // the last use of warp_sum is over
-  if (lane == 31) warp_sum[warp] = inc;
+  if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int w = warp_sum[lane];
+  int w = sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
   *total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
-  return before + inc - x;
+  const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return (warp > 0 ? before : 0) + inc - x;
 }
 
-// The block marks the call's sequences: claim[s] = lowest index that names s.
-__device__ __forceinline__ void claim_seqs(const PageCall& p, const int32_t* seqs) {
-  for (int i = threadIdx.x; i < p.n; i += kBook) {
-    const int s = seqs[i];
-    if (s >= 0 && s < p.c.S) p.claim[s] = INT32_MAX;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.n; i += kBook) {
-    const int s = seqs[i];
-    if (s >= 0 && s < p.c.S) atomicMin(&p.claim[s], i);
+// Which entries are the first to name their sequence.  Up to kSmall entries
+// are compared in shared memory; more go through claim[s] = lowest index that
+// names s.
+constexpr int kSmall = 128;
+struct Names {
+  int mine[kSmall], other[kSmall];
+};
+__device__ __forceinline__ void claim_seqs(const PageCall& p, const int32_t* seqs, Names& names) {
+  if (p.n <= kSmall) {
+    for (int i = threadIdx.x; i < p.n; i += kBook) names.mine[i] = seqs[i];
+  } else {
+    for (int i = threadIdx.x; i < p.n; i += kBook) {
+      const int s = seqs[i];
+      if (s >= 0 && s < p.c.S) p.claim[s] = INT32_MAX;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kBook) {
+      const int s = seqs[i];
+      if (s >= 0 && s < p.c.S) atomicMin(&p.claim[s], i);
+    }
   }
   __syncthreads();
 }
+__device__ __forceinline__ bool first_named(const PageCall& p, const Names& names, int i, int s) {
+  if (p.n > kSmall) return p.claim[s] == i;
+  int before = 0;
+#pragma unroll 8
+  for (int j = 0; j < i; ++j) before |= names.mine[j] == s;
+  return before == 0;
+}
 
-// The `want` lowest free pages into p.list; false (and a flag) if there are fewer.
-__device__ __forceinline__ bool find_pages(const PageCall& p, int want) {
-  constexpr int kPer = 16;
+// 16 reference counts a thread, of the pages from `base` on.
+constexpr int kPer = 16;
+struct Counts {
+  int4 r[kPer / 4];
+};
+__device__ __forceinline__ Counts load_counts(const Cache& c, int base) {
+  Counts k;
+  const int first = base + threadIdx.x * kPer;
+#pragma unroll
+  for (int u = 0; u < kPer / 4; ++u) {
+    const int a = first + 4 * u;
+    if (a + 4 <= c.P) {
+      k.r[u] = *reinterpret_cast<const int4*>(c.refs + a);
+    } else {
+      k.r[u] = make_int4(1, 1, 1, 1);
+      if (a < c.P) k.r[u].x = c.refs[a];
+      if (a + 1 < c.P) k.r[u].y = c.refs[a + 1];
+      if (a + 2 < c.P) k.r[u].z = c.refs[a + 2];
+    }
+  }
+  return k;
+}
+
+// The `want` lowest free pages into p.list; false (and a flag) if there are
+// fewer.  k: the counts of the first pages.
+__device__ __forceinline__ bool find_pages(const PageCall& p, int want, Counts k, int& turn) {
   int found = 0;
   for (int base = 0; base < p.c.P && found < want; base += kBook * kPer) {
-    const int first = base + threadIdx.x * kPer;
-    int4 r[kPer / 4];
-#pragma unroll
-    for (int u = 0; u < kPer / 4; ++u) {
-      const int a = first + 4 * u;
-      if (a + 4 <= p.c.P) {
-        r[u] = *reinterpret_cast<const int4*>(p.c.refs + a);
-      } else {
-        r[u] = make_int4(1, 1, 1, 1);
-        if (a < p.c.P) r[u].x = p.c.refs[a];
-        if (a + 1 < p.c.P) r[u].y = p.c.refs[a + 1];
-        if (a + 2 < p.c.P) r[u].z = p.c.refs[a + 2];
-      }
-    }
+    if (base > 0) k = load_counts(p.c, base);
     uint32_t free_bits = 0;
 #pragma unroll
     for (int u = 0; u < kPer / 4; ++u) {
-      free_bits |= (r[u].x == 0 ? 1u : 0u) << (4 * u) | (r[u].y == 0 ? 2u : 0u) << (4 * u) |
-                   (r[u].z == 0 ? 4u : 0u) << (4 * u) | (r[u].w == 0 ? 8u : 0u) << (4 * u);
+      free_bits |= (k.r[u].x == 0 ? 1u : 0u) << (4 * u) | (k.r[u].y == 0 ? 2u : 0u) << (4 * u) |
+                   (k.r[u].z == 0 ? 4u : 0u) << (4 * u) | (k.r[u].w == 0 ? 8u : 0u) << (4 * u);
     }
     int total;
-    int at = found + block_scan(__popc(free_bits), &total);
+    int at = found + block_scan(__popc(free_bits), &total, turn);
+    const int first = base + threadIdx.x * kPer;
     while (free_bits && at < want) {
       const int bit = __ffs(free_bits) - 1;
       free_bits &= free_bits - 1;
@@ -151,17 +182,19 @@ __global__ void __launch_bounds__(256) free_kernel(const PageCall p) {
 
 // ============================================================== reserve
 __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
+  __shared__ Names names;
   grid_dep_wait();
   const Cache& c = p.c;
-  if (p.seqs) claim_seqs(p, p.seqs);
-  int sum = 0;
+  const Counts counts = load_counts(c, 0);
+  if (p.seqs) claim_seqs(p, p.seqs, names);
+  int sum = 0, turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
     int need = 0, pages = 0;
     long long tokens = -1;                  // new length, -1: the entry is left out
     if (i < p.n) {
       const int s = seq_of(p.seqs, i);
-      if (s < 0 || s >= c.S || (p.seqs && p.claim[s] != i)) {
+      if (s < 0 || s >= c.S || (p.seqs && !first_named(p, names, i, s))) {
         flag(c.status, KVCACHE_FLAG_BAD_SEQ);
       } else {
         const int extra = p.extra[i], len = c.length[s], have = c.count[s];
@@ -177,7 +210,7 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
       }
     }
     int total;
-    const int at = sum + block_scan(need, &total);
+    const int at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
       p.offs[i] = at;
       p.entry[i] = make_int4((int)tokens, pages, need, 0);
@@ -185,7 +218,7 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
     sum += total;
   }
   __syncthreads();
-  if (!find_pages(p, sum)) return;
+  if (!find_pages(p, sum, counts, turn)) return;
   grid_dep_launch();
   for (int k = threadIdx.x; k < sum; k += kBook) {
     const int i = entry_of(p.offs, p.n, k);
@@ -206,34 +239,46 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
 // ============================================================== fork
 // entry: (source, destination or -1, pages held by both, pages of the
 // branch); the list holds the pages of each entry's own copies in order.
-__global__ void __launch_bounds__(kBook) fork_book_kernel(const PageCall p) {
-  grid_dep_wait();
+__device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
   const Cache& c = p.c;
+  const Counts counts = load_counts(c, 0);
   const int32_t *src = p.seqs, *dst = p.other;
-  claim_seqs(p, dst);
-  for (int i = threadIdx.x; i < p.n; i += kBook) {
-    const int d = dst[i];
-    if (d >= 0 && d < c.S) p.mark[d] = 0;
+  if (p.n <= kSmall) {
+    for (int i = threadIdx.x; i < p.n; i += kBook) names.other[i] = src[i];
+  } else {
+    for (int i = threadIdx.x; i < p.n; i += kBook) {
+      const int d = dst[i];
+      if (d >= 0 && d < c.S) p.mark[d] = 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.n; i += kBook) {
+      const int s = src[i];
+      if (s >= 0 && s < c.S) p.mark[s] = 1;
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.n; i += kBook) {
-    const int s = src[i];
-    if (s >= 0 && s < c.S) p.mark[s] = 1;
-  }
-  __syncthreads();
-  int sum = 0;
+  claim_seqs(p, dst, names);
+  auto is_source = [&](int d) {
+    if (p.n > kSmall) return p.mark[d] == 1;
+    int any = 0;
+#pragma unroll 8
+    for (int j = 0; j < p.n; ++j) any |= names.other[j] == d;
+    return any != 0;
+  };
+  int sum = 0, turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
-    int need = 0;
+    int need = 0, len = 0;
     int4 e = make_int4(0, -1, 0, 0);
     if (i < p.n) {
       const int s = src[i], d = dst[i];
-      if (s < 0 || s >= c.S || d < 0 || d >= c.S || p.claim[d] != i || p.mark[d] == 1 || c.count[d] != 0 ||
-          c.length[d] != 0) {
+      if (s < 0 || s >= c.S || d < 0 || d >= c.S) {
         flag(c.status, KVCACHE_FLAG_BAD_SEQ);
       } else {
-        const int len = c.length[s], pages = c.count[s];
-        if (len < 0 || pages < 0 || pages > c.M || pages != pages_for(c, len)) {
+        len = c.length[s];
+        const int pages = c.count[s], d_len = c.length[d], d_pages = c.count[d];
+        if (!first_named(p, names, i, d) || is_source(d) || d_pages != 0 || d_len != 0) {
+          flag(c.status, KVCACHE_FLAG_BAD_SEQ);
+        } else if (len < 0 || pages < 0 || pages > c.M || pages != pages_for(c, len)) {
           flag(c.status, DROPKV_FLAG_BAD_LENGTH);
         } else {
           const int both = p.share ? len >> c.page_log2 : 0;
@@ -243,15 +288,14 @@ __global__ void __launch_bounds__(kBook) fork_book_kernel(const PageCall p) {
       }
     }
     int total;
-    const int at = sum + block_scan(need, &total);
+    const int at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
       p.offs[i] = at;
       p.entry[i] = e;
     }
     sum += total;
   }
-  __syncthreads();
-  const bool ok = find_pages(p, sum);
+  const bool ok = find_pages(p, sum, counts, turn);
   if (threadIdx.x == 0) p.offs[p.n] = ok ? sum : -1;   // -1: nothing to do
   if (!ok) return;
   for (int k = threadIdx.x; k < sum; k += kBook) c.refs[p.list[k]] = 1;
@@ -263,20 +307,18 @@ __global__ void __launch_bounds__(kBook) fork_book_kernel(const PageCall p) {
   }
 }
 
-constexpr int kCopyThreads = 256, kCopyUnroll = 4;
-constexpr int kCopyChunk = kCopyThreads * kCopyUnroll * 16;   // bytes a CTA moves at a time
+constexpr int kCopyTeam = 256, kCopyUnroll = 4;
+constexpr int kCopyChunk = kCopyTeam * kCopyUnroll * 16;   // bytes a CTA moves at a time
 
-// The blocks share out two lists: table rows of the branches in pieces of
-// kCopyThreads entries, then page bytes (page copy, layer, K or V, chunk).
-__global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const PageCall p, int row_pieces, int chunks) {
-  grid_dep_wait();
-  grid_dep_launch();
+// CTA `team` of `teams` (kCopyTeam threads each): its share of two lists,
+// table rows of the branches in pieces of kCopyTeam entries, then page bytes
+// (page copy, layer, K or V, chunk).
+__device__ __forceinline__ void fork_move(const PageCall& p, int row_pieces, int chunks, int team, int teams, int tid) {
   const Cache& c = p.c;
   const int copies = p.offs[p.n];
   if (copies < 0) return;
-  const int tid = threadIdx.x;
-  for (int w = blockIdx.x; w < p.n * row_pieces; w += gridDim.x) {
-    const int i = w / row_pieces, col = (w - i * row_pieces) * kCopyThreads + tid;
+  for (int w = team; w < p.n * row_pieces; w += teams) {
+    const int i = w / row_pieces, col = (w - i * row_pieces) * kCopyTeam + tid;
     const int4 e = p.entry[i];
     if (e.y < 0 || col >= e.w) continue;
     int pg;
@@ -291,7 +333,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const PageCall 
   }
   const size_t page_bytes = (size_t)c.Hkv * c.page * c.d;
   const long long pieces = (long long)copies * c.layers * 2 * chunks;
-  for (long long w = blockIdx.x; w < pieces; w += gridDim.x) {
+  for (long long w = team; w < pieces; w += teams) {
     const int chunk = (int)(w % chunks);
     const long long x = w / chunks;
     const int which = (int)(x & 1);
@@ -310,37 +352,69 @@ __global__ void __launch_bounds__(kCopyThreads) fork_move_kernel(const PageCall 
     uint4 r[kCopyUnroll];
 #pragma unroll
     for (int u = 0; u < kCopyUnroll; ++u)
-      if (at + u * kCopyThreads * 16 < page_bytes)
-        r[u] = __ldcs(reinterpret_cast<const uint4*>(a + at + u * kCopyThreads * 16));
+      if (at + u * kCopyTeam * 16 < page_bytes)
+        r[u] = __ldcs(reinterpret_cast<const uint4*>(a + at + u * kCopyTeam * 16));
 #pragma unroll
     for (int u = 0; u < kCopyUnroll; ++u)
-      if (at + u * kCopyThreads * 16 < page_bytes)
-        __stcs(reinterpret_cast<uint4*>(b + at + u * kCopyThreads * 16), r[u]);
+      if (at + u * kCopyTeam * 16 < page_bytes)
+        __stcs(reinterpret_cast<uint4*>(b + at + u * kCopyTeam * 16), r[u]);
     if (chunk == 0) {
       float* sc = which ? c.vs : c.ks;
-      for (int h = tid; h < c.Hkv; h += kCopyThreads)
+      for (int h = tid; h < c.Hkv; h += kCopyTeam)
         sc[((size_t)layer * c.P + to) * c.Hkv + h] = sc[((size_t)layer * c.P + from) * c.Hkv + h];
     }
   }
 }
 
+__global__ void __launch_bounds__(kBook) fork_book_kernel(const PageCall p) {
+  __shared__ Names names;
+  grid_dep_wait();
+  grid_dep_launch();
+  fork_book(p, names);
+}
+__global__ void __launch_bounds__(kCopyTeam) fork_move_kernel(const PageCall p, int row_pieces, int chunks) {
+  grid_dep_wait();
+  grid_dep_launch();
+  fork_move(p, row_pieces, chunks, blockIdx.x, gridDim.x, threadIdx.x);
+}
 // ============================================================== compact
 // entry: (sequence or -1, old length, old pages, kept tokens).
-__global__ void __launch_bounds__(kBook) compact_book_kernel(const PageCall p) {
-  grid_dep_wait();
+// The table rows of the evicted sequences: old pages lose a reference, the
+// new ones take their place.  Either the bookkeeping does it at once, leaving
+// the old rows in p.rows for the gather (early: rows of up to kEarlyRows
+// entries in all), or a third kernel after the gather (which then reads the
+// table).
+__device__ __forceinline__ void compact_row(const PageCall& p, int i, int col) {
   const Cache& c = p.c;
-  if (p.seqs) claim_seqs(p, p.seqs);
-  int sum = 0;
+  const int4 e = p.entry[i];
+  if (e.x < 0 || col >= e.z) return;
+  int32_t* at = c.table + (size_t)e.x * c.M + col;
+  const int pg = *at;
+  if (p.early) p.rows[(size_t)i * c.M + col] = pg;
+  if (pg < 0 || pg >= c.P) {
+    flag(c.status, KVCACHE_FLAG_BAD_PAGE);
+  } else if (atomicSub(&c.refs[pg], 1) <= 0) {
+    atomicAdd(&c.refs[pg], 1);
+    flag(c.status, KVCACHE_FLAG_BAD_PAGE);
+  }
+  *at = col < pages_for(c, e.w) ? p.list[p.offs[i] + col] : -1;
+}
+
+__device__ __forceinline__ void compact_book(const PageCall& p, Names& names) {
+  const Cache& c = p.c;
+  const Counts counts = load_counts(c, 0);
+  if (p.seqs) claim_seqs(p, p.seqs, names);
+  int sum = 0, turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
     int need = 0;
     int4 e = make_int4(-1, 0, 0, 0);
     if (i < p.n) {
-      const int s = seq_of(p.seqs, i);
-      if (s < 0 || s >= c.S || (p.seqs && p.claim[s] != i)) {
+      const int s = seq_of(p.seqs, i), kept = p.kept_len[i];
+      if (s < 0 || s >= c.S || (p.seqs && !first_named(p, names, i, s))) {
         flag(c.status, KVCACHE_FLAG_BAD_SEQ);
       } else {
-        const int len = c.length[s], have = c.count[s], kept = p.kept_len[i];
+        const int len = c.length[s], have = c.count[s];
         if (len < 0 || have < 0 || have > c.M || have != pages_for(c, len)) {
           flag(c.status, DROPKV_FLAG_BAD_LENGTH);
         } else if (kept < 0 || kept > len || kept > p.kept_stride) {
@@ -352,15 +426,14 @@ __global__ void __launch_bounds__(kBook) compact_book_kernel(const PageCall p) {
       }
     }
     int total;
-    const int at = sum + block_scan(need, &total);
+    const int at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
       p.offs[i] = at;
       p.entry[i] = e;
     }
     sum += total;
   }
-  __syncthreads();
-  const bool ok = find_pages(p, sum);
+  const bool ok = find_pages(p, sum, counts, turn);
   if (threadIdx.x == 0) p.offs[p.n] = ok ? sum : -1;
   if (!ok) return;
   for (int k = threadIdx.x; k < sum; k += kBook) c.refs[p.list[k]] = 1;
@@ -370,28 +443,32 @@ __global__ void __launch_bounds__(kBook) compact_book_kernel(const PageCall p) {
     c.length[e.x] = e.w;
     c.count[e.x] = pages_for(c, e.w);
   }
+  if (p.early)
+    for (int x = threadIdx.x; x < p.n * c.M; x += kBook) compact_row(p, x / c.M, x % c.M);
 }
 
-constexpr int kGatherThreads = 128;
+constexpr int kGatherTeam = 128;
 constexpr int kMaxPage = 128;
+static_assert(kMaxPage <= kGatherTeam, "a thread looks up one row of a page");
+struct Gather {
+  size_t row[kMaxPage];                         // source row, ~0: none
+  float scale[2][kMaxPage];
+  float top[2][kGatherTeam / 32];
+};
 
-// A CTA fills one (new page, layer, head) at a time: the kept positions give
-// each row's source and its scales, the new scale is their largest, then the
-// rows are moved VB bytes at a time.
+// CTA `team` of `teams` (kGatherTeam threads) fills one (new page, layer,
+// head) at a time: the kept positions give each row's source and
+// its scales, the new scale is their largest, then the rows are moved VB bytes
+// at a time.
 template <int VB>
-__global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const PageCall p) {
-  grid_dep_wait();
-  grid_dep_launch();
+__device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int team, int teams, int tid) {
   const Cache& c = p.c;
   const int taken = p.offs[p.n];
   if (taken < 0) return;
-  __shared__ size_t s_row[kMaxPage];            // source row, ~0: none
-  __shared__ float s_scale[2][kMaxPage];
-  __shared__ float s_max[2][kGatherThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = tid & 31, warp = tid >> 5;
   const int units = c.d / VB;
   const long long work = (long long)taken * c.layers * c.Hkv;
-  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+  for (long long w = team; w < work; w += teams) {
     const int h = (int)(w % c.Hkv);
     const long long x = w / c.Hkv;
     const int layer = (int)(x % c.layers), k = (int)(x / c.layers);
@@ -406,7 +483,8 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
       if (idx < 0 || idx >= e.y) {
         flag(c.status, DROPKV_FLAG_BAD_K);
       } else {
-        const int pg = c.table[(size_t)e.x * c.M + (idx >> c.page_log2)];
+        const int col = idx >> c.page_log2;
+        const int pg = p.early ? p.rows[(size_t)i * c.M + col] : c.table[(size_t)e.x * c.M + col];
         if (pg < 0 || pg >= c.P) {
           flag(c.status, KVCACHE_FLAG_BAD_PAGE);
         } else {
@@ -416,9 +494,9 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
           vs = c.vs[u];
         }
       }
-      s_row[tid] = row;
-      s_scale[0][tid] = ks;
-      s_scale[1][tid] = vs;
+      g.row[tid] = row;
+      g.scale[0][tid] = ks;
+      g.scale[1][tid] = vs;
     }
     float km = ks, vm = vs;
 #pragma unroll
@@ -427,15 +505,15 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
       vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
     }
     if (lane == 0) {
-      s_max[0][warp] = km;
-      s_max[1][warp] = vm;
+      g.top[0][warp] = km;
+      g.top[1][warp] = vm;
     }
     __syncthreads();
     float top[2] = {kScaleMin, kScaleMin};
 #pragma unroll
-    for (int q = 0; q < kGatherThreads / 32; ++q) {
-      top[0] = fmaxf(top[0], s_max[0][q]);
-      top[1] = fmaxf(top[1], s_max[1][q]);
+    for (int q = 0; q < kGatherTeam / 32; ++q) {
+      top[0] = fmaxf(top[0], g.top[0][q]);
+      top[1] = fmaxf(top[1], g.top[1][q]);
     }
     const size_t ut = ((size_t)layer * c.P + to) * c.Hkv + h;
     if (tid == 0) {
@@ -443,9 +521,10 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
       c.vs[ut] = top[1];
     }
     using Vec = typename std::conditional<VB == 16, uint4, uint2>::type;
-    for (int u = tid; u < rows * units; u += kGatherThreads) {
+#pragma unroll 4
+    for (int u = tid; u < rows * units; u += kGatherTeam) {
       const int r = u / units, off = (u - r * units) * VB;
-      const size_t row = s_row[r];
+      const size_t row = g.row[r];
       Vec val[2] = {};
       if (row != ~(size_t)0) {
         val[0] = *reinterpret_cast<const Vec*>(c.k + row * c.d + off);
@@ -453,7 +532,7 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float from = s_scale[q][r];
+        const float from = g.scale[q][r];
         if (from != top[q]) {
           const float ratio = from / top[q];
           uint32_t* wv = reinterpret_cast<uint32_t*>(&val[q]);
@@ -465,33 +544,32 @@ __global__ void __launch_bounds__(kGatherThreads) compact_move_kernel(const Page
       *reinterpret_cast<Vec*>(c.k + dst) = val[0];
       *reinterpret_cast<Vec*>(c.v + dst) = val[1];
     }
-    __syncthreads();                        // the shared rows are rewritten next
+    __syncthreads();                        // the team's rows are rewritten next
   }
 }
 
-// The table rows of the evicted sequences: old pages lose a reference, the
-// new ones take their place (after every row has been gathered).
-__global__ void __launch_bounds__(kCopyThreads) compact_commit_kernel(const PageCall p, int row_pieces) {
+__global__ void __launch_bounds__(kBook) compact_book_kernel(const PageCall p) {
+  __shared__ Names names;
   grid_dep_wait();
   grid_dep_launch();
-  const Cache& c = p.c;
+  compact_book(p, names);
+}
+template <int VB>
+__global__ void __launch_bounds__(kGatherTeam) compact_move_kernel(const PageCall p) {
+  __shared__ Gather g;
+  grid_dep_wait();
+  grid_dep_launch();
+  compact_move<VB>(p, g, blockIdx.x, gridDim.x, threadIdx.x);
+}
+__global__ void __launch_bounds__(kCopyTeam) compact_commit_kernel(const PageCall p, int row_pieces) {
+  grid_dep_wait();
+  grid_dep_launch();
   if (p.offs[p.n] < 0) return;
   for (int w = blockIdx.x; w < p.n * row_pieces; w += gridDim.x) {
-    const int i = w / row_pieces, col = (w - i * row_pieces) * kCopyThreads + threadIdx.x;
-    const int4 e = p.entry[i];
-    if (e.x < 0 || col >= e.z) continue;
-    int32_t* at = c.table + (size_t)e.x * c.M + col;
-    const int pg = *at;
-    if (pg < 0 || pg >= c.P) {
-      flag(c.status, KVCACHE_FLAG_BAD_PAGE);
-    } else if (atomicSub(&c.refs[pg], 1) <= 0) {
-      atomicAdd(&c.refs[pg], 1);
-      flag(c.status, KVCACHE_FLAG_BAD_PAGE);
-    }
-    *at = col < pages_for(c, e.w) ? p.list[p.offs[i] + col] : -1;
+    const int i = w / row_pieces;
+    compact_row(p, i, (w - i * row_pieces) * kCopyTeam + threadIdx.x);
   }
 }
-
 }  // namespace
 
 PagePlan make_page_plan(int S, int P) {
@@ -507,6 +585,7 @@ PagePlan make_page_plan(int S, int P) {
   w.offs = take(((size_t)S + 1) * 4);
   w.entry = take((size_t)S * 16);
   w.list = take((size_t)P * 4);
+  w.rows = take((size_t)kEarlyRows * 4);
   w.total = off;
   return w;
 }
@@ -520,24 +599,26 @@ cudaError_t launch_reserve(const PageCall& p, cudaStream_t st) {
 }
 
 cudaError_t launch_fork(const PageCall& p, int sms, cudaStream_t st) {
+  const Cache& c = p.c;
+  const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
+  const int chunks = (int)(((size_t)c.Hkv * c.page * c.d + kCopyChunk - 1) / kCopyChunk);
   const cudaError_t e = launch_pdl(fork_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
-  const int row_pieces = (p.c.M + kCopyThreads - 1) / kCopyThreads;
-  const int chunks = (int)(((size_t)p.c.Hkv * p.c.page * p.c.d + kCopyChunk - 1) / kCopyChunk);
-  return launch_pdl(fork_move_kernel, dim3(sms * 8), dim3(kCopyThreads), 0, st, p, row_pieces, chunks);
+  return launch_pdl(fork_move_kernel, dim3(sms * 8), dim3(kCopyTeam), 0, st, p, row_pieces, chunks);
 }
 
 cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
+  const Cache& c = p.c;
+  const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
   cudaError_t e = launch_pdl(compact_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
   const dim3 grid(sms * 12);
-  if (p.c.d % 16 == 0) e = launch_pdl(compact_move_kernel<16>, grid, dim3(kGatherThreads), 0, st, p);
-  else e = launch_pdl(compact_move_kernel<8>, grid, dim3(kGatherThreads), 0, st, p);
-  if (e != cudaSuccess) return e;
-  const int row_pieces = (p.c.M + kCopyThreads - 1) / kCopyThreads;
+  if (c.d % 16 == 0) e = launch_pdl(compact_move_kernel<16>, grid, dim3(kGatherTeam), 0, st, p);
+  else e = launch_pdl(compact_move_kernel<8>, grid, dim3(kGatherTeam), 0, st, p);
+  if (e != cudaSuccess || p.early) return e;
   const long long pieces = (long long)p.n * row_pieces;
-  return launch_pdl(compact_commit_kernel, dim3((unsigned)std::min<long long>(pieces, sms * 8)), dim3(kCopyThreads), 0,
-                    st, p, row_pieces);
+  return launch_pdl(compact_commit_kernel, dim3((unsigned)std::min<long long>(pieces, sms * 8)), dim3(kCopyTeam), 0, st,
+                    p, row_pieces);
 }
 
 }  // namespace kvcache
