@@ -41,7 +41,7 @@ struct PagePlan {
   size_t rows;                   // [kEarlyRows] old table rows of a compaction
   size_t total;                  // bytes
 };
-constexpr int kEarlyRows = 8192;            // table entries one CTA rewrites by itself
+constexpr int kEarlyRows = 1024;            // table entries one CTA rewrites by itself
 PagePlan make_page_plan(int S, int P);
 
 struct PageCall {
@@ -153,22 +153,55 @@ __device__ __forceinline__ uint32_t int8_code(float x) {   // x divided by its s
   return (uint32_t)min(127, max(-127, __float2int_rn(x))) & 0xFFu;
 }
 
-// Four codes of scale `from` rounded again at scale `to` >= from.  e4m3
-// scales are powers of two: their ratio is exact.
+// Two e4m3 codes times a power of two of at most 1, rounded again.  In fp16
+// the product is exact, or below 2^-20 and rounds to 0 either way.
+__device__ __forceinline__ uint32_t e4m3x2_times(uint32_t codes, uint32_t ratio2) {
+  uint32_t h = e4m3x2_to_half2(codes);
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(ratio2));
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+
+// Four int8 codes rn(y_i) of numbers y_i that are x_i times a factor, where
+// the definition is a division: near[i] = x_i * (rounded factor) is within
+// 2^-22 |y_i| < 2^-14 of the definition's value, so both round alike unless
+// it lies that close to a half; then `exact(i)` gives the definition's value.
+template <typename Exact>
+__device__ __forceinline__ uint32_t int8x4_near(const float (&near)[4], Exact exact) {
+  constexpr float kMagic = 12582912.f;      // 1.5 2^23: adding it rounds to an integer, in the low bits
+  uint32_t w[4];
+  bool close = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = near[i] + kMagic;
+    close |= !(fabsf(near[i] - (t - kMagic)) < 0.4999f) || fabsf(near[i]) > 126.9f;   // (not-a-number too)
+    w[i] = __float_as_uint(t);
+  }
+  if (close) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = int8_code(exact(i));
+  }
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+// Four codes of scale `from` rounded again at scale `to` >= from; ratio =
+// from / to.  e4m3 scales are powers of two: their ratio is exact.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float from, float to, float ratio, int code) {
   if (code == KVCACHE_INT8) {
-    uint32_t r = 0;
+    // a byte as a float: the low bits of 2^23 + (code + 128)
+    const uint32_t x = w ^ 0x80808080u;
+    float c[4], near[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float c = (float)(int8_t)(w >> (8 * i));
-      r |= int8_code(__fdiv_rn(__fmul_rn(c, from), to)) << (8 * i);
+      c[i] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7650 + i)) - 8388736.f;
+      near[i] = c[i] * ratio;
     }
-    return r;
+    return int8x4_near(near, [&](int i) { return __fdiv_rn(__fmul_rn(c[i], from), to); });
   }
-  const uint32_t h0 = e4m3x2_to_half2(w & 0xFFFFu), h1 = e4m3x2_to_half2(w >> 16);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-  return e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(b.x * ratio, b.y * ratio) << 16);
+  const __half2 r2 = __float2half2_rn(ratio);
+  const uint32_t r = *reinterpret_cast<const uint32_t*>(&r2);
+  return e4m3x2_times(w & 0xFFFFu, r) | (e4m3x2_times(w >> 16, r) << 16);
 }
 
 }  // namespace kvcache

@@ -447,7 +447,7 @@ __device__ __forceinline__ void compact_book(const PageCall& p, Names& names) {
     for (int x = threadIdx.x; x < p.n * c.M; x += kBook) compact_row(p, x / c.M, x % c.M);
 }
 
-constexpr int kGatherTeam = 128;
+constexpr int kGatherTeam = 128, kGatherCtas = 12;   // threads of a CTA, CTAs per SM
 constexpr int kMaxPage = 128;
 static_assert(kMaxPage <= kGatherTeam, "a thread looks up one row of a page");
 struct Gather {
@@ -460,13 +460,14 @@ struct Gather {
 // head) at a time: the kept positions give each row's source and
 // its scales, the new scale is their largest, then the rows are moved VB bytes
 // at a time.
-template <int VB>
+template <int VB, int CODE>
 __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int team, int teams, int tid) {
   const Cache& c = p.c;
   const int taken = p.offs[p.n];
   if (taken < 0) return;
   const int lane = tid & 31, warp = tid >> 5;
-  const int units = c.d / VB;
+  const int units = c.d / VB;                   // at most 16
+  const uint32_t per = (65536 + units - 1) / units;   // u / units == u * per >> 16 for u < 2048
   const long long work = (long long)taken * c.layers * c.Hkv;
   for (long long w = team; w < work; w += teams) {
     const int h = (int)(w % c.Hkv);
@@ -523,7 +524,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
     using Vec = typename std::conditional<VB == 16, uint4, uint2>::type;
 #pragma unroll 4
     for (int u = tid; u < rows * units; u += kGatherTeam) {
-      const int r = u / units, off = (u - r * units) * VB;
+      const int r = (int)((uint32_t)u * per >> 16), off = (u - r * units) * VB;
       const size_t row = g.row[r];
       Vec val[2] = {};
       if (row != ~(size_t)0) {
@@ -537,7 +538,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
           const float ratio = from / top[q];
           uint32_t* wv = reinterpret_cast<uint32_t*>(&val[q]);
 #pragma unroll
-          for (int b = 0; b < VB / 4; ++b) wv[b] = rescale4(wv[b], from, top[q], ratio, c.code);
+          for (int b = 0; b < VB / 4; ++b) wv[b] = rescale4(wv[b], from, top[q], ratio, CODE);
         }
       }
       const size_t dst = (ut * c.page + r) * c.d + off;
@@ -554,12 +555,12 @@ __global__ void __launch_bounds__(kBook) compact_book_kernel(const PageCall p) {
   grid_dep_launch();
   compact_book(p, names);
 }
-template <int VB>
-__global__ void __launch_bounds__(kGatherTeam) compact_move_kernel(const PageCall p) {
+template <int VB, int CODE>
+__global__ void __launch_bounds__(kGatherTeam, kGatherCtas) compact_move_kernel(const PageCall p) {
   __shared__ Gather g;
   grid_dep_wait();
   grid_dep_launch();
-  compact_move<VB>(p, g, blockIdx.x, gridDim.x, threadIdx.x);
+  compact_move<VB, CODE>(p, g, blockIdx.x, gridDim.x, threadIdx.x);
 }
 __global__ void __launch_bounds__(kCopyTeam) compact_commit_kernel(const PageCall p, int row_pieces) {
   grid_dep_wait();
@@ -612,9 +613,10 @@ cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
   const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
   cudaError_t e = launch_pdl(compact_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid(sms * 12);
-  if (c.d % 16 == 0) e = launch_pdl(compact_move_kernel<16>, grid, dim3(kGatherTeam), 0, st, p);
-  else e = launch_pdl(compact_move_kernel<8>, grid, dim3(kGatherTeam), 0, st, p);
+  const bool int8 = c.code == KVCACHE_INT8;
+  auto move = c.d % 16 == 0 ? (int8 ? compact_move_kernel<16, KVCACHE_INT8> : compact_move_kernel<16, KVCACHE_E4M3>)
+                            : (int8 ? compact_move_kernel<8, KVCACHE_INT8> : compact_move_kernel<8, KVCACHE_E4M3>);
+  e = launch_pdl(move, dim3(sms * kGatherCtas), dim3(kGatherTeam), 0, st, p);
   if (e != cudaSuccess || p.early) return e;
   const long long pieces = (long long)p.n * row_pieces;
   return launch_pdl(compact_commit_kernel, dim3((unsigned)std::min<long long>(pieces, sms * 8)), dim3(kCopyTeam), 0, st,

@@ -121,16 +121,20 @@ __global__ void __launch_bounds__(PAGE * 2) store_kernel(const StoreCall p) {
       }
     }
   } else {
+    const float inv = 1.0f / scale;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int n = r0 * dv + tid + u * kThreads;
       if (n < r1 * dv) {
         const uint32_t w4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t b[4];
+        uint32_t b[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          b[q] = int8_code(__fdiv_rn(bf_lo(w4[q]), scale)) | (int8_code(__fdiv_rn(bf_hi(w4[q]), scale)) << 8);
-        *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        for (int q = 0; q < 2; ++q) {
+          const float v[4] = {bf_lo(w4[2 * q]), bf_hi(w4[2 * q]), bf_lo(w4[2 * q + 1]), bf_hi(w4[2 * q + 1])};
+          const float near[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+          b[q] = int8x4_near(near, [&](int i) { return __fdiv_rn(v[i], scale); });
+        }
+        *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = make_uint2(b[0], b[1]);
       }
     }
   }
