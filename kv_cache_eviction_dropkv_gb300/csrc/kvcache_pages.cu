@@ -372,6 +372,20 @@ __global__ void __launch_bounds__(kBook) fork_book_kernel(const PageCall p) {
   grid_dep_launch();
   fork_book(p, names);
 }
+// Both in one CTA, where little can be wanted: a launch less.
+__global__ void __launch_bounds__(kBook) fork_one_kernel(const PageCall p, int row_pieces, int chunks) {
+  __shared__ Names names;
+  grid_dep_wait();
+  grid_dep_launch();
+  fork_book(p, names);
+  __syncthreads();
+  fork_move(p, row_pieces, chunks, threadIdx.x / kCopyTeam, kBook / kCopyTeam, threadIdx.x % kCopyTeam);
+}
+// Most bytes copied, and table entries, of the one-CTA form: it copies about
+// 100 KB while a second launch of the other takes its 3 us.
+constexpr double kOneBytes = 1.5e5;
+constexpr int kOneRows = 1024;
+
 __global__ void __launch_bounds__(kCopyTeam) fork_move_kernel(const PageCall p, int row_pieces, int chunks) {
   grid_dep_wait();
   grid_dep_launch();
@@ -448,34 +462,51 @@ __device__ __forceinline__ void compact_book(const PageCall& p, Names& names) {
 }
 
 constexpr int kGatherTeam = 128, kGatherCtas = 12;   // threads of a CTA, CTAs per SM
+constexpr int kGatherWaves = 8;
 constexpr int kMaxPage = 128;
 static_assert(kMaxPage <= kGatherTeam, "a thread looks up one row of a page");
 struct Gather {
   size_t row[kMaxPage];                         // source row, ~0: none
   float scale[2][kMaxPage];
   float top[2][kGatherTeam / 32];
+  int offs[kSmall + 1];                         // the call's entries, where they fit
+  int4 entry[kSmall];
 };
 
 // CTA `team` of `teams` (kGatherTeam threads) fills one (new page, layer,
-// head) at a time: the kept positions give each row's source and
-// its scales, the new scale is their largest, then the rows are moved VB bytes
-// at a time.
+// head) at a time: the kept positions give each row's source, then the first
+// vectors of the rows and the scales are on their way together; the new scale
+// is the largest, and codes of other scales are rounded again.  Bound by the
+// chain position -> table -> row, so the CTAs are many and small.
 template <int VB, int CODE>
 __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int team, int teams, int tid) {
+  using Vec = typename std::conditional<VB == 16, uint4, uint2>::type;
+  constexpr int kBatch = 2;
   const Cache& c = p.c;
   const int taken = p.offs[p.n];
   if (taken < 0) return;
   const int lane = tid & 31, warp = tid >> 5;
   const int units = c.d / VB;                   // at most 16
   const uint32_t per = (65536 + units - 1) / units;   // u / units == u * per >> 16 for u < 2048
+  const int* offs = p.offs;
+  const int4* entry = p.entry;
+  if (p.n <= kSmall) {
+    for (int i = tid; i < p.n; i += kGatherTeam) {
+      g.offs[i] = p.offs[i];
+      g.entry[i] = p.entry[i];
+    }
+    offs = g.offs;
+    entry = g.entry;
+    __syncthreads();
+  }
   const long long work = (long long)taken * c.layers * c.Hkv;
   for (long long w = team; w < work; w += teams) {
     const int h = (int)(w % c.Hkv);
     const long long x = w / c.Hkv;
     const int layer = (int)(x % c.layers), k = (int)(x / c.layers);
-    const int i = entry_of(p.offs, p.n, k);
-    const int4 e = p.entry[i];
-    const int first = (k - p.offs[i]) << c.page_log2;
+    const int i = entry_of(offs, p.n, k);
+    const int4 e = entry[i];
+    const int first = (k - offs[i]) << c.page_log2;
     const int rows = min(c.page, e.w - first), to = p.list[k];
     float ks = 0.f, vs = 0.f;
     if (tid < rows) {
@@ -496,18 +527,37 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
         }
       }
       g.row[tid] = row;
+    }
+    __syncthreads();
+    const int vecs = rows * units;
+    Vec val[kBatch][2];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int u = base + b * kGatherTeam + tid;
+        val[b][0] = val[b][1] = Vec{};
+        if (u >= vecs) continue;
+        const int r = (int)((uint32_t)u * per >> 16), off = (u - r * units) * VB;
+        const size_t row = g.row[r];
+        if (row != ~(size_t)0) {
+          val[b][0] = *reinterpret_cast<const Vec*>(c.k + row * c.d + off);
+          val[b][1] = *reinterpret_cast<const Vec*>(c.v + row * c.d + off);
+        }
+      }
+    };
+    load(0);
+    if (tid < rows) {
       g.scale[0][tid] = ks;
       g.scale[1][tid] = vs;
     }
-    float km = ks, vm = vs;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
-      vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+      ks = fmaxf(ks, __shfl_xor_sync(0xffffffffu, ks, o));
+      vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, o));
     }
     if (lane == 0) {
-      g.top[0][warp] = km;
-      g.top[1][warp] = vm;
+      g.top[0][warp] = ks;
+      g.top[1][warp] = vs;
     }
     __syncthreads();
     float top[2] = {kScaleMin, kScaleMin};
@@ -521,31 +571,29 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
       c.ks[ut] = top[0];
       c.vs[ut] = top[1];
     }
-    using Vec = typename std::conditional<VB == 16, uint4, uint2>::type;
-#pragma unroll 4
-    for (int u = tid; u < rows * units; u += kGatherTeam) {
-      const int r = (int)((uint32_t)u * per >> 16), off = (u - r * units) * VB;
-      const size_t row = g.row[r];
-      Vec val[2] = {};
-      if (row != ~(size_t)0) {
-        val[0] = *reinterpret_cast<const Vec*>(c.k + row * c.d + off);
-        val[1] = *reinterpret_cast<const Vec*>(c.v + row * c.d + off);
-      }
+    for (int base = 0; base < vecs; base += kBatch * kGatherTeam) {
+      if (base > 0) load(base);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float from = g.scale[q][r];
-        if (from != top[q]) {
-          const float ratio = from / top[q];
-          uint32_t* wv = reinterpret_cast<uint32_t*>(&val[q]);
+      for (int b = 0; b < kBatch; ++b) {
+        const int u = base + b * kGatherTeam + tid;
+        if (u >= vecs) continue;
+        const int r = (int)((uint32_t)u * per >> 16), off = (u - r * units) * VB;
 #pragma unroll
-          for (int b = 0; b < VB / 4; ++b) wv[b] = rescale4(wv[b], from, top[q], ratio, CODE);
+        for (int q = 0; q < 2; ++q) {
+          const float from = g.scale[q][r];
+          if (from != top[q]) {
+            const float ratio = from / top[q];
+            uint32_t* wv = reinterpret_cast<uint32_t*>(&val[b][q]);
+#pragma unroll
+            for (int s = 0; s < VB / 4; ++s) wv[s] = rescale4(wv[s], from, top[q], ratio, CODE);
+          }
         }
+        const size_t dst = (ut * c.page + r) * c.d + off;
+        *reinterpret_cast<Vec*>(c.k + dst) = val[b][0];
+        *reinterpret_cast<Vec*>(c.v + dst) = val[b][1];
       }
-      const size_t dst = (ut * c.page + r) * c.d + off;
-      *reinterpret_cast<Vec*>(c.k + dst) = val[0];
-      *reinterpret_cast<Vec*>(c.v + dst) = val[1];
     }
-    __syncthreads();                        // the team's rows are rewritten next
+    __syncthreads();                        // the rows are rewritten next
   }
 }
 
@@ -603,9 +651,12 @@ cudaError_t launch_fork(const PageCall& p, int sms, cudaStream_t st) {
   const Cache& c = p.c;
   const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
   const int chunks = (int)(((size_t)c.Hkv * c.page * c.d + kCopyChunk - 1) / kCopyChunk);
+  const double most = 2.0 * c.layers * c.Hkv * c.page * c.d * p.n * (p.share ? 1 : c.M);
+  if (most <= kOneBytes && (long long)p.n * c.M <= kOneRows)
+    return launch_pdl(fork_one_kernel, dim3(1), dim3(kBook), 0, st, p, row_pieces, chunks);
   const cudaError_t e = launch_pdl(fork_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fork_move_kernel, dim3(sms * 8), dim3(kCopyTeam), 0, st, p, row_pieces, chunks);
+  return launch_pdl(fork_move_kernel, dim3(sms * 16), dim3(kCopyTeam), 0, st, p, row_pieces, chunks);
 }
 
 cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
@@ -616,7 +667,12 @@ cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
   const bool int8 = c.code == KVCACHE_INT8;
   auto move = c.d % 16 == 0 ? (int8 ? compact_move_kernel<16, KVCACHE_INT8> : compact_move_kernel<16, KVCACHE_E4M3>)
                             : (int8 ? compact_move_kernel<8, KVCACHE_INT8> : compact_move_kernel<8, KVCACHE_E4M3>);
-  e = launch_pdl(move, dim3(sms * kGatherCtas), dim3(kGatherTeam), 0, st, p);
+  // a CTA for each (page, layer, head) there can be, up to kGatherWaves full
+  // loads of the GPU: those with nothing to do leave at once, and the others
+  // need not come out even over the resident CTAs
+  const long long most = std::min<long long>(c.P, (long long)p.n * ((p.kept_stride + c.page - 1) / c.page)) * c.layers * c.Hkv;
+  const unsigned grid = (unsigned)std::max(1LL, std::min<long long>(most, (long long)sms * kGatherCtas * kGatherWaves));
+  e = launch_pdl(move, dim3(grid), dim3(kGatherTeam), 0, st, p);
   if (e != cudaSuccess || p.early) return e;
   const long long pieces = (long long)p.n * row_pieces;
   return launch_pdl(compact_commit_kernel, dim3((unsigned)std::min<long long>(pieces, sms * 8)), dim3(kCopyTeam), 0, st,
