@@ -302,8 +302,27 @@ def dropkv_version() -> str:
 
 
 # ------------------------------------------------------------------ include/kvcache.h
-# The cache's calls take the two structures (shape and buffers, built once per
-# cache), raw device addresses (0 or None: NULL) and a raw stream.
+# These calls take raw device addresses (None: NULL) and a raw stream, the
+# cache's calls its two structures (shape and buffers, built once per cache).
+# Plain lookups of the current stream's handle and the current device: a small
+# call (one new token) costs a few microseconds, and building a Stream object
+# would add two.
+_current_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def run_on(device_index, stream, call, *args):
+    """call(*args, raw stream) with that device current; stream None: its current one."""
+    if stream is None:
+        raw = _current_raw_stream(device_index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _current_device() == device_index:
+        call(*args, raw)
+    else:
+        with torch.cuda.device(device_index):
+            call(*args, raw)
+
+
 def kvcache_workspace_size(shape, Hq, T) -> int:
     return int(lib().kvcache_workspace_size(ctypes.byref(shape), int(Hq), int(T)))
 
@@ -338,12 +357,9 @@ def kvcache_free(shape, cache, seqs, n, status, stream):
     _check(lib().kvcache_free(shape, cache, seqs, n, status, stream), "kvcache_free")
 
 
-def kvcache_window_attention(q, k, v, lengths, window, sinks, attn_out, status, stream=None):
-    """q, attn_out [B,Hq,n_max,d], k, v [B,Hkv,n_max,d] bf16, lengths [B] int32 or None."""
-    B, Hq, n_max, d = q.shape
-    _check(lib().kvcache_window_attention(B, Hq, k.shape[1], d, n_max, _ptr(q), _ptr(k), _ptr(v), _ptr(lengths),
-                                          int(window), int(sinks), _ptr(attn_out), _ptr(status), _stream(stream)),
-           "kvcache_window_attention")
+def kvcache_window_attention(B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks, attn_out, status, stream):
+    _check(lib().kvcache_window_attention(B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks, attn_out, status,
+                                          stream), "kvcache_window_attention")
 
 
 def kvcache_read_status(status, stream=None):

@@ -91,16 +91,18 @@ class DropKV:
         tokens kept visible (kvcache_window_attention): row i sees keys j <= i
         with j > i - window or j < sinks; window 0 is prefill_attention's mask.
         The positional baseline next to the scored evictions."""
-        Bn, Hq, Hkv, d, n, _ = self.shape.astuple()
-        for t, heads in ((q, Hq), (k, Hkv), (v, Hkv), (attn_out, Hq)):
-            if t.dtype is not torch.bfloat16 or tuple(t.shape) != (Bn, heads, n, d) or t.device != self.status.device:
-                raise ValueError("expected bf16 [%d, %d, %d, %d] on %s, got %s %s on %s"
-                                 % (Bn, heads, n, d, self.device, t.dtype, tuple(t.shape), t.device))
-        if lengths is not None and (lengths.dtype is not torch.int32 or tuple(lengths.shape) != (Bn,)
-                                    or lengths.device != self.status.device):
-            raise ValueError("lengths: expected int32 [%d] on %s" % (Bn, self.device))
-        with torch.cuda.device(self.status.device):
-            B.kvcache_window_attention(q, k, v, lengths, window, sinks, attn_out, self.status, stream)
+        s, dev = self.shape, self.status.device
+        rows, kv = (s.B, s.Hq, s.n_max, s.d), (s.B, s.Hkv, s.n_max, s.d)
+        for t, shape in ((q, rows), (k, kv), (v, kv), (attn_out, rows)):
+            if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or not t.is_contiguous():
+                raise ValueError("expected a contiguous bf16 %s tensor on %s, got %s %s on %s"
+                                 % (list(shape), dev, t.dtype, list(t.shape), t.device))
+        if lengths is not None and (lengths.dtype is not torch.int32 or lengths.shape != (s.B,)
+                                    or lengths.device != dev or not lengths.is_contiguous()):
+            raise ValueError("lengths: expected int32 [%d] on %s" % (s.B, dev))
+        B.run_on(dev.index, stream, B.kvcache_window_attention, s.B, s.Hq, s.Hkv, s.d, s.n_max, q.data_ptr(),
+                 k.data_ptr(), v.data_ptr(), None if lengths is None else lengths.data_ptr(), window, sinks,
+                 attn_out.data_ptr(), self.status.data_ptr())
 
     def run_separate(self, q, k, v, lengths, evict_k, stream=None, keep_raw=True):
         """The same step as three library calls (score, select, compact)."""
