@@ -12,7 +12,10 @@
 // page, so it has one K and one V scale).  The tiles of the whole call,
 // counted on the device from the lengths and the window, are dealt out to the
 // warps of one resident wave in equal contiguous runs, so ragged batches
-// leave no tail.  A warp is on its own: it copies its tiles with cp.async
+// leave no tail.  More than 16 rows per KV head are dealt as row groups: the
+// warps of one run, one per group, stand side by side and read the same tiles
+// at about the same time, so the cache is read from memory once.  A warp is
+// on its own: it copies its tiles with cp.async
 // into its own ring of kStages tiles (no block barrier anywhere), and keeps
 // its rows' softmax state and outputs in registers.  A run that holds a whole
 // (sequence, head, row group) writes the output; the pieces of one that is
@@ -61,7 +64,7 @@ struct alignas(16) Tile {
   long long at;                             // byte offset of its first row in the layer's K or V
   int tok;                                  // first token
   int len;                                  // tokens of its sequence
-  int unit;                                 // entry * (Hkv * RG) + head * RG + row group
+  int unit;                                 // entry * Hkv + head
   float ks, lv;                             // K scale, log2 of the V scale
   int how;                                  // kPartial, kMasked, kUnreadable
 };
@@ -71,7 +74,7 @@ constexpr int kUnreadable = 4;              // its table entry is no page
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kJoinThreads = 128, kJoinWide = 512;
-constexpr int kTeamTiles = 16;              // most tiles of a unit that one CTA takes
+constexpr int kTeamTiles = 32;              // most tiles of a unit that one CTA takes
 constexpr int kUnitCost = 3;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, c4 = lane & 3;
   const int worker = blockIdx.x * kWarps + warp;
-  const int upb = c.Hkv * p.RG;             // units (head, row group) per sequence
+  const int upb = c.Hkv;                    // units (heads) per sequence
+  const int rg = (p.team ? (int)blockIdx.x : worker) % p.RG;   // the warp's row group
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_s = dropkv::smem_addr(ring);
   // this warp's run: tiles x0, x0 + stride, ... below x1 of the call; entry b0
@@ -300,9 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   int run_last = 0;                         // last run of the unit the next run begins inside
   if (p.team) {
     // the CTA's unit, dealt to its warps tile by tile; tiles are counted from its entry on
-    b0 = blockIdx.x / upb;
+    const int un = blockIdx.x / p.RG;
+    b0 = un / upb;
     const int tiles = span_of(entry_len(p, b0, true), p.T, p.window, p.sinks).tiles;
-    x1 = (long long)(blockIdx.x - b0 * upb + 1) * tiles;
+    x1 = (long long)(un - b0 * upb + 1) * tiles;
     x0 = x1 - tiles + warp;
     stride = kWarps;
   } else {
@@ -311,14 +316,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     for (int b = worker; b < p.n; b += p.workers) {
       if (span_of(entry_len(p, b, true), p.T, p.window, p.sinks).tiles > 0) continue;
       if (p.by_unit)
-        for (int u = lane; u < upb; u += 32) p.cuts[b * upb + u] = make_int2(-1, 0);
+        for (int u = lane; u < upb * p.RG; u += 32) p.cuts[b * upb * p.RG + u] = make_int2(-1, 0);
       uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * p.T * c.d);
       for (int u = lane; u < p.Hq * p.T * (c.d / 8); u += 32) o[u] = make_uint4(0, 0, 0, 0);
     }
     const int mine = lane < p.n ? entry_tiles(p, lane) : 0;
-    const Deal deal = make_deal(sum_cost(p, lane, mine) * upb, p.workers);
-    const Place from = find_place(p, lane, mine, upb, run_start(deal, worker));
-    const Place to = find_place(p, lane, mine, upb, run_start(deal, worker + 1));
+    const int run = worker / p.RG;
+    const Deal deal = make_deal(sum_cost(p, lane, mine) * upb, p.workers / p.RG);
+    const Place from = find_place(p, lane, mine, upb, run_start(deal, run));
+    const Place to = find_place(p, lane, mine, upb, run_start(deal, run + 1));
     x0 = from.tile;
     x1 = to.tile;
     if (to.tiles > 0) run_last = run_of(deal, to.last);
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
       t.lv = 0.f;
       t.how = kPartial | kMasked | kUnreadable;
     } else {
-      const size_t ur = (size_t)pg * c.Hkv + u / p.RG;
+      const size_t ur = (size_t)pg * c.Hkv + u;
       t.at = (long long)(ur * c.page + (tok & (c.page - 1))) * c.d;
       t.ks = c.ks[ur];
       t.lv = __log2f(fmaxf(c.vs[ur], 0x1p-126f));
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   auto load_unit = [&](int un, int ln) {
     unit = un;
     len = ln;
-    const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
+    const int b = un / upb, h = un - b * upb;
     const __nv_bfloat16* q = p.q + ((size_t)b * p.Hq + (size_t)h * p.g) * p.T * c.d;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -506,13 +512,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     if (lane == 0) {
       // who joins it: the run it begins in says so
       if (p.by_unit) {
-        if (whole) p.cuts[unit] = make_int2(-1, 0);
-        else if (slot == 1) p.cuts[unit] = make_int2(worker, run_last);
+        if (whole) p.cuts[unit * p.RG + rg] = make_int2(-1, 0);
+        else if (slot == 1) p.cuts[unit * p.RG + rg] = make_int2(worker / p.RG, run_last);
       } else if (slot == 1 && !whole) {
         p.cuts[worker] = make_int2(unit, run_last);
       }
     }
-    const int b = unit / upb, u = unit - b * upb, h = u / p.RG, rg = u - h * p.RG;
+    const int b = unit / upb, h = unit - b * upb;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -727,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
           ps[rl] = T_run > 0 ? make_float4(m[nr][e], l[nr][e], M[nr][e], 0.f) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
       }
     __syncthreads();
-    const int h = (blockIdx.x % upb) / p.RG, rg = (blockIdx.x % upb) % p.RG;
+    const int h = (blockIdx.x / p.RG) % upb;
     for (int rl = warp; rl < min(RB, p.R - rg * RB); rl += kWarps) {
       Joined a = nothing_joined();
 #pragma unroll
@@ -763,9 +769,9 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int2 cut = p.cuts[blockIdx.x];
   if (cut.x < 0) return;
-  const int un = p.by_unit ? (int)blockIdx.x : cut.x, w0 = p.by_unit ? cut.x : (int)blockIdx.x, w1 = cut.y;
-  const int upb = c.Hkv * p.RG;
-  const int b = un / upb, u = un - b * upb, h = u / p.RG, rg = u - h * p.RG;
+  const int un = p.by_unit ? (int)blockIdx.x / p.RG : cut.x, rg = blockIdx.x % p.RG;
+  const int w0 = p.by_unit ? cut.x : (int)blockIdx.x / p.RG, w1 = cut.y;   // runs
+  const int b = un / c.Hkv, h = un - b * c.Hkv;
   const int rows = min(p.RB, p.R - rg * p.RB);
   const bool cols = lane * 4 < c.d;
   // pieces w0 + first, w0 + first + step, ... of row rl; the unit begins in
@@ -780,7 +786,7 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
         st[k] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
         ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (w <= w1) {
-          const size_t row = ((size_t)w * 2 + (w == w0 ? 1 : 0)) * p.RB + rl;
+          const size_t row = (((size_t)w * p.RG + rg) * 2 + (w == w0 ? 1 : 0)) * p.RB + rl;
           st[k] = p.part_s[row];
           if (cols) ov[k] = *reinterpret_cast<const float4*>(p.part_o + row * c.d + lane * 4);
         }
@@ -847,13 +853,13 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   a->RG = (int)((R + a->RB - 1) / a->RB);
   // most tiles a unit can have
   long long cap = ((long long)s.max_pages * s.page + kTok - 1) / kTok;
-  const long long upb = (long long)s.Hkv * a->RG, units = n * upb;
-  if (cap * upb >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
+  const long long units = (long long)n * s.Hkv * a->RG;   // with their row groups
+  if (cap * s.Hkv >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
   if (window > 0)
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
   // Few short units: a CTA each, its warps join in shared memory, no second kernel.
   a->team = units <= 2LL * sms && cap <= kTeamTiles ? 1 : 0;
-  a->workers = (int)std::min(wave_of(sms), units * cap);
+  a->workers = (int)(std::max(1LL, std::min(wave_of(sms) / a->RG, (long long)n * s.Hkv * cap)) * a->RG);
   // Joins: by row where the rows are fewer than the CTAs they can fill
   a->by_unit = units <= a->workers ? 1 : 0;
   a->rowwise = a->by_unit && units * std::min<long long>(R, a->RB) <= 4LL * sms ? 1 : 0;
@@ -865,7 +871,7 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
 
 size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms) {
   const int RB = rows_per_warp((int)std::min<long long>(1 << 20, (long long)Hq / s.Hkv * T));
-  const long long w = wave_of(sms);
+  const long long w = std::max(wave_of(sms), ((long long)Hq / s.Hkv * T + RB - 1) / RB);
   return pieces_o(w, RB, s.d) + pieces_s(w, RB) + (size_t)w * 8;
 }
 

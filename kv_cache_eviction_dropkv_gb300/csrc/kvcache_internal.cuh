@@ -76,7 +76,7 @@ struct AttnCall {
   int n, Hq, T, g, R;            // R = g * T query rows per KV head
   int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
   int window, sinks;
-  int workers;                   // warps of the grid
+  int workers;                   // warps of the grid: run * RG + row group
   int team;                      // 1: a CTA per unit, joined in shared memory
   int by_unit;                   // 1: cuts is per unit, 0: per run
   int rowwise;                   // 1: a join CTA takes one row
@@ -84,7 +84,7 @@ struct AttnCall {
   __nv_bfloat16* out;
   float* part_o;                 // [workers][2][RB][d]
   float4* part_s;                // [workers][2][RB] (m, l, M, unused)
-  int2* cuts;                    // by_unit: [units] (first run or -1, last run); else [workers] (unit or -1, last run)
+  int2* cuts;                    // by_unit: [units][RG] (first run or -1, last run); else [workers] (unit or -1, last run)
   float scale_log2;
 };
 struct AttnPlan {

@@ -333,6 +333,20 @@ def test_attention_long_split_over_the_gpu(code):
     check_attention(c, r, q[:1, :, :1].contiguous(), seqs=[2])
 
 
+@pytest.mark.parametrize("Hq,Hkv,T,lengths", [(16, 2, 8, [2000, 5, 0, 700]), (24, 1, 7, [900, 901, 1, 64]),
+                                              (40, 1, 40, [33, 500, 1500, 39]), (64, 1, 330, [400, 7, 0, 0])])
+@pytest.mark.parametrize("room", [1, 8])
+def test_attention_many_rows_per_head(Hq, Hkv, T, lengths, room):
+    """Row groups: 56 to 21120 query rows of a KV head, more than a wave of warps."""
+    M = -(-max(lengths) // 64)
+    c, r = pair(seqs=4, Hkv=Hkv, d=64, pages=4 * M, page=64, max_pages=room * M, Hq=Hq, T=T, seed=T)
+    fill(c, r, lengths, spread=0.3)
+    q = draw_rows(4, Hq, T, 64, 5, spread=0.2)
+    check_attention(c, r, q)
+    check_attention(c, r, q, window=100, sinks=3)
+    assert c.check() == 0
+
+
 def test_attention_many_sequences():
     n = 150
     lengths = [(i * 37) % 130 for i in range(n)]
