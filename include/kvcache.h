@@ -124,6 +124,7 @@ DROPKV_API dropkv_status kvcache_store(const kvcache_shape* shape, const kvcache
  * that sees nothing.  Query head h reads KV head h / (Hq / Hkv).
  *   q, out  device bf16 [n][Hq][T][d], must not overlap
  *   window  0 (all tokens; sinks ignored) or >= 1;  sinks >= 0
+ * Supported: n * Hkv * max_pages * page < 2^35; n * Hq * T < 2^30.
  * Numerics: codes and query rows enter the tensor cores as fp16 (each query
  * row scaled by a power of two first; both exact but for query elements 2^-29
  * below their row's largest), probabilities as fp16, sums and softmax

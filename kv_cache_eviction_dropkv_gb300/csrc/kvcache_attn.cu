@@ -171,51 +171,49 @@ __device__ __forceinline__ int entry_len(const AttnCall& p, int i, bool report) 
 // the deal each unit is kUnitCost tiles longer than it is (its query rows are
 // loaded and its output written), and the runs are equal parts of that.
 struct Deal {
-  long long share, more;                    // the first `more` runs have share + 1, the others share
+  uint32_t share, more;                     // the first `more` runs have share + 1, the others share
 };
-__device__ __forceinline__ int cost_of(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+__device__ __forceinline__ uint32_t cost_of(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
 __device__ __forceinline__ int entry_tiles(const AttnCall& p, int b) {
   return span_of(entry_len(p, b, false), p.T, p.window, p.sinks).tiles;
 }
-// Cost per head and row group of all entries, over the warp's lanes (mine:
-// the tiles of entry `lane`, which every scan starts with).
-__device__ __forceinline__ long long sum_cost(const AttnCall& p, int lane, int mine) {
-  long long c = cost_of(mine);
+// Cost per head of all entries, over the warp's lanes (mine: the tiles of
+// entry `lane`, which every scan starts with).
+__device__ __forceinline__ uint32_t sum_cost(const AttnCall& p, int lane, int mine) {
+  uint32_t c = cost_of(mine);
   for (int b = lane + 32; b < p.n; b += 32) c += cost_of(entry_tiles(p, b));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-  return c;
+  return __reduce_add_sync(0xffffffffu, c);
 }
-__device__ __forceinline__ Deal make_deal(long long cost, int workers) {
+__device__ __forceinline__ Deal make_deal(uint32_t cost, uint32_t runs) {
   Deal d;
-  d.share = cost / workers;
-  d.more = cost - d.share * workers;
+  d.share = cost / runs;
+  d.more = cost - d.share * runs;
   return d;
 }
-__device__ __forceinline__ long long run_start(const Deal& d, long long w) { return w * d.share + min(w, d.more); }
+__device__ __forceinline__ uint32_t run_start(const Deal& d, uint32_t w) { return w * d.share + min(w, d.more); }
 // The run that holds cost position x.
-__device__ __forceinline__ int run_of(const Deal& d, long long x) {
-  const long long cut = d.more * (d.share + 1);
-  return (int)(x < cut ? x / (d.share + 1) : d.more + (x - cut) / d.share);
+__device__ __forceinline__ uint32_t run_of(const Deal& d, uint32_t x) {
+  const uint32_t cut = d.more * (d.share + 1);
+  return x < cut ? x / (d.share + 1) : d.more + (x - cut) / d.share;
 }
 // Cost position x as a place among the tiles: entry b, `first` tiles before
 // it, and the tile of the call that x stands at.
 struct Place {
   int b, tiles;                             // entry and its tiles per unit (0: past the end)
-  long long first, tile;
-  long long last;                           // cost position of the last tile of x's unit
+  uint32_t first, tile;
+  uint32_t last;                            // cost position of the last tile of x's unit
 };
-__device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int mine, int upb, long long x) {
+__device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int mine, uint32_t upb, uint32_t x) {
   Place r;
-  long long cost0 = 0, tiles0 = 0;          // before this batch of entries
+  uint32_t cost0 = 0, tiles0 = 0;           // before this batch of entries
   for (int base = 0; base < p.n; base += 32) {
     const int b = base + lane;
     const int t = base == 0 ? mine : b < p.n ? entry_tiles(p, b) : 0;
-    long long cost = (long long)cost_of(t) * upb, tiles = (long long)t * upb;
-    const long long own_cost = cost, own_tiles = tiles;
+    uint32_t cost = cost_of(t) * upb, tiles = t * upb;
+    const uint32_t own_cost = cost, own_tiles = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, cost, o), z = __shfl_up_sync(0xffffffffu, tiles, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, cost, o), z = __shfl_up_sync(0xffffffffu, tiles, o);
       if (lane >= o) {
         cost += y;
         tiles += z;
@@ -227,10 +225,10 @@ __device__ __forceinline__ Place find_place(const AttnCall& p, int lane, int min
       r.b = base + l;
       r.tiles = __shfl_sync(0xffffffffu, t, l);
       r.first = tiles0 + __shfl_sync(0xffffffffu, tiles - own_tiles, l);
-      const long long in = x - (cost0 + __shfl_sync(0xffffffffu, cost - own_cost, l));   // < upb (tiles + kUnitCost)
-      const int per = cost_of(r.tiles);
-      const int u = (int)((unsigned)in / (unsigned)per), k = (int)in - u * per - kUnitCost;
-      r.tile = r.first + (long long)u * r.tiles + max(k, 0);
+      const uint32_t in = x - (cost0 + __shfl_sync(0xffffffffu, cost - own_cost, l));
+      const uint32_t per = cost_of(r.tiles), u = in / per;
+      const int k = (int)(in - u * per) - kUnitCost;
+      r.tile = r.first + u * r.tiles + max(k, 0);
       r.last = x - (k + kUnitCost) + per - 1;
       return r;
     }
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   const uint32_t ring_s = dropkv::smem_addr(ring);
   // this warp's run: tiles x0, x0 + stride, ... below x1 of the call; entry b0
   // holds x0 and begins at tile cum0
-  long long x0, x1, cum0 = 0;
+  uint32_t x0, x1, cum0 = 0;
   int b0, stride = 1;
   bool cut = false;                         // the run begins inside a unit
   int run_last = 0;                         // last run of the unit the next run begins inside
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     const int un = blockIdx.x / p.RG;
     b0 = un / upb;
     const int tiles = span_of(entry_len(p, b0, true), p.T, p.window, p.sinks).tiles;
-    x1 = (long long)(un - b0 * upb + 1) * tiles;
+    x1 = (uint32_t)(un - b0 * upb + 1) * tiles;
     x0 = x1 - tiles + warp;
     stride = kWarps;
   } else {
@@ -330,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     if (to.tiles > 0) run_last = run_of(deal, to.last);
     b0 = from.b;
     cum0 = from.first;
-    cut = from.tiles > 0 && (int)(x0 - cum0) % from.tiles != 0;
+    cut = from.tiles > 0 && (x0 - cum0) % (uint32_t)from.tiles != 0;
     if (!p.by_unit && lane == 0) p.cuts[worker] = make_int2(-1, 0);
     if (x0 >= x1) return;
   }
@@ -346,18 +344,19 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   // two dependent loads, 32 tiles ahead of their use).
   Tile* meta = reinterpret_cast<Tile*>(smem + kRingBytes) + warp * kMeta;
   int wb = b0;                              // entry the lane's cursor stands at
-  long long wcum = cum0;
-  auto describe = [&](long long x, Tile* to) {
+  uint32_t wcum = cum0;
+  auto describe = [&](uint32_t x, Tile* to) {
     if (x >= x1) return;
     int len = entry_len(p, wb, false);
     Span s = span_of(len, p.T, p.window, p.sinks);
-    while (x >= wcum + (long long)s.tiles * upb) {
-      wcum += (long long)s.tiles * upb;
+    while (x >= wcum + s.tiles * upb) {
+      wcum += s.tiles * upb;
       ++wb;
       len = entry_len(p, wb, false);
       s = span_of(len, p.T, p.window, p.sinks);
     }
-    const int y = (int)(x - wcum), u = y / s.tiles, k = y - u * s.tiles;
+    const uint32_t y = x - wcum, u = y / (uint32_t)s.tiles;
+    const int k = (int)(y - u * s.tiles);
     const int tok = (k < s.ns ? k : s.s2 + (k - s.ns)) * kTok;
     const int sq = p.seqs ? p.seqs[wb] : wb;
     const int pg = c.table[(size_t)sq * c.M + (tok >> c.page_log2)];
@@ -854,7 +853,7 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   // most tiles a unit can have
   long long cap = ((long long)s.max_pages * s.page + kTok - 1) / kTok;
   const long long units = (long long)n * s.Hkv * a->RG;   // with their row groups
-  if (cap * s.Hkv >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
+  if ((cap + kUnitCost) * s.Hkv * n >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
   if (window > 0)
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
   // Few short units: a CTA each, its warps join in shared memory, no second kernel.
