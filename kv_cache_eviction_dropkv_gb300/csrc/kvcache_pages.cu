@@ -31,26 +31,27 @@ __device__ __forceinline__ int pages_for(const Cache& c, int tokens) {
 
 // Exclusive sum over the block's threads; *total gets the sum of all.  `turn`
 // counts the calls (it picks one of two buffers, so a call needs one barrier).
-__device__ __forceinline__ int block_scan(int x, int* total, int& turn) {
-  __shared__ int warp_sum[2][kBookWarps];
-  int* sums = warp_sum[turn++ & 1];
+// 64 bits: the pages a call wants may be many times those there are.
+__device__ __forceinline__ long long block_scan(long long x, long long* total, int& turn) {
+  __shared__ long long warp_sum[2][kBookWarps];
+  long long* sums = warp_sum[turn++ & 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = x;
+  long long inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int w = sums[lane];
+  long long w = sums[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    const long long y = __shfl_up_sync(0xffffffffu, w, o);
     if (lane >= o) w += y;
   }
   *total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  const long long before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   return (warp > 0 ? before : 0) + inc - x;
 }
 
@@ -110,8 +111,12 @@ __device__ __forceinline__ Counts load_counts(const Cache& c, int base) {
 
 // The `want` lowest free pages into p.list; false (and a flag) if there are
 // fewer.  k: the counts of the first pages.
-__device__ __forceinline__ bool find_pages(const PageCall& p, int want, Counts k, int& turn) {
+__device__ __forceinline__ bool find_pages(const PageCall& p, long long want, Counts k, int& turn) {
   int found = 0;
+  if (want > p.c.P) {
+    if (threadIdx.x == 0) flag(p.c.status, KVCACHE_FLAG_NO_PAGES);
+    return false;
+  }
   for (int base = 0; base < p.c.P && found < want; base += kBook * kPer) {
     if (base > 0) k = load_counts(p.c, base);
     uint32_t free_bits = 0;
@@ -120,15 +125,15 @@ __device__ __forceinline__ bool find_pages(const PageCall& p, int want, Counts k
       free_bits |= (k.r[u].x == 0 ? 1u : 0u) << (4 * u) | (k.r[u].y == 0 ? 2u : 0u) << (4 * u) |
                    (k.r[u].z == 0 ? 4u : 0u) << (4 * u) | (k.r[u].w == 0 ? 8u : 0u) << (4 * u);
     }
-    int total;
-    int at = found + block_scan(__popc(free_bits), &total, turn);
+    long long total;
+    int at = found + (int)block_scan(__popc(free_bits), &total, turn);
     const int first = base + threadIdx.x * kPer;
     while (free_bits && at < want) {
       const int bit = __ffs(free_bits) - 1;
       free_bits &= free_bits - 1;
       p.list[at++] = first + bit;
     }
-    found += total;
+    found += (int)total;
   }
   __syncthreads();
   if (found < want && threadIdx.x == 0) flag(p.c.status, KVCACHE_FLAG_NO_PAGES);
@@ -187,7 +192,8 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
   const Cache& c = p.c;
   const Counts counts = load_counts(c, 0);
   if (p.seqs) claim_seqs(p, p.seqs, names);
-  int sum = 0, turn = 0;
+  long long sum = 0;                        // pages wanted
+  int turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
     int need = 0, pages = 0;
@@ -209,10 +215,10 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
         }
       }
     }
-    int total;
-    const int at = sum + block_scan(need, &total, turn);
+    long long total;
+    const long long at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
-      p.offs[i] = at;
+      p.offs[i] = (int)at;                  // (read only where the sum fits)
       p.entry[i] = make_int4((int)tokens, pages, need, 0);
     }
     sum += total;
@@ -264,7 +270,8 @@ __device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
     for (int j = 0; j < p.n; ++j) any |= names.other[j] == d;
     return any != 0;
   };
-  int sum = 0, turn = 0;
+  long long sum = 0;                        // pages wanted
+  int turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
     int need = 0, len = 0;
@@ -287,16 +294,16 @@ __device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
         }
       }
     }
-    int total;
-    const int at = sum + block_scan(need, &total, turn);
+    long long total;
+    const long long at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
-      p.offs[i] = at;
+      p.offs[i] = (int)at;                  // (read only where the sum fits)
       p.entry[i] = e;
     }
     sum += total;
   }
   const bool ok = find_pages(p, sum, counts, turn);
-  if (threadIdx.x == 0) p.offs[p.n] = ok ? sum : -1;   // -1: nothing to do
+  if (threadIdx.x == 0) p.offs[p.n] = ok ? (int)sum : -1;   // -1: nothing to do
   if (!ok) return;
   for (int k = threadIdx.x; k < sum; k += kBook) c.refs[p.list[k]] = 1;
   for (int i = threadIdx.x; i < p.n; i += kBook) {
@@ -418,7 +425,8 @@ __device__ __forceinline__ void compact_book(const PageCall& p, Names& names) {
   const Cache& c = p.c;
   const Counts counts = load_counts(c, 0);
   if (p.seqs) claim_seqs(p, p.seqs, names);
-  int sum = 0, turn = 0;
+  long long sum = 0;                        // pages wanted
+  int turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
     int need = 0;
@@ -439,16 +447,16 @@ __device__ __forceinline__ void compact_book(const PageCall& p, Names& names) {
         }
       }
     }
-    int total;
-    const int at = sum + block_scan(need, &total, turn);
+    long long total;
+    const long long at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
-      p.offs[i] = at;
+      p.offs[i] = (int)at;                  // (read only where the sum fits)
       p.entry[i] = e;
     }
     sum += total;
   }
   const bool ok = find_pages(p, sum, counts, turn);
-  if (threadIdx.x == 0) p.offs[p.n] = ok ? sum : -1;
+  if (threadIdx.x == 0) p.offs[p.n] = ok ? (int)sum : -1;
   if (!ok) return;
   for (int k = threadIdx.x; k < sum; k += kBook) c.refs[p.list[k]] = 1;
   for (int i = threadIdx.x; i < p.n; i += kBook) {
