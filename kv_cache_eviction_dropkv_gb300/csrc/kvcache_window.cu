@@ -45,12 +45,13 @@ constexpr float kMove = 24.0f;                    // base-2 logarithm by which a
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
 
 constexpr int kNarrow = 32;
+constexpr int kSplitWindow = 1536;                // windows from which on P goes in halves (even at 1024)
 
 struct Small {
   uint64_t qfull[2], qempty[2];   // group g's Q: landed; its last S of the item complete
   uint64_t full[2], empty[2];     // K and V pairs: landed; released by the groups (one arrival each)
   uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
-  uint64_t pfull[2];   // group g: its P written by the group's four warps
+  uint64_t pfull[2][2];   // group g: the first and the second half of its P written by the group's four warps
   uint64_t odone[2];   // group g: its last P V of the item complete
   uint64_t drain;
   uint32_t tmem_base;
@@ -135,12 +136,15 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // One row against its 128 columns of S: moves the reference, turns S into P in
-// place.  Returns the factor O follows by (l has followed).  Columns [from,
-// to) and [0, first) are seen.  The masked path is kept short: this code runs
-// four warps wide from a small instruction cache, and a cold branch of a few
-// hundred instructions costs more than the exponentials.
-__device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, bool mask, int from, int to, int first,
-                                              float& ref, float& l, bool& need) {
+// place.  Columns [from, to) and [0, first) are seen.  follow(factor) lets O
+// follow the reference (l does here); SPLIT: before half(), which is called
+// when the first half of P is stored, else at the end, when x is dead.  The masked path is
+// kept short: this code runs four warps wide from a small instruction cache,
+// and a cold branch of a few hundred instructions costs more than the
+// exponentials.
+template <bool SPLIT, typename Follow, typename Half>
+__device__ __forceinline__ void softmax_tile(const WindowCall& p, uint32_t tS, bool mask, int from, int to, int first,
+                                             float& ref, float& l, Follow follow, Half half) {
   const float scale = p.scale_log2;
   float x[kQT];
 #pragma unroll
@@ -164,13 +168,14 @@ __device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, 
   for (int u = 8; u < kQT; ++u) m8[u & 7] = fmaxf(m8[u & 7], x[u]);
   const float mt = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * scale;
-  need = mt > ref + kMove;
+  const bool need = mt > ref + kMove;
   float factor = 1.f;
   if (need) {
     factor = ref == -INFINITY ? 0.f : ex2_approx(ref - mt);
     ref = mt;
     l *= factor;
   }
+  if (SPLIT && __any_sync(0xffffffffu, need)) follow(factor);
   // a row that has seen nothing yet keeps P = 0
   const float r0 = ref == -INFINITY ? 0.f : ref;
   // P = 2^(x scale - ref), 16 columns at a time: while the exponentials of
@@ -196,13 +201,15 @@ __device__ __forceinline__ float softmax_tile(const WindowCall& p, uint32_t tS, 
         hw[(u >> 1) & 15] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
       }
       if (c % 2 == 0) tmem_st16(tS + 16 * (c / 2 - 1), hw);
+      if (SPLIT && c == 5) half();
     }
   }
   const uint64_t lsum = f2_add(f2_add(ls2[0], ls2[1]), f2_add(ls2[2], ls2[3]));
   l += f2_lo(lsum) + f2_hi(lsum);
-  return factor;
+  if (!SPLIT && __any_sync(0xffffffffu, need)) follow(factor);
 }
 
+template <bool SPLIT>
 __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem, int warp,
                                               int lane) {
   const int g = warp >> 2, quarter = warp & 3;
@@ -257,31 +264,12 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
       if (speaks && kt == tg) mbar_arrive(&S.qempty[g]);
       // the last row of the tile reaches back to tg 128 + 127 - W + 1
       const bool edge = p.window > 0 && j0 <= tg * kQT + 127 - p.window && j0 + kQT > p.sinks;
-      bool need;
-      // keys j <= pos with j > pos - window or j < sinks; past a narrow tile's
-      // kNarrow columns S holds anything
-      const float factor = softmax_tile(p, tS, kt == tg || edge || i == list.narrow,
-                                        p.window > 0 ? pos - p.window + 1 - j0 : 0, pos + 1 - j0,
-                                        p.window > 0 ? min(p.sinks, pos + 1) - j0 : 0, ref, l, need);
-      // the group's P V of its tile before is complete (the commit its S
-      // signalled came after it): O follows the reference
-      if (!first && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          float o[16];
-          tmem_ld16(tO + 16 * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int u = 0; u < 16; ++u) o[u] *= factor;
-          tmem_st16(tO + 16 * c, o);
-        }
-      }
-      first = false;
-      if (j0 + kQT > w.nb) {
-        // the sequence's last key tile (group 1's alone): rows past the end may
-        // hold anything; zero them so that 0 * NaN never reaches O
+      // the sequence's last key tile (group 1's alone): rows past the end may
+      // hold anything; zero them so that 0 * NaN never reaches O
+      auto zero_tail = [&]() {
+        if (j0 + kQT <= w.nb) return true;
         const uint32_t pr = pair0 + i + 1;
-        if (!wait(&S.full[pr & 1], pr >> 1)) { give_up(); return; }
+        if (!wait(&S.full[pr & 1], pr >> 1)) return false;
         if (j0 + row >= w.nb) {
           uint8_t* vrow = sm + kOffV + (pr & 1) * kTileB + row * 128;
 #pragma unroll
@@ -291,11 +279,38 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
           }
         }
         fence_proxy_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.pfull[g]);
+        return true;
+      };
+      if (SPLIT && !zero_tail()) { give_up(); return; }
+      auto written = [&](int h) {                 // half h of P, and all before it
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.pfull[g][h]);
+      };
+      // keys j <= pos with j > pos - window or j < sinks; past a narrow tile's
+      // kNarrow columns S holds anything
+      softmax_tile<SPLIT>(
+          p, tS, kt == tg || edge || i == list.narrow, p.window > 0 ? pos - p.window + 1 - j0 : 0, pos + 1 - j0,
+          p.window > 0 ? min(p.sinks, pos + 1) - j0 : 0, ref, l,
+          [&](float factor) {
+            // the group's P V of its tile before is complete (the commit its S
+            // signalled came after it): O follows the reference
+            if (first) return;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float o[16];
+              tmem_ld16(tO + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] *= factor;
+              tmem_st16(tO + 16 * c, o);
+            }
+          },
+          [&]() { written(0); });
+      first = false;
+      if (!SPLIT && !zero_tail()) { give_up(); return; }
+      written(1);
       ++seen;
     }
     if (!wait(&S.odone[g], done)) { give_up(); return; }
@@ -329,6 +344,12 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   }
 }
 
+// SPLIT: P V of a tile begins on the first half of P while the softmax is at
+// the second.  With many tiles per item it shortens the chain softmax -> P V ->
+// S that bounds the kernel (32768 tokens, window 4096: 1.45 -> 1.36 ms); with
+// few, most of them masked, the extra barrier costs more (2051 tokens, window
+// 333: 60 -> 65 us).
+template <bool SPLIT>
 __global__ void __launch_bounds__(kWinThreads, 1)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const WindowCall p) {
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.qfull[i], 1); mbar_init(&S.qempty[i], 1);
       mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 2);
-      mbar_init(&S.sfull[i], 1); mbar_init(&S.pfull[i], 4);
+      mbar_init(&S.sfull[i], 1); mbar_init(&S.pfull[i][0], 4); mbar_init(&S.pfull[i][1], 4);
       mbar_init(&S.odone[i], 1);
     }
     mbar_init(&S.drain, 1);
@@ -435,15 +456,20 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_PV = [&](int g, int slot, auto steps, bool first) {
+    // P V of group g, steps s0 .. s1 - 1 of 16 keys
+    auto issue_PV = [&](int g, int slot, auto s0, auto s1, bool first) {
       const uint64_t vg = vd + ((slot * kTileB) >> 4);
       if (leader) {
 #pragma unroll
-        for (int s = 0; s < decltype(steps)::value; ++s)
+        for (int s = decltype(s0)::value; s < decltype(s1)::value; ++s)
           umma_bf16_tmem_a(256 + 128 * g, 128 * g + 8 * s, vg + ((s * 16 * 128) >> 4), idO, !first || s > 0);
       }
       __syncwarp();
     };
+    using Zero = std::integral_constant<int, 0>;
+    using Four = std::integral_constant<int, 4>;
+    using Eight = std::integral_constant<int, 8>;
+    using Narrow = std::integral_constant<int, kNarrow / 16>;
     uint32_t pair0 = 0, seen0 = 0, seen1 = 0, used0 = 0, used1 = 0;   // entries, tiles and items of the groups so far
     Cursor at;
     Item w, w2;                                   // the item, the one after
@@ -478,10 +504,20 @@ __global__ void __launch_bounds__(kWinThreads, 1)
           uint32_t& seen = g ? seen1 : seen0;
           bool& first = g ? first1 : first0;
           if (kPlain || list.takes(g, i)) {
-            if (!wait(&S.pfull[g], seen)) return false;
-            tc_fence_after();
-            if (!kPlain && i == list.narrow) issue_PV(g, pr & 1, std::integral_constant<int, kNarrow / 16>{}, first);
-            else issue_PV(g, pr & 1, std::integral_constant<int, 8>{}, !kPlain && first);
+            if (SPLIT) {
+              if (!wait(&S.pfull[g][0], seen)) return false;
+              tc_fence_after();
+              if (!kPlain && i == list.narrow) issue_PV(g, pr & 1, Zero{}, Narrow{}, first);
+              else issue_PV(g, pr & 1, Zero{}, Four{}, !kPlain && first);
+              if (!wait(&S.pfull[g][1], seen)) return false;
+              tc_fence_after();
+              if (kPlain || i != list.narrow) issue_PV(g, pr & 1, Four{}, Eight{}, false);
+            } else {
+              if (!wait(&S.pfull[g][1], seen)) return false;
+              tc_fence_after();
+              if (!kPlain && i == list.narrow) issue_PV(g, pr & 1, Zero{}, Narrow{}, first);
+              else issue_PV(g, pr & 1, Zero{}, Eight{}, !kPlain && first);
+            }
             first = false;
             ++seen;
             if (!kPlain && list.tile(i) == list.t[g] && leader) umma_commit(&S.odone[g]);
@@ -521,7 +557,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    softmax_group(p, S, sm, tmem, warp, lane);
+    softmax_group<SPLIT>(p, S, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -535,11 +571,14 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           int sms, cudaStream_t st) {
-  const cudaError_t e = allow_smem<window_prefill_kernel>(kWinSmem);
+  const bool split = p.window == 0 || p.window >= kSplitWindow;
+  const cudaError_t e = split ? allow_smem<window_prefill_kernel<true>>(kWinSmem)
+                              : allow_smem<window_prefill_kernel<false>>(kWinSmem);
   if (e != cudaSuccess) return e;
   const long long most = (long long)((p.n_max + 2 * kQT - 1) / (2 * kQT)) * p.Hq * p.B;
-  return launch_pdl(window_prefill_kernel, dim3((unsigned)std::min<long long>(most, sms)), dim3(kWinThreads), kWinSmem, st, tq, tk,
-                    tv, p);
+  const dim3 grid((unsigned)std::min<long long>(most, sms));
+  return launch_pdl(split ? window_prefill_kernel<true> : window_prefill_kernel<false>, grid, dim3(kWinThreads),
+                    kWinSmem, st, tq, tk, tv, p);
 }
 
 }  // namespace kvcache
