@@ -302,64 +302,32 @@ def dropkv_version() -> str:
 
 
 # ------------------------------------------------------------------ include/kvcache.h
-# These calls take raw device addresses (None: NULL) and a raw stream, the
-# cache's calls its two structures (shape and buffers, built once per cache).
-# Plain lookups of the current stream's handle and the current device: a small
-# call (one new token) costs a few microseconds, and building a Stream object
-# would add two.
-_current_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# Small calls (one new token) cost a few microseconds, so these go with raw
+# addresses and streams, and as few layers as can be: the cache's own calls are
+# made by PagedCache through lib() directly.  Plain lookups of the current
+# stream's handle and the current device: building a Stream object would add
+# two microseconds.
+current_raw_stream, current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def run_on(device_index, stream, call, *args):
-    """call(*args, raw stream) with that device current; stream None: its current one."""
-    if stream is None:
-        raw = _current_raw_stream(device_index)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if _current_device() == device_index:
-        call(*args, raw)
-    else:
-        with torch.cuda.device(device_index):
-            call(*args, raw)
+def raw_stream(stream) -> int:
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def kvcache_workspace_size(shape, Hq, T) -> int:
     return int(lib().kvcache_workspace_size(ctypes.byref(shape), int(Hq), int(T)))
 
 
-def kvcache_reserve(shape, cache, seqs, n, extra, workspace, workspace_bytes, status, stream):
-    _check(lib().kvcache_reserve(shape, cache, seqs, n, extra, workspace, workspace_bytes, status, stream),
-           "kvcache_reserve")
-
-
-def kvcache_store(shape, cache, layer, seqs, n, k, v, rows, counts, status, stream):
-    _check(lib().kvcache_store(shape, cache, layer, seqs, n, k, v, rows, counts, status, stream), "kvcache_store")
-
-
-def kvcache_attention(shape, cache, layer, seqs, n, q, Hq, T, window, sinks, out, workspace, workspace_bytes, status,
-                      stream):
-    _check(lib().kvcache_attention(shape, cache, layer, seqs, n, q, Hq, T, window, sinks, out, workspace,
-                                   workspace_bytes, status, stream), "kvcache_attention")
-
-
-def kvcache_fork(shape, cache, src, dst, n, share, workspace, workspace_bytes, status, stream):
-    _check(lib().kvcache_fork(shape, cache, src, dst, n, share, workspace, workspace_bytes, status, stream),
-           "kvcache_fork")
-
-
-def kvcache_compact(shape, cache, seqs, n, kept_idx, kept_stride, kept_len, workspace, workspace_bytes, status,
-                    stream):
-    _check(lib().kvcache_compact(shape, cache, seqs, n, kept_idx, kept_stride, kept_len, workspace, workspace_bytes,
-                                 status, stream), "kvcache_compact")
-
-
-def kvcache_free(shape, cache, seqs, n, status, stream):
-    _check(lib().kvcache_free(shape, cache, seqs, n, status, stream), "kvcache_free")
-
-
-def kvcache_window_attention(B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks, attn_out, status, stream):
+def kvcache_window_attention(device_index, B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks, attn_out, status,
+                             stream=None):
+    """Raw addresses (lengths: or None) on the device of that index."""
+    if current_device() != device_index:
+        with torch.cuda.device(device_index):
+            return kvcache_window_attention(device_index, B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks,
+                                            attn_out, status, stream)
     _check(lib().kvcache_window_attention(B, Hq, Hkv, d, n_max, q, k, v, lengths, window, sinks, attn_out, status,
-                                          stream), "kvcache_window_attention")
+                                          current_raw_stream(device_index) if stream is None else raw_stream(stream)),
+           "kvcache_window_attention")
 
 
 def kvcache_read_status(status, stream=None):

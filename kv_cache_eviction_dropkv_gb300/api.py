@@ -100,9 +100,9 @@ class DropKV:
         if lengths is not None and (lengths.dtype is not torch.int32 or lengths.shape != (s.B,)
                                     or lengths.device != dev or not lengths.is_contiguous()):
             raise ValueError("lengths: expected int32 [%d] on %s" % (s.B, dev))
-        B.run_on(dev.index, stream, B.kvcache_window_attention, s.B, s.Hq, s.Hkv, s.d, s.n_max, q.data_ptr(),
-                 k.data_ptr(), v.data_ptr(), None if lengths is None else lengths.data_ptr(), window, sinks,
-                 attn_out.data_ptr(), self.status.data_ptr())
+        B.kvcache_window_attention(dev.index, s.B, s.Hq, s.Hkv, s.d, s.n_max, q.data_ptr(), k.data_ptr(),
+                                   v.data_ptr(), None if lengths is None else lengths.data_ptr(), window, sinks,
+                                   attn_out.data_ptr(), self.status.data_ptr(), stream)
 
     def run_separate(self, q, k, v, lengths, evict_k, stream=None, keep_raw=True):
         """The same step as three library calls (score, select, compact)."""

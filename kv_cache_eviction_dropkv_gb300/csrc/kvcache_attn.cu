@@ -74,7 +74,7 @@ constexpr int kUnreadable = 4;              // its table entry is no page
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kJoinThreads = 128, kJoinWide = 512;
-constexpr int kTeamTiles = 32;              // most tiles of a unit that one CTA takes
+constexpr int kTeamTiles = 8;               // most tiles a warp takes of a unit that has a team
 constexpr int kUnitCost = 3;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
@@ -98,6 +98,24 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// Rank in the cluster; barrier of all its threads (shared memory written
+// before is visible after); 16 bytes at this CTA's address `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+  float4 v;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -291,7 +309,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   const int g8 = lane >> 2, c4 = lane & 3;
   const int worker = blockIdx.x * kWarps + warp;
   const int upb = c.Hkv;                    // units (heads) per sequence
-  const int rg = (p.team ? (int)blockIdx.x : worker) % p.RG;   // the warp's row group
+  // team: the unit of this CTA's cluster (of p.team CTAs), with its row group
+  const int mate = p.team > 1 ? (int)cluster_rank() : 0, unit_rg = p.team ? (int)blockIdx.x / p.team : 0;
+  const int rg = (p.team ? unit_rg : worker) % p.RG;   // the warp's row group
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_s = dropkv::smem_addr(ring);
   // this warp's run: tiles x0, x0 + stride, ... below x1 of the call; entry b0
@@ -301,13 +321,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
   bool cut = false;                         // the run begins inside a unit
   int run_last = 0;                         // last run of the unit the next run begins inside
   if (p.team) {
-    // the CTA's unit, dealt to its warps tile by tile; tiles are counted from its entry on
-    const int un = blockIdx.x / p.RG;
+    // the unit, dealt to the warps tile by tile; tiles are counted from its entry on
+    const int un = unit_rg / p.RG;
     b0 = un / upb;
     const int tiles = span_of(entry_len(p, b0, true), p.T, p.window, p.sinks).tiles;
     x1 = (uint32_t)(un - b0 * upb + 1) * tiles;
-    x0 = x1 - tiles + warp;
-    stride = kWarps;
+    x0 = x1 - tiles + mate * kWarps + warp;
+    stride = kWarps * p.team;
   } else {
     if (worker >= p.workers) return;
     // rows of sequences with nothing to read
@@ -731,18 +751,28 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
         if (g8 == 0)
           ps[rl] = T_run > 0 ? make_float4(m[nr][e], l[nr][e], M[nr][e], 0.f) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
       }
-    __syncthreads();
-    const int h = (blockIdx.x / p.RG) % upb;
-    for (int rl = warp; rl < min(RB, p.R - rg * RB); rl += kWarps) {
+    // the rows are shared out over the team's warps
+    if (p.team > 1) cluster_sync();
+    else __syncthreads();
+    const uint32_t base = dropkv::smem_addr(smem);
+    const int h = (unit_rg / p.RG) % upb;
+    for (int rl = mate * kWarps + warp; rl < min(RB, p.R - rg * RB); rl += stride) {
       Joined a = nothing_joined();
+      for (int mt = 0; mt < p.team; ++mt) {
+        float4 st[kWarps], ov[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 st = reinterpret_cast<const float4*>(smem + kRingBytes + w * kMeta * sizeof(Tile))[rl];
-        const float* ow = reinterpret_cast<const float*>(smem + w * kStages * kStageBytes) + rl * DP;
-        join_in(a, st.x, st.y, st.z, lane * 4 < DP ? *reinterpret_cast<const float4*>(ow + lane * 4) : a.o);
+        for (int w = 0; w < kWarps; ++w) {
+          const uint32_t sa = base + kRingBytes + w * kMeta * (int)sizeof(Tile) + rl * 16;
+          const uint32_t oa = base + w * kStages * kStageBytes + (rl * DP + lane * 4) * 4;
+          st[w] = ld_cluster(sa, mt);
+          ov[w] = lane * 4 < DP ? ld_cluster(oa, mt) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) join_in(a, st[w].x, st[w].y, st[w].z, ov[w]);
       }
       write_row(p, b0, h, rg * RB + rl, lane, a);
     }
+    if (p.team > 1) cluster_sync();         // no CTA leaves while its shared memory is read
     return;
   }
   // the last part: whole when all tiles of its unit lie in this run; else its
@@ -815,14 +845,33 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
   }
 }
 
+cudaError_t launch_team(void (*kern)(AttnCall), unsigned units, const AttnCall& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * p.team);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.team;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.team > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int CODE, int DP, int NR, bool EXACT>
 cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
   auto kern = attention_kernel<CODE, DP, NR, EXACT>;
   cudaError_t e = allow_smem<attention_kernel<CODE, DP, NR, EXACT>>(kSmem);
   if (e != cudaSuccess) return e;
   const unsigned units = (unsigned)(p.n * p.c.Hkv * p.RG);
-  e = launch_pdl(kern, dim3(p.team ? units : (p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
-  if (e != cudaSuccess || p.team) return e;
+  if (p.team) return launch_team(kern, units, p, st);
+  e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
+  if (e != cudaSuccess) return e;
   if (p.rowwise) return launch_pdl(join_kernel<true>, dim3(units, std::min(p.RB, p.R)), dim3(kJoinWide), 0, st, p);
   return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers), dim3(kJoinThreads), 0, st, p);
 }
@@ -856,8 +905,12 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   if ((cap + kUnitCost) * s.Hkv * n >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
   if (window > 0)
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
-  // Few short units: a CTA each, its warps join in shared memory, no second kernel.
-  a->team = units <= 2LL * sms && cap <= kTeamTiles ? 1 : 0;
+  // Few units of moderate length: a cluster of 1 to 8 CTAs each, joined through
+  // shared memory, no second kernel.  More CTAs while a warp has over 2 tiles
+  // and they fit one wave.
+  int team = 1;
+  while (team < 8 && units * 2 * team <= 2LL * sms && cap > 2LL * kWarps * team) team *= 2;
+  a->team = units <= 2LL * sms && cap <= (long long)kTeamTiles * kWarps * team ? team : 0;
   a->workers = (int)(std::max(1LL, std::min(wave_of(sms) / a->RG, (long long)n * s.Hkv * cap)) * a->RG);
   // Joins: by row where the rows are fewer than the CTAs they can fill
   a->by_unit = units <= a->workers ? 1 : 0;

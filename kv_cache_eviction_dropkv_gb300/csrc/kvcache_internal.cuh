@@ -77,7 +77,7 @@ struct AttnCall {
   int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
   int window, sinks;
   int workers;                   // warps of the grid: run * RG + row group
-  int team;                      // 1: a CTA per unit, joined in shared memory
+  int team;                      // > 0: a cluster of that many CTAs per unit, joined in shared memory
   int by_unit;                   // 1: cuts is per unit, 0: per run
   int rowwise;                   // 1: a join CTA takes one row
   const __nv_bfloat16* q;

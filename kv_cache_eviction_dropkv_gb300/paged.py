@@ -94,12 +94,22 @@ class PagedCache:
             raise ValueError("layer %d of a cache with %d" % (layer, self.layers))
         return layer
 
+    def _call(self, name, stream, *args):
+        """The library's call `name` on the cache, on `stream` (None: the current one of its device)."""
+        if B.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self._call(name, stream, *args)
+        code = getattr(B.lib(), name)(self._shape_ref, self._buffers_ref, *args,
+                                      B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream))
+        if code != 0:
+            raise B.DropKVError(code, name)
+
     # -------------------------------------------------------------- a step
     def reserve(self, extra, seqs=None, stream=None):
         """Room for extra[i] more tokens of sequence seqs[i] (int32 [n]); their
         lengths grow.  All or nothing when pages run out."""
         n = extra.shape[0]
-        B.run_on(self._index, stream, B.kvcache_reserve, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n,
+        self._call("kvcache_reserve", stream, self._entries(seqs, n), n,
                   self._ints("extra", extra, n), self._ws, self._ws_bytes, self._status)
 
     def store(self, layer, k, v, counts=None, seqs=None, stream=None):
@@ -107,7 +117,7 @@ class PagedCache:
         become the last counts[i] tokens of sequence seqs[i] in `layer`."""
         n, _, rows, _ = k.shape
         want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
-        B.run_on(self._index, stream, B.kvcache_store, self._shape_ref, self._buffers_ref, self._layer(layer),
+        self._call("kvcache_store", stream, self._layer(layer),
                   self._entries(seqs, n), n, self._tensor("k", k, bf16, want), self._tensor("v", v, bf16, want), rows,
                   None if counts is None else self._ints("counts", counts, n), self._status)
 
@@ -123,7 +133,7 @@ class PagedCache:
         if T == 0 or n == 0:
             return
         want, bf16 = (n, Hq, T, self.d), torch.bfloat16
-        B.run_on(self._index, stream, B.kvcache_attention, self._shape_ref, self._buffers_ref, self._layer(layer),
+        self._call("kvcache_attention", stream, self._layer(layer),
                   self._entries(seqs, n), n, self._tensor("q", q, bf16, want), Hq, T, window, sinks,
                   self._tensor("out", out, bf16, want), self._ws, self._ws_bytes, self._status)
 
@@ -132,13 +142,13 @@ class PagedCache:
         """Empty sequences dst[i] become branches of src[i] (int32 [n]): full
         pages are shared, the partly filled last one is copied."""
         n = src.shape[0]
-        B.run_on(self._index, stream, B.kvcache_fork, self._shape_ref, self._buffers_ref, self._ints("src", src, n),
+        self._call("kvcache_fork", stream, self._ints("src", src, n),
                   self._ints("dst", dst, n), self._checked(n), 1, self._ws, self._ws_bytes, self._status)
 
     def copy(self, src, dst, stream=None):
         """Empty sequences dst[i] become copies of src[i] that share no page."""
         n = src.shape[0]
-        B.run_on(self._index, stream, B.kvcache_fork, self._shape_ref, self._buffers_ref, self._ints("src", src, n),
+        self._call("kvcache_fork", stream, self._ints("src", src, n),
                   self._ints("dst", dst, n), self._checked(n), 0, self._ws, self._ws_bytes, self._status)
 
     def _checked(self, n):
@@ -150,14 +160,14 @@ class PagedCache:
         kept_idx[layer, i, head, :kept_len[i]] (int32 [layers, n, Hkv, any])."""
         n = kept_len.shape[0]
         stride = kept_idx.shape[-1]
-        B.run_on(self._index, stream, B.kvcache_compact, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n,
+        self._call("kvcache_compact", stream, self._entries(seqs, n), n,
                   self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride), stride,
                   self._ints("kept_len", kept_len, n), self._ws, self._ws_bytes, self._status)
 
     def free(self, seqs, stream=None):
         """Release every page of sequences seqs (int32 [n])."""
         n = seqs.shape[0]
-        B.run_on(self._index, stream, B.kvcache_free, self._shape_ref, self._buffers_ref, self._entries(seqs, n), n, self._status)
+        self._call("kvcache_free", stream, self._entries(seqs, n), n, self._status)
 
     # -------------------------------------------------------------- status
     def check(self, stream=None):
