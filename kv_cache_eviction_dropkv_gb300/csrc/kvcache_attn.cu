@@ -73,7 +73,7 @@ constexpr int kMasked = 2;                  // some row does not see some of its
 constexpr int kUnreadable = 4;              // its table entry is no page
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
-constexpr int kJoinThreads = 128, kJoinWide = 512;
+constexpr int kJoinThreads = 128, kJoinWide = 512;   // 4 rows; 1 row
 constexpr int kTeamTiles = 8;               // most tiles a warp takes of a unit that has a team
 constexpr int kUnitCost = 3;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
@@ -786,10 +786,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
 // there are more units than runs), so nothing is searched for here.
 // ROWWISE: a CTA joins one row of a unit, its warps sharing out the pieces
 // with all loads in flight at once (few units, up to hundreds of pieces
-// each); else each warp joins rows of the unit on its own (few pieces each).
+// each); else each warp joins a row on its own (few pieces each).
 template <bool ROWWISE>
 __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kernel(const AttnCall p) {
-  constexpr int kW = (ROWWISE ? kJoinWide : kJoinThreads) / 32, kBatch = ROWWISE ? 10 : 4;
+  constexpr int kW = (ROWWISE ? kJoinWide : kJoinThreads) / 32, kBatch = ROWWISE ? 10 : 8;
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float4 s_o[kW][32];
@@ -841,7 +841,8 @@ __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kerne
     for (int k = 1; k < kW; ++k) join_in(a, s_m[k], s_l[k], s_M[k], s_o[k][lane]);
     write_row(p, b, h, rg * p.RB + rl, lane, a);
   } else {
-    for (int rl = warp; rl < rows; rl += kW) write_row(p, b, h, rg * p.RB + rl, lane, take(rl, 0, 1));
+    const int rl = blockIdx.y * kW + warp;
+    if (rl < rows) write_row(p, b, h, rg * p.RB + rl, lane, take(rl, 0, 1));
   }
 }
 
@@ -873,7 +874,8 @@ cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
   e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
   if (e != cudaSuccess) return e;
   if (p.rowwise) return launch_pdl(join_kernel<true>, dim3(units, std::min(p.RB, p.R)), dim3(kJoinWide), 0, st, p);
-  return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers), dim3(kJoinThreads), 0, st, p);
+  return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers, (std::min(p.RB, p.R) + 3) / 4),
+                    dim3(kJoinThreads), 0, st, p);
 }
 
 template <int CODE>
@@ -885,8 +887,6 @@ cudaError_t launch_code(const AttnCall& p, cudaStream_t st) {
   return NR == 1 ? launch_t<CODE, 64, 1, false>(p, st) : launch_t<CODE, 64, 2, false>(p, st);
 }
 
-// Query rows a warp holds (one or two MMA column blocks).
-int rows_per_warp(int R) { return R <= 8 ? 8 : 16; }
 // One wave: two CTAs of kWarps warps per SM.
 long long wave_of(int sms) { return (long long)sms * 2 * kWarps; }
 // The workspace: outputs of the pieces, their softmax states, who joins what.
@@ -897,20 +897,29 @@ size_t pieces_s(long long workers, int RB) { return ((size_t)workers * 2 * RB * 
 
 bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, int sinks, int sms, AttnPlan* a) {
   const long long R = (long long)Hq / s.Hkv * T;
-  a->RB = rows_per_warp((int)R);
-  a->RG = (int)((R + a->RB - 1) / a->RB);
   // most tiles a unit can have
   long long cap = ((long long)s.max_pages * s.page + kTok - 1) / kTok;
-  const long long units = (long long)n * s.Hkv * a->RG;   // with their row groups
-  if ((cap + kUnitCost) * s.Hkv * n >= (1LL << 31) || units * a->RB >= (1LL << 31)) return false;
+  if ((cap + kUnitCost) * s.Hkv * n >= (1LL << 31)) return false;
   if (window > 0)
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
+  // Rows a warp holds: 8, or 16 where there are more and each warp has many
+  // tiles (32 rows, 16 x 4000 tokens: 49.9 us against 63.7 with 8; 2 x 16000
+  // tokens, 3 tiles a warp: 18.8 against 16.7)
+  const long long pairs16 = (R + 15) / 16 * n * s.Hkv * cap;
+  a->RB = R > 8 && pairs16 >= 16 * wave_of(sms) ? 16 : 8;
+  a->RG = (int)((R + a->RB - 1) / a->RB);
+  const long long units = (long long)n * s.Hkv * a->RG;   // with their row groups
+  if (units * a->RB >= (1LL << 31)) return false;
   // Few units of moderate length: a cluster of 1 to 8 CTAs each, joined through
   // shared memory, no second kernel.  More CTAs while a warp has over 2 tiles
-  // and they fit one wave.
+  // and they fit one wave; two waves for units of at most 5 tiles a warp (64 x
+  // 300 tokens: 15.8 -> 14.6 us; 48 x 1000 tokens would lose, 26.8 -> 28.9).
   int team = 1;
   while (team < 8 && units * 2 * team <= 2LL * sms && cap > 2LL * kWarps * team) team *= 2;
-  a->team = units <= 2LL * sms && cap <= (long long)kTeamTiles * kWarps * team ? team : 0;
+  a->team = (units <= 2LL * sms && cap <= (long long)kTeamTiles * kWarps * team) ||
+                    (units <= 4LL * sms && cap <= 5 * kWarps)
+                ? team
+                : 0;
   a->workers = (int)(std::max(1LL, std::min(wave_of(sms) / a->RG, (long long)n * s.Hkv * cap)) * a->RG);
   // Joins: by row where the rows are fewer than the CTAs they can fill
   a->by_unit = units <= a->workers ? 1 : 0;
@@ -922,9 +931,13 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
 }
 
 size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms) {
-  const int RB = rows_per_warp((int)std::min<long long>(1 << 20, (long long)Hq / s.Hkv * T));
-  const long long w = std::max(wave_of(sms), ((long long)Hq / s.Hkv * T + RB - 1) / RB);
-  return pieces_o(w, RB, s.d) + pieces_s(w, RB) + (size_t)w * 8;
+  const long long R = (long long)Hq / s.Hkv * T;
+  size_t most = 0;
+  for (int RB = 8; RB <= 16; RB += 8) {
+    const long long w = std::max(wave_of(sms), (R + RB - 1) / RB);
+    most = std::max(most, pieces_o(w, RB, s.d) + pieces_s(w, RB) + (size_t)w * 8);
+  }
+  return most;
 }
 
 cudaError_t launch_attention(const AttnCall& p, cudaStream_t st) {

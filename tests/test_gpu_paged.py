@@ -321,6 +321,16 @@ def test_attention_matches_reference(code, Hq, Hkv, d, page, T, window, sinks, r
 
 
 @pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq,Hkv,d,page,T", [(7, 1, 96, 32, 2), (32, 2, 16, 64, 1), (3, 1, 8, 32, 9), (5, 1, 112, 64, 8),
+                                             (9, 1, 128, 128, 1), (12, 1, 64, 32, 5)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (37, 3)])
+def test_attention_with_room_for_long_sequences(code, Hq, Hkv, d, page, T, window, sinks):
+    """The same lengths in a cache whose sequences could be hundreds of times
+    longer: warps hold 16 rows."""
+    test_attention_matches_reference(code, Hq, Hkv, d, page, T, window, sinks, 800)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
 def test_attention_long_split_over_the_gpu(code):
     """Lengths that are cut into many pieces, and a ragged batch of them."""
     c, r = pair(seqs=3, Hkv=2, d=128, pages=220, page=64, max_pages=160, code=code, Hq=8, T=2, seed=1)
