@@ -20,6 +20,7 @@ namespace {
 using dropkv::grid_dep_launch;
 using dropkv::grid_dep_wait;
 using dropkv::launch_pdl;
+using dropkv::named_bar;
 
 constexpr int kBook = 1024;                // threads of a bookkeeping CTA
 constexpr int kBookWarps = kBook / 32;
@@ -388,10 +389,9 @@ __global__ void __launch_bounds__(kBook) fork_one_kernel(const PageCall p, int r
   __syncthreads();
   fork_move(p, row_pieces, chunks, threadIdx.x / kCopyTeam, kBook / kCopyTeam, threadIdx.x % kCopyTeam);
 }
-// Most bytes copied, and table entries, of the one-CTA form: it copies about
-// 100 KB while a second launch of the other takes its 3 us.
-constexpr double kOneBytes = 1.5e5;
-constexpr int kOneRows = 1024;
+// Most copies (page, layer, K or V, chunk) and table entries of the one-CTA
+// form: two rounds of its teams take as long as the second launch.
+constexpr int kOnePieces = 2 * kBook / kCopyTeam, kOneRows = 1024;
 
 __global__ void __launch_bounds__(kCopyTeam) fork_move_kernel(const PageCall p, int row_pieces, int chunks) {
   grid_dep_wait();
@@ -481,13 +481,13 @@ struct Gather {
   int4 entry[kSmall];
 };
 
-// CTA `team` of `teams` (kGatherTeam threads) fills one (new page, layer,
-// head) at a time: the kept positions give each row's source, then the first
+// Team `team` of `teams` (kGatherTeam threads, barrier `bar`) fills one (new
+// page, layer, head) at a time: the kept positions give each row's source, then the first
 // vectors of the rows and the scales are on their way together; the new scale
 // is the largest, and codes of other scales are rounded again.  Bound by the
 // chain position -> table -> row, so the CTAs are many and small.
 template <int VB, int CODE>
-__device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int team, int teams, int tid) {
+__device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int team, int teams, int tid, uint32_t bar) {
   using Vec = typename std::conditional<VB == 16, uint4, uint2>::type;
   constexpr int kBatch = 2;
   const Cache& c = p.c;
@@ -505,7 +505,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
     }
     offs = g.offs;
     entry = g.entry;
-    __syncthreads();
+    named_bar(bar, kGatherTeam);
   }
   const long long work = (long long)taken * c.layers * c.Hkv;
   for (long long w = team; w < work; w += teams) {
@@ -536,7 +536,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
       }
       g.row[tid] = row;
     }
-    __syncthreads();
+    named_bar(bar, kGatherTeam);
     const int vecs = rows * units;
     Vec val[kBatch][2];
     auto load = [&](int base) {
@@ -567,7 +567,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
       g.top[0][warp] = ks;
       g.top[1][warp] = vs;
     }
-    __syncthreads();
+    named_bar(bar, kGatherTeam);
     float top[2] = {kScaleMin, kScaleMin};
 #pragma unroll
     for (int q = 0; q < kGatherTeam / 32; ++q) {
@@ -601,7 +601,7 @@ __device__ __forceinline__ void compact_move(const PageCall& p, Gather& g, int t
         *reinterpret_cast<Vec*>(c.v + dst) = val[b][1];
       }
     }
-    __syncthreads();                        // the rows are rewritten next
+    named_bar(bar, kGatherTeam);                        // the rows are rewritten next
   }
 }
 
@@ -616,7 +616,21 @@ __global__ void __launch_bounds__(kGatherTeam, kGatherCtas) compact_move_kernel(
   __shared__ Gather g;
   grid_dep_wait();
   grid_dep_launch();
-  compact_move<VB, CODE>(p, g, blockIdx.x, gridDim.x, threadIdx.x);
+  compact_move<VB, CODE>(p, g, blockIdx.x, gridDim.x, threadIdx.x, 1);
+}
+// Both in one CTA, where no team has more than one to fill (1 x 100 tokens, 2
+// heads: a launch less, 16.8 -> 14.5 us with the fork and the free before it;
+// two each would lose).
+template <int VB, int CODE>
+__global__ void __launch_bounds__(kBook) compact_one_kernel(const PageCall p) {
+  __shared__ Names names;
+  __shared__ Gather g[kBook / kGatherTeam];
+  grid_dep_wait();
+  grid_dep_launch();
+  compact_book(p, names);
+  __syncthreads();
+  const int team = threadIdx.x / kGatherTeam;
+  compact_move<VB, CODE>(p, g[team], team, kBook / kGatherTeam, threadIdx.x % kGatherTeam, 1 + team);
 }
 __global__ void __launch_bounds__(kCopyTeam) compact_commit_kernel(const PageCall p, int row_pieces) {
   grid_dep_wait();
@@ -659,8 +673,8 @@ cudaError_t launch_fork(const PageCall& p, int sms, cudaStream_t st) {
   const Cache& c = p.c;
   const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
   const int chunks = (int)(((size_t)c.Hkv * c.page * c.d + kCopyChunk - 1) / kCopyChunk);
-  const double most = 2.0 * c.layers * c.Hkv * c.page * c.d * p.n * (p.share ? 1 : c.M);
-  if (most <= kOneBytes && (long long)p.n * c.M <= kOneRows)
+  const long long pages = (long long)p.n * (p.share ? 1 : c.M);   // that can be copied
+  if (pages * c.layers * 2 * chunks <= kOnePieces && (long long)p.n * c.M <= kOneRows)
     return launch_pdl(fork_one_kernel, dim3(1), dim3(kBook), 0, st, p, row_pieces, chunks);
   const cudaError_t e = launch_pdl(fork_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
@@ -670,15 +684,22 @@ cudaError_t launch_fork(const PageCall& p, int sms, cudaStream_t st) {
 cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
   const Cache& c = p.c;
   const int row_pieces = (c.M + kCopyTeam - 1) / kCopyTeam;
+  const bool int8 = c.code == KVCACHE_INT8;
+  // (new page, layer, head)s there can be
+  const long long most =
+      std::min<long long>(c.P, (long long)p.n * ((p.kept_stride + c.page - 1) / c.page)) * c.layers * c.Hkv;
+  if (most <= kBook / kGatherTeam && p.early) {
+    auto one = c.d % 16 == 0 ? (int8 ? compact_one_kernel<16, KVCACHE_INT8> : compact_one_kernel<16, KVCACHE_E4M3>)
+                             : (int8 ? compact_one_kernel<8, KVCACHE_INT8> : compact_one_kernel<8, KVCACHE_E4M3>);
+    return launch_pdl(one, dim3(1), dim3(kBook), 0, st, p);
+  }
   cudaError_t e = launch_pdl(compact_book_kernel, dim3(1), dim3(kBook), 0, st, p);
   if (e != cudaSuccess) return e;
-  const bool int8 = c.code == KVCACHE_INT8;
   auto move = c.d % 16 == 0 ? (int8 ? compact_move_kernel<16, KVCACHE_INT8> : compact_move_kernel<16, KVCACHE_E4M3>)
                             : (int8 ? compact_move_kernel<8, KVCACHE_INT8> : compact_move_kernel<8, KVCACHE_E4M3>);
   // a CTA for each (page, layer, head) there can be, up to kGatherWaves full
   // loads of the GPU: those with nothing to do leave at once, and the others
   // need not come out even over the resident CTAs
-  const long long most = std::min<long long>(c.P, (long long)p.n * ((p.kept_stride + c.page - 1) / c.page)) * c.layers * c.Hkv;
   const unsigned grid = (unsigned)std::max(1LL, std::min<long long>(most, (long long)sms * kGatherCtas * kGatherWaves));
   e = launch_pdl(move, dim3(grid), dim3(kGatherTeam), 0, st, p);
   if (e != cudaSuccess || p.early) return e;
