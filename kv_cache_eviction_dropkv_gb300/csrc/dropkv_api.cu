@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "dropkv_host.cuh"
 #include "dropkv_internal.cuh"
 
 namespace dropkv {

@@ -67,11 +67,6 @@ struct WsPlan {
   size_t total;
 };
 
-// Host helpers shared by the library's entry points.
-int current_sms(int* dev_out);   // SM count of the current device, -1 without one
-bool encode_rows(CUtensorMap* map, const void* base, int d, int n_max, int depth);
-bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb);
-
 bool make_geom(const dropkv_shape* s, int num_sms, Geom* g);
 WsPlan make_plan(const Geom& g);
 

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/kvcache.h"
+#include "dropkv_host.cuh"
 #include "dropkv_internal.cuh"
 
 namespace kvcache {
