@@ -110,7 +110,7 @@ class PagedCache:
         lengths grow.  All or nothing when pages run out."""
         n = extra.shape[0]
         self._call("kvcache_reserve", stream, self._entries(seqs, n), n,
-                  self._ints("extra", extra, n), self._ws, self._ws_bytes, self._status)
+                   self._ints("extra", extra, n), self._ws, self._ws_bytes, self._status)
 
     def store(self, layer, k, v, counts=None, seqs=None, stream=None):
         """Rows 0 .. counts[i] - 1 (default: all) of k, v [n, Hkv, rows, d] bf16
@@ -118,8 +118,8 @@ class PagedCache:
         n, _, rows, _ = k.shape
         want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
         self._call("kvcache_store", stream, self._layer(layer),
-                  self._entries(seqs, n), n, self._tensor("k", k, bf16, want), self._tensor("v", v, bf16, want), rows,
-                  None if counts is None else self._ints("counts", counts, n), self._status)
+                   self._entries(seqs, n), n, self._tensor("k", k, bf16, want), self._tensor("v", v, bf16, want), rows,
+                   None if counts is None else self._ints("counts", counts, n), self._status)
 
     def attention(self, layer, q, out, window: int = 0, sinks: int = 0, seqs=None, stream=None):
         """Attention of the last T tokens of each sequence, q [n, Hq, T, d] bf16,
@@ -132,10 +132,12 @@ class PagedCache:
                              % (self.Hq, self.T, Hq, T))
         if T == 0 or n == 0:
             return
+        if not (window < 1 << 31 and sinks < 1 << 31):   # (a negative one is refused by the library)
+            raise ValueError("window and sinks are 32-bit counts")
         want, bf16 = (n, Hq, T, self.d), torch.bfloat16
         self._call("kvcache_attention", stream, self._layer(layer),
-                  self._entries(seqs, n), n, self._tensor("q", q, bf16, want), Hq, T, window, sinks,
-                  self._tensor("out", out, bf16, want), self._ws, self._ws_bytes, self._status)
+                   self._entries(seqs, n), n, self._tensor("q", q, bf16, want), Hq, T, window, sinks,
+                   self._tensor("out", out, bf16, want), self._ws, self._ws_bytes, self._status)
 
     # -------------------------------------------------------------- whole sequences
     def fork(self, src, dst, stream=None):
@@ -143,13 +145,13 @@ class PagedCache:
         pages are shared, the partly filled last one is copied."""
         n = src.shape[0]
         self._call("kvcache_fork", stream, self._ints("src", src, n),
-                  self._ints("dst", dst, n), self._checked(n), 1, self._ws, self._ws_bytes, self._status)
+                   self._ints("dst", dst, n), self._checked(n), 1, self._ws, self._ws_bytes, self._status)
 
     def copy(self, src, dst, stream=None):
         """Empty sequences dst[i] become copies of src[i] that share no page."""
         n = src.shape[0]
         self._call("kvcache_fork", stream, self._ints("src", src, n),
-                  self._ints("dst", dst, n), self._checked(n), 0, self._ws, self._ws_bytes, self._status)
+                   self._ints("dst", dst, n), self._checked(n), 0, self._ws, self._ws_bytes, self._status)
 
     def _checked(self, n):
         self._entries(None, n)
@@ -161,8 +163,8 @@ class PagedCache:
         n = kept_len.shape[0]
         stride = kept_idx.shape[-1]
         self._call("kvcache_compact", stream, self._entries(seqs, n), n,
-                  self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride), stride,
-                  self._ints("kept_len", kept_len, n), self._ws, self._ws_bytes, self._status)
+                   self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride), stride,
+                   self._ints("kept_len", kept_len, n), self._ws, self._ws_bytes, self._status)
 
     def free(self, seqs, stream=None):
         """Release every page of sequences seqs (int32 [n])."""

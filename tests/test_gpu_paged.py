@@ -357,6 +357,51 @@ def test_attention_many_rows_per_head(Hq, Hkv, T, lengths, room):
     assert c.check() == 0
 
 
+def test_attention_runs_of_many_tiles():
+    """One sequence named 64 times: every warp walks over a hundred tiles and
+    crosses sequences; all copies get the reference's output, and the same bytes
+    whatever their place in the call but for where runs cut them."""
+    c, r = pair(seqs=64, Hkv=4, d=128, pages=170, page=128, max_pages=170, Hq=8, T=1, seed=2)
+    fill(c, r, [20001], spread=0.2)
+    q = draw_rows(1, 8, 1, 128, 4, spread=0.2)
+    one = check_attention(c, r, q, seqs=[0])
+    out = torch.zeros(64, 8, 1, 128, dtype=torch.bfloat16, device=DEV)
+    c.attention(0, q.to(DEV).expand(64, -1, -1, -1).contiguous(), out, seqs=ints([0] * 64))
+    # two orders of summation differ by at most a bf16 step and the bound's fp16 terms
+    far = (out.float() - one.float()).abs()
+    top = float(np.abs(r.values(0, 0, 0)[1]).max())
+    assert float(far.max()) <= 2.0 ** -7 * float(one.float().abs().max()) + 2.0 ** -9 * top
+    assert c.check() == 0
+
+
+def test_offsets_past_32_bits():
+    """A pool of 5 GiB of K codes: the same calls on pages behind the 4 GiB line
+    and on the first pages give the same bytes."""
+    P, page, H, d = 41000, 128, 8, 128
+    big = PagedCache(4, H, d, P, page, 8, Hq=16, T=1, device=DEV)
+    small = PagedCache(4, H, d, 40, page, 8, Hq=16, T=1, device=DEV)
+    big.refs[:P - 40] = 1                                  # the last 40 pages are free
+    rows = [draw_rows(2, H, 300, d, 5 + i).to(DEV) for i in range(2)]
+    q = draw_rows(3, 16, 1, d, 9).to(DEV)
+    idx = ints(np.sort(np.stack([np.random.default_rng(h).permutation(300)[:200] for h in range(H)]), -1)[None, None].tolist())
+    outs = []
+    for c in (big, small):
+        c.reserve(ints([300, 40]))
+        c.store(0, rows[0], rows[1], ints([300, 40]))
+        c.fork(ints([0]), ints([2]))
+        c.copy(ints([1]), ints([3]))
+        c.compact(idx, ints([200]), ints([2]))
+        out = torch.zeros_like(q)
+        c.attention(0, q, out, seqs=ints([0, 2, 3]))
+        assert c.check() == 0
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1])
+    assert torch.equal(torch.where(small.table >= 0, small.table + P - 40, small.table), big.table)
+    assert torch.equal(big.refs[P - 40:], small.refs)
+    for a, b in ((big.k, small.k), (big.v, small.v)):
+        assert torch.equal(a[:, P - 40:].view(torch.uint8), b.view(torch.uint8))
+
+
 def test_attention_many_sequences():
     n = 150
     lengths = [(i * 37) % 130 for i in range(n)]
@@ -428,6 +473,8 @@ def test_refusals_of_arguments():
         with pytest.raises(DropKVError) as e:
             PagedCache(**{**dict(seqs=3, Hkv=2, d=64, pages=12, device=DEV), **kw})
         assert e.value.code == 6
+    with pytest.raises(ValueError):
+        c.attention(0, q, out, window=1 << 32)
     c.attention(0, q[:0], out[:0])
     torch.cuda.synchronize()
     assert flags_of(c) == 0 and torch.all(out == 0)

@@ -90,6 +90,10 @@ def test_refusals_and_flags():
                  (q, k, v, torch.zeros(2, dtype=torch.int64, device=DEV), out, 5)):
         with pytest.raises(ValueError):
             op.window_attention(*args)
+    with pytest.raises(ValueError):
+        op.window_attention(q, k, v, None, out, 1 << 33)
+    op.window_attention(q, k, v, torch.zeros(2, dtype=torch.int32, device=DEV), out, 5)
+    assert B.kvcache_read_status(op.status) == (0, 0) and torch.all(out == 0)
     op.window_attention(q, k, v, torch.tensor([257, -1], dtype=torch.int32, device=DEV), out, 5)
     assert B.kvcache_read_status(op.status) == (7, B.FLAG_BAD_LENGTH)
     assert torch.all(out == 0)
