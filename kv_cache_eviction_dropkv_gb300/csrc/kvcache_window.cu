@@ -233,10 +233,16 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   // more by this group.
   auto release = [&](int j) {
     if (speaks) mbar_arrive(&S.empty[(pair0 + j) & 1]);
+    __syncwarp();
   };
   // The same for an entry this group does not take: only once it has landed,
   // so that the release counts for it and not for the pair before in its slot.
+  // The warp that releases is the only one to wait: once it has, the slot's
+  // next pair may land, and a warp that came to look only then would find the
+  // barrier one phase on, at the parity of the phase before, and wait for a
+  // pair that cannot come until its own P has.
   auto pass = [&](int j) {
+    if (quarter != 0) return true;
     if (!wait(&S.full[(pair0 + j) & 1], (pair0 + j) >> 1)) return false;
     release(j);
     return true;
@@ -324,6 +330,7 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
 #pragma unroll 1
     for (int c0 = 0; c0 < p.d; c0 += 32) {
       float o[32];
+      __syncwarp();                               // rows past the end stored nothing
       tmem_ld16(tO + c0, o);
       tmem_ld16(tO + c0 + 16, o + 16);
       tmem_wait_ld();

@@ -116,3 +116,25 @@ def test_window_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("lengths,window,sinks", [
+    ([128, 1, 257, 384, 640, 129, 100, 0, 896], 0, 0),      # odd counts of tiles: items of one query tile
+    ([128, 1, 257, 384, 640, 129, 100, 0, 896], 200, 5),
+    ([4096, 3968], 2048, 4), ([4096, 3968], 600, 200), ([4096, 3968], 0, 0)])
+def test_many_items_a_block_again_and_again(lengths, window, sinks):
+    """Blocks that walk many items one after another, pass upon pass: the same
+    bits each time and no wait given up.  (A warp that looked at a barrier two
+    phases late would wait for its own work.)"""
+    B_, n = len(lengths), max(lengths)
+    H = 160 if n < 1000 else 32
+    op = DropKV(B_, H, 4, 128, n, 1, out_rows=1, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k, v = (torch.randn(B_, h, n, 128, generator=g, device=DEV).bfloat16() for h in (H, 4, 4))
+    lens = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    want, out = torch.zeros_like(q), torch.zeros_like(q)
+    op.window_attention(q, k, v, lens, want, window, sinks)
+    for _ in range(20):
+        op.window_attention(q, k, v, lens, out, window, sinks)
+        assert torch.equal(out, want)
+    assert op.check() == 0
