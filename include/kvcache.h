@@ -181,6 +181,37 @@ DROPKV_API dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t
                                                   const int32_t* lengths, int32_t window, int32_t sinks,
                                                   void* attn_out, uint32_t* status, cudaStream_t stream);
 
+/* One of the cache's calls above as a record, for bindings that pay for every
+ * argument they pass: kvcache_run makes the call that `op` names with the
+ * fields that stand beside it and ignores the others.
+ *   op                 in[0]     in[1]     in[2]   out  arg
+ *   KVCACHE_RESERVE    extra
+ *   KVCACHE_STORE      k         v         counts       rows
+ *   KVCACHE_ATTENTION  q                           out  Hq, T, window, sinks
+ *   KVCACHE_FORK       dst                              share    (seqs: src)
+ *   KVCACHE_COMPACT    kept_idx  kept_len               kept_stride
+ *   KVCACHE_FREE */
+#define KVCACHE_RESERVE   0
+#define KVCACHE_STORE     1
+#define KVCACHE_ATTENTION 2
+#define KVCACHE_FORK      3
+#define KVCACHE_COMPACT   4
+#define KVCACHE_FREE      5
+typedef struct {
+  const kvcache_shape* shape;
+  const kvcache_buffers* cache;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* status;
+  cudaStream_t stream;
+  const int32_t* seqs;
+  const void* in[3];
+  void* out;
+  int32_t op, layer, n;
+  int32_t arg[4];
+} kvcache_call;
+DROPKV_API dropkv_status kvcache_run(const kvcache_call* call);
+
 /* dropkv_read_status with this header's flags as well (they map to
  * DROPKV_ERR_DEVICE_ARG). */
 DROPKV_API dropkv_status kvcache_read_status(const uint32_t* status, cudaStream_t stream, uint32_t* flags_out);

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -102,6 +103,7 @@ def _load(path):
             ("kvcache_fork", [CS, CB, P, P, I32, I32, P, SZ, P, P]),
             ("kvcache_compact", [CS, CB, P, I32, P, I32, P, P, SZ, P, P]),
             ("kvcache_free", [CS, CB, P, I32, P, P]),
+            ("kvcache_run", [ctypes.c_char_p]),
             ("kvcache_window_attention", [I32, I32, I32, I32, I32, P, P, P, P, I32, I32, P, P, P]),
             ("kvcache_read_status", [P, P, ctypes.POINTER(ctypes.c_uint32)])):
         getattr(L, name).argtypes = args
@@ -119,9 +121,10 @@ def lib():
     global _lib
     if _active is not None:
         return _active
-    with _lock:
-        if _lib is None:
-            _lib = _load(_build.LIB_PATH)
+    if _lib is None:
+        with _lock:
+            if _lib is None:
+                _lib = _load(_build.LIB_PATH)
     return _lib
 
 
@@ -303,10 +306,14 @@ def dropkv_version() -> str:
 
 # ------------------------------------------------------------------ include/kvcache.h
 # Small calls (one new token) cost a few microseconds, so these go with raw
-# addresses and streams, and as few layers as can be: the cache's own calls are
-# made by PagedCache through lib() directly.  Plain lookups of the current
-# stream's handle and the current device: building a Stream object would add
-# two microseconds.
+# addresses and streams, and as few layers as can be: PagedCache packs a
+# kvcache_call record and makes its calls through lib() directly (an argument
+# that ctypes converts costs 0.1 us, the whole record 0.2).  Plain lookups of
+# the current stream's handle and the current device: building a Stream object
+# would add two microseconds.
+kvcache_call = struct.Struct("@PPPNPPPPPPP7i0P")   # the fields of the record, in order
+RESERVE, STORE, ATTENTION, FORK, COMPACT, FREE = range(6)
+CACHE_CALLS = tuple("kvcache_" + name for name in ("reserve", "store", "attention", "fork", "compact", "free"))
 current_raw_stream, current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 

@@ -91,7 +91,7 @@ class DropKV:
         tokens kept visible (kvcache_window_attention): row i sees keys j <= i
         with j > i - window or j < sinks; window 0 is prefill_attention's mask.
         The positional baseline next to the scored evictions."""
-        if not (window < 1 << 31 and sinks < 1 << 31):   # (a negative one is refused by the library)
+        if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):   # (the library refuses negative ones)
             raise ValueError("window and sinks are 32-bit counts")
         s, dev = self.shape, self.status.device
         rows, kv = (s.B, s.Hq, s.n_max, s.d), (s.B, s.Hkv, s.n_max, s.d)

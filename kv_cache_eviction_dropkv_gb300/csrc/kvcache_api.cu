@@ -220,6 +220,32 @@ dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32
   return launched(launch_window(p, tq, tk, tv, sms, stream));
 }
 
+dropkv_status kvcache_run(const kvcache_call* c) {
+  if (!c) return DROPKV_ERR_INVALID_ARG;
+  const int32_t* in0 = static_cast<const int32_t*>(c->in[0]);
+  switch (c->op) {
+    case KVCACHE_RESERVE:
+      return kvcache_reserve(c->shape, c->cache, c->seqs, c->n, in0, c->workspace, c->workspace_bytes, c->status,
+                             c->stream);
+    case KVCACHE_STORE:
+      return kvcache_store(c->shape, c->cache, c->layer, c->seqs, c->n, c->in[0], c->in[1], c->arg[0],
+                           static_cast<const int32_t*>(c->in[2]), c->status, c->stream);
+    case KVCACHE_ATTENTION:
+      return kvcache_attention(c->shape, c->cache, c->layer, c->seqs, c->n, c->in[0], c->arg[0], c->arg[1], c->arg[2],
+                               c->arg[3], c->out, c->workspace, c->workspace_bytes, c->status, c->stream);
+    case KVCACHE_FORK:
+      return kvcache_fork(c->shape, c->cache, c->seqs, in0, c->n, c->arg[0], c->workspace, c->workspace_bytes,
+                          c->status, c->stream);
+    case KVCACHE_COMPACT:
+      return kvcache_compact(c->shape, c->cache, c->seqs, c->n, in0, c->arg[0],
+                             static_cast<const int32_t*>(c->in[1]), c->workspace, c->workspace_bytes, c->status,
+                             c->stream);
+    case KVCACHE_FREE:
+      return kvcache_free(c->shape, c->cache, c->seqs, c->n, c->status, c->stream);
+    default: return DROPKV_ERR_INVALID_ARG;
+  }
+}
+
 dropkv_status kvcache_read_status(const uint32_t* status, cudaStream_t stream, uint32_t* flags_out) {
   uint32_t f = 0;
   const dropkv_status st = dropkv_read_status(status, stream, &f);

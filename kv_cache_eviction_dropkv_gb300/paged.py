@@ -69,13 +69,13 @@ class PagedCache:
         self._index = self.device.index
         self._buffers = B.kvcache_buffers(*(t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.refs,
                                                                     self.table, self.count, self.length)))
-        self._shape_ref, self._buffers_ref = ctypes.byref(self.shape), ctypes.byref(self._buffers)
-        self._status, self._ws, self._ws_bytes = self.status.data_ptr(), self.workspace.data_ptr(), ws
+        self._fixed = (ctypes.addressof(self.shape), ctypes.addressof(self._buffers), self.workspace.data_ptr(), ws,
+                       self.status.data_ptr())
 
     # -------------------------------------------------------------- arguments
     def _tensor(self, name, t, dtype, shape):
         """Address of a contiguous device tensor of that type and shape."""
-        if t.dtype is not dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise ValueError("%s: expected a contiguous %s %s tensor on %s, got %s %s on %s"
                              % (name, dtype, list(shape), self.device, t.dtype, list(t.shape), t.device))
         return t.data_ptr()
@@ -87,39 +87,39 @@ class PagedCache:
         """Address of the sequence numbers of a call with n entries (None: 0 .. n - 1)."""
         if n > self.seqs:
             raise ValueError("%d entries, but the cache has %d sequences" % (n, self.seqs))
-        return None if seqs is None else self._tensor("seqs", seqs, torch.int32, (n,))
+        return 0 if seqs is None else self._tensor("seqs", seqs, torch.int32, (n,))
 
     def _layer(self, layer):
         if not 0 <= layer < self.layers:
             raise ValueError("layer %d of a cache with %d" % (layer, self.layers))
         return layer
 
-    def _call(self, name, stream, *args):
-        """The library's call `name` on the cache, on `stream` (None: the current one of its device)."""
+    def _call(self, op, stream, n, seqs=0, in0=0, in1=0, in2=0, out=0, layer=0, arg0=0, arg1=0, arg2=0, arg3=0):
+        """The library's call `op` on the cache, on `stream` (None: the current one of its device)."""
         if B.current_device() != self._index:
             with torch.cuda.device(self.device):
-                return self._call(name, stream, *args)
-        code = getattr(B.lib(), name)(self._shape_ref, self._buffers_ref, *args,
-                                      B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream))
+                return self._call(op, stream, n, seqs, in0, in1, in2, out, layer, arg0, arg1, arg2, arg3)
+        code = B.lib().kvcache_run(B.kvcache_call.pack(
+            *self._fixed, B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream),
+            seqs, in0, in1, in2, out, op, layer, n, arg0, arg1, arg2, arg3))
         if code != 0:
-            raise B.DropKVError(code, name)
+            raise B.DropKVError(code, B.CACHE_CALLS[op])
 
     # -------------------------------------------------------------- a step
     def reserve(self, extra, seqs=None, stream=None):
         """Room for extra[i] more tokens of sequence seqs[i] (int32 [n]); their
         lengths grow.  All or nothing when pages run out."""
         n = extra.shape[0]
-        self._call("kvcache_reserve", stream, self._entries(seqs, n), n,
-                   self._ints("extra", extra, n), self._ws, self._ws_bytes, self._status)
+        self._call(B.RESERVE, stream, n, self._entries(seqs, n), self._ints("extra", extra, n))
 
     def store(self, layer, k, v, counts=None, seqs=None, stream=None):
         """Rows 0 .. counts[i] - 1 (default: all) of k, v [n, Hkv, rows, d] bf16
         become the last counts[i] tokens of sequence seqs[i] in `layer`."""
         n, _, rows, _ = k.shape
         want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
-        self._call("kvcache_store", stream, self._layer(layer),
-                   self._entries(seqs, n), n, self._tensor("k", k, bf16, want), self._tensor("v", v, bf16, want), rows,
-                   None if counts is None else self._ints("counts", counts, n), self._status)
+        self._call(B.STORE, stream, n, self._entries(seqs, n), self._tensor("k", k, bf16, want),
+                   self._tensor("v", v, bf16, want), 0 if counts is None else self._ints("counts", counts, n), 0,
+                   self._layer(layer), rows)
 
     def attention(self, layer, q, out, window: int = 0, sinks: int = 0, seqs=None, stream=None):
         """Attention of the last T tokens of each sequence, q [n, Hq, T, d] bf16,
@@ -132,44 +132,40 @@ class PagedCache:
                              % (self.Hq, self.T, Hq, T))
         if T == 0 or n == 0:
             return
-        if not (window < 1 << 31 and sinks < 1 << 31):   # (a negative one is refused by the library)
+        if not (-1 << 31 <= window < 1 << 31 and -1 << 31 <= sinks < 1 << 31):   # (the library refuses negative ones)
             raise ValueError("window and sinks are 32-bit counts")
         want, bf16 = (n, Hq, T, self.d), torch.bfloat16
-        self._call("kvcache_attention", stream, self._layer(layer),
-                   self._entries(seqs, n), n, self._tensor("q", q, bf16, want), Hq, T, window, sinks,
-                   self._tensor("out", out, bf16, want), self._ws, self._ws_bytes, self._status)
+        self._call(B.ATTENTION, stream, n, self._entries(seqs, n), self._tensor("q", q, bf16, want), 0, 0,
+                   self._tensor("out", out, bf16, want), self._layer(layer), Hq, T, window, sinks)
 
     # -------------------------------------------------------------- whole sequences
     def fork(self, src, dst, stream=None):
         """Empty sequences dst[i] become branches of src[i] (int32 [n]): full
         pages are shared, the partly filled last one is copied."""
-        n = src.shape[0]
-        self._call("kvcache_fork", stream, self._ints("src", src, n),
-                   self._ints("dst", dst, n), self._checked(n), 1, self._ws, self._ws_bytes, self._status)
+        self._branch(src, dst, 1, stream)
 
     def copy(self, src, dst, stream=None):
         """Empty sequences dst[i] become copies of src[i] that share no page."""
-        n = src.shape[0]
-        self._call("kvcache_fork", stream, self._ints("src", src, n),
-                   self._ints("dst", dst, n), self._checked(n), 0, self._ws, self._ws_bytes, self._status)
+        self._branch(src, dst, 0, stream)
 
-    def _checked(self, n):
+    def _branch(self, src, dst, share, stream):
+        n = src.shape[0]
         self._entries(None, n)
-        return n
+        self._call(B.FORK, stream, n, self._ints("src", src, n), self._ints("dst", dst, n), arg0=share)
 
     def compact(self, kept_idx, kept_len, seqs=None, stream=None):
         """Evict: sequence seqs[i] keeps the kept_len[i] tokens at positions
         kept_idx[layer, i, head, :kept_len[i]] (int32 [layers, n, Hkv, any])."""
         n = kept_len.shape[0]
         stride = kept_idx.shape[-1]
-        self._call("kvcache_compact", stream, self._entries(seqs, n), n,
-                   self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride), stride,
-                   self._ints("kept_len", kept_len, n), self._ws, self._ws_bytes, self._status)
+        self._call(B.COMPACT, stream, n, self._entries(seqs, n),
+                   self._ints("kept_idx", kept_idx, self.layers, n, self.Hkv, stride),
+                   self._ints("kept_len", kept_len, n), arg0=stride)
 
     def free(self, seqs, stream=None):
         """Release every page of sequences seqs (int32 [n])."""
         n = seqs.shape[0]
-        self._call("kvcache_free", stream, self._entries(seqs, n), n, self._status)
+        self._call(B.FREE, stream, n, self._entries(seqs, n))
 
     # -------------------------------------------------------------- status
     def check(self, stream=None):

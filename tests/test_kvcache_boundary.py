@@ -38,10 +38,47 @@ def calls(s, b, n=2, layer=0, ws=A, wsb=1 << 30, status=A):
             L.kvcache_free(S, C, A, n, status, None)]
 
 
+def recorded(s, b, n=2, layer=0, ws=A, wsb=1 << 30, status=A):
+    """The same calls through kvcache_run."""
+    rec = lambda op, seqs, *rest: B.lib().kvcache_run(B.kvcache_call.pack(
+        ctypes.addressof(s), ctypes.addressof(b), ws or 0, wsb, status or 0, 0, seqs, *rest[:4], op, layer, n, *rest[4:]))
+    return [rec(B.RESERVE, 0, A, 0, 0, 0, 0, 0, 0, 0),
+            rec(B.STORE, 0, A, A, 0, 0, 3, 0, 0, 0),
+            rec(B.ATTENTION, 0, A, 0, 0, A + (1 << 20), 4, 1, 0, 0),
+            rec(B.FORK, A, A, 0, 0, 0, 1, 0, 0, 0),
+            rec(B.COMPACT, 0, A, A, 0, 0, 8, 0, 0, 0),
+            rec(B.FREE, A, 0, 0, 0, 0, 0, 0, 0, 0)]
+
+
+def test_records_make_the_same_calls():
+    assert B.kvcache_call.size == 120
+    s, b = shape(), buffers()
+    for kw in (dict(n=0), dict(n=5), dict(n=-1), dict(layer=2, n=0), dict(wsb=64), dict(ws=None), dict(status=None)):
+        if kw in (dict(wsb=64), dict(ws=None)):       # (the calls without a workspace would launch)
+            got, want = recorded(s, b, n=0, **kw), calls(s, b, n=0, **kw)
+        else:
+            got, want = recorded(s, b, **kw), calls(s, b, **kw)
+        assert got == want, kw
+    rec = [ctypes.addressof(s), ctypes.addressof(b), A, 1 << 30, A, 0, 0, A, A, A, A + (1 << 20), 0, 0, 0, 4, 1, 0, 0]
+    for op in (-1, 6):
+        rec[11] = op
+        assert B.lib().kvcache_run(B.kvcache_call.pack(*rec)) == INVALID
+    assert B.lib().kvcache_run(None) == INVALID
+    # arguments that are the call's own, each refused by the same call
+    run = lambda op, in0, in1, in2, out, *arg: B.lib().kvcache_run(B.kvcache_call.pack(
+        *rec[:7], in0, in1, in2, out, op, 0, 0, *arg))
+    assert run(B.STORE, A, A, 0, 0, -1, 0, 0, 0) == INVALID and run(B.STORE, A, 0, 0, 0, 1, 0, 0, 0) == INVALID
+    assert run(B.ATTENTION, A, 0, 0, A, 3, 1, 0, 0) == INVALID and run(B.ATTENTION, A, 0, 0, A, 4, 1, -1, 0) == INVALID
+    assert run(B.ATTENTION, A, 0, 0, A, 4, 1, 0, -1) == INVALID and run(B.ATTENTION, A, 0, 0, A, 4, 0, 0, 0) == INVALID
+    assert run(B.FORK, A, 0, 0, 0, 1, 0, 0, 0) == INVALID            # no sources
+    assert run(B.COMPACT, A, 0, 0, 0, 1, 0, 0, 0) == INVALID and run(B.COMPACT, A, A, 0, 0, -1, 0, 0, 0) == INVALID
+    assert run(B.RESERVE, 0, 0, 0, 0, 0, 0, 0, 0) == INVALID
+
+
 def test_every_declared_symbol_is_exported_and_bound():
     lib = B.lib()
     names = B.declared_functions(_build.INCLUDE + "/kvcache.h")
-    assert len(names) == 9
+    assert len(names) == 10
     for name in names:
         assert hasattr(lib, name), name
         assert getattr(lib, name).argtypes is not None, name
