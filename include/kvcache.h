@@ -128,7 +128,9 @@ DROPKV_API dropkv_status kvcache_store(const kvcache_shape* shape, const kvcache
  * Numerics: codes and query rows enter the tensor cores as fp16 (each query
  * row scaled by a power of two first; both exact but for query elements 2^-29
  * below their row's largest), probabilities as fp16, sums and softmax
- * statistics are fp32.  Slots that no row sees are never read.  An e4m3
+ * statistics are fp32.  Queries must be finite and logits within fp32's
+ * range; anything else gives its own rows undefined values.  Slots that no row
+ * sees are never read.  An e4m3
  * not-a-number code that one row sees makes every row of its KV head
  * not-a-number. */
 DROPKV_API dropkv_status kvcache_attention(const kvcache_shape* shape, const kvcache_buffers* cache, int32_t layer,
@@ -148,6 +150,7 @@ DROPKV_API dropkv_status kvcache_fork(const kvcache_shape* shape, const kvcache_
  * becomes token m of layer l and head h.
  *   kept_idx  device int32 [layers][n][Hkv][kept_stride] (dropkv_select's
  *             kept_idx per layer), any positions < length, in any order
+ *             (may be NULL when kept_stride is 0)
  *   kept_len  device int32 [n], 0 <= kept_len[i] <= length and kept_stride
  * The kept tokens move to new pages and the old ones are released, so a
  * branch that shares pages is evicted alone; while the call runs both are

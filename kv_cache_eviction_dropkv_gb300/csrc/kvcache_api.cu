@@ -166,7 +166,7 @@ dropkv_status kvcache_compact(const kvcache_shape* shape, const kvcache_buffers*
   PageCall p{};
   const dropkv_status st = open_pages(shape, cache, n, workspace, workspace_bytes, status, &p);
   if (st != DROPKV_OK) return st;
-  if (!kept_idx || !kept_len || kept_stride < 0) return DROPKV_ERR_INVALID_ARG;
+  if ((!kept_idx && kept_stride > 0) || !kept_len || kept_stride < 0) return DROPKV_ERR_INVALID_ARG;
   if (n == 0) return DROPKV_OK;
   p.seqs = seqs;
   p.kept_idx = kept_idx;

@@ -96,6 +96,8 @@ class PagedCache:
 
     def _call(self, op, stream, n, seqs=0, in0=0, in1=0, in2=0, out=0, layer=0, arg0=0, arg1=0, arg2=0, arg3=0):
         """The library's call `op` on the cache, on `stream` (None: the current one of its device)."""
+        if n == 0:                                # (an empty tensor has no address)
+            return
         if B.current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self._call(op, stream, n, seqs, in0, in1, in2, out, layer, arg0, arg1, arg2, arg3)
@@ -117,7 +119,7 @@ class PagedCache:
         become the last counts[i] tokens of sequence seqs[i] in `layer`."""
         n, _, rows, _ = k.shape
         want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
-        self._call(B.STORE, stream, n, self._entries(seqs, n), self._tensor("k", k, bf16, want),
+        self._call(B.STORE, stream, n if rows else 0, self._entries(seqs, n), self._tensor("k", k, bf16, want),
                    self._tensor("v", v, bf16, want), 0 if counts is None else self._ints("counts", counts, n), 0,
                    self._layer(layer), rows)
 

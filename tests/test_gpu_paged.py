@@ -475,9 +475,33 @@ def test_refusals_of_arguments():
         assert e.value.code == 6
     with pytest.raises(ValueError):
         c.attention(0, q, out, window=1 << 32)
+    with pytest.raises(ValueError):
+        c.attention(0, q, out, window=-(1 << 32) + 5)
     c.attention(0, q[:0], out[:0])
     torch.cuda.synchronize()
     assert flags_of(c) == 0 and torch.all(out == 0)
+
+
+def test_calls_with_nothing_to_do():
+    """No entries, no rows, nothing kept: empty tensors have no address."""
+    c, r = pair(seqs=3, max_pages=4, Hq=2)
+    both(c, r, "reserve", [40, 0, 64])
+    k = draw_rows(3, 2, 64, 64, 1)
+    both(c, r, "store", 0, k, k, [40, 0, 64])
+    none = ints([])
+    c.reserve(none, seqs=none)
+    c.store(0, k[:0].to(DEV), k[:0].to(DEV))
+    c.store(0, k[:, :, :0].to(DEV), k[:, :, :0].to(DEV))
+    c.fork(none, none)
+    c.copy(none, none)
+    c.compact(torch.zeros(1, 0, 2, 4, dtype=torch.int32, device=DEV), none)
+    c.free(none)
+    same_state(c, r)
+    same_pool(c, r)
+    c.compact(torch.zeros(1, 2, 2, 0, dtype=torch.int32, device=DEV), ints([0, 0]), seqs=ints([0, 1]))   # keeps nothing
+    assert c.length.tolist() == [0, 0, 64] and c.count.tolist() == [0, 0, 2] and sum(c.refs.tolist()) == 2
+    c.compact(torch.zeros(1, 1, 2, 0, dtype=torch.int32, device=DEV), ints([1]), seqs=ints([2]))          # keeps more
+    assert flags_of(c) == B.FLAG_BAD_K and c.length.tolist() == [0, 0, 64]
 
 
 def test_streams_graphs_and_repeats_give_the_same_bytes():
