@@ -209,7 +209,7 @@ __device__ __forceinline__ void softmax_tile(const WindowCall& p, uint32_t tS, b
   if (!SPLIT && __any_sync(0xffffffffu, need)) follow(factor);
 }
 
-template <bool SPLIT>
+template <bool SPLIT, int DS>
 __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem, int warp,
                                               int lane) {
   const int g = warp >> 2, quarter = warp & 3;
@@ -281,7 +281,7 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(vrow + kHalfB + c * 16) = make_uint4(0, 0, 0, 0);
+            if (DS > 4) *reinterpret_cast<uint4*>(vrow + kHalfB + c * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
@@ -304,7 +304,7 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
             // signalled came after it): O follows the reference
             if (first) return;
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < DS; ++c) {
               float o[16];
               tmem_ld16(tO + 16 * c, o);
               tmem_wait_ld();
@@ -356,10 +356,18 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
 // S that bounds the kernel (32768 tokens, window 4096: 1.45 -> 1.36 ms); with
 // few, most of them masked, the extra barrier costs more (2051 tokens, window
 // 333: 60 -> 65 us).
-template <bool SPLIT>
+//
+// DS: steps of 16 channels, 4, 6 or 8.  A head of up to 64 channels takes one
+// block of 64 columns of Q, K and V, and N = 64 in P V; up to 96 takes six
+// steps for S (P V stays at N = 128: V's columns come in swizzled blocks of
+// 64).  Against eight steps for all: d 64, 8192 tokens, window 2048 197 -> 179
+// us, d 96 202 -> 196; a ragged batch of short prompts 54.7 -> 48.8 and 58.1
+// -> 56.8.
+template <bool SPLIT, int DS>
 __global__ void __launch_bounds__(kWinThreads, 1)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const WindowCall p) {
+  constexpr int kLoadB = DS <= 4 ? kHalfB : kTileB;   // bytes of a tile that are loaded
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Small& S = *reinterpret_cast<Small*>(sm + kOffSmall);
@@ -393,16 +401,16 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       auto put = [&](int k_tile, int k_unit) {    // k_tile -1: the last V alone
         const uint32_t slot = pair & 1;
         if (pair >= 2 && !mbar_wait(&S.empty[slot], ((pair >> 1) + 1) & 1, &S.abort)) return false;
-        mbar_arrive_expect_tx(&S.full[slot], (k_tile >= 0 ? kTileB : 0) + (v_tile >= 0 ? kTileB : 0));
+        mbar_arrive_expect_tx(&S.full[slot], (k_tile >= 0 ? kLoadB : 0) + (v_tile >= 0 ? kLoadB : 0));
         if (v_tile >= 0) {                        // needed first
           uint8_t* dst = sm + kOffV + slot * kTileB;
           tma_load_3d(dst, &tmv, &S.full[slot], 0, v_tile * kQT, v_unit);
-          tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, v_tile * kQT, v_unit);
+          if (DS > 4) tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, v_tile * kQT, v_unit);
         }
         if (k_tile >= 0) {
           uint8_t* dst = sm + kOffK + slot * kTileB;
           tma_load_3d(dst, &tmk, &S.full[slot], 0, k_tile * kQT, k_unit);
-          tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, k_tile * kQT, k_unit);
+          if (DS > 4) tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, k_tile * kQT, k_unit);
         }
         v_tile = k_tile;
         v_unit = k_unit;
@@ -419,9 +427,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         for (int g = 0; ok && g < 2; ++g) {
           if (list.t[g] < 0) continue;
           if (used[g] > 0 && !(ok = mbar_wait(&S.qempty[g], (used[g] - 1) & 1, &S.abort))) break;
-          mbar_arrive_expect_tx(&S.qfull[g], kTileB);
+          mbar_arrive_expect_tx(&S.qfull[g], kLoadB);
           tma_load_3d(sm + kOffQ + g * kTileB, &tmq, &S.qfull[g], 0, list.t[g] * kQT, zq);
-          tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qfull[g], 64, list.t[g] * kQT, zq);
+          if (DS > 4) tma_load_3d(sm + kOffQ + g * kTileB + kHalfB, &tmq, &S.qfull[g], 64, list.t[g] * kQT, zq);
           ++used[g];
         }
         for (int j = 1; ok && j < list.n; ++j) ok = put(list.tile(j), unit);
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     const uint64_t qd = desc_kmajor_sw128(smem_addr(sm + kOffQ), kQT, 0);
     const uint64_t kd = desc_kmajor_sw128(smem_addr(sm + kOffK), kQT, 0);
     const uint64_t vd = desc_mnmajor_sw128(smem_addr(sm + kOffV), kQT, 0);
-    constexpr uint32_t idO = umma_idesc_bf16(128, 128, 0, 1);
+    constexpr uint32_t idO = umma_idesc_bf16(128, DS <= 4 ? 64 : 128, 0, 1);
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort)) != 0;
     };
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       const uint64_t qg = qd + ((g * kTileB) >> 4), kg = kd + ((slot * kTileB) >> 4);
       if (leader) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
+        for (int s = 0; s < DS; ++s) {
           const uint64_t at = ((s >> 2) * kHalfB + (s & 3) * 32) >> 4;   // as desc_kmajor_sw128 steps
           umma_bf16(128 * g, qg + at, kg + at, id, s > 0);
         }
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     }
     __syncwarp();
   } else if (warp < 8) {
-    softmax_group<SPLIT>(p, S, sm, tmem, warp, lane);
+    softmax_group<SPLIT, DS>(p, S, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -576,16 +584,28 @@ __global__ void __launch_bounds__(kWinThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int sms, cudaStream_t st) {
-  const bool split = p.window == 0 || p.window >= kSplitWindow;
-  const cudaError_t e = split ? allow_smem<window_prefill_kernel<true>>(kWinSmem)
-                              : allow_smem<window_prefill_kernel<false>>(kWinSmem);
+namespace {
+template <bool SPLIT, int DS>
+cudaError_t launch(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int sms,
+                   cudaStream_t st) {
+  const cudaError_t e = allow_smem<window_prefill_kernel<SPLIT, DS>>(kWinSmem);
   if (e != cudaSuccess) return e;
   const long long most = (long long)((p.n_max + 2 * kQT - 1) / (2 * kQT)) * p.Hq * p.B;
   const dim3 grid((unsigned)std::min<long long>(most, sms));
-  return launch_pdl(split ? window_prefill_kernel<true> : window_prefill_kernel<false>, grid, dim3(kWinThreads),
-                    kWinSmem, st, tq, tk, tv, p);
+  return launch_pdl(window_prefill_kernel<SPLIT, DS>, grid, dim3(kWinThreads), kWinSmem, st, tq, tk, tv, p);
+}
+}  // namespace
+
+cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int sms, cudaStream_t st) {
+  const bool split = p.window == 0 || p.window >= kSplitWindow;
+  auto pick = [&](auto wide) {
+    constexpr int DS = decltype(wide)::value;
+    return split ? launch<true, DS>(p, tq, tk, tv, sms, st) : launch<false, DS>(p, tq, tk, tv, sms, st);
+  };
+  if (p.d <= 64) return pick(std::integral_constant<int, 4>{});
+  if (p.d <= 96) return pick(std::integral_constant<int, 6>{});
+  return pick(std::integral_constant<int, 8>{});
 }
 
 }  // namespace kvcache
