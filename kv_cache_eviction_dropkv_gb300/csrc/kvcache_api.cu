@@ -60,6 +60,7 @@ dropkv_status open_pages(const kvcache_shape* s, const kvcache_buffers* b, int32
   p->n = n;
   p->claim = reinterpret_cast<int32_t*>(ws + w.claim);
   p->mark = reinterpret_cast<int32_t*>(ws + w.mark);
+  p->from = reinterpret_cast<int32_t*>(ws + w.from);
   p->offs = reinterpret_cast<int32_t*>(ws + w.offs);
   p->entry = reinterpret_cast<int4*>(ws + w.entry);
   p->list = reinterpret_cast<int32_t*>(ws + w.list);

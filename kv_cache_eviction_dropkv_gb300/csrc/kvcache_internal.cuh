@@ -36,6 +36,7 @@ struct Cache {
 struct PagePlan {
   size_t claim;                  // [S] lowest call index that names the sequence
   size_t mark;                   // [S] 1: the sequence is a source of this fork
+  size_t from;                   // [S] fork, shared: the page that copy k is made of
   size_t offs;                   // [S + 1] pages taken by entries before i
   size_t entry;                  // [S][4] per entry: what the second kernel needs
   size_t list;                   // [P] pages taken, in order
@@ -52,7 +53,7 @@ struct PageCall {
   const int32_t* extra;          // reserve
   const int32_t *kept_idx, *kept_len;
   int kept_stride, share;
-  int32_t *claim, *mark, *offs, *list, *rows;
+  int32_t *claim, *mark, *from, *offs, *list, *rows;
   int4* entry;
   int early;                     // compact: the bookkeeping rewrites the tables
 };

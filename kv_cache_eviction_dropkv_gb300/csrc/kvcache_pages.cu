@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(256) free_kernel(const PageCall p) {
     if (threadIdx.x == 0) flag(p.c.status, KVCACHE_FLAG_BAD_SEQ);
     return;
   }
+  int32_t* row = p.c.table + (size_t)s * p.c.M;
+  // read before it is known how many pages are held: a round trip less
+  const int mine = threadIdx.x < p.c.M ? row[threadIdx.x] : -1;
   if (threadIdx.x == 0) {
     held = atomicExch(&p.c.count[s], 0);
     if (held < 0 || held > p.c.M) {
@@ -173,9 +176,8 @@ __global__ void __launch_bounds__(256) free_kernel(const PageCall p) {
     if (held > 0) p.c.length[s] = 0;
   }
   __syncthreads();
-  int32_t* row = p.c.table + (size_t)s * p.c.M;
   for (int col = threadIdx.x; col < held; col += 256) {
-    const int pg = row[col];
+    const int pg = col < 256 ? mine : row[col];
     row[col] = -1;
     if (pg < 0 || pg >= p.c.P) {
       flag(p.c.status, KVCACHE_FLAG_BAD_PAGE);
@@ -275,7 +277,7 @@ __device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
   int turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
-    int need = 0, len = 0;
+    int need = 0, len = 0, last = -1;       // (a sharing branch copies one page at most)
     int4 e = make_int4(0, -1, 0, 0);
     if (i < p.n) {
       const int s = src[i], d = dst[i];
@@ -292,6 +294,7 @@ __device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
           const int both = p.share ? len >> c.page_log2 : 0;
           need = pages - both;
           e = make_int4(s, d, both, pages);
+          if (p.share && need > 0) last = c.table[(size_t)s * c.M + both];
         }
       }
     }
@@ -300,6 +303,7 @@ __device__ __forceinline__ void fork_book(const PageCall& p, Names& names) {
     if (i < p.n) {
       p.offs[i] = (int)at;                  // (read only where the sum fits)
       p.entry[i] = e;
+      if (p.share && need > 0) p.from[at] = last;   // (at < n)
     }
     sum += total;
   }
@@ -346,9 +350,14 @@ __device__ __forceinline__ void fork_move(const PageCall& p, int row_pieces, int
     const long long x = w / chunks;
     const int which = (int)(x & 1);
     const int layer = (int)((x >> 1) % c.layers), k = (int)((x >> 1) / c.layers);
-    const int i = entry_of(p.offs, p.n, k);
-    const int4 e = p.entry[i];
-    const int from = c.table[(size_t)e.x * c.M + e.z + (k - p.offs[i])], to = p.list[k];
+    const int to = p.list[k];
+    int from;
+    if (p.share) {
+      from = p.from[k];
+    } else {
+      const int i = entry_of(p.offs, p.n, k);
+      from = c.table[(size_t)p.entry[i].x * c.M + (k - p.offs[i])];   // (none is shared)
+    }
     if (from < 0 || from >= c.P) {
       if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_PAGE);
       continue;
@@ -652,6 +661,7 @@ PagePlan make_page_plan(int S, int P) {
     return o;
   };
   w.claim = take((size_t)S * 4);
+  w.from = take((size_t)S * 4);
   w.mark = take((size_t)S * 4);
   w.offs = take(((size_t)S + 1) * 4);
   w.entry = take((size_t)S * 16);
