@@ -38,27 +38,14 @@ using namespace dropkv;
 constexpr int kQT = 128;                          // rows of a query tile, keys of a key tile
 constexpr int kTileB = kQT * kDPad * 2;           // 32 KB: two SW128 blocks of 64 columns
 constexpr int kHalfB = kTileB / 2;
-constexpr int kProducer = 8, kIssuer = 9, kWinThreads = 32 * 12;   // warps 10, 11 idle (register shares)
+constexpr int kProducer = 8, kIssuer = 9, kWalker = 10, kWinThreads = 32 * 12;   // warp 11 idle (register shares)
 constexpr int kOffQ = 0, kOffK = 2 * kTileB, kOffV = 4 * kTileB, kOffSmall = 6 * kTileB;
 constexpr uint32_t kCols = 512;                   // group g: S / P at [128 g, +128), O at [256 + 128 g, +128)
 constexpr float kMove = 24.0f;                    // base-2 logarithm by which a maximum may pass its reference
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
 
 constexpr int kNarrow = 32;
-constexpr int kSplitWindow = 1536;                // windows from which on P goes in halves (even at 1024)
-
-struct Small {
-  uint64_t qfull[2], qempty[2];   // group g's Q: landed; its last S of the item complete
-  uint64_t full[2], empty[2];     // K and V pairs: landed; released by the groups (one arrival each)
-  uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
-  uint64_t pfull[2][2];   // group g: the first and the second half of its P written by the group's four warps
-  uint64_t odone[2];   // group g: its last P V of the item complete
-  uint64_t drain;
-  uint32_t tmem_base;
-  int abort;
-};
-constexpr int kWinSmem = kOffSmall + (int)sizeof(Small) + 1024;
-static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
+constexpr int kSplitWindow = 1536;                // windows from which on P goes in halves
 
 // The key tiles of an item: list entry i is key tile tile(i).  Group 0 (query
 // tile t[0], -1: none) takes all entries but the last, group 1 (t[1] = t[0] +
@@ -89,14 +76,14 @@ __device__ __forceinline__ List make_list(const WindowCall& p, int t0, int t1) {
   return l;
 }
 
-// The items of the call in order: sequence by sequence, pairs of query tiles
-// from the sequence's end (the last tile is group 1's), heads innermost.  A
-// CTA takes every gridDim.x-th; each role walks the same cursor.
-struct Cursor {
-  int b = -1, pairs = 0;                          // sequence, its pairs of query tiles
-  int nb = 0;
-  long long first = 0;                            // items before it
-};
+// The items of the call in order: chunks of 32 sequences, in a chunk by
+// position, the last pair of query tiles first (the last tile of a sequence is
+// group 1's), there sequence by sequence, heads innermost.  Round r gives every
+// CTA one item, odd rounds from the last CTA to the first: costs fall along
+// the order, so that evens them out (causal, 8192 tokens, 32 heads: the longest
+// CTA has 1.02 instead of 1.14 of the mean, 385 -> 347 us; eight sequences of 2
+// to 4096 tokens 119 -> 88).  One warp walks the order and hands the items to
+// the others through a ring.
 __device__ __forceinline__ int length_of(const WindowCall& p, int b) {
   const int nb = p.lengths ? p.lengths[b] : p.n_max;
   return nb < 0 || nb > p.n_max ? 0 : nb;
@@ -105,22 +92,90 @@ struct Item {
   int b, hq, nb;
   List list;
 };
-// Item `it`, if there is one.
-__device__ __forceinline__ bool item_at(const WindowCall& p, Cursor& c, long long it, Item* w) {
-  while (c.b < 0 || it >= c.first + (long long)c.pairs * p.Hq) {
-    c.first += (long long)c.pairs * p.Hq;
-    if (++c.b >= p.B) return false;
-    c.nb = length_of(p, c.b);
-    c.pairs = (c.nb + 2 * kQT - 1) / (2 * kQT);
-  }
-  const int y = (int)(it - c.first), x = y / p.Hq;
-  w->b = c.b;
-  w->nb = c.nb;
-  w->hq = y - x * p.Hq;
-  const int t1 = (c.nb + kQT - 1) / kQT - 1 - 2 * x;
-  w->list = make_list(p, t1 - 1, t1);
-  return true;
+// Ring slots.  The softmax warps hold the item they are at; the MMA warp looks
+// one item ahead and may be three before a group that passes over items.
+constexpr int kItems = 8;
+constexpr int kTakers = 10;                       // softmax warps, MMA warp, producer
+struct Ring {
+  uint64_t full[kItems], empty[kItems];
+  int4 item[kItems];                              // sequence (-1: no more), head, length, last query tile
+};
+enum Got { kGaveUp = -1, kEnd = 0, kItem = 1 };
+
+// Item `k` for a taker; wait(barrier, phase) waits, arrive(barrier) arrives once for it.
+template <typename Wait, typename Arrive>
+__device__ __forceinline__ Got take_item(const WindowCall& p, Ring& ring, uint32_t k, Item* w, Wait wait,
+                                         Arrive arrive) {
+  const uint32_t slot = k % kItems;
+  if (!wait(&ring.full[slot], k / kItems)) return kGaveUp;
+  const int4 x = ring.item[slot];
+  arrive(&ring.empty[slot]);
+  if (x.x < 0) return kEnd;
+  w->b = x.x;
+  w->hq = x.y;
+  w->nb = x.z;
+  w->list = make_list(p, x.w - 1, x.w);
+  return kItem;
 }
+
+// The walking warp: false if a wait gave up.
+template <typename Wait>
+__device__ __forceinline__ bool walk_items(const WindowCall& p, Ring& ring, int lane, Wait wait) {
+  long long first = 0, width = 0;                 // items before the level, items of it
+  int b0 = -32, nb = 0, pairs = 0;                // the lane's sequence: b0 + lane
+  int level = 0;                                  // pair of query tiles, from the sequence's start
+  uint32_t at_level = 0;                          // lanes whose sequences have it
+  for (uint32_t r = 0;; ++r) {
+    const long long it = (long long)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    bool more = true;
+    while (more && it >= first + width) {
+      first += width;
+      width = 0;
+      if (--level < 0) {
+        b0 += 32;
+        more = b0 < p.B;
+        nb = b0 + lane < p.B ? length_of(p, b0 + lane) : 0;
+        pairs = (nb + 2 * kQT - 1) / (2 * kQT);
+        level = __reduce_max_sync(0xffffffffu, pairs) - 1;
+      }
+      at_level = __ballot_sync(0xffffffffu, pairs > level && level >= 0);
+      width = (long long)__popc(at_level) * p.Hq;
+    }
+    int4 x = make_int4(-1, 0, 0, 0);
+    if (more) {
+      const int y = (int)(it - first), k = y / p.Hq;
+      uint32_t left = at_level;
+      for (int u = 0; u < k; ++u) left &= left - 1;
+      const int l = __ffs(left) - 1;
+      x.x = b0 + l;
+      x.y = y - k * p.Hq;
+      x.z = __shfl_sync(0xffffffffu, nb, l);
+      x.w = (x.z + kQT - 1) / kQT - 1 - 2 * (__shfl_sync(0xffffffffu, pairs, l) - 1 - level);
+    }
+    const uint32_t slot = r % kItems;
+    if (r >= kItems && !wait(&ring.empty[slot], r / kItems - 1)) return false;
+    if (lane == 0) {
+      ring.item[slot] = x;
+      mbar_arrive(&ring.full[slot]);
+    }
+    __syncwarp();
+    if (!more) return true;
+  }
+}
+
+struct Small {
+  uint64_t qfull[2], qempty[2];   // group g's Q: landed; its last S of the item complete
+  uint64_t full[2], empty[2];     // K and V pairs: landed; released by the groups (one arrival each)
+  uint64_t sfull[2];   // group g: its next S, and every MMA issued before it, complete
+  uint64_t pfull[2][2];   // group g: the first and the second half of its P written by the group's four warps
+  uint64_t odone[2];   // group g: its last P V of the item complete
+  uint64_t drain;
+  Ring ring;           // the items to come
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int kWinSmem = kOffSmall + (int)sizeof(Small) + 1024;
+static_assert(kWinSmem <= 232448, "shared memory exceeds the per-CTA limit");
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -209,6 +264,10 @@ __device__ __forceinline__ void softmax_tile(const WindowCall& p, uint32_t tS, b
   if (!SPLIT && __any_sync(0xffffffffu, need)) follow(factor);
 }
 
+// A value all lanes of the converged warp hold, where the compiler knows that
+// they do: in a uniform register.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 template <bool SPLIT, int DS>
 __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uint8_t* sm, uint32_t tmem, int warp,
                                               int lane) {
@@ -247,15 +306,27 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     release(j);
     return true;
   };
-  Cursor at;
-  Item w;
-  for (long long it = blockIdx.x; item_at(p, at, it, &w); it += gridDim.x) {
-    const List& list = w.list;
+  for (uint32_t k = 0;; ++k) {
+    if (!wait(&S.ring.full[k % kItems], k / kItems)) { give_up(); return; }
+    // The item stays in the ring until its output is written: what only that
+    // needs is read again there.  In uniform registers its list leaves the
+    // tile loop more of the others (32768 tokens, window 4096: 1.44 -> 1.34
+    // ms); with both numbers so, the short form without SPLIT spills (50 -> 55 us).
+    const int4 item = S.ring.item[k % kItems];
+    if (item.x < 0) return;
+    const int nb = SPLIT ? uniform(item.z) : item.z, t1 = uniform(item.w);
+    const List list = make_list(p, t1 - 1, t1);
+    auto leave_item = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.ring.empty[k % kItems]);
+      __syncwarp();
+    };
     const int n = list.n, tg = list.t[g], pos = tg * kQT + row;
     if (tg < 0) {
       for (int j = 0; j < n; ++j)
         if (!pass(j)) { give_up(); return; }
       pair0 += n;
+      leave_item();
       continue;
     }
     float ref = -INFINITY, l = 0.f;
@@ -273,10 +344,10 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
       // the sequence's last key tile (group 1's alone): rows past the end may
       // hold anything; zero them so that 0 * NaN never reaches O
       auto zero_tail = [&]() {
-        if (j0 + kQT <= w.nb) return true;
+        if (j0 + kQT <= nb) return true;
         const uint32_t pr = pair0 + i + 1;
         if (!wait(&S.full[pr & 1], pr >> 1)) return false;
-        if (j0 + row >= w.nb) {
+        if (j0 + row >= nb) {
           uint8_t* vrow = sm + kOffV + (pr & 1) * kTileB + row * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -326,7 +397,9 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
     if (g == 0 && !pass(n - 1)) { give_up(); return; }
     pair0 += n;
     const float inv_l = 1.0f / l;                 // a row sees itself at least
-    __nv_bfloat16* orow = p.out + (((size_t)w.b * p.Hq + w.hq) * p.n_max + pos) * p.d;
+    const int4 x = S.ring.item[k % kItems];
+    __nv_bfloat16* orow = p.out + (((size_t)x.x * p.Hq + x.y) * p.n_max + pos) * p.d;
+    leave_item();
 #pragma unroll 1
     for (int c0 = 0; c0 < p.d; c0 += 32) {
       float o[32];
@@ -334,7 +407,7 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
       tmem_ld16(tO + c0, o);
       tmem_ld16(tO + c0 + 16, o + 16);
       tmem_wait_ld();
-      if (pos < w.nb) {
+      if (pos < nb) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t w4[4];
@@ -353,9 +426,9 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
 
 // SPLIT: P V of a tile begins on the first half of P while the softmax is at
 // the second.  With many tiles per item it shortens the chain softmax -> P V ->
-// S that bounds the kernel (32768 tokens, window 4096: 1.45 -> 1.36 ms); with
-// few, most of them masked, the extra barrier costs more (2051 tokens, window
-// 333: 60 -> 65 us).
+// S that bounds the kernel (32768 tokens, window 4096: 1.45 -> 1.36 ms when it
+// came); with few, most of them masked, the extra barrier costs more (now:
+// 2051 tokens, window 333 50 -> 55 us; 8192 tokens, window 1024 137 -> 141).
 //
 // DS: steps of 16 channels, 4, 6 or 8.  A head of up to 64 channels takes one
 // block of 64 columns of Q, K and V, and N = 64 in P V; up to 96 takes six
@@ -380,6 +453,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       mbar_init(&S.odone[i], 1);
     }
     mbar_init(&S.drain, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&S.ring.full[i], 1);
+      mbar_init(&S.ring.empty[i], kTakers);
+    }
     S.abort = 0;
     fence_mbar_init();
   }
@@ -418,9 +495,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         return true;
       };
       bool ok = true;
-      Cursor at;
       Item w;
-      for (long long it = blockIdx.x; ok && item_at(p, at, it, &w); it += gridDim.x) {
+      for (uint32_t k = 0; ok; ++k) {
+        const Got got = take_item(
+            p, S.ring, k, &w, [&](uint64_t* bar, uint32_t phase) { return mbar_wait(bar, phase & 1, &S.abort); },
+            [](uint64_t* bar) { mbar_arrive(bar); });
+        if (got != kItem) {
+          ok = got == kEnd;
+          break;
+        }
         const List& list = w.list;
         const int zq = w.b * p.Hq + w.hq, unit = w.b * p.Hkv + w.hq / p.g;
         if (!(ok = put(list.tile(0), unit))) break;   // with the last item's last V: before the waits for Q
@@ -486,10 +569,17 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     using Eight = std::integral_constant<int, 8>;
     using Narrow = std::integral_constant<int, kNarrow / 16>;
     uint32_t pair0 = 0, seen0 = 0, seen1 = 0, used0 = 0, used1 = 0;   // entries, tiles and items of the groups so far
-    Cursor at;
     Item w, w2;                                   // the item, the one after
-    long long it = blockIdx.x;
-    bool have = item_at(p, at, it, &w), ok = true;
+    uint32_t taken = 0;
+    auto take = [&](Item* to) {
+      return take_item(p, S.ring, taken++, to, wait, [&](uint64_t* bar) {
+        __syncwarp();
+        if (leader) mbar_arrive(bar);
+        __syncwarp();
+      });
+    };
+    Got got = take(&w);
+    bool have = got == kItem, ok = got != kGaveUp;
     // the first S of group g in an item that begins with pair pr
     auto first_S = [&](int g, const Item& x, uint32_t pr) {
       if (!wait(&S.qfull[g], g ? used1++ : used0++)) return false;
@@ -504,8 +594,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       if (ok && w.list.takes(1, 0)) ok = first_S(1, w, 0);
     }
     while (ok && have) {
-      it += gridDim.x;
-      const bool more = item_at(p, at, it, &w2);
+      got = take(&w2);
+      if (!(ok = got != kGaveUp)) break;
+      const bool more = got == kItem;
       const List& list = w.list;
       bool first0 = true, first1 = true;
       // Entry i: P V of it and S of the entry after it, group 0, then group 1.
@@ -569,6 +660,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     if (leader) {
       umma_commit(&S.drain);
       drain_wait(&S.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == kWalker) {
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort)) != 0;
+    };
+    if (!walk_items(p, S.ring, lane, wait) && lane == 0) {
+      S.abort = 1;
+      atomicOr(p.status, DROPKV_FLAG_TIMEOUT);
     }
     __syncwarp();
   } else if (warp < 8) {

@@ -138,3 +138,22 @@ def test_many_items_a_block_again_and_again(lengths, window, sinks):
         op.window_attention(q, k, v, lens, out, window, sinks)
         assert torch.equal(out, want)
     assert op.check() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3), (300, 200)])
+def test_more_sequences_than_a_warp_has_lanes(window, sinks):
+    """The order of the items goes by chunks of 32 sequences: lengths of every
+    kind in each, none at all in one, and lengths that cannot be served."""
+    lengths = [(37 * b * b) % 401 if b % 5 else 400 for b in range(32)] + [0] * 32 + [400, 1, 129, 0, 256, 257, 383]
+    op = DropKV(len(lengths), 2, 1, 16, 400, 1, out_rows=1, device=DEV)
+    q, k, v = _inputs(len(lengths), 2, 1, 16, 400, lengths, seed=4)
+    want = _check(op, q, k, v, lengths, window, sinks)
+    assert op.check() == 0
+    bad = list(lengths)
+    bad[3], bad[66] = 401, -5                     # left out; the others as they were
+    out = torch.full_like(want, -7.25)
+    op.window_attention(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(bad, dtype=torch.int32, device=DEV), out, window,
+                        sinks)
+    assert B.kvcache_read_status(op.status)[1] == B.FLAG_BAD_LENGTH
+    for b in range(len(lengths)):
+        assert torch.equal(out[b], want[b]) if b not in (3, 66) else torch.all(out[b] == -7.25)
