@@ -35,7 +35,8 @@ class PagedCache:
     def __init__(self, seqs: int, Hkv: int, d: int, pages: int, page: int = 64, max_pages: Optional[int] = None,
                  layers: int = 1, code: str = "e4m3", Hq: Optional[int] = None, T: int = 1, device=None):
         """pages: pages in the pool; page: tokens per page (32, 64 or 128);
-        max_pages: most pages of one sequence (default: all); code: "e4m3" or
+        max_pages: most pages of one sequence (default: all; attention over
+        short sequences is faster with a bound near their length); code: "e4m3" or
         "int8"; Hq, T: query heads (default: Hkv) and most query rows per
         sequence of an attention() call (they size the workspace)."""
         if code not in B.CACHE_CODES:
