@@ -135,7 +135,7 @@ dropkv_status kvcache_attention(const kvcache_shape* shape, const kvcache_buffer
   p.n = n; p.Hq = Hq; p.T = T;
   p.g = Hq / shape->Hkv;
   p.R = p.g * T;
-  p.RB = a.RB; p.RG = a.RG; p.workers = a.workers; p.team = a.team; p.by_unit = a.by_unit; p.rowwise = a.rowwise;
+  p.RB = a.RB; p.RG = a.RG; p.workers = a.workers; p.solo = a.solo; p.team = a.team; p.by_unit = a.by_unit; p.rowwise = a.rowwise;
   p.window = window;
   p.sinks = sinks;
   p.q = static_cast<const __nv_bfloat16*>(q);

@@ -20,7 +20,10 @@
 // its rows' softmax state and outputs in registers.  A run that holds a whole
 // (sequence, head, row group) writes the output; the pieces of one that is
 // cut by run borders go to the workspace and a second kernel joins them in
-// run order (no atomics: results do not depend on timing).
+// run order (no atomics: results do not depend on timing).  Where the table
+// or the window bounds the units tightly, the host skips the deal: few units
+// go to a CTA or a cluster each and are joined through shared memory, many
+// short ones to a warp each (make_attn_plan has the rules and times).
 //
 // Per tile, on mma.m16n8k16 with the tokens on the M side, so that 8 query
 // rows fill the N side (a decode step has g = 1 to 8 rows per KV head; the
@@ -75,6 +78,7 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kJoinThreads = 128, kJoinWide = 512;   // 4 rows; 1 row
 constexpr int kTeamTiles = 8;               // most tiles a warp takes of a unit that has a team
+constexpr int kSoloTiles = 12;              // most tiles of a unit that one warp takes alone
 constexpr int kUnitCost = 3;                // tiles that taking up a unit is worth
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
@@ -328,6 +332,21 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p
     x1 = (uint32_t)(un - b0 * upb + 1) * tiles;
     x0 = x1 - tiles + mate * kWarps + warp;
     stride = kWarps * p.team;
+  } else if (p.solo) {
+    // one unit and row group, all its tiles
+    if (worker >= p.workers) return;
+    const int un = worker / p.RG;
+    b0 = un / upb;
+    const int h = un - b0 * upb;
+    const int tiles = span_of(entry_len(p, b0, true), p.T, p.window, p.sinks).tiles;
+    if (tiles == 0) {                       // its rows see nothing
+      const int r0 = rg * RB, units8 = c.d / 8;
+      uint4* o = reinterpret_cast<uint4*>(p.out + (((size_t)b0 * p.Hq + (size_t)h * p.g) * p.T + r0) * c.d);
+      for (int u = lane; u < min(RB, p.R - r0) * units8; u += 32) o[u] = make_uint4(0, 0, 0, 0);
+      return;
+    }
+    x1 = (uint32_t)(h + 1) * tiles;         // counted from its entry on
+    x0 = x1 - tiles;
   } else {
     if (worker >= p.workers) return;
     // rows of sequences with nothing to read
@@ -872,7 +891,7 @@ cudaError_t launch_t(const AttnCall& p, cudaStream_t st) {
   const unsigned units = (unsigned)(p.n * p.c.Hkv * p.RG);
   if (p.team) return launch_team(kern, units, p, st);
   e = launch_pdl(kern, dim3((p.workers + kWarps - 1) / kWarps), dim3(kThreads), kSmem, st, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.solo) return e;
   if (p.rowwise) return launch_pdl(join_kernel<true>, dim3(units, std::min(p.RB, p.R)), dim3(kJoinWide), 0, st, p);
   return launch_pdl(join_kernel<false>, dim3(p.by_unit ? units : p.workers, (std::min(p.RB, p.R) + 3) / 4),
                     dim3(kJoinThreads), 0, st, p);
@@ -904,12 +923,28 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
     cap = std::min(cap, ((long long)window + T + kTok - 2) / kTok + 1 + ((long long)sinks + kTok - 1) / kTok);
   // Rows a warp holds: 8, or 16 where there are more and each warp has many
   // tiles (32 rows, 16 x 4000 tokens: 49.9 us against 63.7 with 8; 2 x 16000
-  // tokens, 3 tiles a warp: 18.8 against 16.7)
+  // tokens, 3 tiles a warp: 18.8 against 16.7).  Short units that go to one
+  // warp each: 16 where 8 would take more than one wave (128 x 64 tokens, 16
+  // rows: 13.7 -> 10.4; 16 x 64 tokens, 24 rows would lose, 6.7 -> 8.8).
   const long long pairs16 = (R + 15) / 16 * n * s.Hkv * cap;
-  a->RB = R > 8 && pairs16 >= 16 * wave_of(sms) ? 16 : 8;
+  const long long units8 = (R + 7) / 8 * n * s.Hkv, units16 = (R + 15) / 16 * n * s.Hkv, wave = wave_of(sms);
+  const bool shorts = cap <= kSoloTiles;
+  a->RB = R > 8 && (pairs16 >= 16 * wave || (shorts && units8 > wave && units16 <= 4 * wave)) ? 16 : 8;
   a->RG = (int)((R + a->RB - 1) / a->RB);
   const long long units = (long long)n * s.Hkv * a->RG;   // with their row groups
   if (units * a->RB >= (1LL << 31)) return false;
+  // Many short units (more than have a CTA each at once): a warp each, nothing
+  // dealt and nothing to join (8 heads, 152 x 128 tokens: 14.3 -> 8.8 us, 76 x
+  // 256: 12.8 -> 10.7, 512 x 32: 25.4 -> 19.7, 152 x 1-384: 21.0 -> 16.6; over
+  // four waves both take the same, and from 16 tiles on equal lengths lose, 42 x
+  // 512 of 32 heads 42.5 -> 46.7).
+  a->solo = shorts && units > 2LL * sms && units <= 4 * wave ? 1 : 0;
+  if (a->solo) {
+    a->workers = (int)units;
+    a->team = a->by_unit = a->rowwise = 0;
+    a->part_s = a->cuts = a->total = 0;
+    return true;
+  }
   // Few units of moderate length: a cluster of 1 to 8 CTAs each, joined through
   // shared memory, no second kernel.  More CTAs while a warp has over 2 tiles
   // and they fit one wave; two waves for units of at most 5 tiles a warp (64 x

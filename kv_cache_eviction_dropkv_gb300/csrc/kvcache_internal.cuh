@@ -79,6 +79,7 @@ struct AttnCall {
   int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
   int window, sinks;
   int workers;                   // warps of the grid: run * RG + row group
+  int solo;                      // 1: a warp per unit and row group, nothing to join
   int team;                      // > 0: a cluster of that many CTAs per unit, joined in shared memory
   int by_unit;                   // 1: cuts is per unit, 0: per run
   int rowwise;                   // 1: a join CTA takes one row
@@ -90,7 +91,7 @@ struct AttnCall {
   float scale_log2;
 };
 struct AttnPlan {
-  int RB, RG, workers, team, by_unit, rowwise;
+  int RB, RG, workers, solo, team, by_unit, rowwise;
   size_t part_s, cuts, total;    // byte offsets
 };
 // false: more tiles than a 32-bit count holds.

@@ -412,6 +412,31 @@ def test_attention_many_sequences():
     check_attention(c, r, q, seqs=[(i * 7) % n for i in range(n)])
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq,Hkv,d,T,n", [(8, 4, 64, 1, 90), (12, 2, 128, 3, 100), (16, 8, 64, 8, 90), (33, 3, 72, 2, 120),
+                                          (9, 1, 16, 5, 330)])
+def test_attention_many_short_sequences(code, Hq, Hkv, d, T, n):
+    """A warp per unit and row group (8 or 16 rows): empty sequences, fewer
+    tokens than rows, numbers that are no sequence, and with room for long ones
+    where a window bounds what is read."""
+    lengths = [(i * 37) % 150 if i % 9 else 0 for i in range(n)]
+    q = draw_rows(n, Hq, T, d, 8, spread=0.3)
+    for room, masks in ((5, ((0, 0), (1, 0), (40, 5), (64, 100))), (400, ((1, 0), (40, 5), (64, 100)))):
+        c, r = pair(seqs=n, Hkv=Hkv, d=d, pages=n * 5, page=32, max_pages=room, code=code, Hq=Hq, T=T)
+        fill(c, r, lengths, spread=0.3)
+        for window, sinks in masks:
+            check_attention(c, r, q, window=window, sinks=sinks)
+        order = [(i * 7 + 3) % n for i in range(n)]
+        out = check_attention(c, r, q, window=40, sinks=5, seqs=order)
+        assert c.check() == 0
+        order[4], order[n - 1] = n, -1
+        got = torch.full_like(out, 7.0)
+        c.attention(0, q.to(DEV), got, window=40, sinks=5, seqs=ints(order))
+        assert flags_of(c) == B.FLAG_BAD_SEQ
+        for i in range(n):
+            assert torch.equal(got[i], out[i]) if i not in (4, n - 1) else torch.all(got[i] == 0)
+
+
 def test_attention_scales_and_logits_of_very_different_size():
     """Value pages 2^40 apart, one key far above the rest, constant and zero rows."""
     c, r = pair(seqs=2, Hkv=1, d=64, pages=24, page=32, max_pages=12, Hq=2, T=1)
