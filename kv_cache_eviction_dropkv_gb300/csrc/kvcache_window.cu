@@ -95,6 +95,7 @@ struct Item {
 // Ring slots.  The softmax warps hold the item they are at; the MMA warp looks
 // one item ahead and may be three before a group that passes over items.
 constexpr int kItems = 8;
+constexpr int kWalkerWaits = 3600;                // waits (of 1 s) for a slot
 constexpr int kTakers = 10;                       // softmax warps, MMA warp, producer
 struct Ring {
   uint64_t full[kItems], empty[kItems];
@@ -663,8 +664,15 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     }
     __syncwarp();
   } else if (warp == kWalker) {
+    // A slot comes free when the item in it is done, and an item of many
+    // million keys takes longer than a wait's limit: the other roles' waits
+    // tell whether the CTA moves, and their abort ends this one.
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort)) != 0;
+      for (int t = 0; t < kWalkerWaits; ++t) {
+        if (__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort))) return true;
+        if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&S.abort) != 0)) return false;
+      }
+      return false;
     };
     if (!walk_items(p, S.ring, lane, wait) && lane == 0) {
       S.abort = 1;

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cache_eviction_dropkv_gb300 import DropKV, DropKVError, _binding as B
+from kv_cache_eviction_dropkv_gb300 import DropKV, DropKVError, _binding as B, _build
 from tests import _paged as R
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +157,21 @@ def test_more_sequences_than_a_warp_has_lanes(window, sinks):
     assert B.kvcache_read_status(op.status)[1] == B.FLAG_BAD_LENGTH
     for b in range(len(lengths)):
         assert torch.equal(out[b], want[b]) if b not in (3, 66) else torch.all(out[b] == -7.25)
+
+
+def test_items_longer_than_a_waits_limit():
+    """In the build whose waits end after 10 ms: 2^21 causal rows, whose last
+    query tiles take some 20 ms each, are no timeout, and the bytes are those
+    of the library."""
+    n = 1 << 21
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q, k, v = (torch.randn(1, 1, n, 8, generator=g, device=DEV).bfloat16() for _ in range(3))
+    want, out = torch.zeros_like(q), torch.zeros_like(q)
+    op = DropKV(1, 1, 1, 8, n, 1, out_rows=1, device=DEV)
+    op.window_attention(q, k, v, None, want, 0)
+    assert op.check() == 0
+    hooks = _build.build_library(variant="test_hooks")
+    with B.use_library(hooks):
+        op.window_attention(q, k, v, None, out, 0)
+        assert B.kvcache_read_status(op.status) == (0, 0)
+    assert torch.equal(out, want)
