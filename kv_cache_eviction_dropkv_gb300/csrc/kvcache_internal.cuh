@@ -76,7 +76,7 @@ struct AttnCall {
   Cache c;                       // k, v, ks, vs at the layer
   const int32_t* seqs;
   int n, Hq, T, g, R;            // R = g * T query rows per KV head
-  int RB, RG;                    // rows per warp (8, 16 or 32), row groups per KV head
+  int RB, RG;                    // rows per warp (8 or 16), row groups per KV head
   int window, sinks;
   int workers;                   // warps of the grid: run * RG + row group
   int solo;                      // 1: a warp per unit and row group, nothing to join
