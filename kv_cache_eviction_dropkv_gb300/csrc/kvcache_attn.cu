@@ -74,6 +74,12 @@ struct alignas(16) Tile {
 constexpr int kPartial = 1;                 // some of its slots are seen by no row
 constexpr int kMasked = 2;                  // some row does not see some of its tokens
 constexpr int kUnreadable = 4;              // its table entry is no page
+// CTAs per SM: registers allow three where a row has at most 64 channels (with
+// three instead of two, e4m3 and int8: 1 x 131072 tokens, 8 heads, 37.0 -> 34.8
+// and 40.8 -> 35.3 us; 48 x 3-8191, window 2000, 47.7 -> 42.5; 46 x 1347-3921
+// with 35 rows 264 -> 239; only one row per head in e4m3 gains nothing on
+// average, 34.4 and 34.6), two above (three: 51.9 -> 55.2 us).
+__host__ __device__ constexpr int kCtas(int d) { return d <= 64 ? 3 : 2; }
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
 constexpr int kJoinThreads = 128, kJoinWide = 512;   // 4 rows; 1 row
@@ -301,7 +307,7 @@ __device__ __forceinline__ void write_row(const AttnCall& p, int b, int h, int r
 
 // EXACT: d == DP, so that a tile's row offsets are constants.
 template <int CODE, int DP, int NR, bool EXACT>
-__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnCall p) {
+__global__ void __launch_bounds__(kThreads, kCtas(DP)) attention_kernel(const AttnCall p) {
   constexpr int KS = DP / 16;               // MMAs along d for S, and row blocks of O
   constexpr int KB = DP / 4, VB = DP / 8;   // bytes a lane takes of a K row, of a V row
   constexpr int RB = 8 * NR;
@@ -906,8 +912,8 @@ cudaError_t launch_code(const AttnCall& p, cudaStream_t st) {
   return NR == 1 ? launch_t<CODE, 64, 1, false>(p, st) : launch_t<CODE, 64, 2, false>(p, st);
 }
 
-// One wave: two CTAs of kWarps warps per SM.
-long long wave_of(int sms) { return (long long)sms * 2 * kWarps; }
+// One wave.
+long long wave_of(int sms, int d) { return (long long)sms * kCtas(d) * kWarps; }
 // The workspace: outputs of the pieces, their softmax states, who joins what.
 size_t pieces_o(long long workers, int RB, int d) { return ((size_t)workers * 2 * RB * d * 4 + 255) / 256 * 256; }
 size_t pieces_s(long long workers, int RB) { return ((size_t)workers * 2 * RB * 16 + 255) / 256 * 256; }
@@ -927,7 +933,7 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
   // warp each: 16 where 8 would take more than one wave (128 x 64 tokens, 16
   // rows: 13.7 -> 10.4; 16 x 64 tokens, 24 rows would lose, 6.7 -> 8.8).
   const long long pairs16 = (R + 15) / 16 * n * s.Hkv * cap;
-  const long long units8 = (R + 7) / 8 * n * s.Hkv, units16 = (R + 15) / 16 * n * s.Hkv, wave = wave_of(sms);
+  const long long units8 = (R + 7) / 8 * n * s.Hkv, units16 = (R + 15) / 16 * n * s.Hkv, wave = wave_of(sms, s.d);
   const bool shorts = cap <= kSoloTiles;
   a->RB = R > 8 && (pairs16 >= 16 * wave || (shorts && units8 > wave && units16 <= 4 * wave)) ? 16 : 8;
   a->RG = (int)((R + a->RB - 1) / a->RB);
@@ -955,7 +961,7 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
                     (units <= 4LL * sms && cap <= 5 * kWarps)
                 ? team
                 : 0;
-  a->workers = (int)(std::max(1LL, std::min(wave_of(sms) / a->RG, (long long)n * s.Hkv * cap)) * a->RG);
+  a->workers = (int)(std::max(1LL, std::min(wave_of(sms, s.d) / a->RG, (long long)n * s.Hkv * cap)) * a->RG);
   // Joins: by row where the rows are fewer than the CTAs they can fill
   a->by_unit = units <= a->workers ? 1 : 0;
   a->rowwise = a->by_unit && units * std::min<long long>(R, a->RB) <= 4LL * sms ? 1 : 0;
@@ -969,7 +975,7 @@ size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms) {
   const long long R = (long long)Hq / s.Hkv * T;
   size_t most = 0;
   for (int RB = 8; RB <= 16; RB += 8) {
-    const long long w = std::max(wave_of(sms), (R + RB - 1) / RB);
+    const long long w = std::max(wave_of(sms, s.d), (R + RB - 1) / RB);
     most = std::max(most, pieces_o(w, RB, s.d) + pieces_s(w, RB) + (size_t)w * 8);
   }
   return most;
