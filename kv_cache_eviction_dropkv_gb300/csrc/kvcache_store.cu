@@ -48,8 +48,9 @@ __global__ void __launch_bounds__(PAGE * 2) store_kernel(const StoreCall p) {
   }
   const int start = len - cnt;
   const int col = start / PAGE + blockIdx.x;
+  // by page: the grid covers `rows`, and past the longest sequence col * PAGE leaves 32 bits
+  if (cnt == 0 || col > (len - 1) / PAGE) return;
   const int base = col * PAGE;              // first token of the page
-  if (cnt == 0 || base >= len) return;
   const int pg = c.table[(size_t)s * c.M + col];
   if (pg < 0 || pg >= c.P || c.refs[pg] != 1) {
     if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_PAGE);
