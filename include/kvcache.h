@@ -96,7 +96,15 @@ DROPKV_API size_t kvcache_workspace_size(const kvcache_shape* shape, int32_t Hq,
 /* Make room for extra[i] >= 0 (device int32 [n]) more tokens of sequence
  * seqs[i]: length grows by extra[i], and pages are taken as needed.  All or
  * nothing: with too few free pages nothing changes (FLAG_NO_PAGES).  A
- * sequence whose pages would pass max_pages is flagged and left out. */
+ * sequence whose pages would pass max_pages is flagged and left out.
+ *
+ * A refusal is known on the device alone until the status word is read, and a
+ * kvcache_store of `extra` tokens behind it would replace the last tokens that
+ * the sequence has.  So either the status is read first, or the reservation is
+ * made by a record (kvcache_run, KVCACHE_RESERVE_GRANTED), whose `out` is a
+ * device int32 [n]: it takes what each entry was granted, extra[i] or 0, and
+ * goes to kvcache_store as `counts`, which then stores nothing where nothing
+ * was granted. */
 DROPKV_API dropkv_status kvcache_reserve(const kvcache_shape* shape, const kvcache_buffers* cache,
                                          const int32_t* seqs, int32_t n, const int32_t* extra, void* workspace,
                                          size_t workspace_bytes, uint32_t* status, cudaStream_t stream);
@@ -105,7 +113,8 @@ DROPKV_API dropkv_status kvcache_reserve(const kvcache_shape* shape, const kvcac
  * length already holds them) take the codes of rows 0 .. counts[i] - 1.
  *   k, v    device bf16 [n][Hkv][rows][d] (dropkv_compact's k_out and v_out
  *           with out_rows = rows and counts = kept_len, for example)
- *   counts  device int32 [n], 0 <= counts[i] <= rows, or NULL for rows
+ *   counts  device int32 [n], 0 <= counts[i] <= rows, or NULL for rows; what
+ *           kvcache_reserve granted, where it may have refused (see there)
  * Per (page, head): the scale is that of the new values' largest magnitude;
  * in a page that holds earlier tokens it is the larger of that and the old
  * scale, and when it grows the earlier codes are rounded again at the new
@@ -193,13 +202,16 @@ DROPKV_API dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t
  *   KVCACHE_ATTENTION  q                           out  Hq, T, window, sinks
  *   KVCACHE_FORK       dst                              share    (seqs: src)
  *   KVCACHE_COMPACT    kept_idx  kept_len               kept_stride
- *   KVCACHE_FREE */
+ *   KVCACHE_FREE
+ *   KVCACHE_RESERVE_GRANTED   extra, and out: granted (kvcache_reserve says
+ *                      what for) */
 #define KVCACHE_RESERVE   0
 #define KVCACHE_STORE     1
 #define KVCACHE_ATTENTION 2
 #define KVCACHE_FORK      3
 #define KVCACHE_COMPACT   4
 #define KVCACHE_FREE      5
+#define KVCACHE_RESERVE_GRANTED 16
 typedef struct {
   const kvcache_shape* shape;
   const kvcache_buffers* cache;

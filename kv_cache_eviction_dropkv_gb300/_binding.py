@@ -313,6 +313,7 @@ def dropkv_version() -> str:
 # would add two microseconds.
 kvcache_call = struct.Struct("@PPPNPPPPPPP7i0P")   # the fields of the record, in order
 RESERVE, STORE, ATTENTION, FORK, COMPACT, FREE = range(6)
+RESERVE_GRANTED = 16 + RESERVE
 CACHE_CALLS = tuple("kvcache_" + name for name in ("reserve", "store", "attention", "fork", "compact", "free"))
 current_raw_stream, current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 

@@ -70,6 +70,20 @@ dropkv_status open_pages(const kvcache_shape* s, const kvcache_buffers* b, int32
 
 dropkv_status launched(cudaError_t e) { return e == cudaSuccess ? DROPKV_OK : DROPKV_ERR_CUDA; }
 
+dropkv_status reserve(const kvcache_shape* shape, const kvcache_buffers* cache, const int32_t* seqs, int32_t n,
+                      const int32_t* extra, int32_t* granted, void* workspace, size_t workspace_bytes,
+                      uint32_t* status, cudaStream_t stream) {
+  PageCall p{};
+  const dropkv_status st = open_pages(shape, cache, n, workspace, workspace_bytes, status, &p);
+  if (st != DROPKV_OK) return st;
+  if (!extra || !aligned(granted, 4)) return DROPKV_ERR_INVALID_ARG;
+  if (n == 0) return DROPKV_OK;
+  p.seqs = seqs;
+  p.extra = extra;
+  p.granted = granted;
+  return launched(launch_reserve(p, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -85,14 +99,7 @@ size_t kvcache_workspace_size(const kvcache_shape* shape, int32_t Hq, int32_t T)
 dropkv_status kvcache_reserve(const kvcache_shape* shape, const kvcache_buffers* cache, const int32_t* seqs, int32_t n,
                               const int32_t* extra, void* workspace, size_t workspace_bytes, uint32_t* status,
                               cudaStream_t stream) {
-  PageCall p{};
-  const dropkv_status st = open_pages(shape, cache, n, workspace, workspace_bytes, status, &p);
-  if (st != DROPKV_OK) return st;
-  if (!extra) return DROPKV_ERR_INVALID_ARG;
-  if (n == 0) return DROPKV_OK;
-  p.seqs = seqs;
-  p.extra = extra;
-  return launched(launch_reserve(p, stream));
+  return reserve(shape, cache, seqs, n, extra, nullptr, workspace, workspace_bytes, status, stream);
 }
 
 dropkv_status kvcache_store(const kvcache_shape* shape, const kvcache_buffers* cache, int32_t layer,
@@ -228,6 +235,10 @@ dropkv_status kvcache_run(const kvcache_call* c) {
     case KVCACHE_RESERVE:
       return kvcache_reserve(c->shape, c->cache, c->seqs, c->n, in0, c->workspace, c->workspace_bytes, c->status,
                              c->stream);
+    case KVCACHE_RESERVE_GRANTED:
+      if (!c->out) return DROPKV_ERR_INVALID_ARG;
+      return reserve(c->shape, c->cache, c->seqs, c->n, in0, static_cast<int32_t*>(c->out), c->workspace,
+                     c->workspace_bytes, c->status, c->stream);
     case KVCACHE_STORE:
       return kvcache_store(c->shape, c->cache, c->layer, c->seqs, c->n, c->in[0], c->in[1], c->arg[0],
                            static_cast<const int32_t*>(c->in[2]), c->status, c->stream);

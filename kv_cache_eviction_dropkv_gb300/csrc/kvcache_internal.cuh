@@ -51,6 +51,7 @@ struct PageCall {
   const int32_t *seqs, *other;   // sequences (fork: src and dst)
   int n;
   const int32_t* extra;          // reserve
+  int32_t* granted;              // reserve: tokens each entry got, or null
   const int32_t *kept_idx, *kept_len;
   int kept_stride, share;
   int32_t *claim, *mark, *from, *offs, *list, *rows;

@@ -199,14 +199,15 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
   int turn = 0;
   for (int base = 0; base < p.n; base += kBook) {
     const int i = base + threadIdx.x;
-    int need = 0, pages = 0;
+    int need = 0, pages = 0, extra = 0;
     long long tokens = -1;                  // new length, -1: the entry is left out
     if (i < p.n) {
       const int s = seq_of(p.seqs, i);
       if (s < 0 || s >= c.S || (p.seqs && !first_named(p, names, i, s))) {
         flag(c.status, KVCACHE_FLAG_BAD_SEQ);
       } else {
-        const int extra = p.extra[i], len = c.length[s], have = c.count[s];
+        const int len = c.length[s], have = c.count[s];
+        extra = p.extra[i];
         if (extra < 0 || len < 0 || have < 0 || have > c.M || have != pages_for(c, len)) {
           flag(c.status, DROPKV_FLAG_BAD_LENGTH);
         } else if ((long long)len + extra > (long long)c.M * c.page) {
@@ -222,12 +223,16 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
     const long long at = sum + block_scan(need, &total, turn);
     if (i < p.n) {
       p.offs[i] = (int)at;                  // (read only where the sum fits)
-      p.entry[i] = make_int4((int)tokens, pages, need, 0);
+      p.entry[i] = make_int4((int)tokens, pages, need, extra);
     }
     sum += total;
   }
   __syncthreads();
-  if (!find_pages(p, sum, counts, turn)) return;
+  if (!find_pages(p, sum, counts, turn)) {
+    if (p.granted)
+      for (int i = threadIdx.x; i < p.n; i += kBook) p.granted[i] = 0;
+    return;
+  }
   grid_dep_launch();
   for (int k = threadIdx.x; k < sum; k += kBook) {
     const int i = entry_of(p.offs, p.n, k);
@@ -238,6 +243,7 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PageCall p) {
   }
   for (int i = threadIdx.x; i < p.n; i += kBook) {
     const int4 e = p.entry[i];
+    if (p.granted) p.granted[i] = e.x < 0 ? 0 : e.w;
     if (e.x < 0) continue;
     const int s = seq_of(p.seqs, i);
     c.length[s] = e.x;

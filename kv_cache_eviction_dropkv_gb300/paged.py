@@ -26,7 +26,10 @@ class PagedCache:
     in the order they are made; calls on one cache, or on one workspace, that
     would overlap on the GPU are the caller's to order.  Problems found on the
     device (a sequence that does not exist, too few free pages, ...) are
-    reported by check().
+    reported by check().  A store() behind a reserve() that was refused would
+    replace the sequence's last tokens: where pages or table entries can run
+    out between two check()s, pass what was granted on (reserve(granted=),
+    store(counts=)).
 
     Buffers (device tensors, free to read): k, v [layers, pages, Hkv, page, d]
     codes, k_scale, v_scale [layers, pages, Hkv], refs [pages], table
@@ -106,14 +109,18 @@ class PagedCache:
             *self._fixed, B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream),
             seqs, in0, in1, in2, out, op, layer, n, arg0, arg1, arg2, arg3))
         if code != 0:
-            raise B.DropKVError(code, B.CACHE_CALLS[op])
+            raise B.DropKVError(code, B.CACHE_CALLS[op & 15])
 
     # -------------------------------------------------------------- a step
-    def reserve(self, extra, seqs=None, stream=None):
+    def reserve(self, extra, seqs=None, stream=None, granted=None):
         """Room for extra[i] more tokens of sequence seqs[i] (int32 [n]); their
-        lengths grow.  All or nothing when pages run out."""
+        lengths grow.  All or nothing when pages run out.  granted (int32 [n])
+        takes extra[i], or 0 where the entry was refused: as store()'s counts
+        it keeps a refused step from replacing the tokens before it."""
         n = extra.shape[0]
-        self._call(B.RESERVE, stream, n, self._entries(seqs, n), self._ints("extra", extra, n))
+        to = 0 if granted is None else self._ints("granted", granted, n)
+        self._call(B.RESERVE if granted is None else B.RESERVE_GRANTED, stream, n, self._entries(seqs, n),
+                   self._ints("extra", extra, n), out=to)
 
     def store(self, layer, k, v, counts=None, seqs=None, stream=None):
         """Rows 0 .. counts[i] - 1 (default: all) of k, v [n, Hkv, rows, d] bf16

@@ -1,11 +1,10 @@
 """The paged 8-bit cache at the ends of its ranges, against the plain reference
 of tests/_paged.py or the formulas themselves."""
-import numpy as np
 import pytest
 import torch
 
-from kv_cache_eviction_dropkv_gb300 import PagedCache
-from tests.test_gpu_paged import DEV, draw_rows, ints
+from kv_cache_eviction_dropkv_gb300 import PagedCache, _binding as B
+from tests.test_gpu_paged import DEV, both, draw_rows, fill, flags_of, ints, pair, same_pool, same_state
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +35,77 @@ def test_store_behind_the_longest_sequence_touches_nothing_else(page, rows):
     want[1][0, 1, 0, page - 1] = 4.0
     for got, w in zip((c.k.float(), c.v.float(), c.k_scale, c.v_scale), want):
         assert torch.equal(got, w)
+
+
+# ------------------------------------------------------------------ a refused reservation
+def same(c, r):
+    same_state(c, r)
+    same_pool(c, r)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_what_was_granted_is_what_is_stored(code):
+    """Steps whose reservation is refused, wholly or for some entries, store
+    nothing in their place: the tokens before them stay as they were."""
+    c, r = pair(seqs=4, pages=9, max_pages=4, code=code)
+    fill(c, r, [64, 33, 1, 128], seed=2)                    # 2, 2, 1 and 4 pages: all
+    k, v = (draw_rows(4, 2, 3, 64, 7 + j) for j in range(2))
+
+    def step(extra, want, seqs=None):
+        got = ints([9] * len(extra))
+        before = list(r.length)
+        c.reserve(ints(extra), granted=got, seqs=None if seqs is None else ints(seqs))
+        r.reserve(extra, seqs)
+        assert got.tolist() == want
+        who = list(range(len(extra))) if seqs is None else seqs
+        assert [r.length[s] - before[s] if s not in who[:i] else 0 for i, s in enumerate(who)] == want
+        n = len(extra)
+        c.store(0, k[:n].to(DEV), v[:n].to(DEV), got, seqs=None if seqs is None else ints(seqs))
+        r.store(0, k[:n].float().numpy(), v[:n].float().numpy(), want, seqs)
+        same(c, r)
+
+    step([1, 1, 1, 0], [0, 0, 0, 0])                        # a page too few: nothing for anybody
+    assert flags_of(c) == r.flags == B.FLAG_NO_PAGES
+    both(c, r, "free", [2])
+    step([1, 3, 0, 1], [1, 3, 0, 0])                        # past max_pages: that entry alone
+    assert flags_of(c) == r.flags == B.FLAG_NO_PAGES | B.FLAG_OVERFLOW
+    step([2, -1, 2], [2, 0, 0], seqs=[1, 0, 1])             # negative; named twice
+    assert flags_of(c) == r.flags
+    step([2, 1 << 30], [2, 0], seqs=[0, 1])
+    assert flags_of(c) == r.flags
+
+
+def test_captured_steps_stop_where_pages_run_out():
+    """A captured decode step, replayed past the last page."""
+    c, r = pair(seqs=2, Hkv=1, d=16, pages=5, page=32, max_pages=5, Hq=2)
+    fill(c, r, [60, 30], seed=5)
+    k, v = (draw_rows(2, 1, 1, 16, 7 + j) for j in range(2))
+    kd, vd, one, got = k.to(DEV), v.to(DEV), ints([1, 1]), ints([0, 0])
+
+    def step():
+        c.reserve(one, granted=got)
+        c.store(0, kd, vd, got)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(60):
+        graph.replay()
+        before = list(r.length)
+        r.reserve([1, 1])
+        r.store(0, k.float().numpy(), v.float().numpy(), [a - b for a, b in zip(r.length, before)])
+    same(c, r)
+    assert r.length == [94, 64] and got.tolist() == [0, 0]   # sequence 1 wants the sixth page
+    assert flags_of(c) == r.flags == B.FLAG_NO_PAGES
+
+
+def test_granted_over_a_thousand_entries_and_refusals():
+    S = 1300
+    c, r = pair(seqs=S, Hkv=1, d=8, pages=S, page=32, max_pages=1)
+    extra = [(7 * i) % 40 for i in range(S)]                # over 32: past the table
+    got = ints([9] * S)
+    c.reserve(ints(extra), granted=got)
+    assert got.tolist() == [e if e <= 32 else 0 for e in extra]
+    for bad in (got[:5], got.long(), got.cpu(), ints([0, 0] * S)[::2]):
+        with pytest.raises(ValueError):
+            c.reserve(ints(extra), granted=bad)
