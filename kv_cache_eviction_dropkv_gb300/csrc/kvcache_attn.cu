@@ -75,10 +75,10 @@ constexpr int kPartial = 1;                 // some of its slots are seen by no 
 constexpr int kMasked = 2;                  // some row does not see some of its tokens
 constexpr int kUnreadable = 4;              // its table entry is no page
 // CTAs per SM: registers allow three where a row has at most 64 channels (with
-// three instead of two, e4m3 and int8: 1 x 131072 tokens, 8 heads, 37.0 -> 34.8
-// and 40.8 -> 35.3 us; 48 x 3-8191, window 2000, 47.7 -> 42.5; 46 x 1347-3921
-// with 35 rows 264 -> 239; only one row per head in e4m3 gains nothing on
-// average, 34.4 and 34.6), two above (three: 51.9 -> 55.2 us).
+// three instead of two, e4m3 and int8: 1 x 131072 tokens, 8 heads, 37.0 -> 34.9
+// and 40.8 -> 35.3 us; 24 x up to 4000, 32 heads, one row 47.1 -> 39.8 and 52.9
+// -> 40.6; 48 x 3-8191, window 2000, 47.7 -> 42.5; 46 x 1347-3921 with 35 rows
+// 264 -> 239), two above (three: 51.9 -> 55.2 us).
 __host__ __device__ constexpr int kCtas(int d) { return d <= 64 ? 3 : 2; }
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kMeta * (int)sizeof(Tile);
@@ -816,7 +816,14 @@ template <bool ROWWISE>
 __global__ void __launch_bounds__(ROWWISE ? kJoinWide : kJoinThreads) join_kernel(const AttnCall p) {
   constexpr int kW = (ROWWISE ? kJoinWide : kJoinThreads) / 32, kBatch = ROWWISE ? 10 : 8;
   grid_dep_wait();
-  grid_dep_launch();
+  // Three attention CTAs fill an SM's registers.  Started while CTAs of the
+  // join are there, they settle beside them, and the hole that these leave is
+  // too small for the third, which then runs behind the others: there the next
+  // kernel starts once the join is gone (attention after attention, one row
+  // per head, e4m3: 24 x up to 4000 tokens of 32 heads 55.3 -> 39.2 us, 32 x
+  // up to 2000 38.7 -> 31.0; with a store between, which clears the SMs,
+  // 45.0 -> 45.2 and 36.1 -> 37.0, 1 x 131072 tokens 39.9 -> 37.9).
+  if (kCtas(p.c.d) <= 2) grid_dep_launch();
   __shared__ float4 s_o[kW][32];
   __shared__ float s_l[kW], s_m[kW], s_M[kW];
   const Cache& c = p.c;
