@@ -136,8 +136,9 @@ DROPKV_API dropkv_status kvcache_store(const kvcache_shape* shape, const kvcache
  * Supported: n * Hkv * max_pages * page < 2^35; n * Hq * T < 2^30.
  * Numerics: codes and query rows enter the tensor cores as fp16 (each query
  * row scaled by a power of two first; both exact but for query elements 2^-29
- * below their row's largest), probabilities as fp16, sums and softmax
- * statistics are fp32.  Queries must be finite and logits within fp32's
+ * below their row's largest), probabilities as fp16 (off by 2^-11 of
+ * themselves, or 2^-32 of the row's largest where that is more; weighted by
+ * the scales of their values), sums and softmax statistics are fp32.  Queries must be finite and logits within fp32's
  * range; anything else gives its own rows undefined values.  Slots that no row
  * sees are never read.  An e4m3
  * not-a-number code that one row sees makes every row of its KV head

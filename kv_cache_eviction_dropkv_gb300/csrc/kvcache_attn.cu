@@ -89,6 +89,13 @@ constexpr int kUnitCost = 3;                // tiles that taking up a unit is wo
 // A row's reference moves only when a tile's maximum is this far above it
 // (base-2 logarithm), so probabilities stay below 2^8 (fp16 holds 2^16).
 constexpr float kMoveLog2 = 8.0f;
+// Probabilities enter P V as fp16 times 2^7: up to 2^15 of fp16's 2^16 above,
+// so that those far below the reference are not dropped from the output while
+// the sum counts them (2^-25 of the reference is fp16's last bit: a million
+// such tokens behind one dominant key are 1/32 of the output).  What is lost
+// is at most 2^-32 of the reference for each; outputs are multiplied by 2^-7
+// as they are written, apart from the factor of the sum, which may be tiny.
+constexpr float kLiftLog2 = 7.0f, kUnlift = 0x1p-7f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -299,7 +306,8 @@ __device__ __forceinline__ Joined nothing_joined() {
 __device__ __forceinline__ void write_row(const AttnCall& p, int b, int h, int r, int lane, const Joined& a) {
   if (lane * 4 >= p.c.d) return;
   const float f = a.l == 0.f ? 0.f : ex2_approx(a.M - a.m) / a.l;
-  const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.o.x * f, a.o.y * f), h1 = __floats2bfloat162_rn(a.o.z * f, a.o.w * f);
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.o.x * kUnlift * f, a.o.y * kUnlift * f),
+                       h1 = __floats2bfloat162_rn(a.o.z * kUnlift * f, a.o.w * kUnlift * f);
   uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
   if (a.l == 0.f) w = make_uint2(0u, 0u);
   *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * p.c.d + lane * 4) = w;
@@ -572,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, kCtas(DP)) attention_kernel(const At
         const int rl = nr * 8 + 2 * c4 + e, r = rg * RB + rl;
         if (r >= p.R) continue;
         if (whole) {
-          // o stands for o 2^(M - m); a row that saw nothing has l = 0
+          // o stands for o 2^(M - m - 7); a row that saw nothing has l = 0
           const float f = l[nr][e] == 0.f ? 0.f : ex2_approx(M[nr][e] - m[nr][e]) / l[nr][e];
           __nv_bfloat16* dst = p.out + (((size_t)b * p.Hq + (size_t)h * p.g) * p.T + r) * c.d + g8 * VB;
 #pragma unroll
@@ -580,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, kCtas(DP)) attention_kernel(const At
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[nr][s + i][e] * f, o[nr][s + i][2 + e] * f);
+              const __nv_bfloat162 h2 =
+                  __floats2bfloat162_rn(o[nr][s + i][e] * kUnlift * f, o[nr][s + i][2 + e] * kUnlift * f);
               w[i] = l[nr][e] == 0.f ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
             }
             if (g8 * VB + 2 * s < c.d) *reinterpret_cast<uint4*>(dst + 2 * s) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -707,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, kCtas(DP)) attention_kernel(const At
       // rows 2 c4 and 2 c4 + 1 side by side in packed pairs
       const float r0 = m[nr][0] == -INFINITY ? 0.f : m[nr][0], r1 = m[nr][1] == -INFINITY ? 0.f : m[nr][1];
       const uint64_t f2 = f2_pack(f[0], f[1]), n2 = f2_pack(-r0, -r1);
-      // P enters the product as p 2^(lv + m - M) <= 2^8; the cap keeps 0 times it finite
-      const uint64_t cv2 = f2_pack(ex2_approx(fminf(lv + r0 - M[nr][0], 100.f)),
-                                   ex2_approx(fminf(lv + r1 - M[nr][1], 100.f)));
+      // P enters the product as p 2^(lv + m - M + 7) <= 2^15; the cap keeps 0 times it finite
+      const uint64_t cv2 = f2_pack(ex2_approx(fminf(lv + r0 - M[nr][0], 100.f) + kLiftLog2),
+                                   ex2_approx(fminf(lv + r1 - M[nr][1], 100.f) + kLiftLog2));
       uint64_t sum2 = 0ull;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)

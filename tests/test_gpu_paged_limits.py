@@ -1,5 +1,7 @@
 """The paged 8-bit cache at the ends of its ranges, against the plain reference
 of tests/_paged.py or the formulas themselves."""
+import math
+
 import pytest
 import torch
 
@@ -109,3 +111,40 @@ def test_granted_over_a_thousand_entries_and_refusals():
     for bad in (got[:5], got.long(), got.cpu(), ints([0, 0] * S)[::2]):
         with pytest.raises(ValueError):
             c.reserve(ints(extra), granted=bad)
+
+
+# ------------------------------------------------------------------ a long, flat tail
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("first", [True, False])
+def test_a_flat_tail_behind_one_dominant_key(code, first):
+    """2^20 tokens whose weight is 2^-25.5 of the first (or last) token's each,
+    0.022 of the output together, where a warp has a whole sequence to itself.
+
+    All tokens but the dominant one are alike (value 1; the dominant one's is
+    0), so o = N w / (1 + N w).  Bound: the bf16 rounding 2^-8 o; the fp32
+    sums, every addition off by a last place of a sum that only grows: 2^16
+    products of 16 tokens into an accumulator (2^-23 each if it truncates, 2^-7
+    o), 2^15 tiles into the sum of weights (2^-24 each, 2^-9 o); 2^-10 o for
+    the exponentials' fp32 arguments; the probabilities' fp16 rounding, 2^-32
+    each, N 2^-32 together."""
+    n, tokens = 2000, 1 << 20                               # more sequences than a wave has warps
+    c = PagedCache(n, 1, 8, 9000, 128, tokens // 128, 1, code, device=DEV)
+    c.reserve(ints([tokens]))
+    at = 0 if first else tokens - 1
+    k, v = torch.zeros(1, 1, tokens, 8, dtype=torch.bfloat16), torch.ones(1, 1, tokens, 8, dtype=torch.bfloat16)
+    k[0, 0, at, 0] = 26.0                                   # (an e4m3 number)
+    v[0, 0, at] = 0.0
+    c.store(0, k.to(DEV), v.to(DEV))
+    page = int(c.table[0, at // 128])
+    held = float(c.k[0, page, 0, at % 128, 0].float() * c.k_scale[0, page, 0])
+    ones = c.v[0, int(c.table[0, 100]), 0].double() * c.v_scale[0, int(c.table[0, 100]), 0].double()
+    q = torch.zeros(n, 1, 1, 8, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.921875
+    out = torch.zeros_like(q)
+    c.attention(0, q, out, seqs=ints([0] * n))              # every entry reads the one sequence
+    assert c.check() == 0
+    w = (tokens - 1) * math.exp(-1.921875 * held / math.sqrt(8.0))
+    want = float(ones.mean()) * w / (1 + w)
+    assert 0.02 < want < 0.025
+    err = float((out.double() - want).abs().max())
+    assert err <= (2.0 ** -8 + 2.0 ** -7 + 2.0 ** -9 + 2.0 ** -10) * want + tokens * 2.0 ** -32, (err, want)
