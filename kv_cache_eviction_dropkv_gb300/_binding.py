@@ -108,7 +108,7 @@ def _load(path):
             ("kvcache_read_status", [P, P, ctypes.POINTER(ctypes.c_uint32)])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ctypes.c_int
-    for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k"):
+    for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k", "kvcache_test_skip_window_pair"):
         if hasattr(L, hook):
             getattr(L, hook).argtypes = [I32, I32]
             getattr(L, hook).restype = ctypes.c_int

@@ -5,7 +5,7 @@ The library links the shared CUDA runtime (libcudart.so.13), so in a process
 that imported torch first it shares torch's runtime and streams.
 
 The "test_hooks" variant (libdropkv_test_hooks.so, -DDROPKV_TEST_HOOKS) is the
-same source with the hooks of include/dropkv_test_hooks.h and a 10 ms pipeline
+same source with the hooks of include/*_test_hooks.h and a 10 ms pipeline
 wait limit; only the tests build and load it.
 """
 from __future__ import annotations

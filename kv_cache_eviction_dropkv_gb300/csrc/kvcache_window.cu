@@ -425,6 +425,10 @@ __device__ __forceinline__ void softmax_group(const WindowCall& p, Small& S, uin
   }
 }
 
+#ifdef DROPKV_TEST_HOOKS
+__device__ int g_test_skip_pair[2] = {-1, -1};    // CTA and pair that the test build leaves out
+#endif
+
 // SPLIT: P V of a tile begins on the first half of P while the softmax is at
 // the second.  With many tiles per item it shortens the chain softmax -> P V ->
 // S that bounds the kernel (32768 tokens, window 4096: 1.45 -> 1.36 ms when it
@@ -479,13 +483,17 @@ __global__ void __launch_bounds__(kWinThreads, 1)
       auto put = [&](int k_tile, int k_unit) {    // k_tile -1: the last V alone
         const uint32_t slot = pair & 1;
         if (pair >= 2 && !mbar_wait(&S.empty[slot], ((pair >> 1) + 1) & 1, &S.abort)) return false;
-        mbar_arrive_expect_tx(&S.full[slot], (k_tile >= 0 ? kLoadB : 0) + (v_tile >= 0 ? kLoadB : 0));
-        if (v_tile >= 0) {                        // needed first
+        bool load = true;
+#ifdef DROPKV_TEST_HOOKS
+        load = (int)blockIdx.x != g_test_skip_pair[0] || (int)pair != g_test_skip_pair[1];
+#endif
+        if (load) mbar_arrive_expect_tx(&S.full[slot], (k_tile >= 0 ? kLoadB : 0) + (v_tile >= 0 ? kLoadB : 0));
+        if (load && v_tile >= 0) {                // needed first
           uint8_t* dst = sm + kOffV + slot * kTileB;
           tma_load_3d(dst, &tmv, &S.full[slot], 0, v_tile * kQT, v_unit);
           if (DS > 4) tma_load_3d(dst + kHalfB, &tmv, &S.full[slot], 64, v_tile * kQT, v_unit);
         }
-        if (k_tile >= 0) {
+        if (load && k_tile >= 0) {
           uint8_t* dst = sm + kOffK + slot * kTileB;
           tma_load_3d(dst, &tmk, &S.full[slot], 0, k_tile * kQT, k_unit);
           if (DS > 4) tma_load_3d(dst + kHalfB, &tmk, &S.full[slot], 64, k_tile * kQT, k_unit);
@@ -717,3 +725,11 @@ cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUte
 }
 
 }  // namespace kvcache
+
+#ifdef DROPKV_TEST_HOOKS
+#include "../../include/kvcache_test_hooks.h"
+extern "C" dropkv_status kvcache_test_skip_window_pair(int32_t cta, int32_t pair) {
+  const int v[2] = {cta, pair};
+  return cudaMemcpyToSymbol(kvcache::g_test_skip_pair, v, sizeof v) == cudaSuccess ? DROPKV_OK : DROPKV_ERR_CUDA;
+}
+#endif
