@@ -90,8 +90,11 @@ typedef struct {
 DROPKV_API size_t kvcache_workspace_size(const kvcache_shape* shape, int32_t Hq, int32_t T);
 
 /* In all calls `seqs` is a device int32 [n] of sequence numbers, or NULL for
- * 0 .. n - 1 (n <= shape->seqs).  A sequence named twice, or out of range, is
- * flagged and served once or not at all. */
+ * 0 .. n - 1 (n <= shape->seqs and <= 65535).  A number out of range is flagged
+ * and left out (attention writes zeros for it).  A sequence named twice is
+ * flagged and served for its first entry alone by reserve, store, fork (as a
+ * destination) and compact; attention serves every entry, and free releases
+ * the sequence once. */
 
 /* Make room for extra[i] >= 0 (device int32 [n]) more tokens of sequence
  * seqs[i]: length grows by extra[i], and pages are taken as needed.  All or
@@ -133,7 +136,9 @@ DROPKV_API dropkv_status kvcache_store(const kvcache_shape* shape, const kvcache
  * that sees nothing.  Query head h reads KV head h / (Hq / Hkv).
  *   q, out  device bf16 [n][Hq][T][d], must not overlap
  *   window  0 (all tokens; sinks ignored) or >= 1;  sinks >= 0
- * Supported: n * Hkv * max_pages * page < 2^35; n * Hq * T < 2^30.
+ * Supported: Hq * T < 2^24; n * Hkv * (max_pages * page / 32 + 3) < 2^31;
+ * n * Hq * T < 2^31 with each KV head's rows (Hq / Hkv * T) rounded up to a
+ * multiple of 16.
  * Numerics: codes and query rows enter the tensor cores as fp16 (each query
  * row scaled by a power of two first; both exact but for query elements 2^-29
  * below their row's largest), probabilities as fp16 (off by 2^-11 of
@@ -173,8 +178,7 @@ DROPKV_API dropkv_status kvcache_compact(const kvcache_shape* shape, const kvcac
                                          int32_t kept_stride, const int32_t* kept_len, void* workspace,
                                          size_t workspace_bytes, uint32_t* status, cudaStream_t stream);
 
-/* Release every page of the sequences, which become empty.  A sequence named
- * twice is released once (and not flagged). */
+/* Release every page of the sequences, which become empty. */
 DROPKV_API dropkv_status kvcache_free(const kvcache_shape* shape, const kvcache_buffers* cache, const int32_t* seqs,
                                       int32_t n, uint32_t* status, cudaStream_t stream);
 
@@ -187,6 +191,8 @@ DROPKV_API dropkv_status kvcache_free(const kvcache_shape* shape, const kvcache_
  *   lengths      device int32 [B], 0 <= n_b <= n_max, or NULL for n_max
  * Values and keys of live rows must be finite (a key tile of 128 tokens
  * enters the tensor cores whole, and 0 times an infinity is not 0).
+ * Numerics: probabilities enter the product with V as bf16 (off by 2^-8 of
+ * themselves) and are summed unrounded; sums and softmax statistics are fp32.
  * Supported: Hq % Hkv == 0; d a multiple of 8 in [8, 128]; B, Hq <= 65535;
  * n_max <= 2^30; Hq * ceil(n_max / 256) < 2^31. */
 DROPKV_API dropkv_status kvcache_window_attention(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t n_max,

@@ -12,18 +12,20 @@
 // page, so it has one K and one V scale).  The tiles of the whole call,
 // counted on the device from the lengths and the window, are dealt out to the
 // warps of one resident wave in equal contiguous runs, so ragged batches
-// leave no tail.  More than 16 rows per KV head are dealt as row groups: the
-// warps of one run, one per group, stand side by side and read the same tiles
-// at about the same time, so the cache is read from memory once.  A warp is
-// on its own: it copies its tiles with cp.async
-// into its own ring of kStages tiles (no block barrier anywhere), and keeps
-// its rows' softmax state and outputs in registers.  A run that holds a whole
-// (sequence, head, row group) writes the output; the pieces of one that is
-// cut by run borders go to the workspace and a second kernel joins them in
-// run order (no atomics: results do not depend on timing).  Where the table
-// or the window bounds the units tightly, the host skips the deal: few units
-// go to a CTA or a cluster each and are joined through shared memory, many
-// short ones to a warp each (make_attn_plan has the rules and times).
+// leave no tail.  A warp holds 8 or 16 of a KV head's rows; more are dealt as
+// row groups: the warps of one run, one per group, stand side by side and read
+// the same tiles at about the same time, so the cache is read from memory
+// once.  A warp is on its own: it copies its tiles with cp.async into its own
+// ring of kStages tiles and keeps its rows' softmax state and outputs in
+// registers; no barrier of the block stands in its loop.  A run that holds a
+// whole unit (sequence, head, row group) writes the output; the pieces of one
+// that is cut by run borders go to the workspace and a second kernel joins
+// them in run order (no atomics: results do not depend on timing).  Where the
+// table or the window bounds the units tightly, the host skips the deal
+// (make_attn_plan has the rules and times): few units go to a CTA or a cluster
+// each, whose warps take the tiles in turn and join through shared memory
+// behind one barrier (up to two waves of CTAs), and many short ones to a warp
+// each, with nothing to join (up to four waves).
 //
 // Per tile, on mma.m16n8k16 with the tokens on the M side, so that 8 query
 // rows fill the N side (a decode step has g = 1 to 8 rows per KV head; the
@@ -968,7 +970,8 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
     return true;
   }
   // Few units of moderate length: a cluster of 1 to 8 CTAs each, joined through
-  // shared memory, no second kernel.  More CTAs while a warp has over 2 tiles
+  // shared memory, no second kernel.  (The bounds count two CTAs an SM, also
+  // for heads of up to 64 channels, of which three fit.)  More CTAs while a warp has over 2 tiles
   // and they fit one wave; two waves for units of at most 5 tiles a warp (64 x
   // 300 tokens: 15.8 -> 14.6 us; 48 x 1000 tokens would lose, 26.8 -> 28.9).
   int team = 1;

@@ -192,7 +192,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // One row against its 128 columns of S: moves the reference, turns S into P in
-// place.  Columns [from, to) and [0, first) are seen.  follow(factor) lets O
+// place (P is rounded to bf16, which the product with V takes and which holds
+// 2^24 above the reference as well as any value below; its sum, in fp32, is of
+// the unrounded values).  Columns [from, to) and [0, first) are seen.  follow(factor) lets O
 // follow the reference (l does here); SPLIT: before half(), which is called
 // when the first half of P is stored, else at the end, when x is dead.  The masked path is
 // kept short: this code runs four warps wide from a small instruction cache,
