@@ -148,3 +148,49 @@ def test_a_flat_tail_behind_one_dominant_key(code, first):
     assert 0.02 < want < 0.025
     err = float((out.double() - want).abs().max())
     assert err <= (2.0 ** -8 + 2.0 ** -7 + 2.0 ** -9 + 2.0 ** -10) * want + tokens * 2.0 ** -32, (err, want)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_attention_over_the_longest_sequence(code):
+    """2^31 - 128 tokens, all pages one page: positions at the end of 32 bits.
+
+    Without a window the weights are the page's own, repeated (the last row
+    sees every token, the one before all but one of 2^31).  Bound: the tests'
+    2^-8 |o| + 2^-10 V, and the fp32 sums over a warp's 2^26 / 912 tiles at
+    least: two additions a tile into an accumulator, 2^-23 V each if it
+    truncates, one of its sum of weights, 2^-24 |o| each."""
+    page, d = 128, 8
+    M = (1 << 31) // page - 1
+    c = PagedCache(1, 1, d, 2, page, M, 1, code, Hq=2, T=2, device=DEV)
+    c.table.zero_()
+    c.count.fill_(1)
+    c.length.fill_(page)
+    c.refs[0] = 1
+    k, v = (draw_rows(1, 1, page, d, 3 + i) for i in range(2))
+    c.store(0, k.to(DEV), v.to(DEV))
+    kk, vv = (x[0, 0, 0].double() * s[0, 0, 0].double() for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    c.count.fill_(M)
+    c.length.fill_(M * page)
+    q = draw_rows(1, 2, 2, d, 9, spread=0.3).to(DEV)
+    out = torch.full_like(q, 7.0)
+    c.attention(0, q, out)
+    assert c.check() == 0
+    x = q[0].double() @ kk.T / math.sqrt(d)                 # [head][row][page slot]
+    want, top = torch.softmax(x, -1) @ vv, float(vv.abs().max())
+    tiles = (1 << 26) / 912
+    bound = (2.0 ** -8 + tiles * 2.0 ** -24) * want.abs() + (2.0 ** -10 + 2 * tiles * 2.0 ** -23) * top
+    assert torch.all((out[0].double() - want).abs() <= bound)
+    for window, sinks in ((1000, 5), (1, 0), (1, 200), (130, (1 << 31) - 1 if code == "int8" else 64)):
+        out.fill_(7.0)
+        c.attention(0, q, out, window=window, sinks=sinks)
+        assert c.check() == 0
+        for t in range(2):
+            p = M * page - 2 + t
+            seen = list(range(max(0, p - window + 1), p + 1)) if sinks <= 200 else None
+            if seen is None:                                # every token is a first token
+                w, bd = want[:, t], bound[:, t]
+            else:
+                j = torch.tensor(list(range(min(sinks, seen[0]))) + seen, device=DEV) % page
+                w = torch.softmax(x[:, t][:, j], -1) @ vv[j]
+                bd = 1.125 * (2.0 ** -8 * w.abs() + 2.0 ** -10 * top)
+            assert torch.all((out[0, :, t].double() - w).abs() <= bd), (window, sinks, t)
