@@ -703,7 +703,7 @@ cudaError_t launch_compact_pages(const PageCall& p, int sms, cudaStream_t st) {
   const bool int8 = c.code == KVCACHE_INT8;
   // (new page, layer, head)s there can be
   const long long most =
-      std::min<long long>(c.P, (long long)p.n * ((p.kept_stride + c.page - 1) / c.page)) * c.layers * c.Hkv;
+      std::min<long long>(c.P, p.n * (((long long)p.kept_stride + c.page - 1) / c.page)) * c.layers * c.Hkv;
   if (most <= kBook / kGatherTeam && p.early) {
     auto one = c.d % 16 == 0 ? (int8 ? compact_one_kernel<16, KVCACHE_INT8> : compact_one_kernel<16, KVCACHE_E4M3>)
                              : (int8 ? compact_one_kernel<8, KVCACHE_INT8> : compact_one_kernel<8, KVCACHE_E4M3>);
