@@ -9,3 +9,4 @@ from ._binding import (DropKVError, dropkv_compact, dropkv_read_status, dropkv_s
                        dropkv_shape, dropkv_version, dropkv_workspace_size, make_shape)
 from .api import DropKV  # noqa: F401
 from .paged import PagedCache  # noqa: F401
+from .rotary import Rotary  # noqa: F401

@@ -1,5 +1,5 @@
-"""ctypes binding of libdropkv.so (include/dropkv.h and include/kvcache.h), same
-names as the C ABI.
+"""ctypes binding of libdropkv.so (include/dropkv.h, include/kvcache.h and
+include/kvcache_step.h), same names as the C ABI.
 
 Argument marshalling only: tensors are passed as device pointers and the
 current torch stream as the CUDA stream; every step runs in the library.  If
@@ -47,6 +47,14 @@ class kvcache_shape(ctypes.Structure):
 class kvcache_buffers(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale", "refs", "table", "count", "length")]
 
+
+class kvcache_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("d", ctypes.c_int32), ("dims", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("amplitude", ctypes.c_float)]
+
+
+STEP_CALLS = ("kvcache_rotate", "kvcache_rotate_store", "kvcache_read", "kvcache_shared_attention")
 
 _lock = threading.Lock()
 _lib = None
@@ -107,6 +115,11 @@ def _load(path):
             ("kvcache_window_attention", [I32, I32, I32, I32, I32, P, P, P, P, I32, I32, P, P, P]),
             ("kvcache_read_status", [P, P, ctypes.POINTER(ctypes.c_uint32)])):
         getattr(L, name).argtypes = args
+        getattr(L, name).restype = ctypes.c_int
+    L.kvcache_shared_workspace_size.argtypes = [CS, I32, I32, I32, I32]
+    L.kvcache_shared_workspace_size.restype = SZ
+    for name in STEP_CALLS:
+        getattr(L, name).argtypes = [ctypes.c_char_p]
         getattr(L, name).restype = ctypes.c_int
     for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k", "kvcache_test_skip_window_pair"):
         if hasattr(L, hook):
@@ -343,3 +356,51 @@ def kvcache_read_status(status, stream=None):
     flags = ctypes.c_uint32(0)
     code = lib().kvcache_read_status(_ptr(status), _stream(stream), ctypes.byref(flags))
     return int(code), int(flags.value)
+
+
+# ------------------------------------------------------------------ include/kvcache_step.h
+# Its calls take one record each, packed here field by field.
+rotate_call = struct.Struct("@P" + "P3q" * 2 + "6P" + "5i0P")
+rotate_store_call = struct.Struct("@3P" + "P3q" * 3 + "6P" + "5i0P")
+read_call = struct.Struct("@9P3i0P")
+shared_attention_call = struct.Struct("@7PN2P5i0P")
+address_of = ctypes.addressof
+
+
+def step_call(name, record):
+    code = getattr(lib(), name)(record)
+    if code != 0:
+        raise DropKVError(code, name)
+
+
+def tensor_address(name, t, dtype, shape, device_index):
+    """Address of a contiguous tensor of that type and shape on the device of that index."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device_index or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous %s %s tensor on device %d, got %s %s on %s"
+                         % (name, dtype, list(shape), device_index, t.dtype, list(t.shape), t.device))
+    return t.data_ptr()
+
+
+def rows_of(name, t, shape, device_index):
+    """Address and strides of bf16 rows [sequences][heads][rows][d] (kvcache_rows)."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device_index:
+        raise ValueError("%s: expected a bf16 %s tensor on device %d, got %s %s on %s"
+                         % (name, list(shape), device_index, t.dtype, list(t.shape), t.device))
+    a, (s0, s1, s2, s3) = t.data_ptr(), t.stride()
+    if s3 != 1 or a & 15 or (s0 | s1 | s2) & 7 and any(s & 7 and n > 1 for s, n in zip((s0, s1, s2), shape)):
+        raise ValueError("%s: rows of adjacent channels on 16-byte boundaries are wanted, got strides %s"
+                         % (name, list(t.stride())))
+    return a, s0, s1, s2
+
+
+def positions_of(positions, n, rows, device_index):
+    """Address and kind of a call's positions (None, int32 [n] or [n, rows])."""
+    if positions is None:
+        return 0, 0
+    if positions.dim() == 2:
+        return tensor_address("positions", positions, torch.int32, (n, rows), device_index), 1
+    return tensor_address("positions", positions, torch.int32, (n,), device_index), 0
+
+
+def kvcache_shared_workspace_size(shape, n, Hq, T, G) -> int:
+    return int(lib().kvcache_shared_workspace_size(ctypes.byref(shape), int(n), int(Hq), int(T), int(G)))

@@ -8,9 +8,7 @@ using namespace kvcache;
 using dropkv::current_sms;
 using dropkv::ranges_overlap;
 
-namespace {
-
-bool aligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+namespace kvcache {
 
 dropkv_status check_shape(const kvcache_shape* s) {
   if (!s) return DROPKV_ERR_INVALID_ARG;
@@ -23,7 +21,6 @@ dropkv_status check_shape(const kvcache_shape* s) {
   return DROPKV_OK;
 }
 
-// The parts of a call that every entry point checks; fills the kernels' view.
 dropkv_status open_cache(const kvcache_shape* s, const kvcache_buffers* b, int32_t layer, int32_t n, uint32_t* status,
                          Cache* c) {
   const dropkv_status st = check_shape(s);
@@ -50,6 +47,10 @@ dropkv_status open_cache(const kvcache_shape* s, const kvcache_buffers* b, int32
   return DROPKV_OK;
 }
 
+}  // namespace kvcache
+
+namespace {
+
 dropkv_status open_pages(const kvcache_shape* s, const kvcache_buffers* b, int32_t n, void* workspace,
                          size_t workspace_bytes, uint32_t* status, PageCall* p) {
   const dropkv_status st = open_cache(s, b, 0, n, status, &p->c);
@@ -67,8 +68,6 @@ dropkv_status open_pages(const kvcache_shape* s, const kvcache_buffers* b, int32
   p->rows = reinterpret_cast<int32_t*>(ws + w.rows);
   return DROPKV_OK;
 }
-
-dropkv_status launched(cudaError_t e) { return e == cudaSuccess ? DROPKV_OK : DROPKV_ERR_CUDA; }
 
 dropkv_status reserve(const kvcache_shape* shape, const kvcache_buffers* cache, const int32_t* seqs, int32_t n,
                       const int32_t* extra, int32_t* granted, void* workspace, size_t workspace_bytes,

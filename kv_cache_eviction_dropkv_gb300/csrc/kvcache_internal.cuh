@@ -112,6 +112,13 @@ struct WindowCall {
 cudaError_t launch_window(const WindowCall& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           int sms, cudaStream_t st);
 
+// What every call on a cache checks; open_cache fills the kernels' view, at the layer.
+dropkv_status check_shape(const kvcache_shape* s);
+dropkv_status open_cache(const kvcache_shape* s, const kvcache_buffers* b, int32_t layer, int32_t n, uint32_t* status,
+                         Cache* c);
+inline bool aligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline dropkv_status launched(cudaError_t e) { return e == cudaSuccess ? DROPKV_OK : DROPKV_ERR_CUDA; }
+
 // Allow a kernel its dynamic shared memory on the current device, once per
 // device (the setting stays; making it at every launch costs host time).
 template <auto Kernel>
@@ -187,6 +194,42 @@ __device__ __forceinline__ uint32_t int8x4_near(const float (&near)[4], Exact ex
     for (int i = 0; i < 4; ++i) w[i] = int8_code(exact(i));
   }
   return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+// Of 8 bf16 values: the largest bit patterns without sign, low and high
+// halves apart; and the largest that is no infinity or not-a-number.
+__device__ __forceinline__ uint32_t largest2(const uint4& x) {
+  return __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+}
+__device__ __forceinline__ uint32_t largest_finite(const uint4& x) {
+  const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t lo = w4[q] & 0x7FFFu, hi = (w4[q] >> 16) & 0x7FFFu;
+    if (lo < 0x7F80u) m = max(m, lo);
+    if (hi < 0x7F80u) m = max(m, hi);
+  }
+  return m;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// The codes of 8 bf16 values at a scale (inv = 1 / scale: exact for e4m3,
+// whose scales are powers of two).
+__device__ __forceinline__ uint2 codes8(const uint4& x, float scale, float inv, int code) {
+  if (code == KVCACHE_E4M3)
+    return make_uint2(e4m3x2(bf_lo(x.x) * inv, bf_hi(x.x) * inv) | (e4m3x2(bf_lo(x.y) * inv, bf_hi(x.y) * inv) << 16),
+                      e4m3x2(bf_lo(x.z) * inv, bf_hi(x.z) * inv) | (e4m3x2(bf_lo(x.w) * inv, bf_hi(x.w) * inv) << 16));
+  const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+  uint32_t b[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float v[4] = {bf_lo(w4[2 * q]), bf_hi(w4[2 * q]), bf_lo(w4[2 * q + 1]), bf_hi(w4[2 * q + 1])};
+    const float near[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
+    b[q] = int8x4_near(near, [&](int i) { return __fdiv_rn(v[i], scale); });
+  }
+  return make_uint2(b[0], b[1]);
 }
 
 // Four codes of scale `from` rounded again at scale `to` >= from; ratio =

@@ -1,0 +1,374 @@
+// Norm and rotation of queries and keys, alone (rotate_kernel) and with the
+// store of the keys and values (rotate_store_kernel).
+//
+//   y = x rsqrt(mean(x^2) + eps) w,   (y_a, y_b) <- A (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+//
+// Both are bound by memory: each row is read once and written once, and the
+// rest has to stay under that.  A row of d <= 128 channels belongs to 16 lanes
+// (8 where d <= 64), 8 channels to a lane: channels that turn together are
+// always one lane's, so the rotation needs no exchange and the norm one sum
+// over the row's lanes.  With pairs (i, i + dims / 2) a lane has 4 channels of
+// either half and moves 8 bytes at a time, the other channels and the other
+// pairing are 8 adjacent ones.
+//
+// Angles: a position times 2^-64 turns, modulo a turn, is the low 64 bits of
+// one integer product, so no position is too far; its upper 32 bits as a
+// signed fraction of a turn go to the hardware's sine and cosine (absolute
+// error 2^-21.2 on [-pi, pi], and 3 roundings of the argument: below 2^-19
+// together, against 2^-9 for the rounding of the result to bf16).
+#include "kvcache_step_internal.cuh"
+#include "sm103_ptx.cuh"
+
+namespace kvcache {
+namespace {
+
+using dropkv::grid_dep_launch;
+using dropkv::grid_dep_wait;
+using dropkv::launch_pdl;
+
+// The 8 channels of a lane, as two runs of 4: [c0, c0 + 4), [c1, c1 + 4).
+struct Part {
+  int c0, c1;
+  bool live, turns;              // it has channels; they turn
+};
+__device__ __forceinline__ Part part_of(const Turning& how, int lane, bool half) {
+  Part a;
+  a.live = lane * 8 < how.d;
+  a.turns = lane * 8 < how.dims;
+  a.c0 = half && a.turns ? 4 * lane : 8 * lane;
+  a.c1 = half && a.turns ? how.dims / 2 + 4 * lane : 8 * lane + 4;
+  return a;
+}
+// Cosines and sines, times the amplitude, of a lane's four pairs at a position.
+struct Angle {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Angle angle_of(const Turning& how, const Part& a, int lane, long long position) {
+  Angle r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    r.c[e] = 1.f;
+    r.s[e] = 0.f;
+    if (!a.turns) continue;
+    const unsigned long long t = (unsigned long long)position * __ldg(how.turns + 4 * lane + e);
+    const float x = __fmul_rn((float)(int)(t >> 32), 1.4629180792671596e-9f);   // 2 pi / 2^32
+    r.c[e] = __fmul_rn(__cosf(x), how.amplitude);
+    r.s[e] = __fmul_rn(__sinf(x), how.amplitude);
+  }
+  return r;
+}
+__device__ __forceinline__ long long position_of(const int32_t* positions, int each, int i, int rows, int t, int first) {
+  return !positions ? (long long)first + t : each ? positions[(size_t)i * rows + t] : (long long)positions[i] + t;
+}
+
+struct Weight {
+  float w[8];
+};
+__device__ __forceinline__ Weight weight_of(const float* w, const Part& a) {
+  Weight r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r.w[e] = w && a.live ? __ldg(w + (e < 4 ? a.c0 + e : a.c1 + e - 4)) : 1.f;
+  return r;
+}
+
+// A lane's part of a row through norm and rotation, rounded to bf16 (words in
+// the order of its channels).  All L lanes of the row call it.  The operations
+// are spelt out so that both kernels round alike.
+template <bool HALF, int L>
+__device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Weight& w, const Angle& g, const Turning& how) {
+  const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w4[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
+  }
+  if (norm) {
+    auto sum_squares = [&](float scale) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = __fmul_rn(x[e], scale);
+        ss = __fmaf_rn(v, v, ss);
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+      return ss;
+    };
+    const float inv_d = __fdiv_rn(1.f, (float)how.d);
+    float ss = sum_squares(1.f), r;
+    // squares past fp32 (elements above 2^63): once more at 2^-80, where eps is
+    // nothing against them.  (All lanes: the row's own sum decides.)
+    if (__any_sync(0xffffffffu, ss == INFINITY)) {
+      const float small = sum_squares(0x1p-80f);
+      r = ss == INFINITY ? __fmul_rn(rsqrtf(__fmul_rn(small, inv_d)), 0x1p-80f)
+                         : rsqrtf(__fmaf_rn(ss, inv_d, how.eps));
+    } else {
+      r = rsqrtf(__fmaf_rn(ss, inv_d, how.eps));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w.w[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int a = HALF ? e : 2 * e, b = HALF ? 4 + e : 2 * e + 1;
+    const float xa = x[a], xb = x[b];
+    x[a] = __fmaf_rn(xa, g.c[e], -__fmul_rn(xb, g.s[e]));
+    x[b] = __fmaf_rn(xb, g.c[e], __fmul_rn(xa, g.s[e]));
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint4 load_part(const __nv_bfloat16* row, const Part& a) {
+  if (!HALF) return __ldcs(reinterpret_cast<const uint4*>(row + a.c0));
+  const uint2 lo = __ldcs(reinterpret_cast<const uint2*>(row + a.c0)), hi = __ldcs(reinterpret_cast<const uint2*>(row + a.c1));
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+template <bool HALF>
+__device__ __forceinline__ void store_part(__nv_bfloat16* row, const Part& a, const uint4& x) {
+  if (!HALF) {
+    *reinterpret_cast<uint4*>(row + a.c0) = x;
+  } else {
+    *reinterpret_cast<uint2*>(row + a.c0) = make_uint2(x.x, x.y);
+    *reinterpret_cast<uint2*>(row + a.c1) = make_uint2(x.z, x.w);
+  }
+}
+
+constexpr int kRotThreads = 256, kBatch = 4;    // heads whose loads are in flight together
+
+// A CTA takes kRotThreads / L tokens (adjacent rows, so that a head's rows are
+// one piece of memory) and `chunk` heads of either the queries or the keys:
+// angles and weights are computed once per token and chunk.
+template <bool HALF, int L>
+__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateCall p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x % L;
+  const int token = blockIdx.x * (kRotThreads / L) + threadIdx.x / L;
+  const int b = token / p.n, t = token - b * p.n;
+  const int which = (int)blockIdx.y >= p.chunks ? 1 : 0;
+  const int h0 = ((int)blockIdx.y - (which ? p.chunks : 0)) * p.chunk, h1 = min(h0 + p.chunk, p.heads[which]);
+  const Part a = part_of(p.how, lane, HALF);
+  const bool norm = p.weight[which] != nullptr;
+  bool live = b < p.B;
+  if (live && p.lengths) {
+    const int len = p.lengths[b];
+    if (len < 0 || len > p.n) {
+      if (t == 0 && lane == 0 && h0 == 0) flag(p.status, DROPKV_FLAG_BAD_LENGTH);
+      live = false;
+    } else {
+      live = t < len;
+    }
+  }
+  const Weight w = weight_of(p.weight[which], a);
+  const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
+  const Rows& in = p.in[which];
+  const __nv_bfloat16* src = in.p + (live ? b * in.seq + t * in.row : 0);
+  __nv_bfloat16* dst = p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0);
+  const long long step = (long long)p.n * p.how.d;
+  const bool mine = live && a.live;
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (mine && h + u < h1) x[u] = load_part<HALF>(src + (h + u) * in.head, a);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (h + u >= h1) break;               // (the same for all lanes)
+      x[u] = turn<HALF, L>(x[u], norm, w, g, p.how);
+      if (mine) store_part<HALF>(dst + (h + u) * step, a, x[u]);
+    }
+  }
+}
+
+// As store_kernel: a CTA holds one (page, head) of K or V in registers, so its
+// largest magnitude is known before any code is written; the rows are laid out
+// over lanes as above, and K goes through norm and rotation on the way in.
+// Further CTAs of an entry take its queries, kQueries rows per L lanes.
+constexpr int kQueries = 4;
+template <int PAGE, bool HALF, int L>
+__global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStoreCall p) {
+  constexpr int kThreads = PAGE * 2, kWarps = kThreads / 32, kPer = kThreads / L, kPasses = PAGE / kPer;
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ uint32_t s_max[kWarps];
+  const Cache& c = p.c;
+  const int tid = threadIdx.x, lane = tid % L, group = tid / L;
+  const int i = blockIdx.z;
+  const int s = p.seqs ? p.seqs[i] : i;
+  bool again = false;                       // the sequence was named before: that entry stores it
+  if (p.seqs)
+    for (int j = tid; j < i; j += kThreads) again |= p.seqs[j] == s;
+  const bool dup = p.seqs ? __syncthreads_or(again) : false;
+  if (s < 0 || s >= c.S || dup) {
+    if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_SEQ);
+    return;
+  }
+  const int len = c.length[s], held = c.count[s], cnt = p.counts ? p.counts[i] : p.rows;
+  if (cnt < 0 || cnt > p.rows || cnt > len || held < 0 || held > c.M || (long long)len > (long long)held * PAGE) {
+    if (tid == 0) flag(c.status, DROPKV_FLAG_BAD_LENGTH);
+    return;
+  }
+  const int start = len - cnt;
+  const int store_ctas = p.touched * 2 * c.Hkv;
+  if ((int)blockIdx.x >= store_ctas) {
+    // queries: items (head, row) in the order of q_out
+    const Part a = part_of(p.how, lane, HALF);
+    const Weight w = weight_of(p.q_weight, a);
+    const int first = ((int)blockIdx.x - store_ctas) * kPer * kQueries + group;
+    uint4 x[kQueries];
+    int head[kQueries], row[kQueries];
+#pragma unroll
+    for (int u = 0; u < kQueries; ++u) {
+      const int f = first + u * kPer;
+      head[u] = f / p.rows;
+      row[u] = f - head[u] * p.rows;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (head[u] >= p.Hq || row[u] >= cnt) row[u] = -1;
+      else if (a.live) x[u] = load_part<HALF>(p.q.p + i * p.q.seq + head[u] * p.q.head + row[u] * p.q.row, a);
+    }
+#pragma unroll
+    for (int u = 0; u < kQueries; ++u) {
+      const long long at = row[u] < 0 ? 0 : position_of(p.positions, p.each, i, p.rows, row[u], start);
+      x[u] = turn<HALF, L>(x[u], p.q_weight != nullptr, w, angle_of(p.how, a, lane, at), p.how);
+      if (row[u] >= 0 && a.live)
+        store_part<HALF>(p.q_out + (((size_t)i * p.Hq + head[u]) * p.rows + row[u]) * p.how.d, a, x[u]);
+    }
+    return;
+  }
+  const int which = blockIdx.x & 1, h = ((int)blockIdx.x >> 1) % c.Hkv;
+  const int col = start / PAGE + ((int)blockIdx.x >> 1) / c.Hkv;
+  if (cnt == 0 || col > (len - 1) / PAGE) return;
+  const int base = col * PAGE;              // first token of the page
+  const int r0 = max(0, start - base), r1 = min(PAGE, len - base);   // slots of the new tokens
+  const int pg = c.table[(size_t)s * c.M + col];
+  // the values' lanes have 8 adjacent channels, which do not turn
+  Part a = part_of(p.how, lane, HALF);
+  if (which) {
+    a.c0 = 8 * lane;
+    a.c1 = a.c0 + 4;
+    a.turns = false;
+  }
+  const Rows& in = p.kv[which];
+  const __nv_bfloat16* src = in.p + i * in.seq + h * in.head + ((long long)base - start) * in.row;   // of slot 0
+  uint4 x[kPasses];
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    const int r = r0 + group + u * kPer;
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (r < r1 && a.live) x[u] = load_part<HALF>(src + r * in.row, a);
+  }
+  if (pg < 0 || pg >= c.P || c.refs[pg] != 1) {
+    if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_PAGE);
+    return;
+  }
+  const size_t unit = (size_t)pg * c.Hkv + h;
+  float* scales = which ? c.vs : c.ks;
+  const float held_scale = r0 > 0 ? scales[unit] : 0.f;
+  uint8_t* dst = (which ? c.v : c.k) + unit * PAGE * c.d;
+  if (!which) {
+    const Weight w = weight_of(p.k_weight, a);
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      if (r0 + u * kPer >= r1) break;       // (the same for all threads)
+      const int r = r0 + group + u * kPer;
+      const long long at = r < r1 ? position_of(p.positions, p.each, i, p.rows, base + r - start, start) : 0;
+      x[u] = turn<HALF, L>(x[u], p.k_weight != nullptr, w, angle_of(p.how, a, lane, at), p.how);
+    }
+  }
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) m2 = __vmaxu2(m2, largest2(x[u]));
+  auto block_max = [&](uint32_t m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) s_max[tid >> 5] = m;
+    __syncthreads();
+    uint32_t r = s_max[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) r = max(r, s_max[w]);
+    __syncthreads();
+    return r;
+  };
+  uint32_t top = block_max(max(m2 & 0xFFFFu, m2 >> 16));
+  if (top >= 0x7F80u) {                     // an infinity or not-a-number: the scale is that of the others
+    uint32_t m = 0;
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) m = max(m, largest_finite(x[u]));
+    top = block_max(m);
+    if (tid == 0) flag(c.status, DROPKV_FLAG_NONFINITE);
+  }
+  const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale), inv = 1.0f / scale;
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    const int r = r0 + group + u * kPer;
+    if (r < r1 && a.live) {
+      const uint2 o = codes8(x[u], scale, inv, c.code);
+      if (HALF) {
+        *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c0) = o.x;
+        *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c1) = o.y;
+      } else {
+        *reinterpret_cast<uint2*>(dst + r * c.d + a.c0) = o;
+      }
+    }
+  }
+  if (r0 > 0 && scale > held_scale) {       // earlier tokens of the page at the new scale
+    const float ratio = held_scale / scale;
+    for (int n = tid; n < r0 * (c.d / 8); n += kThreads) {
+      uint2 o = *reinterpret_cast<const uint2*>(dst + (size_t)n * 8);
+      o.x = rescale4(o.x, held_scale, scale, ratio, c.code);
+      o.y = rescale4(o.y, held_scale, scale, ratio, c.code);
+      *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = o;
+    }
+  }
+  if (tid == 0) scales[unit] = scale;
+}
+
+}  // namespace
+
+cudaError_t launch_rotate(RotateCall p, int sms, cudaStream_t st) {
+  const int L = p.how.d <= 64 ? 8 : 16, tokens = kRotThreads / L;
+  const long long groups = ((long long)p.B * p.n + tokens - 1) / tokens;
+  const int heads[2] = {p.in[0].p ? p.heads[0] : 0, p.in[1].p ? p.heads[1] : 0};
+  // as many heads per CTA as leave every SM a few CTAs
+  p.chunk = 8;
+  while (p.chunk > 1 && groups * ((heads[0] + p.chunk - 1) / p.chunk + (heads[1] + p.chunk - 1) / p.chunk) < 8LL * sms)
+    p.chunk /= 2;
+  p.chunks = (heads[0] + p.chunk - 1) / p.chunk;
+  const dim3 grid((unsigned)groups, p.chunks + (heads[1] + p.chunk - 1) / p.chunk);
+  auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(kRotThreads), 0, st, p); };
+  if (L == 8) return p.how.half ? go(rotate_kernel<true, 8>) : go(rotate_kernel<false, 8>);
+  return p.how.half ? go(rotate_kernel<true, 16>) : go(rotate_kernel<false, 16>);
+}
+
+namespace {
+template <int PAGE>
+cudaError_t launch_rs(RotateStoreCall p, cudaStream_t st) {
+  const int L = p.how.d <= 64 ? 8 : 16, items = 2 * PAGE / L * kQueries;
+  p.touched = (int)(((long long)p.rows + PAGE - 2) / PAGE) + 1;   // most pages `rows` tokens touch
+  p.q_ctas = p.q.p ? (int)(((long long)p.Hq * p.rows + items - 1) / items) : 0;
+  const dim3 grid((unsigned)(p.touched * 2 * p.c.Hkv + p.q_ctas), 1, p.n);
+  auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(2 * PAGE), 0, st, p); };
+  if (L == 8) return p.how.half ? go(rotate_store_kernel<PAGE, true, 8>) : go(rotate_store_kernel<PAGE, false, 8>);
+  return p.how.half ? go(rotate_store_kernel<PAGE, true, 16>) : go(rotate_store_kernel<PAGE, false, 16>);
+}
+}  // namespace
+
+cudaError_t launch_rotate_store(RotateStoreCall p, cudaStream_t st) {
+  switch (p.c.page) {
+    case 32: return launch_rs<32>(p, st);
+    case 64: return launch_rs<64>(p, st);
+    case 128: return launch_rs<128>(p, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvcache

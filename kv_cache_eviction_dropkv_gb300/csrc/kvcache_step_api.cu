@@ -1,0 +1,179 @@
+// Host side of include/kvcache_step.h: argument checks and launches.  Nothing
+// here allocates device memory.
+#include <cmath>
+
+#include "kvcache_step_internal.cuh"
+
+using namespace kvcache;
+using dropkv::current_sms;
+using dropkv::ranges_overlap;
+
+namespace {
+
+dropkv_status open_rotary(const kvcache_rotary* r, Turning* t) {
+  if (!r) return DROPKV_ERR_INVALID_ARG;
+  if (r->d < 1 || r->dims < 0 || r->dims > r->d || (r->layout != KVCACHE_HALF && r->layout != KVCACHE_INTERLEAVED) ||
+      !(r->eps > 0.f) || !std::isfinite(r->eps) || !std::isfinite(r->amplitude) || (r->dims > 0 && !r->turns) ||
+      !aligned(r->turns) || !aligned(r->q_norm) || !aligned(r->k_norm))
+    return DROPKV_ERR_INVALID_ARG;
+  if (r->d % 8 != 0 || r->d > dropkv::kDPad || r->dims % 8 != 0) return DROPKV_ERR_UNSUPPORTED;
+  t->turns = reinterpret_cast<const unsigned long long*>(r->turns);
+  t->d = r->d;
+  t->dims = r->dims;
+  t->half = r->layout == KVCACHE_HALF;
+  t->eps = r->eps;
+  t->amplitude = r->amplitude;
+  return DROPKV_OK;
+}
+
+// Rows of n sequences with `heads` heads of `rows` rows each; *bytes: from the
+// first to behind the last of them.  A stride over a single item is not used.
+bool open_rows(const kvcache_rows& r, long long n, long long heads, long long rows, int d, Rows* to, size_t* bytes) {
+  const long long count[3] = {n, heads, rows};
+  long long stride[3] = {r.seq, r.head, r.row}, end = d;
+  if (!r.data || !aligned(r.data)) return false;
+  for (int i = 0; i < 3; ++i) {
+    if (count[i] <= 1) stride[i] = 0;
+    if (stride[i] < 0 || stride[i] % 8 != 0 || stride[i] > (1LL << 46) / std::max(1LL, count[i])) return false;
+    end += stride[i] * std::max(0LL, count[i] - 1);
+  }
+  to->p = static_cast<const __nv_bfloat16*>(r.data);
+  to->seq = stride[0];
+  to->head = stride[1];
+  to->row = stride[2];
+  *bytes = (size_t)end * 2;
+  return true;
+}
+
+bool dense(const Rows& r, long long n, long long heads, long long rows, int d) {
+  return (rows <= 1 || r.row == d) && (heads <= 1 || r.head == rows * d) && (n <= 1 || r.seq == heads * rows * d);
+}
+
+}  // namespace
+
+extern "C" {
+
+dropkv_status kvcache_rotate(const kvcache_rotate_call* call) {
+  if (!call) return DROPKV_ERR_INVALID_ARG;
+  RotateCall p{};
+  const dropkv_status st = open_rotary(call->rotary, &p.how);
+  if (st != DROPKV_OK) return st;
+  const int d = p.how.d;
+  if (call->B < 0 || call->n < 0 || call->Hq < 1 || call->Hkv < 1 || !call->status || !aligned(call->status, 4) ||
+      !aligned(call->positions, 4) || !aligned(call->lengths, 4) ||
+      (call->position_kind != KVCACHE_FIRST && call->position_kind != KVCACHE_EACH))
+    return DROPKV_ERR_INVALID_ARG;
+  if ((long long)call->Hq + call->Hkv > 65535 || (long long)call->B * call->n >= (1LL << 31)) return DROPKV_ERR_UNSUPPORTED;
+  if (call->B == 0 || call->n == 0 || (!call->q.data && !call->k.data)) return DROPKV_OK;
+  const kvcache_rows* in[2] = {&call->q, &call->k};
+  void* out[2] = {call->q_out, call->k_out};
+  size_t in_bytes[2] = {0, 0}, out_bytes[2] = {0, 0};
+  p.heads[0] = call->Hq;
+  p.heads[1] = call->Hkv;
+  for (int w = 0; w < 2; ++w) {
+    if (!in[w]->data) continue;
+    if (!open_rows(*in[w], call->B, p.heads[w], call->n, d, &p.in[w], &in_bytes[w]) || !out[w] || !aligned(out[w]))
+      return DROPKV_ERR_INVALID_ARG;
+    p.out[w] = static_cast<__nv_bfloat16*>(out[w]);
+    out_bytes[w] = (size_t)call->B * p.heads[w] * call->n * d * 2;
+  }
+  for (int w = 0; w < 2; ++w)
+    for (int x = 0; x < 2; ++x) {
+      if (!in[w]->data || !in[x]->data) continue;
+      const bool in_place = w == x && in[x]->data == out[w] && dense(p.in[x], call->B, p.heads[x], call->n, d);
+      if (!in_place && ranges_overlap(out[w], out_bytes[w], in[x]->data, in_bytes[x])) return DROPKV_ERR_INVALID_ARG;
+      if (w != x && ranges_overlap(out[w], out_bytes[w], out[x], out_bytes[x])) return DROPKV_ERR_INVALID_ARG;
+    }
+  p.weight[0] = call->rotary->q_norm;
+  p.weight[1] = call->rotary->k_norm;
+  p.positions = call->positions;
+  p.each = call->position_kind == KVCACHE_EACH;
+  p.lengths = call->lengths;
+  p.B = call->B;
+  p.n = call->n;
+  p.status = call->status;
+  const int sms = current_sms(nullptr);
+  if (sms <= 0) return DROPKV_ERR_CUDA;
+  return launched(launch_rotate(p, sms, call->stream));
+}
+
+dropkv_status kvcache_rotate_store(const kvcache_rotate_store_call* call) {
+  if (!call) return DROPKV_ERR_INVALID_ARG;
+  RotateStoreCall p{};
+  dropkv_status st = open_cache(call->shape, call->cache, call->layer, call->n, call->status, &p.c);
+  if (st != DROPKV_OK) return st;
+  st = open_rotary(call->rotary, &p.how);
+  if (st != DROPKV_OK) return st;
+  const int n = call->n, rows = call->rows, d = p.c.d, Hkv = p.c.Hkv;
+  if (p.how.d != d || rows < 0 || (call->q.data && call->Hq < 1) || !aligned(call->seqs, 4) ||
+      !aligned(call->counts, 4) || !aligned(call->positions, 4) ||
+      (call->position_kind != KVCACHE_FIRST && call->position_kind != KVCACHE_EACH))
+    return DROPKV_ERR_INVALID_ARG;
+  if (n == 0 || rows == 0) return DROPKV_OK;
+  const long long Hq = call->q.data ? call->Hq : 0;
+  if (Hq * rows >= (1LL << 30) || (rows / (long long)p.c.page + 2) * 2 * Hkv + Hq * rows / 16 >= (1LL << 31))
+    return DROPKV_ERR_UNSUPPORTED;
+  size_t bytes[3] = {0, 0, 0};
+  if (!open_rows(call->k, n, Hkv, rows, d, &p.kv[0], &bytes[0]) ||
+      !open_rows(call->v, n, Hkv, rows, d, &p.kv[1], &bytes[1]))
+    return DROPKV_ERR_INVALID_ARG;
+  if (call->q.data) {
+    const size_t out = (size_t)n * Hq * rows * d * 2;
+    if (!open_rows(call->q, n, Hq, rows, d, &p.q, &bytes[2]) || !call->q_out || !aligned(call->q_out) ||
+        ranges_overlap(call->q_out, out, call->q.data, bytes[2]) ||
+        ranges_overlap(call->q_out, out, call->k.data, bytes[0]) ||
+        ranges_overlap(call->q_out, out, call->v.data, bytes[1]))
+      return DROPKV_ERR_INVALID_ARG;
+  }
+  p.q_out = static_cast<__nv_bfloat16*>(call->q_out);
+  p.q_weight = call->rotary->q_norm;
+  p.k_weight = call->rotary->k_norm;
+  p.seqs = call->seqs;
+  p.counts = call->counts;
+  p.positions = call->positions;
+  p.each = call->position_kind == KVCACHE_EACH;
+  p.n = n;
+  p.Hq = (int)Hq;
+  p.rows = rows;
+  return launched(launch_rotate_store(p, call->stream));
+}
+
+dropkv_status kvcache_read(const kvcache_read_call* call) {
+  if (!call) return DROPKV_ERR_INVALID_ARG;
+  ReadCall p{};
+  const dropkv_status st = open_cache(call->shape, call->cache, call->layer, call->n, call->status, &p.c);
+  if (st != DROPKV_OK) return st;
+  if (call->rows < 0 || !aligned(call->seqs, 4) || !aligned(call->starts, 4) || !aligned(call->counts, 4))
+    return DROPKV_ERR_INVALID_ARG;
+  if (call->n == 0 || call->rows == 0) return DROPKV_OK;
+  const size_t bytes = (size_t)call->n * p.c.Hkv * call->rows * p.c.d * 2;
+  if (!call->k_out || !call->v_out || !aligned(call->k_out) || !aligned(call->v_out) ||
+      ranges_overlap(call->k_out, bytes, call->v_out, bytes))
+    return DROPKV_ERR_INVALID_ARG;
+  p.seqs = call->seqs;
+  p.starts = call->starts;
+  p.counts = call->counts;
+  p.k = static_cast<__nv_bfloat16*>(call->k_out);
+  p.v = static_cast<__nv_bfloat16*>(call->v_out);
+  p.n = call->n;
+  p.rows = call->rows;
+  return launched(launch_read(p, call->stream));
+}
+
+size_t kvcache_shared_workspace_size(const kvcache_shape* shape, int32_t n, int32_t Hq, int32_t T, int32_t G) {
+  if (check_shape(shape) != DROPKV_OK || G < 1 || G > n || n > shape->seqs || (long long)n * Hq * T > kMaxSharedRows) return 0;
+  return kvcache_workspace_size(shape, Hq, T);
+}
+
+dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call) {
+  if (!call) return DROPKV_ERR_INVALID_ARG;
+  if (call->n > 0) {
+    if (call->Hq < 1 || call->T < 1 || call->G < 1 || call->G > call->n || !call->groups || !aligned(call->groups, 4))
+      return DROPKV_ERR_INVALID_ARG;
+    if ((long long)call->Hq * call->T > kMaxSharedRows / call->n) return DROPKV_ERR_UNSUPPORTED;
+  }
+  return kvcache_attention(call->shape, call->cache, call->layer, call->seqs, call->n, call->q, call->Hq, call->T, 0, 0,
+                           call->out, call->workspace, call->workspace_bytes, call->status, call->stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,56 @@
+// Internal declarations of what surrounds the cache in a step
+// (include/kvcache_step.h): parameter blocks and launchers.
+#pragma once
+#include "../../include/kvcache_step.h"
+#include "kvcache_internal.cuh"
+
+namespace kvcache {
+
+constexpr long long kMaxSharedRows = 1 << 22;   // query rows of a shared attention call
+
+struct Rows {
+  const __nv_bfloat16* p;        // null: left out
+  long long seq, head, row;      // strides in elements
+};
+struct Turning {
+  const unsigned long long* turns;   // [dims / 2], 2^-64 turns per position
+  int d, dims, half;             // half: pair i is (i, i + dims / 2), else (2 i, 2 i + 1)
+  float eps, amplitude;
+};
+
+struct RotateCall {
+  Turning how;
+  Rows in[2];                    // queries, keys
+  __nv_bfloat16* out[2];
+  const float* weight[2];
+  int heads[2];
+  const int32_t *positions, *lengths;
+  int each;                      // 1: a position per row
+  int B, n;
+  int chunk, chunks;             // heads a CTA takes; CTAs that take the queries' heads
+  uint32_t* status;
+};
+cudaError_t launch_rotate(RotateCall p, int sms, cudaStream_t st);
+
+struct RotateStoreCall {
+  Cache c;                       // k, v, ks, vs at the layer
+  Turning how;
+  Rows q, kv[2];
+  __nv_bfloat16* q_out;
+  const float *q_weight, *k_weight;
+  const int32_t *seqs, *counts, *positions;
+  int each;
+  int n, Hq, rows;
+  int touched, q_ctas;           // pages that `rows` tokens touch at most; CTAs per entry for its queries
+};
+cudaError_t launch_rotate_store(RotateStoreCall p, cudaStream_t st);
+
+struct ReadCall {
+  Cache c;                       // k, v, ks, vs at the layer
+  const int32_t *seqs, *starts, *counts;
+  __nv_bfloat16 *k, *v;
+  int n, rows;
+};
+cudaError_t launch_read(const ReadCall& p, cudaStream_t st);
+
+}  // namespace kvcache

@@ -20,9 +20,6 @@ using dropkv::launch_pdl;
 
 constexpr int kVecs = 8;                   // vectors of 8 values a thread holds
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 template <int PAGE>
 __global__ void __launch_bounds__(PAGE * 2) store_kernel(const StoreCall p) {
   constexpr int kThreads = PAGE * 2, kWarps = kThreads / 32;   // d <= 128: PAGE * d / 8 / kThreads <= 8
@@ -74,12 +71,7 @@ __global__ void __launch_bounds__(PAGE * 2) store_kernel(const StoreCall p) {
     if (n < r1 * dv) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + (long long)n * 8));
   }
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    m2 = __vmaxu2(m2, x[u].x & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, x[u].y & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, x[u].z & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, x[u].w & 0x7FFF7FFFu);
-  }
+  for (int u = 0; u < kVecs; ++u) m2 = __vmaxu2(m2, largest2(x[u]));
   auto block_max = [&](uint32_t m) {
     m = __reduce_max_sync(0xffffffffu, m);
     if ((tid & 31) == 0) s_max[tid >> 5] = m;
@@ -94,50 +86,15 @@ __global__ void __launch_bounds__(PAGE * 2) store_kernel(const StoreCall p) {
   if (top >= 0x7F80u) {                     // an infinity or not-a-number: the scale is that of the others
     uint32_t m = 0;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const uint32_t w4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = w4[q] & 0x7FFFu, hi = (w4[q] >> 16) & 0x7FFFu;
-        if (lo < 0x7F80u) m = max(m, lo);
-        if (hi < 0x7F80u) m = max(m, hi);
-      }
-    }
+    for (int u = 0; u < kVecs; ++u) m = max(m, largest_finite(x[u]));
     top = block_max(m);
     if (tid == 0) flag(c.status, DROPKV_FLAG_NONFINITE);
   }
-  const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale);
-  if (c.code == KVCACHE_E4M3) {
-    const float inv = 1.0f / scale;         // a power of two: exact
+  const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale), inv = 1.0f / scale;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int n = r0 * dv + tid + u * kThreads;
-      if (n < r1 * dv) {
-        uint2 o;
-        o.x = e4m3x2(bf_lo(x[u].x) * inv, bf_hi(x[u].x) * inv) |
-              (e4m3x2(bf_lo(x[u].y) * inv, bf_hi(x[u].y) * inv) << 16);
-        o.y = e4m3x2(bf_lo(x[u].z) * inv, bf_hi(x[u].z) * inv) |
-              (e4m3x2(bf_lo(x[u].w) * inv, bf_hi(x[u].w) * inv) << 16);
-        *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = o;
-      }
-    }
-  } else {
-    const float inv = 1.0f / scale;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int n = r0 * dv + tid + u * kThreads;
-      if (n < r1 * dv) {
-        const uint32_t w4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t b[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float v[4] = {bf_lo(w4[2 * q]), bf_hi(w4[2 * q]), bf_lo(w4[2 * q + 1]), bf_hi(w4[2 * q + 1])};
-          const float near[4] = {v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv};
-          b[q] = int8x4_near(near, [&](int i) { return __fdiv_rn(v[i], scale); });
-        }
-        *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = make_uint2(b[0], b[1]);
-      }
-    }
+  for (int u = 0; u < kVecs; ++u) {
+    const int n = r0 * dv + tid + u * kThreads;
+    if (n < r1 * dv) *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = codes8(x[u], scale, inv, c.code);
   }
   if (r0 > 0 && scale > held_scale) {       // earlier tokens of the page at the new scale
     const float ratio = held_scale / scale;

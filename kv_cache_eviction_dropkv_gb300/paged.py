@@ -36,18 +36,20 @@ class PagedCache:
     [seqs, max_pages], count and length [seqs]."""
 
     def __init__(self, seqs: int, Hkv: int, d: int, pages: int, page: int = 64, max_pages: Optional[int] = None,
-                 layers: int = 1, code: str = "e4m3", Hq: Optional[int] = None, T: int = 1, device=None):
+                 layers: int = 1, code: str = "e4m3", Hq: Optional[int] = None, T: int = 1, device=None,
+                 groups: int = 0):
         """pages: pages in the pool; page: tokens per page (32, 64 or 128);
         max_pages: most pages of one sequence (default: all; attention over
         short sequences is faster with a bound near their length); code: "e4m3" or
         "int8"; Hq, T: query heads (default: Hkv) and most query rows per
-        sequence of an attention() call (they size the workspace)."""
+        sequence of an attention() call (they size the workspace), groups: most
+        groups of a shared_attention() call (0: there are none)."""
         if code not in B.CACHE_CODES:
             raise ValueError("code must be one of %s" % sorted(B.CACHE_CODES))
         max_pages = pages if max_pages is None else max_pages
         self.layers, self.Hkv, self.d, self.page, self.pages = int(layers), int(Hkv), int(d), int(page), int(pages)
         self.seqs, self.max_pages, self.code = int(seqs), int(max_pages), code
-        self.Hq, self.T = int(Hkv if Hq is None else Hq), int(T)
+        self.Hq, self.T, self.groups = int(Hkv if Hq is None else Hq), int(T), int(groups)
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         if self.device.type != "cuda":
             raise ValueError("the cache lives on a CUDA device")
@@ -58,6 +60,11 @@ class PagedCache:
             ws = B.kvcache_workspace_size(self.shape, self.Hq, self.T)
             if ws == 0:
                 raise B.DropKVError(6, "kvcache_workspace_size")
+            if self.groups:
+                shared = B.kvcache_shared_workspace_size(self.shape, self.seqs, self.Hq, self.T, self.groups)
+                if shared == 0:
+                    raise B.DropKVError(6, "kvcache_shared_workspace_size")
+                ws = max(ws, shared)
             dev = self.device
             self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
             self.status = torch.zeros(1, dtype=torch.int32, device=dev)
@@ -147,6 +154,74 @@ class PagedCache:
         want, bf16 = (n, Hq, T, self.d), torch.bfloat16
         self._call(B.ATTENTION, stream, n, self._entries(seqs, n), self._tensor("q", q, bf16, want), 0, 0,
                    self._tensor("out", out, bf16, want), self._layer(layer), Hq, T, window, sinks)
+
+    def store_rotated(self, layer, rotary, q, k, v, q_out, positions=None, counts=None, seqs=None, stream=None):
+        """store() of keys that go through `rotary` (a Rotary of this device and
+        d) on the way, and the same tokens' queries into q_out: what
+        rotary.apply() and store() do in two calls, with the same results.  q
+        [n, Hq, rows, d] (or None, with q_out None), k, v [n, Hkv, rows, d] bf16 of
+        any strides with adjacent channels; q_out contiguous.  positions: int32
+        [n] (row t stands at positions[i] + t) or [n, rows]; None: each token at
+        its place in its sequence, which after an eviction is not its position.
+        Queries from counts[i] on are left as they were."""
+        n, _, rows, _ = k.shape
+        want, i = (n, self.Hkv, rows, self.d), self._index
+        if rotary._index != i or rotary.d != self.d:
+            raise ValueError("the rotary is one of %d channels on device %d" % (rotary.d, rotary._index))
+        Hq = 0 if q is None else q.shape[1]
+        of_q = (0, 0, 0, 0) if q is None else B.rows_of("q", q, (n, Hq, rows, self.d), i)
+        of_k, of_v = B.rows_of("k", k, want, i), B.rows_of("v", v, want, i)
+        out = 0 if q is None else self._tensor("q_out", q_out, torch.bfloat16, (n, Hq, rows, self.d))
+        at, kind = B.positions_of(positions, n, rows, i)
+        cnt = 0 if counts is None else self._ints("counts", counts, n)
+        entries, layer = self._entries(seqs, n), self._layer(layer)
+        if n == 0 or rows == 0:
+            return
+        if Hq == 0:
+            of_q = (0, 0, 0, 0)
+        self._step("kvcache_rotate_store", stream, lambda st: B.rotate_store_call.pack(
+            *self._fixed[:2], rotary.address, *of_q, *of_k, *of_v, out, entries, cnt, at, self._fixed[4], st,
+            layer, n, Hq, rows, kind))
+
+    def read(self, layer, k_out, v_out, starts=None, counts=None, seqs=None, stream=None):
+        """Tokens starts[i] .. starts[i] + counts[i] - 1 (int32 [n]; default: all
+        from the first on) of sequence seqs[i] in `layer` as bf16 rows 0 .. of
+        k_out, v_out [n, Hkv, rows, d]; rows from counts[i] on are left as they
+        were.  What a scoring of the cached tokens reads."""
+        n, _, rows, _ = k_out.shape
+        want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
+        out = (self._tensor("k_out", k_out, bf16, want), self._tensor("v_out", v_out, bf16, want))
+        ints = [0 if t is None else self._ints(name, t, n) for name, t in (("starts", starts), ("counts", counts))]
+        entries, layer = self._entries(seqs, n), self._layer(layer)
+        if n == 0 or rows == 0:
+            return
+        self._step("kvcache_read", stream, lambda st: B.read_call.pack(
+            *self._fixed[:2], entries, *ints, *out, self._fixed[4], st, layer, n, rows))
+
+    def shared_attention(self, layer, q, out, groups, seqs=None, stream=None):
+        """attention() without a window for entries in groups (int32 [G + 1]:
+        group j is entries groups[j] .. groups[j + 1] - 1) of sequences that begin
+        with the same pages, forks of one sequence for instance: those pages
+        are found by their numbers and read once for the whole group."""
+        n, Hq, T, _ = q.shape
+        G = groups.shape[0] - 1
+        if T > self.T or Hq != self.Hq or G > self.groups:
+            raise ValueError("the workspace is sized for %d query heads, at most %d rows and %d groups, got %d, %d and %d"
+                             % (self.Hq, self.T, self.groups, Hq, T, G))
+        want, bf16 = (n, Hq, T, self.d), torch.bfloat16
+        at, to, starts = self._tensor("q", q, bf16, want), self._tensor("out", out, bf16, want), self._ints("groups", groups, G + 1)
+        entries, layer = self._entries(seqs, n), self._layer(layer)
+        if T == 0 or n == 0:
+            return
+        self._step("kvcache_shared_attention", stream, lambda st: B.shared_attention_call.pack(
+            *self._fixed[:2], entries, starts, at, to, *self._fixed[2:5], st, layer, n, Hq, T, G))
+
+    def _step(self, name, stream, record):
+        """The library's call `name`; record(stream) packs it."""
+        if B.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self._step(name, stream, record)
+        B.step_call(name, record(B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream)))
 
     # -------------------------------------------------------------- whole sequences
     def fork(self, src, dst, stream=None):
