@@ -35,7 +35,7 @@ extern "C" {
  * turns[i] / 2^64.  The other channels keep y.  A position is any 32-bit
  * number: position * turns[i] modulo 2^64 is the angle without error, so far
  * positions lose nothing.  Sums and products are fp32 (the sine and cosine are
- * off by 2^-19 at most), results are rounded once, to bf16.
+ * off by 2^-23 at most), results are rounded once, to bf16.
  * Supported: d a multiple of 8 in [8, 128]; dims a multiple of 8 in [0, d];
  * eps > 0; both finite. */
 typedef struct {

@@ -90,6 +90,9 @@ struct AttnCall {
   float4* part_s;                // [workers][2][RB] (m, l, M, unused)
   int2* cuts;                    // by_unit: [units][RG] (first run or -1, last run); else [workers] (unit or -1, last run)
   float scale_log2;
+  const int32_t* from;           // a shared attention's second half: first token of each entry
+  float* own_o;                  // and what it leaves of units that no run border cuts: [n * Hq * T][d]
+  float4* own_s;                 // [n * Hq * T] (m, l, M, unused)
 };
 struct AttnPlan {
   int RB, RG, workers, solo, team, by_unit, rowwise;
@@ -100,6 +103,7 @@ bool make_attn_plan(const kvcache_shape& s, int n, int Hq, int T, int window, in
 // Workspace bytes that hold for every attention call of at most T rows on the cache.
 size_t attn_workspace_bound(const kvcache_shape& s, int Hq, int T, int sms);
 cudaError_t launch_attention(const AttnCall& p, cudaStream_t st);
+cudaError_t launch_own_attention(const AttnCall& p, cudaStream_t st);   // a shared attention's second half
 
 struct WindowCall {
   const __nv_bfloat16* q;        // [B][Hq][n_max][d]
@@ -194,6 +198,22 @@ __device__ __forceinline__ uint32_t int8x4_near(const float (&near)[4], Exact ex
     for (int i = 0; i < 4; ++i) w[i] = int8_code(exact(i));
   }
   return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+// Four codes (bytes 0..3 of w) as two fp16 pairs (0, 1) and (2, 3).
+template <int CODE>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  if constexpr (CODE == KVCACHE_E4M3) {
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(h01), "=r"(h23)
+        : "r"(w));
+  } else {
+    // bytes as the low bits of fp16 1024 + (code + 128), minus 1152: exact
+    const uint32_t x = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h01) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h23) : "r"(b), "r"(0x64806480u));
+  }
 }
 
 // Of 8 bf16 values: the largest bit patterns without sign, low and high

@@ -12,10 +12,13 @@
 // pairing are 8 adjacent ones.
 //
 // Angles: a position times 2^-64 turns, modulo a turn, is the low 64 bits of
-// one integer product, so no position is too far; its upper 32 bits as a
-// signed fraction of a turn go to the hardware's sine and cosine (absolute
-// error 2^-21.2 on [-pi, pi], and 3 roundings of the argument: below 2^-19
-// together, against 2^-9 for the rounding of the result to bf16).
+// one integer product, so no position is too far.  The nearest quarter turn
+// comes off in integers too; what is left is at most an eighth of a turn and
+// goes through the Taylor series of sine and cosine in turns (terms left out
+// below 2^-29; the results are within 1.3 2^-24, which the hardware's own sine
+// and cosine, 2^-20 off with their argument, are not: with those, five times
+// as many keys came out of the rounding to bf16 as a neighbour of the value
+// that 64 bits give).
 #include "kvcache_step_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -43,6 +46,25 @@ __device__ __forceinline__ Part part_of(const Turning& how, int lane, bool half)
 struct Angle {
   float c[4], s[4];
 };
+__device__ __forceinline__ void cos_sin_turns(unsigned long long t, float& c, float& s) {
+  const uint32_t top = (uint32_t)(t >> 32), q = (top + 0x20000000u) >> 30;
+  const float u = __fmul_rn((float)(int)(top - (q << 30)), 0x1p-32f), z = __fmul_rn(u, u);   // |u| <= 1/8 turn
+  // sin(2 pi u) = u (2 pi - (2 pi)^3 u^2 / 6 + ...), 2 pi as a sum of two numbers
+  float a = __fmaf_rn(z, 42.058693f, -76.70586f);
+  a = __fmaf_rn(z, a, 81.60525f);
+  a = __fmaf_rn(z, a, -41.3417f);
+  a = __fmaf_rn(z, a, -1.7484555e-7f);
+  a = __fmaf_rn(u, 6.2831855f, __fmul_rn(u, a));
+  float b = __fmaf_rn(z, -26.426256f, 60.24464f);
+  b = __fmaf_rn(z, b, -85.45682f);
+  b = __fmaf_rn(z, b, 64.93939f);
+  b = __fmaf_rn(z, b, -19.739208f);
+  b = __fmaf_rn(z, b, 1.f);
+  // quarter turns: (c, s) -> (-s, c)
+  const float x = q & 1 ? a : b, y = q & 1 ? b : a;
+  c = (q + 1) & 2 ? -x : x;
+  s = q & 2 ? -y : y;
+}
 __device__ __forceinline__ Angle angle_of(const Turning& how, const Part& a, int lane, long long position) {
   Angle r;
 #pragma unroll
@@ -50,10 +72,9 @@ __device__ __forceinline__ Angle angle_of(const Turning& how, const Part& a, int
     r.c[e] = 1.f;
     r.s[e] = 0.f;
     if (!a.turns) continue;
-    const unsigned long long t = (unsigned long long)position * __ldg(how.turns + 4 * lane + e);
-    const float x = __fmul_rn((float)(int)(t >> 32), 1.4629180792671596e-9f);   // 2 pi / 2^32
-    r.c[e] = __fmul_rn(__cosf(x), how.amplitude);
-    r.s[e] = __fmul_rn(__sinf(x), how.amplitude);
+    cos_sin_turns((unsigned long long)position * __ldg(how.turns + 4 * lane + e), r.c[e], r.s[e]);
+    r.c[e] = __fmul_rn(r.c[e], how.amplitude);
+    r.s[e] = __fmul_rn(r.s[e], how.amplitude);
   }
   return r;
 }
@@ -84,11 +105,11 @@ __device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Weight&
     x[2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
   }
   if (norm) {
-    auto sum_squares = [&](float scale) {
+    auto sum_squares = [&](auto scale) {
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = __fmul_rn(x[e], scale);
+        const float v = scale(x[e]);
         ss = __fmaf_rn(v, v, ss);
       }
 #pragma unroll
@@ -96,11 +117,11 @@ __device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Weight&
       return ss;
     };
     const float inv_d = __fdiv_rn(1.f, (float)how.d);
-    float ss = sum_squares(1.f), r;
+    float ss = sum_squares([](float v) { return v; }), r;
     // squares past fp32 (elements above 2^63): once more at 2^-80, where eps is
     // nothing against them.  (All lanes: the row's own sum decides.)
     if (__any_sync(0xffffffffu, ss == INFINITY)) {
-      const float small = sum_squares(0x1p-80f);
+      const float small = sum_squares([](float v) { return __fmul_rn(v, 0x1p-80f); });
       r = ss == INFINITY ? __fmul_rn(rsqrtf(__fmul_rn(small, inv_d)), 0x1p-80f)
                          : rsqrtf(__fmaf_rn(ss, inv_d, how.eps));
     } else {
@@ -141,7 +162,32 @@ __device__ __forceinline__ void store_part(__nv_bfloat16* row, const Part& a, co
   }
 }
 
-constexpr int kRotThreads = 256, kBatch = 4;    // heads whose loads are in flight together
+constexpr int kBatch = 4;                       // heads whose loads are in flight together
+
+// One token's rows of heads [h0, h1), `from` and `to` those of head 0.  All
+// lanes of the warp walk `chunk` heads.
+template <bool HALF, int L>
+__device__ __forceinline__ void turn_heads(const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
+                                           long long to_step, int h0, int h1, int chunk, bool norm, const Weight& w,
+                                           const Angle& g, const Part& a, const Turning& how) {
+#pragma unroll 1
+  for (int k = 0; k < chunk; k += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (a.live && h0 + k + u < h1) x[u] = load_part<HALF>(from + (h0 + k + u) * from_step, a);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (k + u >= chunk) break;
+      x[u] = turn<HALF, L>(x[u], norm, w, g, how);
+      if (a.live && h0 + k + u < h1) store_part<HALF>(to + (h0 + k + u) * to_step, a, x[u]);
+    }
+  }
+}
+
+constexpr int kRotThreads = 256;
 
 // A CTA takes kRotThreads / L tokens (adjacent rows, so that a head's rows are
 // one piece of memory) and `chunk` heads of either the queries or the keys:
@@ -170,31 +216,17 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateCall p)
   const Weight w = weight_of(p.weight[which], a);
   const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
   const Rows& in = p.in[which];
-  const __nv_bfloat16* src = in.p + (live ? b * in.seq + t * in.row : 0);
-  __nv_bfloat16* dst = p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0);
-  const long long step = (long long)p.n * p.how.d;
-  const bool mine = live && a.live;
-  for (int h = h0; h < h1; h += kBatch) {
-    uint4 x[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (mine && h + u < h1) x[u] = load_part<HALF>(src + (h + u) * in.head, a);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (h + u >= h1) break;               // (the same for all lanes)
-      x[u] = turn<HALF, L>(x[u], norm, w, g, p.how);
-      if (mine) store_part<HALF>(dst + (h + u) * step, a, x[u]);
-    }
-  }
+  turn_heads<HALF, L>(in.p + (live ? b * in.seq + t * in.row : 0), in.head,
+                      p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0),
+                      (long long)p.n * p.how.d, h0, live ? h1 : 0, p.chunk, norm, w, g, a, p.how);
 }
 
 // As store_kernel: a CTA holds one (page, head) of K or V in registers, so its
 // largest magnitude is known before any code is written; the rows are laid out
 // over lanes as above, and K goes through norm and rotation on the way in.
-// Further CTAs of an entry take its queries, kQueries rows per L lanes.
-constexpr int kQueries = 4;
+// Further CTAs of an entry take its queries: L lanes one token's of q_chunk
+// heads, so that the angles (as much work as a row's norm and rotation) are
+// computed once for all of them.
 template <int PAGE, bool HALF, int L>
 __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStoreCall p) {
   constexpr int kThreads = PAGE * 2, kWarps = kThreads / 32, kPer = kThreads / L, kPasses = PAGE / kPer;
@@ -221,28 +253,15 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
   const int start = len - cnt;
   const int store_ctas = p.touched * 2 * c.Hkv;
   if ((int)blockIdx.x >= store_ctas) {
-    // queries: items (head, row) in the order of q_out
+    const int item = ((int)blockIdx.x - store_ctas) * kPer + group;
+    const int row = item % p.rows, h0 = item / p.rows * p.q_chunk;
+    const int h1 = row < cnt ? min(h0 + p.q_chunk, p.Hq) : 0;
     const Part a = part_of(p.how, lane, HALF);
     const Weight w = weight_of(p.q_weight, a);
-    const int first = ((int)blockIdx.x - store_ctas) * kPer * kQueries + group;
-    uint4 x[kQueries];
-    int head[kQueries], row[kQueries];
-#pragma unroll
-    for (int u = 0; u < kQueries; ++u) {
-      const int f = first + u * kPer;
-      head[u] = f / p.rows;
-      row[u] = f - head[u] * p.rows;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (head[u] >= p.Hq || row[u] >= cnt) row[u] = -1;
-      else if (a.live) x[u] = load_part<HALF>(p.q.p + i * p.q.seq + head[u] * p.q.head + row[u] * p.q.row, a);
-    }
-#pragma unroll
-    for (int u = 0; u < kQueries; ++u) {
-      const long long at = row[u] < 0 ? 0 : position_of(p.positions, p.each, i, p.rows, row[u], start);
-      x[u] = turn<HALF, L>(x[u], p.q_weight != nullptr, w, angle_of(p.how, a, lane, at), p.how);
-      if (row[u] >= 0 && a.live)
-        store_part<HALF>(p.q_out + (((size_t)i * p.Hq + head[u]) * p.rows + row[u]) * p.how.d, a, x[u]);
-    }
+    const Angle g = angle_of(p.how, a, lane, position_of(p.positions, p.each, i, p.rows, row, start));
+    turn_heads<HALF, L>(p.q.p + i * p.q.seq + row * p.q.row, p.q.head,
+                        p.q_out + ((size_t)i * p.Hq * p.rows + row) * p.how.d, (long long)p.rows * p.how.d, h0, h1,
+                        p.q_chunk, p.q_weight != nullptr, w, g, a, p.how);
     return;
   }
   const int which = blockIdx.x & 1, h = ((int)blockIdx.x >> 1) % c.Hkv;
@@ -352,10 +371,11 @@ cudaError_t launch_rotate(RotateCall p, int sms, cudaStream_t st) {
 namespace {
 template <int PAGE>
 cudaError_t launch_rs(RotateStoreCall p, cudaStream_t st) {
-  const int L = p.how.d <= 64 ? 8 : 16, items = 2 * PAGE / L * kQueries;
+  const int L = p.how.d <= 64 ? 8 : 16, per = 2 * PAGE / L;
   p.touched = (int)(((long long)p.rows + PAGE - 2) / PAGE) + 1;   // most pages `rows` tokens touch
-  p.q_ctas = p.q.p ? (int)(((long long)p.Hq * p.rows + items - 1) / items) : 0;
-  const dim3 grid((unsigned)(p.touched * 2 * p.c.Hkv + p.q_ctas), 1, p.n);
+  p.q_chunk = p.rows >= PAGE ? 8 : 4;
+  const int q_ctas = p.q.p ? (int)(((long long)((p.Hq + p.q_chunk - 1) / p.q_chunk) * p.rows + per - 1) / per) : 0;
+  const dim3 grid((unsigned)(p.touched * 2 * p.c.Hkv + q_ctas), 1, p.n);
   auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(2 * PAGE), 0, st, p); };
   if (L == 8) return p.how.half ? go(rotate_store_kernel<PAGE, true, 8>) : go(rotate_store_kernel<PAGE, false, 8>);
   return p.how.half ? go(rotate_store_kernel<PAGE, true, 16>) : go(rotate_store_kernel<PAGE, false, 16>);

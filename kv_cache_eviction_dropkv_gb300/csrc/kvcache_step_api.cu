@@ -49,6 +49,35 @@ bool dense(const Rows& r, long long n, long long heads, long long rows, int d) {
   return (rows <= 1 || r.row == d) && (heads <= 1 || r.head == rows * d) && (n <= 1 || r.seq == heads * rows * d);
 }
 
+// The workspace of a shared attention (byte offsets); the second half's parts
+// and cuts have the sizes given.
+struct SharedSpace {
+  size_t plan, entries, groups, piece_o, piece_s, own_o, own_s, part_o, part_s, cuts, total;
+};
+SharedSpace make_shared_space(const kvcache_shape& s, int n, int Hq, int T, int G, int sms, size_t part_o, size_t part_s,
+                              size_t cuts) {
+  SharedSpace w;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += (bytes + 255) / 256 * 256;
+    return x;
+  };
+  const size_t rows = (size_t)n * Hq * T, pieces = (size_t)sms * 256 + 2 * rows;
+  w.plan = take(sizeof(SharedPlan));
+  w.entries = take((size_t)n * 3 * 4);
+  w.groups = take(((size_t)G * 4 + 1) * 4);
+  w.piece_o = take(pieces * s.d * 4);
+  w.piece_s = take(pieces * 16);
+  w.own_o = take(rows * s.d * 4);
+  w.own_s = take(rows * 16);
+  w.part_o = take(part_o);
+  w.part_s = take(part_s);
+  w.cuts = take(cuts);
+  w.total = at;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -161,19 +190,71 @@ dropkv_status kvcache_read(const kvcache_read_call* call) {
 }
 
 size_t kvcache_shared_workspace_size(const kvcache_shape* shape, int32_t n, int32_t Hq, int32_t T, int32_t G) {
-  if (check_shape(shape) != DROPKV_OK || G < 1 || G > n || n > shape->seqs || (long long)n * Hq * T > kMaxSharedRows) return 0;
-  return kvcache_workspace_size(shape, Hq, T);
+  const int sms = current_sms(nullptr);
+  if (sms <= 0 || check_shape(shape) != DROPKV_OK || Hq < 1 || T < 1 || Hq % shape->Hkv != 0 || G < 1 || G > n ||
+      n > shape->seqs || n > 65535 || (long long)Hq * T > kMaxSharedRows / n)
+    return 0;
+  // the second half's pieces at their most, for any number of entries up to n
+  SharedSpace w = make_shared_space(*shape, n, Hq, T, G, sms, 0, 0, 0);
+  return w.total + attn_workspace_bound(*shape, Hq, T, sms) + (size_t)n * shape->Hkv * ((Hq / shape->Hkv * T + 7) / 8) * 8 + 256;
 }
 
 dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call) {
   if (!call) return DROPKV_ERR_INVALID_ARG;
-  if (call->n > 0) {
-    if (call->Hq < 1 || call->T < 1 || call->G < 1 || call->G > call->n || !call->groups || !aligned(call->groups, 4))
-      return DROPKV_ERR_INVALID_ARG;
-    if ((long long)call->Hq * call->T > kMaxSharedRows / call->n) return DROPKV_ERR_UNSUPPORTED;
-  }
-  return kvcache_attention(call->shape, call->cache, call->layer, call->seqs, call->n, call->q, call->Hq, call->T, 0, 0,
-                           call->out, call->workspace, call->workspace_bytes, call->status, call->stream);
+  SharedCall p{};
+  AttnCall& a = p.own;
+  const dropkv_status st = open_cache(call->shape, call->cache, call->layer, call->n, call->status, &a.c);
+  if (st != DROPKV_OK) return st;
+  const kvcache_shape& shape = *call->shape;
+  const int n = call->n, Hq = call->Hq, T = call->T;
+  if (!call->q || !call->out || !aligned(call->q) || !aligned(call->out) || Hq < 1 || T < 1 || Hq % shape.Hkv != 0 ||
+      !aligned(call->seqs, 4))
+    return DROPKV_ERR_INVALID_ARG;
+  if (n == 0) return DROPKV_OK;
+  if (call->G < 1 || call->G > n || !call->groups || !aligned(call->groups, 4)) return DROPKV_ERR_INVALID_ARG;
+  if ((long long)Hq * T > kMaxSharedRows / n) return DROPKV_ERR_UNSUPPORTED;
+  const size_t bytes = (size_t)n * Hq * T * shape.d * 2;
+  if (ranges_overlap(call->q, bytes, call->out, bytes)) return DROPKV_ERR_INVALID_ARG;
+  const int sms = current_sms(nullptr);
+  if (sms <= 0) return DROPKV_ERR_CUDA;
+  AttnPlan plan{};
+  if (!make_attn_plan(shape, n, Hq, T, 0, 0, sms, &plan)) return DROPKV_ERR_UNSUPPORTED;
+  const bool by_runs = !plan.team && !plan.solo;
+  const SharedSpace w = make_shared_space(shape, n, Hq, T, call->G, sms, by_runs ? plan.part_s : 0,
+                                          by_runs ? plan.cuts - plan.part_s : 0,
+                                          by_runs ? (size_t)n * shape.Hkv * plan.RG * 8 : 0);
+  if (!call->workspace || call->workspace_bytes < w.total || !aligned(call->workspace)) return DROPKV_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(call->workspace);
+  a.seqs = call->seqs;
+  a.n = n; a.Hq = Hq; a.T = T;
+  a.g = Hq / shape.Hkv;
+  a.R = a.g * T;
+  a.RB = plan.RB; a.RG = plan.RG; a.workers = plan.workers; a.solo = plan.solo; a.team = plan.team;
+  a.by_unit = 1;
+  a.q = static_cast<const __nv_bfloat16*>(call->q);
+  a.out = static_cast<__nv_bfloat16*>(call->out);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_s = reinterpret_cast<float4*>(ws + w.part_s);
+  a.cuts = reinterpret_cast<int2*>(ws + w.cuts);
+  a.own_o = reinterpret_cast<float*>(ws + w.own_o);
+  a.own_s = reinterpret_cast<float4*>(ws + w.own_s);
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)shape.d));
+  p.by_runs = by_runs;
+  p.groups = call->groups;
+  p.G = call->G;
+  p.sms = sms;
+  p.plan = reinterpret_cast<SharedPlan*>(ws + w.plan);
+  p.from = reinterpret_cast<int32_t*>(ws + w.entries);
+  p.group = p.from + n;
+  p.bound = p.group + n;
+  p.lead = reinterpret_cast<int32_t*>(ws + w.groups);
+  p.active = p.lead + call->G;
+  p.prefix = p.active + call->G;
+  p.first = reinterpret_cast<uint32_t*>(p.prefix + call->G);
+  p.piece_o = reinterpret_cast<float*>(ws + w.piece_o);
+  p.piece_s = reinterpret_cast<float4*>(ws + w.piece_s);
+  a.from = p.from;
+  return launched(launch_shared(p, call->stream));
 }
 
 }  // extern "C"

@@ -41,7 +41,8 @@ struct RotateStoreCall {
   const int32_t *seqs, *counts, *positions;
   int each;
   int n, Hq, rows;
-  int touched, q_ctas;           // pages that `rows` tokens touch at most; CTAs per entry for its queries
+  int touched;                   // pages that `rows` tokens touch at most
+  int q_chunk;                   // heads of one token that its lanes take
 };
 cudaError_t launch_rotate_store(RotateStoreCall p, cudaStream_t st);
 
@@ -52,5 +53,24 @@ struct ReadCall {
   int n, rows;
 };
 cudaError_t launch_read(const ReadCall& p, cudaStream_t st);
+
+// A shared attention: what its plan kernel finds out, for the kernels behind it.
+struct SharedPlan {
+  uint32_t total, runs;          // tiles of all shared parts; runs that they are dealt to
+  int unit_rows;                 // rows of a unit: 128 where no group has more per KV head, else 256
+};
+struct SharedCall {
+  AttnCall own;                  // the second half (from, own_o, own_s, parts, cuts)
+  int by_runs;                   // 1: it is dealt to runs, and cuts say which units they cut
+  const int32_t* groups;
+  int G, sms;
+  SharedPlan* plan;
+  int32_t *from, *group, *bound; // per entry: first token of its own, group, full pages before its last T tokens
+  int32_t *lead, *active, *prefix;   // per group: first sequence that takes part, how many do, shared pages
+  uint32_t* first;               // [G + 1] per group: tiles before it
+  float* piece_o;                // [sms * 256 + 2 n Hq T][d]
+  float4* piece_s;
+};
+cudaError_t launch_shared(const SharedCall& p, cudaStream_t st);
 
 }  // namespace kvcache
