@@ -39,7 +39,7 @@ using namespace dropkv;
 
 // ------------------------------------------------------------------ the plan
 constexpr int kPlanThreads = 512;
-constexpr int kCols = 128;                       // table entries a warp compares at a time
+constexpr int kPlanEntries = 1024;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -68,22 +68,45 @@ __device__ __forceinline__ int group_of(const int32_t* groups, int G, int i) {
   return lo;
 }
 
+// (The passes between two calls of this kernel sweep its code out of every
+// cache: what it takes is mostly the fetching of its instructions, so its loops
+// are short and little is unrolled.  The comparing unrolled over 8 entries took
+// 9.6 us of 15, for 64 sequences with 512 shared pages.)
+// Up to kPlanEntries entries: every CTA of the cluster works out the groups by
+// itself, in shared memory, and the CTAs share out the comparing only.  More:
+// the entries are shared out too, and the groups stand in global memory.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedCall p) {
+  __shared__ int s_start[kPlanEntries + 1], s_seq[kPlanEntries], s_bound[kPlanEntries], s_group[kPlanEntries];
+  __shared__ int s_lead[kPlanEntries], s_active[kPlanEntries], s_prefix[kPlanEntries], s_found[kPlanEntries];
+  __shared__ uint32_t s_first[kPlanEntries], s_sum[kPlanThreads / 32];
+  __shared__ int s_most;
   grid_dep_wait();
   grid_dep_launch();
   const AttnCall& a = p.own;
   const Cache& c = a.c;
-  const int threads = kPlanThreads * cluster_ctas(), me = cluster_rank() * kPlanThreads + threadIdx.x;
-  const int lane = threadIdx.x & 31;
-  __shared__ uint32_t s_sum[kPlanThreads / 32];
-  __shared__ int s_most;
+  const int tid = threadIdx.x, lane = tid & 31, rank = cluster_rank(), ctas = cluster_ctas();
+  const int threads = kPlanThreads * ctas, me = rank * kPlanThreads + tid;
+  const bool small = a.n <= kPlanEntries;
+  const int first = small ? tid : me, step = small ? kPlanThreads : threads;   // of entries and groups
+  const int32_t* start = small ? s_start : p.groups;
+  int *bound = small ? s_bound : p.bound, *group = small ? s_group : p.group;
+  int *lead = small ? s_lead : p.lead, *active = small ? s_active : p.active, *prefix = small ? s_prefix : p.prefix;
+  auto seq_of = [&](int i) { return small ? s_seq[i] : a.seqs ? a.seqs[i] : i; };
   // groups that cover the entries in order
   bool bad = false;
-  for (int j = threadIdx.x; j <= p.G; j += kPlanThreads) {
-    const int x = p.groups[j];
-    bad |= j == 0 ? x != 0 : x < p.groups[j - 1];
-    bad |= j == p.G && x != a.n;
+  for (int j = tid; j <= p.G; j += kPlanThreads) {
+    const int x = p.groups[j], y = j > 0 ? p.groups[j - 1] : 0;
+    if (small) s_start[j] = x;
+    bad |= x < y || (j == 0 && x != 0) || (j == p.G && x != a.n);
   }
+  if (small)
+    for (int i = tid; i < a.n; i += kPlanThreads) s_seq[i] = a.seqs ? a.seqs[i] : i;
+  for (int j = first; j < p.G; j += step) {
+    lead[j] = prefix[j] = INT_MAX;
+    active[j] = 0;
+    if (small) s_found[j] = INT_MAX;
+  }
+  if (tid == 0) s_most = 0;
   if (__syncthreads_or(bad)) {
     if (me == 0) {
       flag(c.status, DROPKV_FLAG_BAD_LENGTH);
@@ -91,93 +114,116 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedCall p) 
       p.plan->runs = 1;
       p.plan->unit_rows = 128;
     }
-    for (int i = me; i < a.n; i += threads) p.from[i] = 0;
+    for (int i = me; i < a.n; i += threads) {
+      p.from[i] = 0;
+      p.info[i] = make_int4(0, 0, 0, 0);
+    }
     return;
   }
-  for (int j = me; j < p.G; j += threads) {
-    p.lead[j] = p.prefix[j] = INT_MAX;
-    p.active[j] = 0;
-  }
-  cluster_sync();
+  // (small: what the others add to the first CTA's s_found comes behind its
+  // start; they wait for that only then)
+  if (small) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  else cluster_sync();
   // sequences that hold a full page before the first row's token take part
-  for (int i = me; i < a.n; i += threads) {
-    const int s = a.seqs ? a.seqs[i] : i, g = group_of(p.groups, p.G, i);
-    int bound = 0;
+  for (int i = first; i < a.n; i += step) {
+    const int s = seq_of(i), g = group_of(start, p.G, i);
+    int full = 0;
     if (s >= 0 && s < c.S) {
       const int len = c.length[s], held = c.count[s];
       if (len >= a.T && held >= 0 && held <= c.M && (long long)len <= (long long)held << c.page_log2)
-        bound = (len - a.T + 1) >> c.page_log2;
+        full = (len - a.T + 1) >> c.page_log2;
     }
-    p.bound[i] = bound;
-    p.group[i] = g;
-    if (bound > 0) {
-      atomicMin(p.lead + g, i);
-      atomicAdd(p.active + g, 1);
-      atomicMin(p.prefix + g, bound);
+    bound[i] = full;
+    group[i] = g;
+    if (full > 0) {
+      atomicMin(lead + g, i);
+      atomicAdd(active + g, 1);
+      atomicMin(prefix + g, full);
     }
   }
-  cluster_sync();
-  const int chunks = (c.M + kCols - 1) / kCols;
-  for (long long item = me >> 5; item < (long long)a.n * chunks; item += threads >> 5) {
-    const int i = (int)(item / chunks), col0 = (int)(item - (long long)i * chunks) * kCols;
-    const int g = p.group[i], end = min(p.prefix[g], col0 + kCols);   // (others may lower it meanwhile: it stays an end)
-    if (p.bound[i] == 0 || p.active[g] < 2 || col0 >= end) continue;
-    const int lead = p.lead[g];
-    const int32_t* mine = c.table + (size_t)(a.seqs ? a.seqs[i] : i) * c.M;
-    const int32_t* other = c.table + (size_t)(a.seqs ? a.seqs[lead] : lead) * c.M;
+  if (small) __syncthreads();
+  else cluster_sync();
+  // `parts` warps compare an entry's columns with those of its group's first
+  int* found = small ? s_found : p.prefix;
+  const int warps = threads >> 5, parts = max(1, warps / a.n);
+  for (long long item = me >> 5; item < (long long)a.n * parts; item += warps) {
+    const int i = (uint32_t)item % (uint32_t)a.n, part = (uint32_t)item / (uint32_t)a.n, g = group[i];
+    if (bound[i] == 0 || active[g] < 2) continue;
+    const int32_t* mine = c.table + (size_t)seq_of(i) * c.M;
+    const int32_t* other = c.table + (size_t)seq_of(lead[g]) * c.M;
+    const int end = prefix[g];                    // (others may lower it meanwhile: it stays an end)
     int differs = INT_MAX;
-#pragma unroll
-    for (int u = 0; u < kCols / 32; ++u) {
-      const int col = col0 + u * 32 + lane;
-      if (col >= end) continue;
-      const int x = mine[col];
-      if (x != other[col] || x < 0 || x >= c.P) differs = min(differs, col);
+#pragma unroll 4
+    for (int col = part * 32 + lane; col < end; col += 32 * parts) {
+      const int x = mine[col], y = other[col];
+      if (x != y || (uint32_t)x >= (uint32_t)c.P) differs = min(differs, col);
     }
     differs = __reduce_min_sync(0xffffffffu, differs);
-    if (lane == 0 && differs != INT_MAX) atomicMin(p.prefix + g, differs);
+    if (lane == 0 && differs != INT_MAX) atomicMin(found + g, differs);
+  }
+  if (small) {
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (rank > 0)
+      for (int j = tid; j < p.G; j += kPlanThreads)
+        if (s_found[j] != INT_MAX) {
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(s_found + j)), "r"(0));
+          asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(at), "r"(s_found[j]) : "memory");
+        }
   }
   cluster_sync();
-  for (int i = me; i < a.n; i += threads) {
-    const int g = p.group[i];
-    p.from[i] = p.bound[i] > 0 && p.active[g] >= 2 ? p.prefix[g] << c.page_log2 : 0;
+  if (rank != 0) return;
+  if (small) {
+    for (int j = tid; j < p.G; j += kPlanThreads) prefix[j] = min(prefix[j], s_found[j]);
+    __syncthreads();
   }
-  if (cluster_rank() != 0) return;
-  // the widest unit, then tiles before each group
-  if (threadIdx.x == 0) s_most = 0;
-  __syncthreads();
-  for (int j = threadIdx.x; j < p.G; j += kPlanThreads)
-    if (p.active[j] >= 2 && p.prefix[j] > 0) atomicMax(&s_most, (p.groups[j + 1] - p.groups[j]) * a.R);
+  // the widest unit, then tiles before each group, then what the kernels behind need
+  for (int j = tid; j < p.G; j += kPlanThreads)
+    if (active[j] >= 2 && prefix[j] > 0) atomicMax(&s_most, (start[j + 1] - start[j]) * a.R);
   __syncthreads();
   const int unit_rows = s_most > 128 ? 256 : 128;
   uint32_t before = 0;
   for (int j0 = 0; j0 < p.G; j0 += kPlanThreads) {
-    const int j = j0 + threadIdx.x;
+    const int j = j0 + tid;
     uint32_t tiles = 0;
-    if (j < p.G && p.active[j] >= 2 && p.prefix[j] > 0)
-      tiles = (uint32_t)tiles_of(p.prefix[j] << c.page_log2) * c.Hkv *
-              (((p.groups[j + 1] - p.groups[j]) * a.R + unit_rows - 1) / unit_rows);
+    if (j < p.G && active[j] >= 2 && prefix[j] > 0)
+      tiles = (uint32_t)tiles_of(prefix[j] << c.page_log2) * c.Hkv *
+              (((start[j + 1] - start[j]) * a.R + unit_rows - 1) / unit_rows);
     uint32_t sum = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
-    if (lane == 31) s_sum[threadIdx.x >> 5] = sum;
+    if (lane == 31) s_sum[tid >> 5] = sum;
     __syncthreads();
     uint32_t all = 0;
     for (int w = 0; w < kPlanThreads / 32; ++w) {
-      if (w < (int)threadIdx.x >> 5) sum += s_sum[w];
+      if (w < tid >> 5) sum += s_sum[w];
       all += s_sum[w];
     }
-    if (j < p.G) p.first[j] = before + sum - tiles;
+    if (j < p.G) {
+      p.first[j] = before + sum - tiles;
+      if (small) {
+        s_first[j] = before + sum - tiles;
+        p.lead[j] = lead[j];
+        p.prefix[j] = prefix[j];
+      }
+    }
     before += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     p.first[p.G] = before;
     p.plan->total = before;
     p.plan->runs = max(1u, min((uint32_t)p.sms, before / 2));
     p.plan->unit_rows = unit_rows;
+  }
+  for (int i = tid; i < a.n; i += kPlanThreads) {
+    const int g = group[i], from = bound[i] > 0 && active[g] >= 2 ? prefix[g] << c.page_log2 : 0;
+    p.from[i] = from;
+    p.info[i] = make_int4(from, start[g], (start[g + 1] - start[g]) * a.R, from > 0 ? (int)(small ? s_first[g] : p.first[g]) : 0);
   }
 }
 
@@ -200,7 +246,10 @@ struct Segment {
   long long before;                               // rows of the units before this one
   __device__ __forceinline__ bool wide() const { return rows > 128; }
 };
-__device__ __forceinline__ Segment segment_at(const SharedCall& p, int unit_rows, uint32_t x, uint32_t end) {
+// (Out of line, as everything here that runs once per segment: the roles of the
+// kernel below share an instruction cache, and 110 KB of code left each waiting
+// for its next instruction most of the time.)
+__device__ __noinline__ Segment segment_at(const SharedCall& p, int unit_rows, uint32_t x, uint32_t end) {
   Segment s;
   int lo = 0, hi = p.G;                           // the group with first[g] <= x < first[g + 1]
   while (hi - lo > 1) {
@@ -227,11 +276,17 @@ __device__ __forceinline__ Segment segment_at(const SharedCall& p, int unit_rows
 
 // ------------------------------------------------------------------ the shared tokens
 constexpr int kTile = 128;
-constexpr int kConvert = 8, kIssuer = 12, kLoader = 13, kThreads = 32 * 14;   // warps 0 .. 7: softmax
-constexpr float kMoveLog2 = 8.0f, kLiftLog2 = 7.0f;   // as in kvcache_attn.cuh: P <= 2^15 in fp16
+// Warps 0 .. 7: softmax; two for K's codes, two for V's, one that issues, one
+// that loads (128 registers a thread).
+constexpr int kConvert = 8, kIssuer = 12, kLoader = 13, kThreads = 32 * 14;
+// The largest P of fresh references is 2^4: room for logits to rise by some ten
+// before they move again (each move costs a tile's time and a half), and what
+// is lost of an output is at most 2^-29 of the largest P's for each token.
+constexpr float kLiftLog2 = 4.0f, kPieceLift = 7.0f - kLiftLog2;   // (pieces are told in 2^7)
+constexpr float kMost = 32768.f;                  // most that P of a row and 32 tokens may sum up to (fp16 holds 65504)
 constexpr float kLowLog2 = -60.0f;                // least exponent of the factor of P: below it P is 0 in fp16 anyway
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
-constexpr int kMaxStages = 5, kMeta = 8;           // kMeta >= kMaxStages + 2
+constexpr int kMaxStages = 5, kMeta = 16;          // kMeta >= kMaxStages + 4
 
 template <int DS>
 struct Layout {                                   // DS: steps of 16 channels
@@ -245,17 +300,22 @@ struct Layout {                                   // DS: steps of 16 channels
 
 struct Scales {                                   // of a tile's four blocks of 32 tokens
   float ks[4], lv[4];                             // K scale, log2 of the V scale
+  int tokens;                                     // tokens of the tile
 };
 struct Small {
   uint64_t sk_full[kMaxStages], sk_empty[kMaxStages], sv_full[kMaxStages], sv_empty[kMaxStages];   // codes
   uint64_t kf_full[2], kf_empty[2], vf_full[2], vf_empty[2];                                       // fp16 tiles
-  uint64_t meta_full[kMeta];
   uint64_t q_full[2], q_free;      // group g's Q written; both groups' last S of a segment complete
-  uint64_t s_full[2], p_full[2][2], o_done[2], drain;
+  uint64_t s_full[2], p_full[2], o_done[2], drain;
   Scales meta[kMeta];
   uint32_t tmem_base;
   int abort;
 };
+template <int DS>
+__device__ __forceinline__ uint8_t* stage_of(uint8_t* sm, int s) {   // one more in the place of the second Q
+  using L = Layout<DS>;
+  return sm + (s < L::kStages ? L::kStage + s * L::kStageB : L::kQ + L::kTileB);
+}
 template <int DS>
 constexpr int kSmem = Layout<DS>::kSmall + (int)sizeof(Small) + 1024;
 static_assert(kSmem<8> <= 232448 && kSmem<4> <= 232448, "shared memory exceeds the per-CTA limit");
@@ -269,6 +329,14 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(bar, parity); ++it)
     if (global_timer_ns() - t0 > kDrain) break;
+}
+// A wait whose first look fails.
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+  return __all_sync(0xffffffffu, slow_wait(bar, phase & 1, abort)) != 0;
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
@@ -284,143 +352,235 @@ constexpr uint32_t idesc_f16(uint32_t N, uint32_t b_mn) {   // both operands fp1
   return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Codes of a tile (row pitch d bytes) as fp16 in the swizzled layout; rows from
-// `tokens` on are zero.  128 threads, t of them.
+// 16 bytes of a swizzled tile: chunk ch of row r.
+__device__ __forceinline__ uint8_t* chunk_of(uint8_t* tile, int r, int ch) {
+  return tile + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+// 16 codes as two chunks.
+template <int CODE>
+__device__ __forceinline__ void convert16(const uint4& w, uint8_t* lo, uint8_t* hi) {
+  uint4 a, b;
+  codes_to_half<CODE>(w.x, a.x, a.y);
+  codes_to_half<CODE>(w.y, a.z, a.w);
+  codes_to_half<CODE>(w.z, b.x, b.y);
+  codes_to_half<CODE>(w.w, b.z, b.w);
+  *reinterpret_cast<uint4*>(lo) = a;
+  *reinterpret_cast<uint4*>(hi) = b;
+}
+// Codes of a tile (row pitch d bytes) as fp16 in the swizzled layout, rows from
+// `tokens` on zero: rows [row0, row0 + 64), by a warp (t: the lane).
+template <int CODE>
+__device__ __noinline__ void convert_odd(const uint8_t* from, uint8_t* to, int d, int tokens, int row0, int t) {
+  const int per = d >> 3;
+#pragma unroll 2
+  for (int x = t; x < 64 * per; x += 32) {
+    const int r = row0 + x / per, c = x % per;
+    const uint2 w = r < tokens ? *reinterpret_cast<const uint2*>(from + r * d + 8 * c) : make_uint2(0, 0);
+    uint4 v;
+    codes_to_half<CODE>(w.x, v.x, v.y);
+    codes_to_half<CODE>(w.y, v.z, v.w);
+    *reinterpret_cast<uint4*>(chunk_of(to, r, c)) = v;
+  }
+}
+// The same for d = 16 DS.  Eight lanes take 4 pieces of 16 codes of two
+// adjacent rows, one row's from the first block of 64 columns, the other's from
+// the second, so that their 128-bit accesses touch all banks once, reading and
+// writing.
 template <int CODE, int DS>
-__device__ __forceinline__ void convert_tile(const uint8_t* from, uint8_t* to, int d, int tokens, int t) {
-  constexpr int kBlockB = Layout<DS>::kBlockB;
-  auto chunk = [&](int r, int ch) {               // 16-byte chunk ch of row r
-    return reinterpret_cast<uint4*>(to + (ch >> 3) * kBlockB + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-  };
-  if (d == 16 * DS) {
-    constexpr int kBatch = DS % 4 == 0 ? 4 : 3;
+__device__ __forceinline__ void convert_tile(const uint8_t* from, uint8_t* to, int tokens, int row0, int t) {
+  constexpr int kPitch = 16 * DS, kBlockB = kTile * 128, kBatch = 4;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int u = t & 3, r7 = t >> 2;
+  const int first = DS == 8 ? r7 & 1 : 0;                  // the block that comes first
+  const uint8_t* src = from + (row0 + r7) * kPitch + 16 * u;
+  uint8_t* lo = to + (row0 + r7) * 128 + (((2 * u) ^ r7) << 4);
+  uint8_t* hi = to + (row0 + r7) * 128 + (((2 * u + 1) ^ r7) << 4);
+  constexpr int kBlocks = DS == 8 ? 2 : 1;
 #pragma unroll
-    for (int it0 = 0; it0 < DS; it0 += kBatch) {
+  for (int b = 0; b < kBlocks; ++b) {
+    const int block = b ? 1 - first : first;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 64; k0 += 8 * kBatch) {
       uint4 w[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int x = t + 128 * (it0 + u);
-        w[u] = x / DS < tokens ? *reinterpret_cast<const uint4*>(from + 16 * x) : make_uint4(0, 0, 0, 0);
-      }
+      for (int k = 0; k < kBatch; ++k)
+        w[k] = row0 + r7 + k0 + 8 * k < tokens
+                   ? *reinterpret_cast<const uint4*>(src + (k0 + 8 * k) * kPitch + 64 * block)
+                   : zero;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int x = t + 128 * (it0 + u), r = x / DS, c = x % DS;
-        uint4 lo, hi;
-        codes_to_half<CODE>(w[u].x, lo.x, lo.y);
-        codes_to_half<CODE>(w[u].y, lo.z, lo.w);
-        codes_to_half<CODE>(w[u].z, hi.x, hi.y);
-        codes_to_half<CODE>(w[u].w, hi.z, hi.w);
-        // lanes of the second block of columns begin with the odd chunk: all banks at once
-        const bool swap = c & 4;
-        *chunk(r, 2 * c + swap) = swap ? hi : lo;
-        *chunk(r, 2 * c + !swap) = swap ? lo : hi;
-      }
+      for (int k = 0; k < kBatch; ++k)
+        convert16<CODE>(w[k], lo + (k0 + 8 * k) * 128 + block * kBlockB, hi + (k0 + 8 * k) * 128 + block * kBlockB);
     }
-  } else {
-    const int per = d >> 3;
-    for (int x = t; x < kTile * per; x += 128) {
-      const int r = x / per, c = x - r * per;
-      const uint2 w = r < tokens ? *reinterpret_cast<const uint2*>(from + 8 * x) : make_uint2(0, 0);
-      uint4 v;
-      codes_to_half<CODE>(w.x, v.x, v.y);
-      codes_to_half<CODE>(w.y, v.z, v.w);
-      *chunk(r, c) = v;
+  }
+  if (DS == 6) {                                           // columns 64 to 95
+#pragma unroll 2
+    for (int r = row0 + (t >> 1); r < row0 + 64; r += 16) {
+      const uint4 w = r < tokens ? *reinterpret_cast<const uint4*>(from + r * kPitch + 64 + 16 * (t & 1)) : zero;
+      convert16<CODE>(w, chunk_of(to, r, 8 + 2 * (t & 1)), chunk_of(to, r, 9 + 2 * (t & 1)));
     }
   }
 }
 
-// 32 columns of the thread's row; read them behind wait_ld32.
-__device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr));
-}
-// (The values pass through, so that nothing that uses them comes before.)
-__device__ __forceinline__ void wait_ld32(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
+// Values of loads from tensor memory pass through here behind the wait for
+// them, so that nothing that uses them comes before it.
+__device__ __forceinline__ void pin16(float* v) {
+  asm volatile(""
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
-                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
-                 "+f"(v[30]), "+f"(v[31])
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
+}
+__device__ __forceinline__ void ld64(uint32_t taddr, float (&v)[64]) {
+#pragma unroll
+  for (int u = 0; u < 64; u += 16) tmem_ld16(taddr + u, v + u);
+}
+__device__ __forceinline__ void wait_ld64(float (&v)[64]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int u = 0; u < 64; u += 16) pin16(v + u);
+}
+// Packed halves in `columns` columns of tensor memory, times `factor`.
+__device__ __noinline__ void scale_halves(uint32_t taddr, int columns, float factor) {
+  for (int c = 0; c < columns; c += 8) {
+    float w[8];
+    tmem_ld8(taddr + c, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      asm volatile("" : "+f"(w[u]));
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[u]));
+      w[u] = __uint_as_float(pack_half2(h.x * factor, h.y * factor));
+    }
+    tmem_st8(taddr + c, w);
+  }
+  tmem_wait_st();
 }
 
 // A thread's row of a tile: S in its columns of tensor memory becomes P.
 //   x_c = s f_c (base-2 logits; f_c: the row's factor times block c's K scale),
-//   P = 2^(x - m + e_c), e_c = lv_c + m - M + 7,  l += sum of 2^(x - m)
+//   P = 2^(x - m + e_c), e_c = lv_c + m - M + 4,  l += sum of 2^(x - m)
 // m and M are references of the sums and of the outputs (which carry the V
-// scales); they move only when a tile's maximum is 2^8 above, so P <= 2^15.
-// follow(factor) lets O follow M, half() says that P's first half is stored.
-template <typename Follow, typename Half>
+// scales).  No maximum is looked for: P is made on the references as they are,
+// and only where the sum of a block of 32 shows that some P is too large for
+// fp16 the references move (to whole numbers, at least the maxima of the half
+// row at hand) and the half row is made again from S, which its P has not yet
+// replaced.  follow(factor) lets O follow M, and P of the first half follows
+// too.  A row's first tile always takes that way.
+template <typename Follow>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, int blocks, float fq, float& m, float& M,
-                                             float& l, Follow follow, Half half) {
-  float f[4], lv[4], v[2][32];
-  float mt = -INFINITY, Mt = -INFINITY;
-  ld32(tS, v[0]);
+                                             float& l, Follow follow) {
+  float v[64], hw[32];
+  ld64(tS, v);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    float s[2], e[2];
+    for (int round = 0;; ++round) {
+      wait_ld64(v);
+      uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull}, f2[2], n2[2];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    f[c] = fmaxf(fq * scales.ks[c], 0x1p-126f);
-    lv[c] = scales.lv[c];
-  }
+      for (int b = 0; b < 2; ++b) {
+        const int c = 2 * h + b;
+        const float f = fmaxf(fq * scales.ks[c], 0x1p-126f);
+        e[b] = fmaxf(scales.lv[c] + m - M + kLiftLog2, kLowLog2);
+        const float n = c < blocks ? e[b] - m : -INFINITY;   // (no tokens: P = 0)
+        f2[b] = f2_pack(f, f);
+        n2[b] = f2_pack(n, n);
+      }
+      // 16 columns at a time: while the exponentials of one run, those before
+      // are summed and packed, and make room for the next half row
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    wait_ld32(v[c & 1]);
-    ld32(tS + 32 * ((c + 1) & 3), v[(c + 1) & 1]);         // (after the last block, the first again)
-    float m4[4];
+      for (int k = 0; k <= 4; ++k) {
+        if (k < 4) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) m4[u] = v[c & 1][u];
+          for (int u = 16 * k; u < 16 * k + 16; u += 2) {
+            const uint64_t y = f2_fma(f2_pack(v[u], v[u + 1]), f2[k >> 1], n2[k >> 1]);
+            v[u] = ex2_approx(f2_lo(y));
+            v[u + 1] = ex2_approx(f2_hi(y));
+          }
+        }
+        if (k > 0) {
 #pragma unroll
-    for (int u = 4; u < 32; ++u) m4[u & 3] = fmaxf(m4[u & 3], v[c & 1][u]);
-    if (c < blocks) {
-      const float x = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f[c];
-      mt = fmaxf(mt, x);
-      Mt = fmaxf(Mt, x + lv[c]);
+          for (int u = 16 * k - 16; u < 16 * k; u += 2) {
+            uint64_t& a = sum2[((k - 1) & 2) + ((u >> 1) & 1)];
+            a = f2_add(a, f2_pack(v[u], v[u + 1]));
+            hw[u / 2] = __uint_as_float(pack_half2(v[u], v[u + 1]));
+          }
+          if (h == 0) tmem_ld16(tS + 64 + 16 * (k - 1), v + 16 * (k - 1));
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint64_t a = f2_add(sum2[2 * b], sum2[2 * b + 1]);
+        s[b] = f2_lo(a) + f2_hi(a);
+      }
+      const bool over = fmaxf(s[0], s[1]) > kMost;
+      if (round == 1 || !__any_sync(0xffffffffu, over)) break;
+      if (h == 0) wait_ld64(v);                            // (what came for the next half row is loaded again)
+      ld64(tS + 64 * h, v);
+      wait_ld64(v);
+      float mt = -INFINITY, Mt = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int c = 2 * h + b;
+        float x = v[32 * b], z = v[32 * b + 1];
+#pragma unroll
+        for (int u = 2; u < 32; u += 2) {
+          x = fmaxf(x, v[32 * b + u]);
+          z = fmaxf(z, v[32 * b + u + 1]);
+        }
+        x = fmaxf(x, z) * fmaxf(fq * scales.ks[c], 0x1p-126f);
+        if (c < blocks) {
+          mt = fmaxf(mt, x);
+          Mt = fmaxf(Mt, x + scales.lv[c]);
+        }
+      }
+      const float mn = over ? fmaxf(m, ceilf(mt)) : m, Mn = over ? fmaxf(M, ceilf(Mt)) : M;
+      l *= m == mn ? 1.f : ex2_approx(m - mn);             // (from nothing: 0 times 0)
+      const float factor = M == Mn ? 1.f : ex2_approx(M - Mn);
+      m = mn;
+      M = Mn;
+      follow(factor);
+      if (h == 1) scale_halves(tS, 32, factor);
     }
-  }
-  const bool need = mt > m + kMoveLog2 || Mt > M + kMoveLog2;
-  if (__any_sync(0xffffffffu, need)) {
-    const float mn = mt > m + kMoveLog2 ? mt : m, Mn = Mt > M + kMoveLog2 ? Mt : M;
-    l *= m == mn ? 1.f : ex2_approx(m - mn);               // (from nothing: 0 times 0)
-    const float factor = M == Mn ? 1.f : ex2_approx(M - Mn);
-    m = mn;
-    M = Mn;
-    // the first block waits in registers meanwhile
-    wait_ld32(v[0]);
-    follow(factor);
-  }
-  float hw[32];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    wait_ld32(v[c & 1]);
-    if (c < 3) ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-    const float e = fmaxf(lv[c] + m - M + kLiftLog2, kLowLog2);
-    const uint64_t f2 = f2_pack(f[c], f[c]), n2 = f2_pack(e - m, e - m);
-    uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-    for (int u = 0; u < 32; u += 2) {
-      uint64_t y = f2_fma(f2_pack(v[c & 1][u], v[c & 1][u + 1]), f2, n2);
-      if (c >= blocks) y = f2_pack(-INFINITY, -INFINITY);
-      const float a = ex2_approx(f2_lo(y)), b = ex2_approx(f2_hi(y));
-      sum2[(u >> 1) & 1] = f2_add(sum2[(u >> 1) & 1], f2_pack(a, b));
-      hw[(c & 1) * 16 + u / 2] = __uint_as_float(pack_half2(a, b));
-    }
-    const uint64_t sum = f2_add(sum2[0], sum2[1]);
-    l += (f2_lo(sum) + f2_hi(sum)) * ex2_approx(-e);
-    tmem_st16(tS + 16 * c, hw + (c & 1) * 16);
-    if (c == 1) half();
+    l += s[0] * ex2_approx(-e[0]) + s[1] * ex2_approx(-e[1]);
+    tmem_st16(tS + 32 * h, hw);
+    tmem_st16(tS + 32 * h + 16, hw + 16);
   }
 }
 
 // A value all lanes of the converged warp hold, in a uniform register.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// A thread's query row as fp16 to `to` (a row of a swizzled tile, or null),
+// times a power of two that brings its largest element to [2^14, 2^15);
+// returns the factor of its logits.
+template <int DS>
+__device__ __noinline__ float load_query(const AttnCall& a, const Segment& s, int gi, int row, uint8_t* to) {
+  const int r = (s.wide() ? gi * 128 : 0) + row, d = a.c.d;
+  uint4 w[2 * DS];
+#pragma unroll
+  for (int u = 0; u < 2 * DS; ++u) w[u] = make_uint4(0, 0, 0, 0);
+  if (r < s.rows) {
+    const int y = s.row0 + r, member = y / a.R, rr = y - member * a.R;
+    const __nv_bfloat16* q = a.q + (((size_t)(s.entry0 + member) * a.Hq + (size_t)s.h * a.g) * a.T + rr) * d;
+#pragma unroll
+    for (int u = 0; u < 2 * DS; ++u)
+      if (8 * u < d) w[u] = *reinterpret_cast<const uint4*>(q + 8 * u);
+  }
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int u = 0; u < 2 * DS; ++u) m2 = __vmaxu2(m2, largest2(w[u]));
+  const int e = min(126, max(-113, 14 - ((int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127)));
+  const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+  if (to) {
+#pragma unroll
+    for (int u = 0; u < 2 * DS; ++u)
+      *reinterpret_cast<uint4*>(to + (u >> 3) * (kTile * 128) + (((u & 7) ^ (row & 7)) << 4)) =
+          make_uint4(pack_half2(bf_lo(w[u].x) * up, bf_hi(w[u].x) * up), pack_half2(bf_lo(w[u].y) * up, bf_hi(w[u].y) * up),
+                     pack_half2(bf_lo(w[u].z) * up, bf_hi(w[u].z) * up), pack_half2(bf_lo(w[u].w) * up, bf_hi(w[u].w) * up));
+  }
+  return down * a.scale_log2;
+}
 
 template <int DS>
 __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uint8_t* sm, uint32_t tmem, int warp,
@@ -436,45 +596,19 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
       atomicOr(a.c.status, DROPKV_FLAG_TIMEOUT);
     }
   };
-  auto wait = [&](uint64_t* bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort));
-  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_phase(bar, phase, &S.abort); };
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
     __syncwarp();
   };
-  // The thread's query row as fp16 into its place in shared memory (`write`),
-  // times a power of two that brings its largest element to [2^14, 2^15);
-  // returns the factor of its logits.
   auto load_q = [&](const Segment& s, bool write) {
-    const int r = (s.wide() ? gi * 128 : 0) + row;
-    uint4 w[2 * DS];
-#pragma unroll
-    for (int u = 0; u < 2 * DS; ++u) w[u] = make_uint4(0, 0, 0, 0);
-    if (r < s.rows) {
-      const int y = s.row0 + r, member = y / a.R, rr = y - member * a.R;
-      const __nv_bfloat16* q = a.q + (((size_t)(s.entry0 + member) * a.Hq + (size_t)s.h * a.g) * a.T + rr) * d;
-#pragma unroll
-      for (int u = 0; u < 2 * DS; ++u)
-        if (8 * u < d) w[u] = *reinterpret_cast<const uint4*>(q + 8 * u);
-    }
-    uint32_t m2 = 0;
-#pragma unroll
-    for (int u = 0; u < 2 * DS; ++u) m2 = __vmaxu2(m2, largest2(w[u]));
-    const int e = min(126, max(-113, 14 - ((int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7) - 127)));
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+    const float f = load_query<DS>(a, s, gi, row, write ? sm + L::kQ + (s.wide() ? gi * L::kTileB : 0) + row * 128 : nullptr);
     if (write) {
-      uint8_t* to = sm + L::kQ + (s.wide() ? gi * L::kTileB : 0) + row * 128;
-#pragma unroll
-      for (int u = 0; u < 2 * DS; ++u)
-        *reinterpret_cast<uint4*>(to + (u >> 3) * L::kBlockB + (((u & 7) ^ (row & 7)) << 4)) =
-            make_uint4(pack_half2(bf_lo(w[u].x) * up, bf_hi(w[u].x) * up), pack_half2(bf_lo(w[u].y) * up, bf_hi(w[u].y) * up),
-                       pack_half2(bf_lo(w[u].z) * up, bf_hi(w[u].z) * up), pack_half2(bf_lo(w[u].w) * up, bf_hi(w[u].w) * up));
       fence_proxy_async_smem();
       arrive(&S.q_full[gi]);
     }
-    return down * a.scale_log2;
+    return f;
   };
 
   uint32_t tile0 = 0, mine = 0, outputs = 0, segments = 0;
@@ -491,18 +625,11 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
     }
 #pragma unroll 1
     for (int j = start; j < n; j += step) {
+      const uint32_t i = tile0 + j;
       if (!wait(&S.s_full[gi], mine)) { give_up(); return; }
       tc_fence_after();
       if (j + step >= n) arrive(&S.q_free);
-      const uint32_t i = tile0 + j;
-      if (!wait(&S.meta_full[i % kMeta], i / kMeta)) { give_up(); return; }
-      auto written = [&](int h) {
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&S.p_full[gi][h]);
-      };
-      const int blocks = min(4, (s.tokens - (s.k0 + j) * kTile + 31) / 32);
-      softmax_tile(tS, S.meta[i % kMeta], blocks, fq, m, M, l,
+      softmax_tile(tS, S.meta[i % kMeta], S.meta[i % kMeta].tokens / 32, fq, m, M, l,
                    [&](float factor) {
                      // the group's P V of its tile before is complete: the
                      // commit that its S signalled came behind it
@@ -516,9 +643,10 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
                        for (int u = 0; u < 16; ++u) o[u] *= factor;
                        tmem_st16(tO + 16 * c, o);
                      }
-                   },
-                   [&]() { written(0); });
-      written(1);
+                   });
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(&S.p_full[gi]);
       ++mine;
     }
     tile0 += n;
@@ -555,7 +683,7 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
       }
       tc_fence_before();
     }
-    if (r < s.rows) p.piece_s[at] = make_float4(m, l, M, 0.f);
+    if (r < s.rows) p.piece_s[at] = make_float4(m, l, M + kPieceLift, 0.f);
     if (!more) return;
     s = next;
     fq = fq_next;
@@ -572,16 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&S.sk_full[i], 1); mbar_init(&S.sk_empty[i], 4);
-      mbar_init(&S.sv_full[i], 1); mbar_init(&S.sv_empty[i], 4);
+      mbar_init(&S.sk_full[i], 1); mbar_init(&S.sk_empty[i], 2);
+      mbar_init(&S.sv_full[i], 1); mbar_init(&S.sv_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.kf_full[i], 4); mbar_init(&S.kf_empty[i], 1);
-      mbar_init(&S.vf_full[i], 4); mbar_init(&S.vf_empty[i], 1);
+      mbar_init(&S.kf_full[i], 2); mbar_init(&S.kf_empty[i], 1);
+      mbar_init(&S.vf_full[i], 2); mbar_init(&S.vf_empty[i], 1);
       mbar_init(&S.q_full[i], 4); mbar_init(&S.s_full[i], 1); mbar_init(&S.o_done[i], 1);
-      mbar_init(&S.p_full[i][0], 4); mbar_init(&S.p_full[i][1], 4);
+      mbar_init(&S.p_full[i], 4);
     }
-    for (int i = 0; i < kMeta; ++i) mbar_init(&S.meta_full[i], 1);
     mbar_init(&S.q_free, 8);
     mbar_init(&S.drain, 1);
     S.abort = 0;
@@ -603,10 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   const int unit_rows = plan.unit_rows, stages = L::kStages + (unit_rows == 128 ? 1 : 0);
   const bool work = plan.total > 0 && blockIdx.x < plan.runs;
   const uint32_t x0 = work ? run_start(plan, blockIdx.x) : 0, x1 = work ? run_start(plan, blockIdx.x + 1) : 0;
-  auto stage = [&](int s) { return sm + (s < L::kStages ? L::kStage + s * L::kStageB : L::kQ + L::kTileB); };
-  auto wait = [&](uint64_t* bar, uint32_t phase) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, &S.abort)) != 0;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_phase(bar, phase, &S.abort); };
   auto give_up = [&]() {
     if (lane == 0) {
       S.abort = 1;
@@ -659,14 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const uint32_t pages = __popc(__ballot_sync(0xffffffffu, mine));
       const uint32_t slot = i % stages, round = i / stages;
       const size_t at = mine ? ((size_t)pg[0] * c.Hkv + head[0]) * bytes : 0;
-      uint8_t* dst = stage(slot) + j * bytes;
+      uint8_t* dst = stage_of<DS>(sm, slot) + j * bytes;
       if (round > 0 && !(ok = wait(&S.sk_empty[slot], round - 1))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&S.sk_full[slot], pages * bytes);
-      __syncwarp();
-      if (mine) bulk_load(dst, c.k + at, bytes, &S.sk_full[slot]);
-      if (round > 0 && !(ok = wait(&S.sv_empty[slot], round - 1))) { ++i; break; }
-      // V of tile i - stages is converted, so P V of tile i - stages - 2 is
-      // complete, and the softmax of tile i - kMeta long before
+      // K of tile i - stages is converted, so S of tile i - stages - 2 is
+      // complete and the softmax of tile i - kMeta long done
       if (here) {
         const int first = j << (c.page_log2 - 5), blocks = 1 << (c.page_log2 - 5);
         for (int b = first; b < first + blocks; ++b) {
@@ -674,11 +794,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           S.meta[i % kMeta].lv[b] = mine ? __log2f(fmaxf(vs[0], 0x1p-126f)) : 0.f;
         }
       }
+      if (lane == 0) S.meta[i % kMeta].tokens = pages << c.page_log2;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&S.meta_full[i % kMeta]);
-        mbar_arrive_expect_tx(&S.sv_full[slot], pages * bytes);
-      }
+      if (lane == 0) mbar_arrive_expect_tx(&S.sk_full[slot], pages * bytes);
+      __syncwarp();
+      if (mine) bulk_load(dst, c.k + at, bytes, &S.sk_full[slot]);
+      if (round > 0 && !(ok = wait(&S.sv_empty[slot], round - 1))) { ++i; break; }
+      if (lane == 0) mbar_arrive_expect_tx(&S.sv_full[slot], pages * bytes);
       __syncwarp();
       if (mine) bulk_load(dst + L::kStageB / 2, c.v + at, bytes, &S.sv_full[slot]);
     }
@@ -690,34 +812,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
     __syncwarp();
   } else if (warp >= kConvert && warp < kIssuer) {
-    const int t = tid - 32 * kConvert;
+    const int v = (warp - kConvert) >> 1, row0 = 64 * (warp & 1);   // K's or V's, half a tile
+    uint64_t *coded = v ? S.sv_full : S.sk_full, *read = v ? S.sv_empty : S.sk_empty;
+    uint64_t *made = v ? S.vf_full : S.kf_full, *used = v ? S.vf_empty : S.kf_empty;
     bool ok = true;
-    uint32_t i = 0;
-    auto arrive = [&](uint64_t* bar, uint64_t* bar2) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < x1 - x0; ++i) {
+      const uint32_t slot = i % stages;
+      ok = wait(coded + slot, i / stages) && (i < 2 || wait(used + (i & 1), (i >> 1) - 1));
+      if (!ok) break;
+      const uint8_t* from = stage_of<DS>(sm, slot) + v * (L::kStageB / 2);
+      uint8_t* to = sm + (v ? L::kV : L::kK) + (i & 1) * L::kTileB;
+      const int tokens = S.meta[i % kMeta].tokens;
+      if (c.d == 16 * DS) convert_tile<CODE, DS>(from, to, tokens, row0, lane);
+      else convert_odd<CODE>(from, to, c.d, tokens, row0, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar);
-        mbar_arrive(bar2);
+        mbar_arrive(made + (i & 1));
+        mbar_arrive(read + slot);
       }
       __syncwarp();
-    };
-    for (uint32_t x = x0; ok && x < x1;) {
-      const Segment s = segment_at(p, unit_rows, x, x1);
-      for (int k = 0; ok && k < s.n; ++k, ++i) {
-        const int tokens = min(kTile, s.tokens - (s.k0 + k) * kTile);
-        const uint32_t slot = i % stages, round = i / stages;
-        uint8_t* from = stage(slot);
-        ok = wait(&S.sk_full[slot], round) && (i < 2 || wait(&S.kf_empty[i & 1], (i >> 1) - 1));
-        if (!ok) break;
-        convert_tile<CODE, DS>(from, sm + L::kK + (i & 1) * L::kTileB, c.d, tokens, t);
-        arrive(&S.kf_full[i & 1], &S.sk_empty[slot]);
-        ok = wait(&S.sv_full[slot], round) && (i < 2 || wait(&S.vf_empty[i & 1], (i >> 1) - 1));
-        if (!ok) break;
-        convert_tile<CODE, DS>(from + L::kStageB / 2, sm + L::kV + (i & 1) * L::kTileB, c.d, tokens, t);
-        arrive(&S.vf_full[i & 1], &S.sv_empty[slot]);
-      }
-      x += s.n;
     }
     if (!ok) give_up();
     __syncwarp();
@@ -784,44 +899,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       return true;
     };
     enter(x0, 0);
-    bool ok = pump();
-    uint32_t i = 0, seen0 = 0, seen1 = 0;
+    bool ok = true;
+    uint32_t tile0 = 0, seen0 = 0, seen1 = 0;
     for (uint32_t x = x0; ok && x < x1;) {
       const Segment s = segment_at(p, unit_rows, x, x1);
       const int n = uniform(s.n);
       const bool wide = uniform(s.wide()) != 0;
-      for (int j = 0; ok && j < n; ++j, ++i) {
-        const uint32_t slot = i & 1;
+      const int products = wide ? 2 * n : n;      // P V of the segment: tile by tile, in a wide one both groups'
+#pragma unroll 1
+      for (int y = 0; ok && y < products; ++y) {
+        if (!(ok = pump())) break;
+        const int j = wide ? y >> 1 : y, g = y & 1;
+        const uint32_t i = tile0 + j, slot = i & 1, seen = g ? seen1 : seen0;
+        const bool first = j == (wide ? 0 : g), last = j + (wide ? 1 : 2) >= n;
         const uint64_t vg = vd + ((slot * L::kTileB) >> 4);
-        if (!(ok = wait(&S.vf_full[slot], i >> 1))) break;
+        if ((!wide || g == 0) && !(ok = wait(&S.vf_full[slot], i >> 1))) break;
+        if (!(ok = wait(&S.p_full[g], seen))) break;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (!wide && (j & 1) != g) continue;
-          uint32_t& seen = g ? seen1 : seen0;
-          const bool first = j == (wide ? 0 : g), last = j + (wide ? 1 : 2) >= n;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!(ok = wait(&S.p_full[g][h], seen))) break;
-            tc_fence_after();
-            if (leader) {
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                umma_bf16_tmem_a(256 + 128 * g, 128 * g + 8 * k, vg + ((k * 16 * 128) >> 4), idO, !first || k > 0);
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-          ++seen;
-          if (leader) {
-            if (!wide || g == 1) umma_commit(&S.vf_empty[slot]);
-            if (last) umma_commit(&S.o_done[g]);
-          }
-          __syncwarp();
-          if (g) busy1 = false;
-          else busy0 = false;
-          if (!(ok = pump())) break;
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_tmem_a(256 + 128 * g, 128 * g + 8 * k, vg + ((k * 16 * 128) >> 4), idO, !first || k > 0);
         }
+        __syncwarp();
+        if (g) ++seen1;
+        else ++seen0;
+        if (leader) {
+          if (!wide || g == 1) umma_commit(&S.vf_empty[slot]);
+          if (last) umma_commit(&S.o_done[g]);
+        }
+        __syncwarp();
+        if (g) busy1 = false;
+        else busy0 = false;
       }
+      tile0 += n;
       x += n;
     }
     if (!ok) give_up();
@@ -843,89 +954,128 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ the join
-constexpr int kJoinWarps = 4, kJoinBatch = 8;
-// A warp joins the pieces of a row: those of the shared tokens, in run order,
-// and those of its own (one, or where its unit was cut, one per run).
-__global__ void __launch_bounds__(32 * kJoinWarps) final_kernel(const SharedCall p) {
+// The pieces of a row are joined in an order that does not depend on timing:
+// those of the shared tokens, in run order, then those of its own (one, or
+// where its unit was cut, one per run).  A warp takes every step-th of them,
+// kBatch with all loads in flight at once.  (Short code here too: see plan_kernel.)
+struct Joined {
+  float m, M, l;
+  float4 o;
+};
+template <int N>
+__device__ __forceinline__ void join_in(Joined& a, const float4 (&st)[N], const float4 (&x)[N]) {
+  float mn = a.m, Mn = a.M;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    mn = fmaxf(mn, st[u].x);
+    Mn = fmaxf(Mn, st[u].z);
+  }
+  const float m0 = mn == -INFINITY ? 0.f : mn, M0 = Mn == -INFINITY ? 0.f : Mn;   // (nothing yet: all factors 0)
+  const float f = ex2_approx(a.m - m0), F = ex2_approx(a.M - M0);
+  a.l *= f;
+  a.o.x *= F;
+  a.o.y *= F;
+  a.o.z *= F;
+  a.o.w *= F;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const bool none = st[u].x == -INFINITY && st[u].y == 0.f;   // perhaps no outputs were written either
+    const float G = ex2_approx(st[u].z - M0);
+    a.l += st[u].y * ex2_approx(st[u].x - m0);
+    a.o.x += none ? 0.f : x[u].x * G;
+    a.o.y += none ? 0.f : x[u].y * G;
+    a.o.z += none ? 0.f : x[u].z * G;
+    a.o.w += none ? 0.f : x[u].w * G;
+  }
+  a.m = mn;
+  a.M = Mn;
+}
+constexpr int kJoinWarps = 4;
+// WHOLE: a CTA joins one row, its warps a quarter of the pieces each (few rows
+// of up to 300 pieces); else a warp joins a row.
+template <bool WHOLE>
+__global__ void __launch_bounds__(32 * kJoinWarps, WHOLE ? 12 : 8) final_kernel(const SharedCall p) {
+  constexpr int kBatch = 5;
+  __shared__ float4 s_o[kJoinWarps][32], s_s[kJoinWarps];
   grid_dep_wait();
   grid_dep_launch();
   const AttnCall& a = p.own;
-  const int lane = threadIdx.x & 31, d = a.c.d;
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)a.n * a.Hq * a.T) return;
-  const int b = (int)(row / (a.Hq * a.T)), in = (int)(row - (long long)b * a.Hq * a.T), h = in / a.R, r = in - h * a.R;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = a.c.d, b = blockIdx.y;
+  const uint32_t in = WHOLE ? blockIdx.x : blockIdx.x * kJoinWarps + warp, h = in / (uint32_t)a.R, r = in - h * a.R;
+  if (!WHOLE && in >= (uint32_t)a.Hq * a.T) return;
+  const size_t row = (size_t)b * a.Hq * a.T + in;
+  const uint32_t rg = a.RB == 8 ? r >> 3 : r >> 4;
   const bool cols = lane * 4 < d;
-  float m = -INFINITY, M = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto join = [&](const float4& st, const float4& x) {
-    if (st.x == -INFINITY && st.y == 0.f) return; // nothing there, perhaps no outputs either
-    const float mn = fmaxf(m, st.x), Mn = fmaxf(M, st.z);
-    const float fa = m == mn ? 1.f : ex2_approx(m - mn), fb = st.x == mn ? 1.f : ex2_approx(st.x - mn);
-    const float Fa = M == Mn ? 1.f : ex2_approx(M - Mn), Fb = st.z == Mn ? 1.f : ex2_approx(st.z - Mn);
-    l = l * fa + st.y * fb;
-    o.x = o.x * Fa + x.x * Fb;
-    o.y = o.y * Fa + x.y * Fb;
-    o.z = o.z * Fa + x.z * Fb;
-    o.w = o.w * Fa + x.w * Fb;
-    m = mn;
-    M = Mn;
-  };
-  // pieces at rows at(0), at(1), ..., at(n - 1) of a pair of arrays
+  const int4 info = p.info[b];                    // shared tokens, first entry of the group, its rows, its first tile
+  const SharedPlan plan = *p.plan;
+  const int2 cut = p.by_runs ? a.cuts[((size_t)b * a.c.Hkv + h) * a.RG + rg] : make_int2(-1, 0);
+  Joined j;
+  j.m = j.M = -INFINITY;
+  j.l = 0.f;
+  j.o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kStep = WHOLE ? kJoinWarps : 1;
+  // pieces first, first + kStep, ... of n; at(k): the row of piece k
   auto take = [&](const float4* states, const float* outputs, int n, auto at) {
-    for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
-      float4 st[kJoinBatch], x[kJoinBatch];
+#pragma unroll 1
+    for (int k0 = WHOLE ? warp : 0; k0 < n; k0 += kStep * kBatch) {
+      float4 st[kBatch], x[kBatch];
 #pragma unroll
-      for (int u = 0; u < kJoinBatch; ++u) {
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * kStep;
         st[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
         x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + u < n) {
-          const size_t y = at(k0 + u);
+        if (k < n) {
+          const size_t y = at(k);
           st[u] = states[y];
           if (cols) x[u] = *reinterpret_cast<const float4*>(outputs + y * d + lane * 4);
         }
       }
-#pragma unroll
-      for (int u = 0; u < kJoinBatch; ++u) join(st[u], x[u]);
+      join_in(j, st, x);
     }
   };
-  const int from = p.from[b];
-  if (from > 0) {
-    const SharedPlan plan = *p.plan;
-    const int g = p.group[b], entry0 = p.groups[g], Mg = (p.groups[g + 1] - entry0) * a.R;
-    const int per_head = (Mg + plan.unit_rows - 1) / plan.unit_rows, tiles = tiles_of(from);
-    const int y = (b - entry0) * a.R + r, part = y / plan.unit_rows, rows = min(plan.unit_rows, Mg - part * plan.unit_rows);
-    const uint32_t t0 = p.first[g] + ((uint32_t)h * per_head + part) * tiles;
-    const int w0 = run_of(plan, t0), w1 = run_of(plan, t0 + tiles - 1), k = y - part * plan.unit_rows;
-    const size_t before = 2 * ((size_t)entry0 * a.R * a.c.Hkv + (size_t)h * Mg + (size_t)part * plan.unit_rows) + k;
-    if (rows > 128)
-      take(p.piece_s, p.piece_o, w1 - w0 + 1, [&](int u) { return (size_t)(w0 + u) * 256 + before; });
-    else                                          // two pieces per run, one of either group
-      take(p.piece_s, p.piece_o, 2 * (w1 - w0 + 1),
-           [&](int u) { return (size_t)(w0 + (u >> 1)) * 256 + before + (size_t)(u & 1) * rows; });
+  if (info.x > 0) {
+    // runs w0 .. w1, two pieces each where the groups of warps took turns
+    const int shift = plan.unit_rows == 256 ? 8 : 7, per_head = (info.z + plan.unit_rows - 1) >> shift;
+    const int y = (b - info.y) * a.R + r, part = y >> shift, rows = min(plan.unit_rows, info.z - (part << shift));
+    const int tiles = tiles_of(info.x), both = rows > 128 ? 0 : 1;
+    const uint32_t t0 = (uint32_t)info.w + (h * per_head + part) * tiles;
+    const uint32_t w0 = run_of(plan, t0), w1 = run_of(plan, t0 + tiles - 1);
+    const uint32_t at = w0 * 256 + 2 * ((uint32_t)info.y * a.R * a.c.Hkv + h * info.z + (part << shift)) + (y - (part << shift));
+    take(p.piece_s, p.piece_o, (w1 - w0 + 1) << both,
+         [&](int k) { return at + (k >> both) * 256 + (both & k ? rows : 0); });
   }
-  int2 cut = make_int2(-1, 0);
-  const int rg = r / a.RB;
-  if (p.by_runs) cut = a.cuts[((size_t)b * a.c.Hkv + h) * a.RG + rg];
-  if (cut.x < 0)
-    take(a.own_s, a.own_o, 1, [&](int) { return (size_t)row; });
-  else
-    take(a.part_s, a.part_o, cut.y - cut.x + 1, [&](int u) {
-      return (((size_t)(cut.x + u) * a.RG + rg) * 2 + (u == 0 ? 1 : 0)) * a.RB + (r - rg * a.RB);
-    });
+  // (the own pieces begin with the warp behind those that had one more: any order will do, it is always the same)
+  const bool whole = cut.x < 0;
+  const uint32_t first = whole ? 0 : (((uint32_t)cut.x * a.RG + rg) * 2) * a.RB + (r - rg * a.RB), pitch = 2 * a.RB * a.RG;
+  take(whole ? a.own_s : a.part_s, whole ? a.own_o : a.part_o, whole ? 1 : cut.y - cut.x + 1,
+       [&](int k) { return whole ? row : (size_t)(first + k * pitch + (k == 0 ? a.RB : 0)); });
+  if (WHOLE) {
+    s_o[warp][lane] = j.o;
+    if (lane == 0) s_s[warp] = make_float4(j.m, j.l, j.M, 0.f);
+    __syncthreads();
+    if (warp > 0) return;
+    float4 st[kJoinWarps - 1], x[kJoinWarps - 1];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+      st[w - 1] = s_s[w];
+      x[w - 1] = s_o[w][lane];
+    }
+    join_in(j, st, x);
+  }
   if (!cols) return;
   // o stands for o 2^(M - m - 7); a row that saw nothing has l = 0
-  const float f = l == 0.f ? 0.f : ex2_approx(M - m) / l, unlift = 0x1p-7f;
-  const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x * unlift * f, o.y * unlift * f),
-                       h1 = __floats2bfloat162_rn(o.z * unlift * f, o.w * unlift * f);
+  const float f = j.l == 0.f ? 0.f : ex2_approx(j.M - j.m) / j.l, unlift = 0x1p-7f;
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(j.o.x * unlift * f, j.o.y * unlift * f),
+                       h1 = __floats2bfloat162_rn(j.o.z * unlift * f, j.o.w * unlift * f);
   uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-  if (l == 0.f) w = make_uint2(0u, 0u);
+  if (j.l == 0.f) w = make_uint2(0u, 0u);
   *reinterpret_cast<uint2*>(a.out + row * d + lane * 4) = w;
 }
 
 cudaError_t launch_plan(const SharedCall& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   // more CTAs only where there is much to compare
-  const unsigned ctas = (long long)p.own.n * p.own.c.M > 8192 || p.own.n > 4 * kPlanThreads ? 8 : 1;
+  const unsigned ctas = (long long)p.own.n * p.own.c.M > 8192 || p.own.n > kPlanEntries ? 8 : 1;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
@@ -957,12 +1107,16 @@ cudaError_t launch_prefix(const SharedCall& p, cudaStream_t st) {
 
 cudaError_t launch_shared(const SharedCall& p, cudaStream_t st) {
   cudaError_t e = launch_plan(p, st);
+  // (own tokens first: the shared tokens' pieces, some 20 MB, are then still in
+  // the L2 cache when they are joined: FIGURE)
+  if (e == cudaSuccess) e = launch_own_attention(p.own, st);
   if (e == cudaSuccess)
     e = p.own.c.code == KVCACHE_INT8 ? launch_prefix<KVCACHE_INT8>(p, st) : launch_prefix<KVCACHE_E4M3>(p, st);
-  if (e == cudaSuccess) e = launch_own_attention(p.own, st);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.own.n * p.own.Hq * p.own.T;
-  return launch_pdl(final_kernel, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(32 * kJoinWarps), 0, st, p);
+  const unsigned per = (unsigned)(p.own.Hq * p.own.T);
+  if (rows <= 64LL * p.sms) return launch_pdl(final_kernel<true>, dim3(per, p.own.n), dim3(32 * kJoinWarps), 0, st, p);
+  return launch_pdl(final_kernel<false>, dim3((per + kJoinWarps - 1) / kJoinWarps, p.own.n), dim3(32 * kJoinWarps), 0, st, p);
 }
 
 }  // namespace kvcache

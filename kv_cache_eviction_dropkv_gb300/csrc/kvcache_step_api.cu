@@ -52,7 +52,7 @@ bool dense(const Rows& r, long long n, long long heads, long long rows, int d) {
 // The workspace of a shared attention (byte offsets); the second half's parts
 // and cuts have the sizes given.
 struct SharedSpace {
-  size_t plan, entries, groups, piece_o, piece_s, own_o, own_s, part_o, part_s, cuts, total;
+  size_t plan, entries, info, groups, piece_o, piece_s, own_o, own_s, part_o, part_s, cuts, total;
 };
 SharedSpace make_shared_space(const kvcache_shape& s, int n, int Hq, int T, int G, int sms, size_t part_o, size_t part_s,
                               size_t cuts) {
@@ -66,6 +66,7 @@ SharedSpace make_shared_space(const kvcache_shape& s, int n, int Hq, int T, int 
   const size_t rows = (size_t)n * Hq * T, pieces = (size_t)sms * 256 + 2 * rows;
   w.plan = take(sizeof(SharedPlan));
   w.entries = take((size_t)n * 3 * 4);
+  w.info = take((size_t)n * 16);
   w.groups = take(((size_t)G * 4 + 1) * 4);
   w.piece_o = take(pieces * s.d * 4);
   w.piece_s = take(pieces * 16);
@@ -247,6 +248,7 @@ dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call
   p.from = reinterpret_cast<int32_t*>(ws + w.entries);
   p.group = p.from + n;
   p.bound = p.group + n;
+  p.info = reinterpret_cast<int4*>(ws + w.info);
   p.lead = reinterpret_cast<int32_t*>(ws + w.groups);
   p.active = p.lead + call->G;
   p.prefix = p.active + call->G;

@@ -66,7 +66,8 @@ struct SharedCall {
   int G, sms;
   SharedPlan* plan;
   int32_t *from, *group, *bound; // per entry: first token of its own, group, full pages before its last T tokens
-  int32_t *lead, *active, *prefix;   // per group: first sequence that takes part, how many do, shared pages
+  int32_t *lead, *active, *prefix;   // per group: first entry that takes part, how many do, shared pages
+  int4* info;                    // per entry: shared tokens, first entry and rows per KV head of its group, its first tile
   uint32_t* first;               // [G + 1] per group: tiles before it
   float* piece_o;                // [sms * 256 + 2 n Hq T][d]
   float4* piece_s;
