@@ -137,7 +137,11 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  * is found on the device, so the results are kvcache_attention's whatever the
  * groups (up to the rounding of another order of summation).  Sequences that
  * hold less than a full page before their last T tokens take no part in the
- * sharing.  Groups that share nothing cost more than in kvcache_attention.
+ * sharing.
+ *   least   where n * max_pages * page * Hkv * d * 2, the most bytes of keys and
+ *           values that kvcache_attention could have to read, is below this,
+ *           the call is kvcache_attention and the groups are not looked at
+ *           (sharing adds three short kernels); negative: 320 MB
  *   groups  device int32 [G + 1], groups[0] = 0, not decreasing, groups[G] =
  *           n; anything else is flagged (DROPKV_FLAG_BAD_LENGTH) and nothing
  *           is shared
@@ -153,6 +157,7 @@ typedef struct {
   size_t workspace_bytes;
   uint32_t* status;
   cudaStream_t stream;
+  int64_t least;
   int32_t layer, n, Hq, T, G;
 } kvcache_shared_attention_call;
 DROPKV_API dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call);

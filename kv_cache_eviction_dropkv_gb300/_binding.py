@@ -363,43 +363,49 @@ def kvcache_read_status(status, stream=None):
 rotate_call = struct.Struct("@P" + "P3q" * 2 + "6P" + "5i0P")
 rotate_store_call = struct.Struct("@3P" + "P3q" * 3 + "6P" + "5i0P")
 read_call = struct.Struct("@9P3i0P")
-shared_attention_call = struct.Struct("@7PN2P5i0P")
+shared_attention_call = struct.Struct("@7PN2Pq5i0P")
 address_of = ctypes.addressof
 
 
-def step_call(name, record):
-    code = getattr(lib(), name)(record)
-    if code != 0:
-        raise DropKVError(code, name)
+def bad_tensor(name, t, dtype, shape, device_index):
+    """What a call says of a tensor that it has no use for."""
+    return ValueError("%s: expected a contiguous %s %s tensor on device %d, got %s %s on %s"
+                      % (name, dtype, list(shape), device_index, t.dtype, list(t.shape), t.device))
 
 
 def tensor_address(name, t, dtype, shape, device_index):
     """Address of a contiguous tensor of that type and shape on the device of that index."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device_index or not t.is_contiguous():
-        raise ValueError("%s: expected a contiguous %s %s tensor on device %d, got %s %s on %s"
-                         % (name, dtype, list(shape), device_index, t.dtype, list(t.shape), t.device))
+        raise bad_tensor(name, t, dtype, shape, device_index)
     return t.data_ptr()
+
+
+bf16, int32 = torch.bfloat16, torch.int32
 
 
 def rows_of(name, t, shape, device_index):
     """Address and strides of bf16 rows [sequences][heads][rows][d] (kvcache_rows)."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device_index:
+    if t.dtype is not bf16 or t.shape != shape or t.get_device() != device_index:
         raise ValueError("%s: expected a bf16 %s tensor on device %d, got %s %s on %s"
                          % (name, list(shape), device_index, t.dtype, list(t.shape), t.device))
-    a, (s0, s1, s2, s3) = t.data_ptr(), t.stride()
-    if s3 != 1 or a & 15 or (s0 | s1 | s2) & 7 and any(s & 7 and n > 1 for s, n in zip((s0, s1, s2), shape)):
+    a = t.data_ptr()
+    s0, s1, s2, s3 = strides = t.stride()
+    if (s3 != 1 or a & 15 or (s0 | s1 | s2) & 7) and (
+            s3 != 1 or a & 15 or any(s & 7 and n > 1 for s, n in zip(strides[:3], shape))):
         raise ValueError("%s: rows of adjacent channels on 16-byte boundaries are wanted, got strides %s"
-                         % (name, list(t.stride())))
+                         % (name, list(strides)))
     return a, s0, s1, s2
+
+
+NO_ROWS = (0, 0, 0, 0)
 
 
 def positions_of(positions, n, rows, device_index):
     """Address and kind of a call's positions (None, int32 [n] or [n, rows])."""
     if positions is None:
         return 0, 0
-    if positions.dim() == 2:
-        return tensor_address("positions", positions, torch.int32, (n, rows), device_index), 1
-    return tensor_address("positions", positions, torch.int32, (n,), device_index), 0
+    each = positions.dim() == 2
+    return tensor_address("positions", positions, int32, (n, rows) if each else (n,), device_index), int(each)
 
 
 def kvcache_shared_workspace_size(shape, n, Hq, T, G) -> int:

@@ -196,7 +196,7 @@ size_t kvcache_shared_workspace_size(const kvcache_shape* shape, int32_t n, int3
       n > shape->seqs || n > 65535 || (long long)Hq * T > kMaxSharedRows / n)
     return 0;
   // the second half's pieces at their most, for any number of entries up to n
-  SharedSpace w = make_shared_space(*shape, n, Hq, T, G, sms, 0, 0, 0);
+  const SharedSpace w = make_shared_space(*shape, n, Hq, T, G, sms, 0, 0, 0);
   return w.total + attn_workspace_bound(*shape, Hq, T, sms) + (size_t)n * shape->Hkv * ((Hq / shape->Hkv * T + 7) / 8) * 8 + 256;
 }
 
@@ -216,6 +216,14 @@ dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call
   if ((long long)Hq * T > kMaxSharedRows / n) return DROPKV_ERR_UNSUPPORTED;
   const size_t bytes = (size_t)n * Hq * T * shape.d * 2;
   if (ranges_overlap(call->q, bytes, call->out, bytes)) return DROPKV_ERR_INVALID_ARG;
+  // Sharing pays from some 300 MB of unshared reading on (8 heads of 128
+  // channels, 8 and 16 x 16000 tokens, 266 and 533 MB: attention 40 and 69 us,
+  // shared 55 and 59; 32 heads of 96, 8 and 16 x 4000, 208 and 415 MB: 47 and
+  // 84 against 47 and 50; 64 x 32768 443 against 114).
+  const double most = 2.0 * n * shape.max_pages * shape.page * shape.Hkv * shape.d;
+  if (most < (call->least < 0 ? 320e6 : (double)call->least))
+    return kvcache_attention(call->shape, call->cache, call->layer, call->seqs, n, call->q, Hq, T, 0, 0, call->out,
+                             call->workspace, call->workspace_bytes, call->status, call->stream);
   const int sms = current_sms(nullptr);
   if (sms <= 0) return DROPKV_ERR_CUDA;
   AttnPlan plan{};

@@ -165,23 +165,32 @@ class PagedCache:
         its place in its sequence, which after an eviction is not its position.
         Queries from counts[i] on are left as they were."""
         n, _, rows, _ = k.shape
-        want, i = (n, self.Hkv, rows, self.d), self._index
-        if rotary._index != i or rotary.d != self.d:
+        i, d = self._index, self.d
+        want = (n, self.Hkv, rows, d)
+        if rotary._index != i or rotary.d != d:
             raise ValueError("the rotary is one of %d channels on device %d" % (rotary.d, rotary._index))
-        Hq = 0 if q is None else q.shape[1]
-        of_q = (0, 0, 0, 0) if q is None else B.rows_of("q", q, (n, Hq, rows, self.d), i)
         of_k, of_v = B.rows_of("k", k, want, i), B.rows_of("v", v, want, i)
-        out = 0 if q is None else self._tensor("q_out", q_out, torch.bfloat16, (n, Hq, rows, self.d))
+        Hq, of_q, out = 0, B.NO_ROWS, 0
+        if q is not None and q.shape[1] > 0:
+            Hq = q.shape[1]
+            want = (n, Hq, rows, d)
+            of_q, out = B.rows_of("q", q, want, i), self._tensor("q_out", q_out, B.bf16, want)
         at, kind = B.positions_of(positions, n, rows, i)
-        cnt = 0 if counts is None else self._ints("counts", counts, n)
-        entries, layer = self._entries(seqs, n), self._layer(layer)
+        cnt = 0 if counts is None else self._tensor("counts", counts, B.int32, (n,))
+        entries = self._entries(seqs, n)
+        if not 0 <= layer < self.layers:
+            self._layer(layer)
         if n == 0 or rows == 0:
             return
-        if Hq == 0:
-            of_q = (0, 0, 0, 0)
-        self._step("kvcache_rotate_store", stream, lambda st: B.rotate_store_call.pack(
-            *self._fixed[:2], rotary.address, *of_q, *of_k, *of_v, out, entries, cnt, at, self._fixed[4], st,
-            layer, n, Hq, rows, kind))
+        if B.current_device() != i:
+            with torch.cuda.device(self.device):
+                return self.store_rotated(layer, rotary, q, k, v, q_out, positions, counts, seqs, stream)
+        shape, cache, _, _, status = self._fixed
+        code = B.lib().kvcache_rotate_store(B.rotate_store_call.pack(
+            shape, cache, rotary.address, *of_q, *of_k, *of_v, out, entries, cnt, at, status,
+            B.current_raw_stream(i) if stream is None else B.raw_stream(stream), layer, n, Hq, rows, kind))
+        if code != 0:
+            raise B.DropKVError(code, "kvcache_rotate_store")
 
     def read(self, layer, k_out, v_out, starts=None, counts=None, seqs=None, stream=None):
         """Tokens starts[i] .. starts[i] + counts[i] - 1 (int32 [n]; default: all
@@ -189,39 +198,56 @@ class PagedCache:
         k_out, v_out [n, Hkv, rows, d]; rows from counts[i] on are left as they
         were.  What a scoring of the cached tokens reads."""
         n, _, rows, _ = k_out.shape
-        want, bf16 = (n, self.Hkv, rows, self.d), torch.bfloat16
-        out = (self._tensor("k_out", k_out, bf16, want), self._tensor("v_out", v_out, bf16, want))
-        ints = [0 if t is None else self._ints(name, t, n) for name, t in (("starts", starts), ("counts", counts))]
-        entries, layer = self._entries(seqs, n), self._layer(layer)
+        i, want = self._index, (n, self.Hkv, rows, self.d)
+        k, v = self._tensor("k_out", k_out, B.bf16, want), self._tensor("v_out", v_out, B.bf16, want)
+        a = 0 if starts is None else self._tensor("starts", starts, B.int32, (n,))
+        cnt = 0 if counts is None else self._tensor("counts", counts, B.int32, (n,))
+        entries = self._entries(seqs, n)
+        if not 0 <= layer < self.layers:
+            self._layer(layer)
         if n == 0 or rows == 0:
             return
-        self._step("kvcache_read", stream, lambda st: B.read_call.pack(
-            *self._fixed[:2], entries, *ints, *out, self._fixed[4], st, layer, n, rows))
+        if B.current_device() != i:
+            with torch.cuda.device(self.device):
+                return self.read(layer, k_out, v_out, starts, counts, seqs, stream)
+        shape, cache, _, _, status = self._fixed
+        code = B.lib().kvcache_read(B.read_call.pack(
+            shape, cache, entries, a, cnt, k, v, status,
+            B.current_raw_stream(i) if stream is None else B.raw_stream(stream), layer, n, rows))
+        if code != 0:
+            raise B.DropKVError(code, "kvcache_read")
 
-    def shared_attention(self, layer, q, out, groups, seqs=None, stream=None):
+    def shared_attention(self, layer, q, out, groups, seqs=None, stream=None, least: int = -1):
         """attention() without a window for entries in groups (int32 [G + 1]:
         group j is entries groups[j] .. groups[j + 1] - 1) of sequences that begin
         with the same pages, forks of one sequence for instance: those pages
-        are found by their numbers and read once for the whole group."""
-        n, Hq, T, _ = q.shape
+        are found by their numbers and read once for the whole group.  Where
+        the cache's table has no room for `least` bytes of the entries' keys and
+        values (-1: 320 MB, from which on sharing is the faster way) the call
+        is attention(), and the groups are not looked at."""
+        n, Hq, T, d = q.shape
         G = groups.shape[0] - 1
         if T > self.T or Hq != self.Hq or G > self.groups:
             raise ValueError("the workspace is sized for %d query heads, at most %d rows and %d groups, got %d, %d and %d"
                              % (self.Hq, self.T, self.groups, Hq, T, G))
-        want, bf16 = (n, Hq, T, self.d), torch.bfloat16
-        at, to, starts = self._tensor("q", q, bf16, want), self._tensor("out", out, bf16, want), self._ints("groups", groups, G + 1)
-        entries, layer = self._entries(seqs, n), self._layer(layer)
+        if not -1 << 63 <= least < 1 << 63:
+            raise ValueError("least is a 64-bit count")
+        i, want = self._index, (n, Hq, T, self.d)
+        at, to = self._tensor("q", q, B.bf16, want), self._tensor("out", out, B.bf16, want)
+        starts = self._tensor("groups", groups, B.int32, (G + 1,))
+        entries = self._entries(seqs, n)
+        if not 0 <= layer < self.layers:
+            self._layer(layer)
         if T == 0 or n == 0:
             return
-        self._step("kvcache_shared_attention", stream, lambda st: B.shared_attention_call.pack(
-            *self._fixed[:2], entries, starts, at, to, *self._fixed[2:5], st, layer, n, Hq, T, G))
-
-    def _step(self, name, stream, record):
-        """The library's call `name`; record(stream) packs it."""
-        if B.current_device() != self._index:
+        if B.current_device() != i:
             with torch.cuda.device(self.device):
-                return self._step(name, stream, record)
-        B.step_call(name, record(B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream)))
+                return self.shared_attention(layer, q, out, groups, seqs, stream, least)
+        code = B.lib().kvcache_shared_attention(B.shared_attention_call.pack(
+            *self._fixed[:2], entries, starts, at, to, *self._fixed[2:],
+            B.current_raw_stream(i) if stream is None else B.raw_stream(stream), least, layer, n, Hq, T, G))
+        if code != 0:
+            raise B.DropKVError(code, "kvcache_shared_attention")
 
     # -------------------------------------------------------------- whole sequences
     def fork(self, src, dst, stream=None):

@@ -100,7 +100,7 @@ class Rotary:
         address = lambda t: None if t is None or t.numel() == 0 else t.data_ptr()
         self._record = B.kvcache_rotary(address(self.turns), address(self.q_norm), address(self.k_norm), self.d,
                                         self.dims, LAYOUTS[layout], self.eps, self.amplitude)
-        self.address = B.address_of(self._record)
+        self.address, self._status = B.address_of(self._record), self.status.data_ptr()
 
     def _weight(self, name, w):
         if w is None:
@@ -119,28 +119,33 @@ class Rotary:
         were.  Problems found on the device are reported by check()."""
         if q is None and k is None:
             return
+        i, d = self._index, self.d
         n_seq, _, n, _ = (k if q is None else q).shape
-        heads = [1, 1]
-        packed = []
-        for i, (name, x, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
-            if x is None:
-                packed += [0, 0, 0, 0, 0]
-                continue
-            heads[i] = x.shape[1]
-            want = (n_seq, heads[i], n, self.d)
-            packed += [*B.rows_of(name, x, want, self._index),
-                       B.tensor_address(name + "_out", out, torch.bfloat16, want, self._index)]
-        at, kind = B.positions_of(positions, n_seq, n, self._index)
-        to = 0 if lengths is None else B.tensor_address("lengths", lengths, torch.int32, (n_seq,), self._index)
-        if n_seq == 0 or n == 0 or not all(heads):
+        Hq = Hkv = 1
+        of_q = of_k = B.NO_ROWS
+        to_q = to_k = 0
+        if q is not None:
+            Hq = q.shape[1]
+            want = (n_seq, Hq, n, d)
+            of_q = B.rows_of("q", q, want, i)
+            to_q = B.tensor_address("q_out", q_out, B.bf16, want, i)
+        if k is not None:
+            Hkv = k.shape[1]
+            want = (n_seq, Hkv, n, d)
+            of_k = B.rows_of("k", k, want, i)
+            to_k = B.tensor_address("k_out", k_out, B.bf16, want, i)
+        at, kind = B.positions_of(positions, n_seq, n, i)
+        to = 0 if lengths is None else B.tensor_address("lengths", lengths, B.int32, (n_seq,), i)
+        if not (n_seq and n and Hq and Hkv):
             return
-        if B.current_device() != self._index:
+        if B.current_device() != i:
             with torch.cuda.device(self.device):
                 return self.apply(q, k, q_out, k_out, positions, lengths, stream)
-        B.step_call("kvcache_rotate", B.rotate_call.pack(
-            self.address, *packed[:4], *packed[5:9], packed[4], packed[9], at, to, self.status.data_ptr(),
-            B.current_raw_stream(self._index) if stream is None else B.raw_stream(stream),
-            n_seq, heads[0], heads[1], n, kind))
+        code = B.lib().kvcache_rotate(B.rotate_call.pack(
+            self.address, *of_q, *of_k, to_q, to_k, at, to, self._status,
+            B.current_raw_stream(i) if stream is None else B.raw_stream(stream), n_seq, Hq, Hkv, n, kind))
+        if code != 0:
+            raise B.DropKVError(code, "kvcache_rotate")
 
     def check(self, stream=None):
         """Sync and raise if the device status word reports an error."""

@@ -79,7 +79,7 @@ def definition(c, q, seqs, layer=0):
 
 def check(c, q, seqs, starts, layer=0):
     out = torch.full_like(q, 7.0)
-    c.shared_attention(layer, q, out, ints(starts), seqs=ints(seqs))
+    c.shared_attention(layer, q, out, ints(starts), seqs=ints(seqs), least=0)
     want, vmax = definition(c, q, seqs, layer)
     n = int(c.length.max())
     err = (out.double() - want).abs()
@@ -205,7 +205,7 @@ def test_flags_and_refusals():
     q = queries(4, 4, 1, 64, 3)
     for bad in ([1, 4], [0, 3], [0, 3, 2, 4], [0, 5], [0, -1, 4], [4, 4]):
         out = torch.full_like(q, 7.0)
-        c.shared_attention(0, q, out, ints(bad), seqs=ints(seqs))
+        c.shared_attention(0, q, out, ints(bad), seqs=ints(seqs), least=0)
         assert flags_of(c) == B.FLAG_BAD_LENGTH
         c.reset_status()
         plain = torch.empty_like(q)
@@ -215,10 +215,10 @@ def test_flags_and_refusals():
     kept = c.table.clone()
     c.table[seqs[1], 3] = -1
     out = torch.empty_like(q)
-    c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs))
+    c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs), least=0)
     assert flags_of(c) == B.FLAG_BAD_PAGE
     c.table[seqs, 2] = c.pages
-    c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs))
+    c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs), least=0)
     assert flags_of(c) == B.FLAG_BAD_PAGE
     c.table.copy_(kept)
     c.reset_status()
@@ -234,6 +234,22 @@ def test_flags_and_refusals():
     assert c.check() == 0
 
 
+def test_small_calls_are_attention():
+    """Below `least` bytes the call is attention(), bit by bit."""
+    c, seqs, starts = forked([200], [[5, 9, 1, 40]], 2, 2, 64, 32, seed=9)
+    q = queries(4, 4, 1, 64, 3)
+    plain, out = torch.empty_like(q), torch.empty_like(q)
+    c.attention(0, q, plain, seqs=ints(seqs))
+    most = 2 * 4 * c.max_pages * 32 * 2 * 64
+    for least in (-1, most + 1):
+        c.shared_attention(0, q, out.fill_(7.0), ints(starts), seqs=ints(seqs), least=least)
+        assert torch.equal(out, plain)
+    c.shared_attention(0, q, out.fill_(7.0), ints([1, 2]), seqs=ints(seqs))     # (not looked at)
+    assert torch.equal(out, plain) and c.check() == 0
+    c.shared_attention(0, q, out, ints([1, 2]), seqs=ints(seqs), least=most)
+    assert flags_of(c) == B.FLAG_BAD_LENGTH
+
+
 def test_not_a_number_codes_reach_their_rows_only():
     c, seqs, starts = forked([200, 200], [[5, 9], [1, 40]], 2, 2, 64, 32, seed=9)
     q = queries(4, 4, 1, 64, 3)
@@ -243,7 +259,7 @@ def test_not_a_number_codes_reach_their_rows_only():
         was = pool.view(torch.uint8)[0, pg, 1, 3, 5].clone()
         pool.view(torch.uint8)[0, pg, 1, 3, 5] = 0x7F
         out = torch.empty_like(q)
-        c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs))
+        c.shared_attention(0, q, out, ints(starts), seqs=ints(seqs), least=0)
         pool.view(torch.uint8)[0, pg, 1, 3, 5] = was
         assert torch.equal(out[2:], good[2:]) and torch.equal(out[:, :2], good[:, :2])
         assert bool(out[:2, 2:].isnan().any(-1).all())
@@ -258,7 +274,7 @@ def test_two_captured_calls_and_other_streams():
 
     def step():
         for layer in range(2):
-            c.shared_attention(layer, q, outs[layer], groups, seqs=members)
+            c.shared_attention(layer, q, outs[layer], groups, seqs=members, least=0)
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -43,10 +43,10 @@ def read(s=None, b=None, seqs=0, starts=0, counts=0, k=A, v=FAR, status=A, layer
                                                  status, 0, layer, n, rows))
 
 
-def shared(s=None, b=None, seqs=0, groups=A, q=A, out=FAR, ws=A, wsb=1 << 40, status=A, layer=0, n=2, Hq=4, T=1, G=1):
+def shared(s=None, b=None, seqs=0, groups=A, q=A, out=FAR, ws=A, wsb=1 << 40, status=A, layer=0, n=2, Hq=4, T=1, G=1, least=0):
     s, b = shape() if s is None else s, buffers() if b is None else b
     return B.lib().kvcache_shared_attention(B.shared_attention_call.pack(
-        ctypes.addressof(s), ctypes.addressof(b), seqs, groups, q, out, ws, wsb, status, 0, layer, n, Hq, T, G))
+        ctypes.addressof(s), ctypes.addressof(b), seqs, groups, q, out, ws, wsb, status, 0, least, layer, n, Hq, T, G))
 
 
 def test_every_declared_symbol_is_exported_and_bound():
@@ -66,7 +66,7 @@ def test_records_have_the_size_of_the_structures():
     assert B.rotate_call.size == 8 + 2 * rows + 6 * 8 + up(5 * 4)
     assert B.rotate_store_call.size == 3 * 8 + 3 * rows + 6 * 8 + up(5 * 4)
     assert B.read_call.size == 9 * 8 + up(3 * 4)
-    assert B.shared_attention_call.size == 10 * 8 + up(5 * 4)
+    assert B.shared_attention_call.size == 11 * 8 + up(5 * 4)
     assert ctypes.sizeof(B.kvcache_rotary) == 3 * 8 + up(5 * 4)
 
 
