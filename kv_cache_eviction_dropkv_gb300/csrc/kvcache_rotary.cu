@@ -27,6 +27,11 @@ namespace {
 
 using dropkv::grid_dep_launch;
 using dropkv::grid_dep_wait;
+using dropkv::f2_fma;
+using dropkv::f2_hi;
+using dropkv::f2_lo;
+using dropkv::f2_mul;
+using dropkv::f2_pack;
 using dropkv::launch_pdl;
 
 // The 8 channels of a lane, as two runs of 4: [c0, c0 + 4), [c1, c1 + 4).
@@ -42,9 +47,11 @@ __device__ __forceinline__ Part part_of(const Turning& how, int lane, bool half)
   a.c1 = half && a.turns ? how.dims / 2 + 4 * lane : 8 * lane + 4;
   return a;
 }
-// Cosines and sines, times the amplitude, of a lane's four pairs at a position.
+// Cosines and sines, times the amplitude, of a lane's four pairs at a position,
+// two by two.
 struct Angle {
-  float c[4], s[4];
+  uint64_t c[2], s[2];
+  bool turns;
 };
 __device__ __forceinline__ void cos_sin_turns(unsigned long long t, float& c, float& s) {
   const uint32_t top = (uint32_t)(t >> 32), q = (top + 0x20000000u) >> 30;
@@ -67,14 +74,18 @@ __device__ __forceinline__ void cos_sin_turns(unsigned long long t, float& c, fl
 }
 __device__ __forceinline__ Angle angle_of(const Turning& how, const Part& a, int lane, long long position) {
   Angle r;
+  r.turns = a.turns;
+  float c[4], s[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    r.c[e] = 1.f;
-    r.s[e] = 0.f;
-    if (!a.turns) continue;
-    cos_sin_turns((unsigned long long)position * __ldg(how.turns + 4 * lane + e), r.c[e], r.s[e]);
-    r.c[e] = __fmul_rn(r.c[e], how.amplitude);
-    r.s[e] = __fmul_rn(r.s[e], how.amplitude);
+    c[e] = s[e] = 0.f;
+    if (a.turns) cos_sin_turns((unsigned long long)position * __ldg(how.turns + 4 * lane + e), c[e], s[e]);
+  }
+  const uint64_t amplitude = f2_pack(how.amplitude, how.amplitude);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    r.c[e] = f2_mul(f2_pack(c[2 * e], c[2 * e + 1]), amplitude);
+    r.s[e] = f2_mul(f2_pack(s[2 * e], s[2 * e + 1]), amplitude);
   }
   return r;
 }
@@ -82,68 +93,94 @@ __device__ __forceinline__ long long position_of(const int32_t* positions, int e
   return !positions ? (long long)first + t : each ? positions[(size_t)i * rows + t] : (long long)positions[i] + t;
 }
 
-struct Weight {
-  float w[8];
+// A lane's 8 numbers two by two, so that packed arithmetic does the rotation:
+// first and second members of pairs 0 and 1, then of pairs 2 and 3.
+//   half:         (x0, x1), (x4, x5);  (x2, x3), (x6, x7)     of its two runs x0 .. x3, x4 .. x7
+//   interleaved:  (x0, x2), (x1, x3);  (x4, x6), (x5, x7)
+struct Pairs {
+  uint64_t a[2], b[2];
 };
-__device__ __forceinline__ Weight weight_of(const float* w, const Part& a) {
-  Weight r;
+template <bool HALF>
+__device__ __forceinline__ Pairs pairs_of(const float (&x)[8]) {
+  Pairs p;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r.w[e] = w && a.live ? __ldg(w + (e < 4 ? a.c0 + e : a.c1 + e - 4)) : 1.f;
-  return r;
+  for (int e = 0; e < 2; ++e) {
+    p.a[e] = HALF ? f2_pack(x[2 * e], x[2 * e + 1]) : f2_pack(x[4 * e], x[4 * e + 2]);
+    p.b[e] = HALF ? f2_pack(x[4 + 2 * e], x[5 + 2 * e]) : f2_pack(x[4 * e + 1], x[4 * e + 3]);
+  }
+  return p;
+}
+template <bool HALF>
+__device__ __forceinline__ Pairs weight_of(const float* w, const Part& a) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = w && a.live ? __ldg(w + (e < 4 ? a.c0 + e : a.c1 + e - 4)) : 1.f;
+  return pairs_of<HALF>(x);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // A lane's part of a row through norm and rotation, rounded to bf16 (words in
 // the order of its channels).  All L lanes of the row call it.  The operations
-// are spelt out so that both kernels round alike.
+// are spelt out so that both kernels round alike, and packed two by two.
 template <bool HALF, int L>
-__device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Weight& w, const Angle& g, const Turning& how) {
+__device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Pairs& w, const Angle& g, const Turning& how) {
   const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w4[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w4[i] & 0xFFFF0000u);
+    x[2 * i] = bf_lo(w4[i]);
+    x[2 * i + 1] = bf_hi(w4[i]);
   }
+  Pairs y = pairs_of<HALF>(x);
   if (norm) {
-    auto sum_squares = [&](auto scale) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = scale(x[e]);
-        ss = __fmaf_rn(v, v, ss);
-      }
+    auto sum_squares = [&](const Pairs& v) {
+      uint64_t s2 = f2_mul(v.a[0], v.a[0]);
+      s2 = f2_fma(v.a[1], v.a[1], s2);
+      s2 = f2_fma(v.b[0], v.b[0], s2);
+      s2 = f2_fma(v.b[1], v.b[1], s2);
+      float ss = __fadd_rn(f2_lo(s2), f2_hi(s2));
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
       return ss;
     };
-    const float inv_d = __fdiv_rn(1.f, (float)how.d);
-    float ss = sum_squares([](float v) { return v; }), r;
+    const float ss = sum_squares(y);
+    float r = rsqrtf(__fmaf_rn(ss, how.inv_d, how.eps));
     // squares past fp32 (elements above 2^63): once more at 2^-80, where eps is
     // nothing against them.  (All lanes: the row's own sum decides.)
     if (__any_sync(0xffffffffu, ss == INFINITY)) {
-      const float small = sum_squares([](float v) { return __fmul_rn(v, 0x1p-80f); });
-      r = ss == INFINITY ? __fmul_rn(rsqrtf(__fmul_rn(small, inv_d)), 0x1p-80f)
-                         : rsqrtf(__fmaf_rn(ss, inv_d, how.eps));
-    } else {
-      r = rsqrtf(__fmaf_rn(ss, inv_d, how.eps));
+      const uint64_t down = f2_pack(0x1p-80f, 0x1p-80f);
+      Pairs z;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        z.a[e] = f2_mul(y.a[e], down);
+        z.b[e] = f2_mul(y.b[e], down);
+      }
+      const float small = sum_squares(z);
+      if (ss == INFINITY) r = __fmul_rn(rsqrtf(__fmul_rn(small, how.inv_d)), 0x1p-80f);
     }
+    const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w.w[e]);
+    for (int e = 0; e < 2; ++e) {
+      y.a[e] = f2_mul(f2_mul(y.a[e], r2), w.a[e]);
+      y.b[e] = f2_mul(f2_mul(y.b[e], r2), w.b[e]);
+    }
   }
+  if (g.turns) {                              // (0 times an infinity of a channel that does not turn would be none)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int a = HALF ? e : 2 * e, b = HALF ? 4 + e : 2 * e + 1;
-    const float xa = x[a], xb = x[b];
-    x[a] = __fmaf_rn(xa, g.c[e], -__fmul_rn(xb, g.s[e]));
-    x[b] = __fmaf_rn(xb, g.c[e], __fmul_rn(xa, g.s[e]));
+    for (int e = 0; e < 2; ++e) {
+      const uint64_t a = y.a[e], b = y.b[e], minus = b ^ 0x8000000080000000ull;
+      y.a[e] = f2_fma(a, g.c[e], f2_mul(minus, g.s[e]));
+      y.b[e] = f2_fma(b, g.c[e], f2_mul(a, g.s[e]));
+    }
   }
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  if (HALF)
+    return make_uint4(pack_bf16(f2_lo(y.a[0]), f2_hi(y.a[0])), pack_bf16(f2_lo(y.a[1]), f2_hi(y.a[1])),
+                      pack_bf16(f2_lo(y.b[0]), f2_hi(y.b[0])), pack_bf16(f2_lo(y.b[1]), f2_hi(y.b[1])));
+  return make_uint4(pack_bf16(f2_lo(y.a[0]), f2_lo(y.b[0])), pack_bf16(f2_hi(y.a[0]), f2_hi(y.b[0])),
+                    pack_bf16(f2_lo(y.a[1]), f2_lo(y.b[1])), pack_bf16(f2_hi(y.a[1]), f2_hi(y.b[1])));
 }
 
 template <bool HALF>
@@ -165,42 +202,59 @@ __device__ __forceinline__ void store_part(__nv_bfloat16* row, const Part& a, co
 constexpr int kBatch = 4;                       // heads whose loads are in flight together
 
 // One token's rows of heads [h0, h1), `from` and `to` those of head 0.  All
-// lanes of the warp walk `chunk` heads.
+// lanes of the warp walk `chunk` heads, a batch's loads ahead of its work: the
+// first one's are made by load_heads before the angles are computed.
+struct Batch {
+  uint4 x[kBatch];
+};
+template <bool HALF>
+__device__ __forceinline__ Batch load_heads(const __nv_bfloat16* from, long long step, int h, int h1, const Part& a) {
+  Batch b;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    b.x[u] = make_uint4(0, 0, 0, 0);
+    if (a.live && h + u < h1) b.x[u] = load_part<HALF>(from + (h + u) * step, a);
+  }
+  return b;
+}
 template <bool HALF, int L>
-__device__ __forceinline__ void turn_heads(const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
-                                           long long to_step, int h0, int h1, int chunk, bool norm, const Weight& w,
+__device__ __forceinline__ void turn_heads(Batch x, const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
+                                           long long to_step, int h0, int h1, int chunk, bool norm, const Pairs& w,
                                            const Angle& g, const Part& a, const Turning& how) {
 #pragma unroll 1
-  for (int k = 0; k < chunk; k += kBatch) {
-    uint4 x[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (a.live && h0 + k + u < h1) x[u] = load_part<HALF>(from + (h0 + k + u) * from_step, a);
-    }
+  for (int k = 0;;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (k + u >= chunk) break;
-      x[u] = turn<HALF, L>(x[u], norm, w, g, how);
-      if (a.live && h0 + k + u < h1) store_part<HALF>(to + (h0 + k + u) * to_step, a, x[u]);
+      x.x[u] = turn<HALF, L>(x.x[u], norm, w, g, how);
+      if (a.live && h0 + k + u < h1) store_part<HALF>(to + (h0 + k + u) * to_step, a, x.x[u]);
     }
+    k += kBatch;
+    if (k >= chunk) break;
+    x = load_heads<HALF>(from, from_step, h0 + k, h1, a);
   }
 }
 
-constexpr int kRotThreads = 256;
+// Most heads a CTA of rotate_kernel takes, and a token's lanes in the store (8
+// and 16: 32K prompt 117 and 124 us, four chunks of up to 8192 tokens stored 118
+// and 114; a batch's loads under the work of the one before, which costs a
+// fifth of the threads that fit: 127 and 111).
+constexpr int kRotThreads = 256, kMostHeads = 8, kStoreHeads = 16;
+constexpr int kStoreKvHeads = 4;                // KV heads that a CTA of many new tokens takes, one after the other
 
 // A CTA takes kRotThreads / L tokens (adjacent rows, so that a head's rows are
 // one piece of memory) and `chunk` heads of either the queries or the keys:
 // angles and weights are computed once per token and chunk.
 template <bool HALF, int L>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateCall p) {
+__global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall p) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % L;
   const int token = blockIdx.x * (kRotThreads / L) + threadIdx.x / L;
   const int b = token / p.n, t = token - b * p.n;
   const int which = (int)blockIdx.y >= p.chunks ? 1 : 0;
-  const int h0 = ((int)blockIdx.y - (which ? p.chunks : 0)) * p.chunk, h1 = min(h0 + p.chunk, p.heads[which]);
+  const int h0 = ((int)blockIdx.y - (which ? p.chunks : 0)) * p.chunk;
+  int h1 = min(h0 + p.chunk, p.heads[which]);
   const Part a = part_of(p.how, lane, HALF);
   const bool norm = p.weight[which] != nullptr;
   bool live = b < p.B;
@@ -213,29 +267,49 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateCall p)
       live = t < len;
     }
   }
-  const Weight w = weight_of(p.weight[which], a);
-  const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
+  if (!__any_sync(0xffffffffu, live)) return;
   const Rows& in = p.in[which];
-  turn_heads<HALF, L>(in.p + (live ? b * in.seq + t * in.row : 0), in.head,
-                      p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0),
-                      (long long)p.n * p.how.d, h0, live ? h1 : 0, p.chunk, norm, w, g, a, p.how);
+  const __nv_bfloat16* from = in.p + (live ? b * in.seq + t * in.row : 0);
+  if (!live) h1 = 0;
+  const Batch x = load_heads<HALF>(from, in.head, h0, h1, a);
+  const Pairs w = weight_of<HALF>(p.weight[which], a);
+  const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
+  turn_heads<HALF, L>(x, from, in.head, p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0),
+                      (long long)p.n * p.how.d, h0, h1, p.chunk, norm, w, g, a, p.how);
 }
 
 // As store_kernel: a CTA holds one (page, head) of K or V in registers, so its
 // largest magnitude is known before any code is written; the rows are laid out
-// over lanes as above, and K goes through norm and rotation on the way in.
+// over lanes as above, and K goes through norm and rotation on the way in.  Of
+// many new tokens it takes several heads one after the other, the angles of its
+// rows kept in shared memory (a thread's own; four chunks of up to 8192 tokens
+// with 32 and 8 heads of 128: 114 -> 103 us, the floor is 62).
 // Further CTAs of an entry take its queries: L lanes one token's of q_chunk
 // heads, so that the angles (as much work as a row's norm and rotation) are
 // computed once for all of them.
+// (Four threads per token of the page instead of two, with half the registers
+// each: the same 114 us for four chunks of up to 8192 tokens, and 9.1 instead of
+// 7.6 for a step of 64 single ones.)
 template <int PAGE, bool HALF, int L>
 __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStoreCall p) {
   constexpr int kThreads = PAGE * 2, kWarps = kThreads / 32, kPer = kThreads / L, kPasses = PAGE / kPer;
   grid_dep_wait();
   grid_dep_launch();
   __shared__ uint32_t s_max[kWarps];
+  extern __shared__ ulonglong2 s_angle[];   // a thread's own: [pass][cosines, sines][thread]
   const Cache& c = p.c;
   const int tid = threadIdx.x, lane = tid % L, group = tid / L;
   const int i = blockIdx.z;
+  const int cnt = p.counts ? p.counts[i] : p.rows;
+  const int shares = (c.Hkv + p.kv_heads - 1) / p.kv_heads, store_ctas = p.touched * 2 * shares;
+  // the grid covers `rows`: CTAs behind the entry's tokens end on one load (its
+  // first CTA tells what is wrong with the entry)
+  if (cnt >= 0 && cnt <= p.rows && blockIdx.x > 0) {
+    const int x = blockIdx.x, ahead = (x >> 1) / shares;   // pages between the first token's and this CTA's
+    if (x < store_ctas ? ahead > 0 && (long long)(ahead - 1) * PAGE + 1 >= cnt
+                       : ((x - store_ctas) * kPer) % p.rows >= cnt && (x - store_ctas) * kPer % p.rows + kPer <= p.rows)
+      return;
+  }
   const int s = p.seqs ? p.seqs[i] : i;
   bool again = false;                       // the sequence was named before: that entry stores it
   if (p.seqs)
@@ -245,27 +319,28 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_SEQ);
     return;
   }
-  const int len = c.length[s], held = c.count[s], cnt = p.counts ? p.counts[i] : p.rows;
+  const int len = c.length[s], held = c.count[s];
   if (cnt < 0 || cnt > p.rows || cnt > len || held < 0 || held > c.M || (long long)len > (long long)held * PAGE) {
     if (tid == 0) flag(c.status, DROPKV_FLAG_BAD_LENGTH);
     return;
   }
   const int start = len - cnt;
-  const int store_ctas = p.touched * 2 * c.Hkv;
   if ((int)blockIdx.x >= store_ctas) {
     const int item = ((int)blockIdx.x - store_ctas) * kPer + group;
     const int row = item % p.rows, h0 = item / p.rows * p.q_chunk;
     const int h1 = row < cnt ? min(h0 + p.q_chunk, p.Hq) : 0;
+    if (!__any_sync(0xffffffffu, h0 < h1)) return;
     const Part a = part_of(p.how, lane, HALF);
-    const Weight w = weight_of(p.q_weight, a);
+    const __nv_bfloat16* from = p.q.p + i * p.q.seq + row * p.q.row;
+    const Batch x = load_heads<HALF>(from, p.q.head, h0, h1, a);
+    const Pairs w = weight_of<HALF>(p.q_weight, a);
     const Angle g = angle_of(p.how, a, lane, position_of(p.positions, p.each, i, p.rows, row, start));
-    turn_heads<HALF, L>(p.q.p + i * p.q.seq + row * p.q.row, p.q.head,
-                        p.q_out + ((size_t)i * p.Hq * p.rows + row) * p.how.d, (long long)p.rows * p.how.d, h0, h1,
-                        p.q_chunk, p.q_weight != nullptr, w, g, a, p.how);
+    turn_heads<HALF, L>(x, from, p.q.head, p.q_out + ((size_t)i * p.Hq * p.rows + row) * p.how.d,
+                        (long long)p.rows * p.how.d, h0, h1, p.q_chunk, p.q_weight != nullptr, w, g, a, p.how);
     return;
   }
-  const int which = blockIdx.x & 1, h = ((int)blockIdx.x >> 1) % c.Hkv;
-  const int col = start / PAGE + ((int)blockIdx.x >> 1) / c.Hkv;
+  const int which = blockIdx.x & 1, h0 = ((int)blockIdx.x >> 1) % shares * p.kv_heads, h1 = min(h0 + p.kv_heads, c.Hkv);
+  const int col = start / PAGE + ((int)blockIdx.x >> 1) / shares;
   if (cnt == 0 || col > (len - 1) / PAGE) return;
   const int base = col * PAGE;              // first token of the page
   const int r0 = max(0, start - base), r1 = min(PAGE, len - base);   // slots of the new tokens
@@ -276,79 +351,99 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     a.c0 = 8 * lane;
     a.c1 = a.c0 + 4;
     a.turns = false;
-  }
-  const Rows& in = p.kv[which];
-  const __nv_bfloat16* src = in.p + i * in.seq + h * in.head + ((long long)base - start) * in.row;   // of slot 0
-  uint4 x[kPasses];
-#pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int r = r0 + group + u * kPer;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (r < r1 && a.live) x[u] = load_part<HALF>(src + r * in.row, a);
+  } else {
+    // the angles of the thread's rows, for all its heads
+#pragma unroll 1
+    for (int u = 0; r0 + group + u * kPer < r1; ++u) {
+      const Angle g = angle_of(p.how, a, lane, position_of(p.positions, p.each, i, p.rows, base + r0 + group + u * kPer - start, start));
+      s_angle[(2 * u) * kThreads + tid] = make_ulonglong2(g.c[0], g.c[1]);
+      s_angle[(2 * u + 1) * kThreads + tid] = make_ulonglong2(g.s[0], g.s[1]);
+    }
   }
   if (pg < 0 || pg >= c.P || c.refs[pg] != 1) {
     if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_PAGE);
     return;
   }
-  const size_t unit = (size_t)pg * c.Hkv + h;
+  const Rows& in = p.kv[which];
+  const Pairs w = weight_of<HALF>(which ? nullptr : p.k_weight, a);
   float* scales = which ? c.vs : c.ks;
-  const float held_scale = r0 > 0 ? scales[unit] : 0.f;
-  uint8_t* dst = (which ? c.v : c.k) + unit * PAGE * c.d;
-  if (!which) {
-    const Weight w = weight_of(p.k_weight, a);
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const __nv_bfloat16* src = in.p + i * in.seq + h * in.head + ((long long)base - start) * in.row;   // of slot 0
+    uint4 x[kPasses];
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-      if (r0 + u * kPer >= r1) break;       // (the same for all threads)
       const int r = r0 + group + u * kPer;
-      const long long at = r < r1 ? position_of(p.positions, p.each, i, p.rows, base + r - start, start) : 0;
-      x[u] = turn<HALF, L>(x[u], p.k_weight != nullptr, w, angle_of(p.how, a, lane, at), p.how);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (r < r1 && a.live) x[u] = load_part<HALF>(src + r * in.row, a);
     }
-  }
-  uint32_t m2 = 0;
+    const size_t unit = (size_t)pg * c.Hkv + h;
+    const float held_scale = r0 > 0 ? scales[unit] : 0.f;
+    uint8_t* dst = (which ? c.v : c.k) + unit * PAGE * c.d;
+    if (!which) {
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u) m2 = __vmaxu2(m2, largest2(x[u]));
-  auto block_max = [&](uint32_t m) {
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((tid & 31) == 0) s_max[tid >> 5] = m;
-    __syncthreads();
-    uint32_t r = s_max[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) r = max(r, s_max[w]);
-    __syncthreads();
-    return r;
-  };
-  uint32_t top = block_max(max(m2 & 0xFFFFu, m2 >> 16));
-  if (top >= 0x7F80u) {                     // an infinity or not-a-number: the scale is that of the others
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < kPasses; ++u) m = max(m, largest_finite(x[u]));
-    top = block_max(m);
-    if (tid == 0) flag(c.status, DROPKV_FLAG_NONFINITE);
-  }
-  const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale), inv = 1.0f / scale;
-#pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int r = r0 + group + u * kPer;
-    if (r < r1 && a.live) {
-      const uint2 o = codes8(x[u], scale, inv, c.code);
-      if (HALF) {
-        *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c0) = o.x;
-        *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c1) = o.y;
-      } else {
-        *reinterpret_cast<uint2*>(dst + r * c.d + a.c0) = o;
+      for (int u = 0; u < kPasses; ++u) {
+        if (r0 + u * kPer >= r1) break;       // (the same for all threads)
+        Angle g;
+        g.turns = a.turns;
+        if (r0 + group + u * kPer < r1) {
+          const ulonglong2 cc = s_angle[(2 * u) * kThreads + tid], ss = s_angle[(2 * u + 1) * kThreads + tid];
+          g.c[0] = cc.x;
+          g.c[1] = cc.y;
+          g.s[0] = ss.x;
+          g.s[1] = ss.y;
+        } else {
+          g.c[0] = g.c[1] = g.s[0] = g.s[1] = 0ull;
+        }
+        x[u] = turn<HALF, L>(x[u], p.k_weight != nullptr, w, g, p.how);
       }
     }
-  }
-  if (r0 > 0 && scale > held_scale) {       // earlier tokens of the page at the new scale
-    const float ratio = held_scale / scale;
-    for (int n = tid; n < r0 * (c.d / 8); n += kThreads) {
-      uint2 o = *reinterpret_cast<const uint2*>(dst + (size_t)n * 8);
-      o.x = rescale4(o.x, held_scale, scale, ratio, c.code);
-      o.y = rescale4(o.y, held_scale, scale, ratio, c.code);
-      *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = o;
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) m2 = __vmaxu2(m2, largest2(x[u]));
+    auto block_max = [&](uint32_t m) {
+      m = __reduce_max_sync(0xffffffffu, m);
+      if ((tid & 31) == 0) s_max[tid >> 5] = m;
+      __syncthreads();
+      uint32_t r = s_max[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) r = max(r, s_max[w]);
+      __syncthreads();
+      return r;
+    };
+    uint32_t top = block_max(max(m2 & 0xFFFFu, m2 >> 16));
+    if (top >= 0x7F80u) {                     // an infinity or not-a-number: the scale is that of the others
+      uint32_t m = 0;
+#pragma unroll
+      for (int u = 0; u < kPasses; ++u) m = max(m, largest_finite(x[u]));
+      top = block_max(m);
+      if (tid == 0) flag(c.status, DROPKV_FLAG_NONFINITE);
     }
+    const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale), inv = 1.0f / scale;
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      const int r = r0 + group + u * kPer;
+      if (r < r1 && a.live) {
+        const uint2 o = codes8(x[u], scale, inv, c.code);
+        if (HALF) {
+          *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c0) = o.x;
+          *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c1) = o.y;
+        } else {
+          *reinterpret_cast<uint2*>(dst + r * c.d + a.c0) = o;
+        }
+      }
+    }
+    if (r0 > 0 && scale > held_scale) {       // earlier tokens of the page at the new scale
+      const float ratio = held_scale / scale;
+      for (int n = tid; n < r0 * (c.d / 8); n += kThreads) {
+        uint2 o = *reinterpret_cast<const uint2*>(dst + (size_t)n * 8);
+        o.x = rescale4(o.x, held_scale, scale, ratio, c.code);
+        o.y = rescale4(o.y, held_scale, scale, ratio, c.code);
+        *reinterpret_cast<uint2*>(dst + (size_t)n * 8) = o;
+      }
+    }
+    if (tid == 0) scales[unit] = scale;
   }
-  if (tid == 0) scales[unit] = scale;
 }
 
 }  // namespace
@@ -358,7 +453,7 @@ cudaError_t launch_rotate(RotateCall p, int sms, cudaStream_t st) {
   const long long groups = ((long long)p.B * p.n + tokens - 1) / tokens;
   const int heads[2] = {p.in[0].p ? p.heads[0] : 0, p.in[1].p ? p.heads[1] : 0};
   // as many heads per CTA as leave every SM a few CTAs
-  p.chunk = 8;
+  p.chunk = kMostHeads;
   while (p.chunk > 1 && groups * ((heads[0] + p.chunk - 1) / p.chunk + (heads[1] + p.chunk - 1) / p.chunk) < 8LL * sms)
     p.chunk /= 2;
   p.chunks = (heads[0] + p.chunk - 1) / p.chunk;
@@ -373,12 +468,19 @@ template <int PAGE>
 cudaError_t launch_rs(RotateStoreCall p, cudaStream_t st) {
   const int L = p.how.d <= 64 ? 8 : 16, per = 2 * PAGE / L;
   p.touched = (int)(((long long)p.rows + PAGE - 2) / PAGE) + 1;   // most pages `rows` tokens touch
-  p.q_chunk = p.rows >= PAGE ? 8 : 4;
+  p.q_chunk = p.rows >= PAGE ? kStoreHeads : 4;
+  p.kv_heads = p.rows >= PAGE ? kStoreKvHeads : 1;
   const int q_ctas = p.q.p ? (int)(((long long)((p.Hq + p.q_chunk - 1) / p.q_chunk) * p.rows + per - 1) / per) : 0;
-  const dim3 grid((unsigned)(p.touched * 2 * p.c.Hkv + q_ctas), 1, p.n);
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(2 * PAGE), 0, st, p); };
-  if (L == 8) return p.how.half ? go(rotate_store_kernel<PAGE, true, 8>) : go(rotate_store_kernel<PAGE, false, 8>);
-  return p.how.half ? go(rotate_store_kernel<PAGE, true, 16>) : go(rotate_store_kernel<PAGE, false, 16>);
+  const dim3 grid((unsigned)(p.touched * 2 * ((p.c.Hkv + p.kv_heads - 1) / p.kv_heads) + q_ctas), 1, p.n);
+  constexpr int kMost = 2 * PAGE * 2 * 8 * 16;   // angles of 8 passes (4 where L is 8)
+  auto go = [&](auto kern, cudaError_t e) {
+    return e != cudaSuccess ? e : launch_pdl(kern, grid, dim3(2 * PAGE), L == 8 ? kMost / 2 : kMost, st, p);
+  };
+  if (L == 8)
+    return p.how.half ? go(rotate_store_kernel<PAGE, true, 8>, allow_smem<rotate_store_kernel<PAGE, true, 8>>(kMost))
+                      : go(rotate_store_kernel<PAGE, false, 8>, allow_smem<rotate_store_kernel<PAGE, false, 8>>(kMost));
+  return p.how.half ? go(rotate_store_kernel<PAGE, true, 16>, allow_smem<rotate_store_kernel<PAGE, true, 16>>(kMost))
+                    : go(rotate_store_kernel<PAGE, false, 16>, allow_smem<rotate_store_kernel<PAGE, false, 16>>(kMost));
 }
 }  // namespace
 

@@ -1108,7 +1108,7 @@ cudaError_t launch_prefix(const SharedCall& p, cudaStream_t st) {
 cudaError_t launch_shared(const SharedCall& p, cudaStream_t st) {
   cudaError_t e = launch_plan(p, st);
   // (own tokens first: the shared tokens' pieces, some 20 MB, are then still in
-  // the L2 cache when they are joined: FIGURE)
+  // the L2 cache when they are joined)
   if (e == cudaSuccess) e = launch_own_attention(p.own, st);
   if (e == cudaSuccess)
     e = p.own.c.code == KVCACHE_INT8 ? launch_prefix<KVCACHE_INT8>(p, st) : launch_prefix<KVCACHE_E4M3>(p, st);

@@ -23,6 +23,7 @@ dropkv_status open_rotary(const kvcache_rotary* r, Turning* t) {
   t->half = r->layout == KVCACHE_HALF;
   t->eps = r->eps;
   t->amplitude = r->amplitude;
+  t->inv_d = 1.0f / (float)r->d;
   return DROPKV_OK;
 }
 

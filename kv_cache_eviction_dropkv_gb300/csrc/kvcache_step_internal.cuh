@@ -15,7 +15,7 @@ struct Rows {
 struct Turning {
   const unsigned long long* turns;   // [dims / 2], 2^-64 turns per position
   int d, dims, half;             // half: pair i is (i, i + dims / 2), else (2 i, 2 i + 1)
-  float eps, amplitude;
+  float eps, amplitude, inv_d;
 };
 
 struct RotateCall {
@@ -42,7 +42,7 @@ struct RotateStoreCall {
   int each;
   int n, Hq, rows;
   int touched;                   // pages that `rows` tokens touch at most
-  int q_chunk;                   // heads of one token that its lanes take
+  int q_chunk, kv_heads;         // query heads of one token that its lanes take, KV heads of a page that a CTA takes
 };
 cudaError_t launch_rotate_store(RotateStoreCall p, cudaStream_t st);
 

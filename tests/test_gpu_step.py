@@ -156,6 +156,18 @@ def test_rotation_of_extreme_rows():
     assert plan.check() == 0
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_channels_that_do_not_turn_keep_to_themselves(layout):
+    x = draw_rows(1, 2, 3, 64, 3)
+    x[..., 40], x[..., 63] = float("inf"), float("nan")
+    out = torch.empty(1, 2, 3, 64, dtype=torch.bfloat16, device=DEV)
+    for dims in (0, 16, 32):
+        Rotary(64, dims=dims, layout=layout, device=DEV).apply(x.to(DEV), None, out, None, positions=ints([1000]))
+        # (a not-a-number leaves the rounding as the canonical one)
+        torch.testing.assert_close(out[..., 32:].cpu(), x[..., 32:], rtol=0, atol=0, equal_nan=True)
+        assert bool(out[..., :32].isfinite().all())
+
+
 def test_rotation_refusals():
     plan = Rotary(64, device=DEV)
     q, k = rows(2, 4, 3, 64, 1), rows(2, 2, 3, 64, 2)
