@@ -286,6 +286,7 @@ constexpr float kLiftLog2 = 4.0f, kPieceLift = 7.0f - kLiftLog2;   // (pieces ar
 constexpr float kMost = 32768.f;                  // most that P of a row and 32 tokens may sum up to (fp16 holds 65504)
 constexpr float kLowLog2 = -60.0f;                // least exponent of the factor of P: below it P is 0 in fp16 anyway
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
+constexpr int kAhead = 6;                         // below 8, the fewest tiles of a batch of descriptions
 constexpr int kMaxStages = 5, kMeta = 16;          // kMeta >= kMaxStages + 4
 
 template <int DS>
@@ -342,6 +343,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
                "l"(src), "r"(bytes), "r"(smem_addr(bar))
                : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {   // 16-byte aligned, a multiple of 16
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
@@ -766,6 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     };
     describe(x0 + lane / per, 0);
     const uint32_t bytes = (uint32_t)c.page * c.d;
+    // The stages hold one or two tiles, which is less than memory's latency:
+    // tiles up to kAhead further on are on their way to L2.
+    auto ahead = [&](int w, bool take) {
+      if (!take || pg[w] < 0) return;
+      const size_t at = ((size_t)pg[w] * c.Hkv + head[w]) * bytes;
+      prefetch_l2(c.k + at, bytes);
+      prefetch_l2(c.v + at, bytes);
+    };
+    ahead(0, lane / per < kAhead);
     bool ok = true;
     uint32_t i = 0, n = x1 - x0;
     for (; ok && i < n; ++i) {
@@ -779,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         describe(x0 + i + tiles + lane / per, 1);
       }
+      ahead(t + kAhead < tiles ? 0 : 1, lane / per == (t + kAhead) % tiles);
       const bool here = lane / per == t, mine = here && pg[0] >= 0;
       const uint32_t pages = __popc(__ballot_sync(0xffffffffu, mine));
       const uint32_t slot = i % stages, round = i / stages;
@@ -990,12 +1004,12 @@ __device__ __forceinline__ void join_in(Joined& a, const float4 (&st)[N], const 
   a.m = mn;
   a.M = Mn;
 }
-constexpr int kJoinWarps = 4;
-// WHOLE: a CTA joins one row, its warps a quarter of the pieces each (few rows
-// of up to 300 pieces); else a warp joins a row.
-template <bool WHOLE>
-__global__ void __launch_bounds__(32 * kJoinWarps, WHOLE ? 12 : 8) final_kernel(const SharedCall p) {
-  constexpr int kBatch = 5;
+// W > 1: a CTA of W warps joins one row, of up to some 300 pieces; else a warp
+// each joins a row (4 to a CTA).
+template <int W>
+__global__ void __launch_bounds__(32 * (W > 1 ? W : 4), W > 1 ? 48 / W : 8) final_kernel(const SharedCall p) {
+  constexpr bool WHOLE = W > 1;
+  constexpr int kBatch = 5, kJoinWarps = WHOLE ? W : 4;
   __shared__ float4 s_o[kJoinWarps][32], s_s[kJoinWarps];
   grid_dep_wait();
   grid_dep_launch();
@@ -1054,13 +1068,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WHOLE ? 12 : 8) final_kernel(
     if (lane == 0) s_s[warp] = make_float4(j.m, j.l, j.M, 0.f);
     __syncthreads();
     if (warp > 0) return;
-    float4 st[kJoinWarps - 1], x[kJoinWarps - 1];
-#pragma unroll
+#pragma unroll 1
     for (int w = 1; w < kJoinWarps; ++w) {
-      st[w - 1] = s_s[w];
-      x[w - 1] = s_o[w][lane];
+      const float4 st[1] = {s_s[w]}, x[1] = {s_o[w][lane]};
+      join_in(j, st, x);
     }
-    join_in(j, st, x);
   }
   if (!cols) return;
   // o stands for o 2^(M - m - 7); a row that saw nothing has l = 0
@@ -1115,8 +1127,9 @@ cudaError_t launch_shared(const SharedCall& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.own.n * p.own.Hq * p.own.T;
   const unsigned per = (unsigned)(p.own.Hq * p.own.T);
-  if (rows <= 64LL * p.sms) return launch_pdl(final_kernel<true>, dim3(per, p.own.n), dim3(32 * kJoinWarps), 0, st, p);
-  return launch_pdl(final_kernel<false>, dim3((per + kJoinWarps - 1) / kJoinWarps, p.own.n), dim3(32 * kJoinWarps), 0, st, p);
+  if (rows <= 4LL * p.sms) return launch_pdl(final_kernel<8>, dim3(per, p.own.n), dim3(256), 0, st, p);
+  if (rows <= 64LL * p.sms) return launch_pdl(final_kernel<4>, dim3(per, p.own.n), dim3(128), 0, st, p);
+  return launch_pdl(final_kernel<1>, dim3((per + 3) / 4, p.own.n), dim3(128), 0, st, p);
 }
 
 }  // namespace kvcache
