@@ -145,8 +145,10 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  *   groups  device int32 [G + 1], groups[0] = 0, not decreasing, groups[G] =
  *           n; anything else is flagged (DROPKV_FLAG_BAD_LENGTH) and nothing
  *           is shared
- * Numerics as kvcache_attention's.  Supported: what kvcache_attention
- * supports with n * Hq * T <= 2^22, 1 <= G <= n. */
+ * Numerics: probabilities of the shared tokens are off by 2^-11 of themselves
+ * or 2^-29 of the row's largest, the rest as kvcache_attention's.  Supported:
+ * what kvcache_attention supports with n * Hq * T <= 2^22, 1 <= G <= n and
+ * (max_pages * page / 128 + 1) * (n * Hq * T / 128 + G * Hkv) < 2^31. */
 typedef struct {
   const kvcache_shape* shape;
   const kvcache_buffers* cache;

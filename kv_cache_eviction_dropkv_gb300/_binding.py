@@ -121,7 +121,8 @@ def _load(path):
     for name in STEP_CALLS:
         getattr(L, name).argtypes = [ctypes.c_char_p]
         getattr(L, name).restype = ctypes.c_int
-    for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k", "kvcache_test_skip_window_pair"):
+    for hook in ("dropkv_test_skip_pass2_k", "dropkv_test_skip_prefill_k", "kvcache_test_skip_window_pair",
+                 "kvcache_test_skip_shared_load"):
         if hasattr(L, hook):
             getattr(L, hook).argtypes = [I32, I32]
             getattr(L, hook).restype = ctypes.c_int

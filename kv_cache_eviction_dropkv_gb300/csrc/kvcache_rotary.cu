@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x % L;
-  const int token = blockIdx.x * (kRotThreads / L) + threadIdx.x / L;
-  const int b = token / p.n, t = token - b * p.n;
+  const uint32_t token = blockIdx.x * (kRotThreads / L) + threadIdx.x / L;   // (up to 2^31 + 30)
+  const int b = token / (uint32_t)p.n, t = token - (uint32_t)b * p.n;
   const int which = (int)blockIdx.y >= p.chunks ? 1 : 0;
   const int h0 = ((int)blockIdx.y - (which ? p.chunks : 0)) * p.chunk;
   int h1 = min(h0 + p.chunk, p.heads[which]);

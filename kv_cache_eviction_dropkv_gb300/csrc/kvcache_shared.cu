@@ -694,6 +694,10 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
   }
 }
 
+#ifdef DROPKV_TEST_HOOKS
+__device__ int g_test_skip_load[2] = {-1, -1};    // CTA and load that the test build leaves out
+#endif
+
 template <int CODE, int DS>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ SharedCall p) {
   using L = Layout<DS>;
@@ -810,13 +814,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       }
       if (lane == 0) S.meta[i % kMeta].tokens = pages << c.page_log2;
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&S.sk_full[slot], pages * bytes);
+      bool load[2] = {true, true};
+#ifdef DROPKV_TEST_HOOKS
+      if ((int)blockIdx.x == g_test_skip_load[0] && (int)i == g_test_skip_load[1] >> 1) load[g_test_skip_load[1] & 1] = false;
+#endif
+      if (lane == 0 && load[0]) mbar_arrive_expect_tx(&S.sk_full[slot], pages * bytes);
       __syncwarp();
-      if (mine) bulk_load(dst, c.k + at, bytes, &S.sk_full[slot]);
+      if (mine && load[0]) bulk_load(dst, c.k + at, bytes, &S.sk_full[slot]);
       if (round > 0 && !(ok = wait(&S.sv_empty[slot], round - 1))) { ++i; break; }
-      if (lane == 0) mbar_arrive_expect_tx(&S.sv_full[slot], pages * bytes);
+      if (lane == 0 && load[1]) mbar_arrive_expect_tx(&S.sv_full[slot], pages * bytes);
       __syncwarp();
-      if (mine) bulk_load(dst + L::kStageB / 2, c.v + at, bytes, &S.sv_full[slot]);
+      if (mine && load[1]) bulk_load(dst + L::kStageB / 2, c.v + at, bytes, &S.sv_full[slot]);
     }
     if (!ok) give_up();
     // every copy has landed before the CTA can leave
@@ -1133,3 +1141,11 @@ cudaError_t launch_shared(const SharedCall& p, cudaStream_t st) {
 }
 
 }  // namespace kvcache
+
+#ifdef DROPKV_TEST_HOOKS
+#include "../../include/kvcache_step_test_hooks.h"
+extern "C" dropkv_status kvcache_test_skip_shared_load(int32_t cta, int32_t load) {
+  const int v[2] = {cta, load};
+  return cudaMemcpyToSymbol(kvcache::g_test_skip_load, v, sizeof v) == cudaSuccess ? DROPKV_OK : DROPKV_ERR_CUDA;
+}
+#endif

@@ -50,6 +50,12 @@ bool dense(const Rows& r, long long n, long long heads, long long rows, int d) {
   return (rows <= 1 || r.row == d) && (heads <= 1 || r.head == rows * d) && (n <= 1 || r.seq == heads * rows * d);
 }
 
+// The tiles of all units' shared tokens, at their most, in 32 bits.
+bool counts_fit(const kvcache_shape& s, int n, int Hq, int T, int G) {
+  const double tiles = (double)s.max_pages * s.page / 128 + 1, units = (double)n * Hq * T / 128 + (double)G * s.Hkv;
+  return tiles * units < 2147483648.0;
+}
+
 // The workspace of a shared attention (byte offsets); the second half's parts
 // and cuts have the sizes given.
 struct SharedSpace {
@@ -194,7 +200,7 @@ dropkv_status kvcache_read(const kvcache_read_call* call) {
 size_t kvcache_shared_workspace_size(const kvcache_shape* shape, int32_t n, int32_t Hq, int32_t T, int32_t G) {
   const int sms = current_sms(nullptr);
   if (sms <= 0 || check_shape(shape) != DROPKV_OK || Hq < 1 || T < 1 || Hq % shape->Hkv != 0 || G < 1 || G > n ||
-      n > shape->seqs || n > 65535 || (long long)Hq * T > kMaxSharedRows / n)
+      n > shape->seqs || n > 65535 || (long long)Hq * T > kMaxSharedRows / n || !counts_fit(*shape, n, Hq, T, G))
     return 0;
   // the second half's pieces at their most, for any number of entries up to n
   const SharedSpace w = make_shared_space(*shape, n, Hq, T, G, sms, 0, 0, 0);
@@ -228,7 +234,7 @@ dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call
   const int sms = current_sms(nullptr);
   if (sms <= 0) return DROPKV_ERR_CUDA;
   AttnPlan plan{};
-  if (!make_attn_plan(shape, n, Hq, T, 0, 0, sms, &plan)) return DROPKV_ERR_UNSUPPORTED;
+  if (!make_attn_plan(shape, n, Hq, T, 0, 0, sms, &plan) || !counts_fit(shape, n, Hq, T, call->G)) return DROPKV_ERR_UNSUPPORTED;
   const bool by_runs = !plan.team && !plan.solo;
   const SharedSpace w = make_shared_space(shape, n, Hq, T, call->G, sms, by_runs ? plan.part_s : 0,
                                           by_runs ? plan.cuts - plan.part_s : 0,

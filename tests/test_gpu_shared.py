@@ -295,3 +295,42 @@ def test_two_captured_calls_and_other_streams():
             want = check(c, q, members.tolist(), groups.tolist(), layer)
             assert torch.equal(outs[layer], want)
     assert c.check() == 0
+
+
+def test_more_entries_than_one_cta_plans():
+    """1300 entries: the groups stand in global memory."""
+    sizes = [400, 1, 0, 500, 3, 396]
+    c, seqs, starts = forked([130, 64, 32, 257, 40, 96], [[1 + (i + j) % 5 for i in range(m)] for j, m in enumerate(sizes)],
+                             1, 2, 16, 32, seed=5)
+    q = queries(len(seqs), 2, 1, 16, 3)
+    check(c, q, seqs, starts)
+    c.table[seqs[3], 1] = c.table[seqs[1000], 0]                 # one member of the first group differs in its second page
+    check(c, q, seqs, starts)
+    assert c.check() == 0
+    c.shared_attention(0, q, torch.empty_like(q), ints([0, 1299]), seqs=ints(seqs), least=0)
+    assert flags_of(c) == B.FLAG_BAD_LENGTH
+
+
+def test_offsets_past_32_bits():
+    """Pages whose codes lie more than 2^32 bytes into the pool: shared, read back and stored to."""
+    from kv_cache_eviction_dropkv_gb300 import Rotary
+
+    c = PagedCache(4, 8, 128, 36000, 128, 24, 1, "e4m3", Hq=16, T=1, device=DEV, groups=1)
+    c.refs[:35900] = 1                                          # the free pages are the last ones
+    assert 35900 * 8 * 128 * 128 > 2 ** 32
+    put(c, [0], [2000], 3)
+    c.fork(ints([0, 0, 0]), ints([1, 2, 3]))
+    put(c, [1, 2, 3], [5, 200, 40], 7)
+    assert int(c.table[1, 0]) >= 35900
+    check(c, queries(3, 16, 1, 128, 3), [1, 2, 3], [0, 3])
+    k, v, q = (draw_rows(3, h, 4, 128, 9 + h).to(DEV) for h in (8, 8, 16))
+    c.reserve(ints([4, 4, 4]), seqs=ints([1, 2, 3]))
+    plan, q_out = Rotary(128, dims=0, device=DEV), torch.empty_like(q)
+    c.store_rotated(0, plan, q, k, v, q_out, seqs=ints([1, 2, 3]))
+    assert torch.equal(q_out, q)
+    got = [torch.empty_like(k) for _ in range(2)]
+    c.read(0, *got, starts=c.length[1:] - 4, seqs=ints([1, 2, 3]))
+    for a, b in zip(got, (k, v)):                               # e4m3: half a step of four bits, or of the smallest number
+        scale = torch.maximum(c.k_scale.max(), c.v_scale.max()).item()
+        assert bool(((a.double() - b.double()).abs() <= 2.0 ** -4 * b.double().abs() + 2.0 ** -10 * scale).all())
+    assert c.check() == 0
