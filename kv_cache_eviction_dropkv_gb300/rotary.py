@@ -22,13 +22,13 @@ def frequencies(dims: int, base: float = 10000.0, scaling: Optional[dict] = None
     by `scaling` (Rotary's), and the amplitude: ([float], float)."""
     if not (math.isfinite(base) and base > 0):
         raise ValueError("base must be positive")
-    how = dict(scaling or {})
+    how = {k: v for k, v in (scaling or {}).items() if v is not None}
     kind = how.pop("kind", None)
     if scaling:
         if kind not in _SCALINGS or not {"factor"} <= set(how) <= _SCALINGS[kind]:
             raise ValueError("scaling: kind is one of %s, with %s" % (sorted(_SCALINGS), {k: sorted(v) for k, v in
                                                                                           _SCALINGS.items()}))
-        if any(v is not None and not (math.isfinite(v) and v > 0) for v in how.values()):
+        if any(not (math.isfinite(v) and v > 0) for v in how.values()):
             raise ValueError("scaling: positive numbers are wanted")
     factor, amplitude = float(how.get("factor", 1.0)), 1.0
     if kind == "ntk" and dims > 2:
@@ -46,6 +46,8 @@ def frequencies(dims: int, base: float = 10000.0, scaling: Optional[dict] = None
             keep = min(1.0, max(0.0, (how["original"] * f / (2 * math.pi) - low) / (high - low)))
             freq[i] = f / factor * (1 - keep) + f * keep
     elif kind == "yarn":
+        if base <= 1:
+            raise ValueError("scaling: yarn needs a base above 1")
         edge = lambda turns: dims * math.log(how["original"] / (2 * math.pi * turns)) / (2 * math.log(base))
         lo = max(0, math.floor(edge(float(how.get("fast", 32.0)))))
         hi = min(dims - 1, math.ceil(edge(float(how.get("slow", 1.0)))))

@@ -193,3 +193,14 @@ def test_rows_of_views():
         B.rows_of("q", odd, (2, 1, 5, 64), -1)
     one = torch.zeros(64, dtype=torch.bfloat16).as_strided((1, 1, 1, 64), (3, 5, 7, 1))
     B.rows_of("q", one, (1, 1, 1, 64), -1)                        # strides over single items are not used
+
+
+def test_frequencies_without_a_ramp_are_refused():
+    with pytest.raises(ValueError):                    # the ramp stands on powers of the base
+        rotary.frequencies(64, 1.0, dict(kind="yarn", factor=2.0, original=4096))
+    for kind in ("yarn", "bands"):
+        with pytest.raises(ValueError):
+            rotary.frequencies(64, 10000.0, dict(kind=kind, factor=2.0, original=None))
+        with pytest.raises(ValueError):
+            rotary.frequencies(64, 10000.0, dict(kind=kind, factor=None, original=4096))
+    assert rotary.frequencies(64, 1.0, dict(kind="linear", factor=2.0)) == ([0.5] * 32, 1.0)
