@@ -183,55 +183,62 @@ __device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Pairs& 
                     pack_bf16(f2_lo(y.a[1]), f2_lo(y.b[1])), pack_bf16(f2_hi(y.a[1]), f2_hi(y.b[1])));
 }
 
+// `at`: the lane's first channel c0; `apart`: c1 - c0.
 template <bool HALF>
-__device__ __forceinline__ uint4 load_part(const __nv_bfloat16* row, const Part& a) {
-  if (!HALF) return __ldcs(reinterpret_cast<const uint4*>(row + a.c0));
-  const uint2 lo = __ldcs(reinterpret_cast<const uint2*>(row + a.c0)), hi = __ldcs(reinterpret_cast<const uint2*>(row + a.c1));
+__device__ __forceinline__ uint4 load_part(const __nv_bfloat16* at, int apart) {
+  if (!HALF) return __ldcs(reinterpret_cast<const uint4*>(at));
+  const uint2 lo = __ldcs(reinterpret_cast<const uint2*>(at)), hi = __ldcs(reinterpret_cast<const uint2*>(at + apart));
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 template <bool HALF>
-__device__ __forceinline__ void store_part(__nv_bfloat16* row, const Part& a, const uint4& x) {
+__device__ __forceinline__ void store_part(__nv_bfloat16* at, int apart, const uint4& x) {
   if (!HALF) {
-    *reinterpret_cast<uint4*>(row + a.c0) = x;
+    *reinterpret_cast<uint4*>(at) = x;
   } else {
-    *reinterpret_cast<uint2*>(row + a.c0) = make_uint2(x.x, x.y);
-    *reinterpret_cast<uint2*>(row + a.c1) = make_uint2(x.z, x.w);
+    *reinterpret_cast<uint2*>(at) = make_uint2(x.x, x.y);
+    *reinterpret_cast<uint2*>(at + apart) = make_uint2(x.z, x.w);
   }
 }
 
 constexpr int kBatch = 4;                       // heads whose loads are in flight together
 
-// One token's rows of heads [h0, h1), `from` and `to` those of head 0.  All
-// lanes of the warp walk `chunk` heads, a batch's loads ahead of its work: the
-// first one's are made by load_heads before the angles are computed.
+// One token's rows of `mine` heads, `from` and `to` the lane's part of the
+// first.  All lanes of the warp walk `heads`, the most any has, a batch's loads
+// ahead of its work: the first one's are made by load_heads before the angles
+// are computed.
+// (Addresses go along by a step each: a product per head and access was a
+// third of the instructions, which bound the kernel.)
 struct Batch {
   uint4 x[kBatch];
 };
 template <bool HALF>
-__device__ __forceinline__ Batch load_heads(const __nv_bfloat16* from, long long step, int h, int h1, const Part& a) {
+__device__ __forceinline__ Batch load_heads(const __nv_bfloat16*& from, long long step, int mine, int apart) {
   Batch b;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
     b.x[u] = make_uint4(0, 0, 0, 0);
-    if (a.live && h + u < h1) b.x[u] = load_part<HALF>(from + (h + u) * step, a);
+    if (u < mine) b.x[u] = load_part<HALF>(from, apart);
+    from += step;
   }
   return b;
 }
 template <bool HALF, int L>
 __device__ __forceinline__ void turn_heads(Batch x, const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
-                                           long long to_step, int h0, int h1, int chunk, bool norm, const Pairs& w,
-                                           const Angle& g, const Part& a, const Turning& how) {
+                                           long long to_step, int heads, int mine, bool norm, const Pairs& w,
+                                           const Angle& g, int apart, const Turning& how) {
 #pragma unroll 1
-  for (int k = 0;;) {
+  for (;;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (k + u >= chunk) break;
+      if (u >= heads) break;
       x.x[u] = turn<HALF, L>(x.x[u], norm, w, g, how);
-      if (a.live && h0 + k + u < h1) store_part<HALF>(to + (h0 + k + u) * to_step, a, x.x[u]);
+      if (u < mine) store_part<HALF>(to, apart, x.x[u]);
+      to += to_step;
     }
-    k += kBatch;
-    if (k >= chunk) break;
-    x = load_heads<HALF>(from, from_step, h0 + k, h1, a);
+    heads -= kBatch;
+    mine -= kBatch;
+    if (heads <= 0) break;
+    x = load_heads<HALF>(from, from_step, mine, apart);
   }
 }
 
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall
   const int b = token / (uint32_t)p.n, t = token - (uint32_t)b * p.n;
   const int which = (int)blockIdx.y >= p.chunks ? 1 : 0;
   const int h0 = ((int)blockIdx.y - (which ? p.chunks : 0)) * p.chunk;
-  int h1 = min(h0 + p.chunk, p.heads[which]);
+  const int heads = min(p.chunk, p.heads[which] - h0);
   const Part a = part_of(p.how, lane, HALF);
   const bool norm = p.weight[which] != nullptr;
   bool live = b < p.B;
@@ -269,13 +276,15 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall
   }
   if (!__any_sync(0xffffffffu, live)) return;
   const Rows& in = p.in[which];
-  const __nv_bfloat16* from = in.p + (live ? b * in.seq + t * in.row : 0);
-  if (!live) h1 = 0;
-  const Batch x = load_heads<HALF>(from, in.head, h0, h1, a);
+  const int mine = live && a.live ? heads : 0, apart = a.c1 - a.c0;
+  const __nv_bfloat16* from = in.p + (mine > 0 ? b * in.seq + t * in.row + h0 * in.head + a.c0 : 0);
+  const Batch x = load_heads<HALF>(from, in.head, mine, apart);
   const Pairs w = weight_of<HALF>(p.weight[which], a);
   const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
-  turn_heads<HALF, L>(x, from, in.head, p.out[which] + (live ? ((long long)b * p.heads[which] * p.n + t) * p.how.d : 0),
-                      (long long)p.n * p.how.d, h0, h1, p.chunk, norm, w, g, a, p.how);
+  const long long to_step = (long long)p.n * p.how.d;
+  __nv_bfloat16* to =
+      p.out[which] + (mine > 0 ? ((long long)b * p.heads[which] + h0) * to_step + (long long)t * p.how.d + a.c0 : 0);
+  turn_heads<HALF, L>(x, from, in.head, to, to_step, heads, mine, norm, w, g, apart, p.how);
 }
 
 // As store_kernel: a CTA holds one (page, head) of K or V in registers, so its
@@ -328,15 +337,18 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
   if ((int)blockIdx.x >= store_ctas) {
     const int item = ((int)blockIdx.x - store_ctas) * kPer + group;
     const int row = item % p.rows, h0 = item / p.rows * p.q_chunk;
-    const int h1 = row < cnt ? min(h0 + p.q_chunk, p.Hq) : 0;
-    if (!__any_sync(0xffffffffu, h0 < h1)) return;
     const Part a = part_of(p.how, lane, HALF);
-    const __nv_bfloat16* from = p.q.p + i * p.q.seq + row * p.q.row;
-    const Batch x = load_heads<HALF>(from, p.q.head, h0, h1, a);
+    const int own = row < cnt ? max(0, min(p.q_chunk, p.Hq - h0)) : 0, heads = __reduce_max_sync(0xffffffffu, own);
+    if (heads == 0) return;
+    const int mine = a.live ? own : 0, apart = a.c1 - a.c0;
+    const __nv_bfloat16* from = p.q.p + (mine > 0 ? i * p.q.seq + row * p.q.row + h0 * p.q.head + a.c0 : 0);
+    const Batch x = load_heads<HALF>(from, p.q.head, mine, apart);
     const Pairs w = weight_of<HALF>(p.q_weight, a);
     const Angle g = angle_of(p.how, a, lane, position_of(p.positions, p.each, i, p.rows, row, start));
-    turn_heads<HALF, L>(x, from, p.q.head, p.q_out + ((size_t)i * p.Hq * p.rows + row) * p.how.d,
-                        (long long)p.rows * p.how.d, h0, h1, p.q_chunk, p.q_weight != nullptr, w, g, a, p.how);
+    const long long to_step = (long long)p.rows * p.how.d;
+    __nv_bfloat16* to =
+        p.q_out + (mine > 0 ? ((long long)i * p.Hq + h0) * to_step + (long long)row * p.how.d + a.c0 : 0);
+    turn_heads<HALF, L>(x, from, p.q.head, to, to_step, heads, mine, p.q_weight != nullptr, w, g, apart, p.how);
     return;
   }
   const int which = blockIdx.x & 1, h0 = ((int)blockIdx.x >> 1) % shares * p.kv_heads, h1 = min(h0 + p.kv_heads, c.Hkv);
@@ -367,15 +379,19 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
   const Rows& in = p.kv[which];
   const Pairs w = weight_of<HALF>(which ? nullptr : p.k_weight, a);
   float* scales = which ? c.vs : c.ks;
+  // the lane's part of the first of its group's rows, and how many of them are new
+  const int mine = a.live ? max(0, (r1 - r0 - group + kPer - 1) / kPer) : 0, apart = a.c1 - a.c0;
+  const __nv_bfloat16* first =
+      in.p + (mine > 0 ? i * in.seq + ((long long)base - start + r0 + group) * in.row + a.c0 : 0);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
-    const __nv_bfloat16* src = in.p + i * in.seq + h * in.head + ((long long)base - start) * in.row;   // of slot 0
     uint4 x[kPasses];
+    const __nv_bfloat16* src = first + h * in.head;
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-      const int r = r0 + group + u * kPer;
       x[u] = make_uint4(0, 0, 0, 0);
-      if (r < r1 && a.live) x[u] = load_part<HALF>(src + r * in.row, a);
+      if (u < mine) x[u] = load_part<HALF>(src, apart);
+      src += kPer * in.row;
     }
     const size_t unit = (size_t)pg * c.Hkv + h;
     const float held_scale = r0 > 0 ? scales[unit] : 0.f;
@@ -422,14 +438,14 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     const float scale = fmaxf(page_scale(__uint_as_float(top << 16), c.code), held_scale), inv = 1.0f / scale;
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
-      const int r = r0 + group + u * kPer;
-      if (r < r1 && a.live) {
+      if (u < mine) {
         const uint2 o = codes8(x[u], scale, inv, c.code);
+        uint8_t* at = dst + (r0 + group + u * kPer) * c.d + a.c0;
         if (HALF) {
-          *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c0) = o.x;
-          *reinterpret_cast<uint32_t*>(dst + r * c.d + a.c1) = o.y;
+          *reinterpret_cast<uint32_t*>(at) = o.x;
+          *reinterpret_cast<uint32_t*>(at + apart) = o.y;
         } else {
-          *reinterpret_cast<uint2*>(dst + r * c.d + a.c0) = o;
+          *reinterpret_cast<uint2*>(at) = o;
         }
       }
     }
