@@ -4,7 +4,8 @@
 //   y = x rsqrt(mean(x^2) + eps) w,   (y_a, y_b) <- A (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
 //
 // Both are bound by memory: each row is read once and written once, and the
-// rest has to stay under that.  A row of d <= 128 channels belongs to 16 lanes
+// rest has to stay under that (a 32K prompt of 32 and 8 heads of 128 in 106 us,
+// 6.3 TB/s, 95 % of a copy).  A row of d <= 128 channels belongs to 16 lanes
 // (8 where d <= 64), 8 channels to a lane: channels that turn together are
 // always one lane's, so the rotation needs no exchange and the norm one sum
 // over the row's lanes.  With pairs (i, i + dims / 2) a lane has 4 channels of
@@ -206,48 +207,53 @@ constexpr int kBatch = 4;                       // heads whose loads are in flig
 // first.  All lanes of the warp walk `heads`, the most any has, a batch's loads
 // ahead of its work: the first one's are made by load_heads before the angles
 // are computed.
-// (Addresses go along by a step each: a product per head and access was a
-// third of the instructions, which bound the kernel.)
+// (Addresses go along by a step each: with a product per head and access the
+// kernel issued 170 instructions a row of two tokens instead of 132, and was
+// bound by that: 32K prompt 117 -> 106 us.)
+template <int N>
 struct Batch {
-  uint4 x[kBatch];
+  uint4 x[N];
 };
-template <bool HALF>
-__device__ __forceinline__ Batch load_heads(const __nv_bfloat16*& from, long long step, int mine, int apart) {
-  Batch b;
+template <bool HALF, int N>
+__device__ __forceinline__ Batch<N> load_heads(const __nv_bfloat16*& from, long long step, int mine, int apart) {
+  Batch<N> b;
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
+  for (int u = 0; u < N; ++u) {
     b.x[u] = make_uint4(0, 0, 0, 0);
     if (u < mine) b.x[u] = load_part<HALF>(from, apart);
     from += step;
   }
   return b;
 }
-template <bool HALF, int L>
-__device__ __forceinline__ void turn_heads(Batch x, const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
+template <bool HALF, int L, int N>
+__device__ __forceinline__ void turn_heads(Batch<N> x, const __nv_bfloat16* from, long long from_step, __nv_bfloat16* to,
                                            long long to_step, int heads, int mine, bool norm, const Pairs& w,
                                            const Angle& g, int apart, const Turning& how) {
 #pragma unroll 1
   for (;;) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < N; ++u) {
       if (u >= heads) break;
       x.x[u] = turn<HALF, L>(x.x[u], norm, w, g, how);
       if (u < mine) store_part<HALF>(to, apart, x.x[u]);
       to += to_step;
     }
-    heads -= kBatch;
-    mine -= kBatch;
+    heads -= N;
+    mine -= N;
     if (heads <= 0) break;
-    x = load_heads<HALF>(from, from_step, mine, apart);
+    x = load_heads<HALF, N>(from, from_step, mine, apart);
   }
 }
 
-// Most heads a CTA of rotate_kernel takes, and a token's lanes in the store (8
-// and 16: 32K prompt 117 and 124 us, four chunks of up to 8192 tokens stored 118
-// and 114; a batch's loads under the work of the one before, which costs a
-// fifth of the threads that fit: 127 and 111).
-constexpr int kRotThreads = 256, kMostHeads = 8, kStoreHeads = 16;
-constexpr int kStoreKvHeads = 4;                // KV heads that a CTA of many new tokens takes, one after the other
+// Most heads a CTA of rotate_kernel takes (8 and 16: 32K prompt 117 and 124 us;
+// a batch's loads under the work of the one before, which costs a fifth of the
+// threads that fit: 127).  In the store, of a chunk's queries, a token's lanes
+// take up to 32, eight loads in flight (its CTAs are few to an SM), and a CTA 4
+// of the KV heads, one after the other.  Four chunks of up to 8192 tokens with 32
+// and 8 heads: 16 and 32 query heads 97 and 92 us, batches of 4 and 8 heads 88 and
+// 87, 2, 4 and 8 KV heads 91, 87 and 100.
+constexpr int kRotThreads = 256, kMostHeads = 8;
+constexpr int kStoreHeads = 32, kStoreBatch = 8, kStoreKvHeads = 4;
 
 // A CTA takes kRotThreads / L tokens (adjacent rows, so that a head's rows are
 // one piece of memory) and `chunk` heads of either the queries or the keys:
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall
   const Rows& in = p.in[which];
   const int mine = live && a.live ? heads : 0, apart = a.c1 - a.c0;
   const __nv_bfloat16* from = in.p + (mine > 0 ? b * in.seq + t * in.row + h0 * in.head + a.c0 : 0);
-  const Batch x = load_heads<HALF>(from, in.head, mine, apart);
+  const Batch<kBatch> x = load_heads<HALF, kBatch>(from, in.head, mine, apart);
   const Pairs w = weight_of<HALF>(p.weight[which], a);
   const Angle g = angle_of(p.how, a, lane, live ? position_of(p.positions, p.each, b, p.n, t, 0) : 0);
   const long long to_step = (long long)p.n * p.how.d;
@@ -287,12 +293,15 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const RotateCall
   turn_heads<HALF, L>(x, from, in.head, to, to_step, heads, mine, norm, w, g, apart, p.how);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+
 // As store_kernel: a CTA holds one (page, head) of K or V in registers, so its
 // largest magnitude is known before any code is written; the rows are laid out
 // over lanes as above, and K goes through norm and rotation on the way in.  Of
 // many new tokens it takes several heads one after the other, the angles of its
 // rows kept in shared memory (a thread's own; four chunks of up to 8192 tokens
-// with 32 and 8 heads of 128: 114 -> 103 us, the floor is 62).
+// with 32 and 8 heads of 128: 114 -> 103 us when it came; 87 now, 4.8 TB/s, the
+// floor is 62: 18 to 20 warps an SM hide no more of the loads).
 // Further CTAs of an entry take its queries: L lanes one token's of q_chunk
 // heads, so that the angles (as much work as a row's norm and rotation) are
 // computed once for all of them.
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     if (heads == 0) return;
     const int mine = a.live ? own : 0, apart = a.c1 - a.c0;
     const __nv_bfloat16* from = p.q.p + (mine > 0 ? i * p.q.seq + row * p.q.row + h0 * p.q.head + a.c0 : 0);
-    const Batch x = load_heads<HALF>(from, p.q.head, mine, apart);
+    const Batch<kStoreBatch> x = load_heads<HALF, kStoreBatch>(from, p.q.head, mine, apart);
     const Pairs w = weight_of<HALF>(p.q_weight, a);
     const Angle g = angle_of(p.how, a, lane, position_of(p.positions, p.each, i, p.rows, row, start));
     const long long to_step = (long long)p.rows * p.how.d;
@@ -363,7 +372,27 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     a.c0 = 8 * lane;
     a.c1 = a.c0 + 4;
     a.turns = false;
-  } else {
+  }
+  const Rows& in = p.kv[which];
+  // the lane's part of the first of its group's rows, and how many of them are new
+  const int mine = a.live ? max(0, (r1 - r0 - group + kPer - 1) / kPer) : 0, apart = a.c1 - a.c0;
+  const __nv_bfloat16* first =
+      in.p + (mine > 0 ? i * in.seq + ((long long)base - start + r0 + group) * in.row + a.c0 : 0);
+  // a head's rows on their way to L2 while something else is worked out (four
+  // chunks of up to 8192 tokens: 90 -> 86 us)
+  auto ahead = [&](int h) {
+    const __nv_bfloat16* at = first + h * in.head;
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      if (u < mine) {
+        prefetch_l2(at);
+        if (HALF) prefetch_l2(at + apart);
+      }
+      at += kPer * in.row;
+    }
+  };
+  if (!which) {
+    ahead(h0);
     // the angles of the thread's rows, for all its heads
 #pragma unroll 1
     for (int u = 0; r0 + group + u * kPer < r1; ++u) {
@@ -376,13 +405,8 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
     if (tid == 0) flag(c.status, KVCACHE_FLAG_BAD_PAGE);
     return;
   }
-  const Rows& in = p.kv[which];
   const Pairs w = weight_of<HALF>(which ? nullptr : p.k_weight, a);
   float* scales = which ? c.vs : c.ks;
-  // the lane's part of the first of its group's rows, and how many of them are new
-  const int mine = a.live ? max(0, (r1 - r0 - group + kPer - 1) / kPer) : 0, apart = a.c1 - a.c0;
-  const __nv_bfloat16* first =
-      in.p + (mine > 0 ? i * in.seq + ((long long)base - start + r0 + group) * in.row + a.c0 : 0);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     uint4 x[kPasses];
@@ -393,6 +417,7 @@ __global__ void __launch_bounds__(PAGE * 2) rotate_store_kernel(const RotateStor
       if (u < mine) x[u] = load_part<HALF>(src, apart);
       src += kPer * in.row;
     }
+    if (h + 1 < h1) ahead(h + 1);
     const size_t unit = (size_t)pg * c.Hkv + h;
     const float held_scale = r0 > 0 ? scales[unit] : 0.f;
     uint8_t* dst = (which ? c.v : c.k) + unit * PAGE * c.d;
