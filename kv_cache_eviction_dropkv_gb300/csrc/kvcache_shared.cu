@@ -10,8 +10,8 @@
 // Four kernels in a row:
 //   plan_kernel    one cluster finds each group's common pages by comparing the
 //                  page tables, and lays out the work
-//   prefix_kernel  the shared tokens, on tcgen05; leaves pieces (O, m, l, M)
 //   attention_kernel<SHARED> (kvcache_attn.cuh)  each entry's own tokens
+//   prefix_kernel  the shared tokens, on tcgen05; leaves pieces (O, m, l, M)
 //   final_kernel   joins a row's pieces
 //
 // prefix_kernel.  A unit is (group, KV head, 128 or 256 of its rows); its
@@ -978,46 +978,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 // ------------------------------------------------------------------ the join
 // The pieces of a row are joined in an order that does not depend on timing:
 // those of the shared tokens, in run order, then those of its own (one, or
-// where its unit was cut, one per run).  A warp takes every step-th of them,
-// kBatch with all loads in flight at once.  (Short code here too: see plan_kernel.)
+// where its unit was cut, one per run).  A lane holds the state of a piece and
+// works out its factor; then the warp adds up the outputs, 4 channels a lane,
+// the factors handed round.  (Short code here too: see plan_kernel.)
 struct Joined {
   float m, M, l;
   float4 o;
 };
-template <int N>
-__device__ __forceinline__ void join_in(Joined& a, const float4 (&st)[N], const float4 (&x)[N]) {
-  float mn = a.m, Mn = a.M;
+// The factor of the lane's piece with state st (m, l, M), when 32 pieces join j;
+// l and the references of j follow, o has to be multiplied by *follow.
+__device__ __forceinline__ float join_state(Joined& j, const float4& st, float* follow) {
+  float mn = fmaxf(j.m, st.x), Mn = fmaxf(j.M, st.z);
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    mn = fmaxf(mn, st[u].x);
-    Mn = fmaxf(Mn, st[u].z);
+  for (int o = 16; o > 0; o >>= 1) {
+    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
   }
   const float m0 = mn == -INFINITY ? 0.f : mn, M0 = Mn == -INFINITY ? 0.f : Mn;   // (nothing yet: all factors 0)
-  const float f = ex2_approx(a.m - m0), F = ex2_approx(a.M - M0);
-  a.l *= f;
-  a.o.x *= F;
-  a.o.y *= F;
-  a.o.z *= F;
-  a.o.w *= F;
+  float sum = st.y * ex2_approx(st.x - m0);
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    const bool none = st[u].x == -INFINITY && st[u].y == 0.f;   // perhaps no outputs were written either
-    const float G = ex2_approx(st[u].z - M0);
-    a.l += st[u].y * ex2_approx(st[u].x - m0);
-    a.o.x += none ? 0.f : x[u].x * G;
-    a.o.y += none ? 0.f : x[u].y * G;
-    a.o.z += none ? 0.f : x[u].z * G;
-    a.o.w += none ? 0.f : x[u].w * G;
-  }
-  a.m = mn;
-  a.M = Mn;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  j.l = j.l * ex2_approx(j.m - m0) + sum;
+  *follow = ex2_approx(j.M - M0);
+  j.m = mn;
+  j.M = Mn;
+  // of nothing perhaps no outputs were written either: they are passed over
+  return st.x == -INFINITY && st.y == 0.f ? 0.f : ex2_approx(st.z - M0);
 }
-// W > 1: a CTA of W warps joins one row, of up to some 300 pieces; else a warp
-// each joins a row (4 to a CTA).
+__device__ __forceinline__ void scale4(float4& o, float f) {
+  o.x *= f;
+  o.y *= f;
+  o.z *= f;
+  o.w *= f;
+}
+__device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
+  if (f == 0.f) return;                           // (the same for all lanes)
+  o.x = fmaf(x.x, f, o.x);
+  o.y = fmaf(x.y, f, o.y);
+  o.z = fmaf(x.z, f, o.z);
+  o.w = fmaf(x.w, f, o.w);
+}
+// W > 1: a CTA of W warps joins one row, of up to some 300 pieces, a warp every
+// W-th; else a warp each joins a row (4 to a CTA).  Whole calls with 1, 4 and 8
+// warps a row: 512 rows of 39 pieces 124, 117, 112 us; 1456 rows 90.6, 88.5, 95.2;
+// 2048 rows of 20 pieces 110.7, 114.6, 119.5; 20 rows to an SM 69.8, 76.4, 86.4.
 template <int W>
 __global__ void __launch_bounds__(32 * (W > 1 ? W : 4), W > 1 ? 48 / W : 8) final_kernel(const SharedCall p) {
   constexpr bool WHOLE = W > 1;
-  constexpr int kBatch = 5, kJoinWarps = WHOLE ? W : 4;
+  constexpr int kBatch = 8, kJoinWarps = WHOLE ? W : 4, kStep = WHOLE ? W : 1;
   __shared__ float4 s_o[kJoinWarps][32], s_s[kJoinWarps];
   grid_dep_wait();
   grid_dep_launch();
@@ -1031,56 +1039,71 @@ __global__ void __launch_bounds__(32 * (W > 1 ? W : 4), W > 1 ? 48 / W : 8) fina
   const int4 info = p.info[b];                    // shared tokens, first entry of the group, its rows, its first tile
   const SharedPlan plan = *p.plan;
   const int2 cut = p.by_runs ? a.cuts[((size_t)b * a.c.Hkv + h) * a.RG + rg] : make_int2(-1, 0);
+  // its pieces of the shared tokens, in runs w0 .. w1, two each where the groups
+  // of warps took turns, and of its own
+  int shared = 0, both = 0, rows = 0;
+  uint32_t at = 0;
+  if (info.x > 0) {
+    const int shift = plan.unit_rows == 256 ? 8 : 7, per_head = (info.z + plan.unit_rows - 1) >> shift;
+    const int y = (b - info.y) * a.R + r, part = y >> shift;
+    rows = min(plan.unit_rows, info.z - (part << shift));
+    both = rows > 128 ? 0 : 1;
+    const int tiles = tiles_of(info.x);
+    const uint32_t t0 = (uint32_t)info.w + (h * per_head + part) * tiles;
+    const uint32_t w0 = run_of(plan, t0), w1 = run_of(plan, t0 + tiles - 1);
+    shared = (w1 - w0 + 1) << both;
+    at = w0 * 256 + 2 * ((uint32_t)info.y * a.R * a.c.Hkv + h * info.z + (part << shift)) + (y - (part << shift));
+  }
+  const bool whole = cut.x < 0;
+  const uint32_t first = whole ? (uint32_t)row : (((uint32_t)cut.x * a.RG + rg) * 2) * a.RB + (r - rg * a.RB);
+  const uint32_t pitch = 2 * a.RB * a.RG;
+  const float4* own_s = whole ? a.own_s : a.part_s;
+  const float* own_o = whole ? a.own_o : a.part_o;
+  const int pieces = shared + (whole ? 1 : cut.y - cut.x + 1);
   Joined j;
   j.m = j.M = -INFINITY;
   j.l = 0.f;
   j.o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kStep = WHOLE ? kJoinWarps : 1;
-  // pieces first, first + kStep, ... of n; at(k): the row of piece k
-  auto take = [&](const float4* states, const float* outputs, int n, auto at) {
 #pragma unroll 1
-    for (int k0 = WHOLE ? warp : 0; k0 < n; k0 += kStep * kBatch) {
-      float4 st[kBatch], x[kBatch];
+  for (int k0 = WHOLE ? warp : 0; k0 < pieces; k0 += 32 * kStep) {
+    const int k = k0 + lane * kStep, q = k - shared, n = min(32, (pieces - k0 + kStep - 1) / kStep);
+    const uint32_t y = q < 0 ? at + (k >> both) * 256 + (both & k ? rows : 0)
+                             : whole ? first : first + q * pitch + (q == 0 ? a.RB : 0);
+    float4 st = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (k < pieces) st = (q < 0 ? p.piece_s : own_s)[y];
+    float G = 0.f;
+#pragma unroll 1
+    for (int u0 = 0; u0 < n; u0 += kBatch) {
+      float4 x[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + u * kStep;
-        st[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        const uint32_t yu = __shfl_sync(0xffffffffu, y, u0 + u);
         x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < n) {
-          const size_t y = at(k);
-          st[u] = states[y];
-          if (cols) x[u] = *reinterpret_cast<const float4*>(outputs + y * d + lane * 4);
-        }
+        if (cols && u0 + u < n)
+          x[u] = *reinterpret_cast<const float4*>((k0 + (u0 + u) * kStep < shared ? p.piece_o : own_o) + (size_t)yu * d + lane * 4);
       }
-      join_in(j, st, x);
+      if (u0 == 0) {                              // (behind the loads)
+        float follow;
+        G = join_state(j, st, &follow);
+        scale4(j.o, follow);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) add4(j.o, x[u], __shfl_sync(0xffffffffu, G, u0 + u));
     }
-  };
-  if (info.x > 0) {
-    // runs w0 .. w1, two pieces each where the groups of warps took turns
-    const int shift = plan.unit_rows == 256 ? 8 : 7, per_head = (info.z + plan.unit_rows - 1) >> shift;
-    const int y = (b - info.y) * a.R + r, part = y >> shift, rows = min(plan.unit_rows, info.z - (part << shift));
-    const int tiles = tiles_of(info.x), both = rows > 128 ? 0 : 1;
-    const uint32_t t0 = (uint32_t)info.w + (h * per_head + part) * tiles;
-    const uint32_t w0 = run_of(plan, t0), w1 = run_of(plan, t0 + tiles - 1);
-    const uint32_t at = w0 * 256 + 2 * ((uint32_t)info.y * a.R * a.c.Hkv + h * info.z + (part << shift)) + (y - (part << shift));
-    take(p.piece_s, p.piece_o, (w1 - w0 + 1) << both,
-         [&](int k) { return at + (k >> both) * 256 + (both & k ? rows : 0); });
   }
-  // (the own pieces begin with the warp behind those that had one more: any order will do, it is always the same)
-  const bool whole = cut.x < 0;
-  const uint32_t first = whole ? 0 : (((uint32_t)cut.x * a.RG + rg) * 2) * a.RB + (r - rg * a.RB), pitch = 2 * a.RB * a.RG;
-  take(whole ? a.own_s : a.part_s, whole ? a.own_o : a.part_o, whole ? 1 : cut.y - cut.x + 1,
-       [&](int k) { return whole ? row : (size_t)(first + k * pitch + (k == 0 ? a.RB : 0)); });
   if (WHOLE) {
     s_o[warp][lane] = j.o;
     if (lane == 0) s_s[warp] = make_float4(j.m, j.l, j.M, 0.f);
     __syncthreads();
     if (warp > 0) return;
-#pragma unroll 1
-    for (int w = 1; w < kJoinWarps; ++w) {
-      const float4 st[1] = {s_s[w]}, x[1] = {s_o[w][lane]};
-      join_in(j, st, x);
-    }
+    const float4 st = lane < kJoinWarps ? s_s[lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    j.m = j.M = -INFINITY;
+    j.l = 0.f;
+    j.o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float follow;
+    const float G = join_state(j, st, &follow);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) add4(j.o, s_o[w][lane], __shfl_sync(0xffffffffu, G, w));
   }
   if (!cols) return;
   // o stands for o 2^(M - m - 7); a row that saw nothing has l = 0
@@ -1136,7 +1159,7 @@ cudaError_t launch_shared(const SharedCall& p, cudaStream_t st) {
   const long long rows = (long long)p.own.n * p.own.Hq * p.own.T;
   const unsigned per = (unsigned)(p.own.Hq * p.own.T);
   if (rows <= 4LL * p.sms) return launch_pdl(final_kernel<8>, dim3(per, p.own.n), dim3(256), 0, st, p);
-  if (rows <= 64LL * p.sms) return launch_pdl(final_kernel<4>, dim3(per, p.own.n), dim3(128), 0, st, p);
+  if (rows <= 12LL * p.sms) return launch_pdl(final_kernel<4>, dim3(per, p.own.n), dim3(128), 0, st, p);
   return launch_pdl(final_kernel<1>, dim3((per + 3) / 4, p.own.n), dim3(128), 0, st, p);
 }
 
