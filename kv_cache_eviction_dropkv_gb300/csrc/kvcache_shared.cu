@@ -372,18 +372,55 @@ __device__ __forceinline__ void convert16(const uint4& w, uint8_t* lo, uint8_t* 
   *reinterpret_cast<uint4*>(hi) = b;
 }
 // Codes of a tile (row pitch d bytes) as fp16 in the swizzled layout, rows from
-// `tokens` on zero: rows [row0, row0 + 64), by a warp (t: the lane).
-template <int CODE>
+// `tokens` on zero: rows [row0, row0 + 64), by a warp (t: the lane).  V codes at a
+// time, V = 16 where d is a multiple of 16, else 8: the rows lie one behind the
+// other, so the lanes read them as they come, and where a piece belongs is counted
+// along.
+template <int CODE, int V>
 __device__ __noinline__ void convert_odd(const uint8_t* from, uint8_t* to, int d, int tokens, int row0, int t) {
-  const int per = d >> 3;
-#pragma unroll 2
-  for (int x = t; x < 64 * per; x += 32) {
-    const int r = row0 + x / per, c = x % per;
-    const uint2 w = r < tokens ? *reinterpret_cast<const uint2*>(from + r * d + 8 * c) : make_uint2(0, 0);
-    uint4 v;
-    codes_to_half<CODE>(w.x, v.x, v.y);
-    codes_to_half<CODE>(w.y, v.z, v.w);
-    *reinterpret_cast<uint4*>(chunk_of(to, r, c)) = v;
+  constexpr int kBatch = 4;
+  const int per = d / V, n = 64 * per, step_r = 32 / per, step_c = 32 - step_r * per;
+  const uint8_t* src = from + row0 * d;
+  const int r0 = t / per;
+  int r = row0 + r0, c = t - r0 * per;
+#pragma unroll 1
+  for (int x0 = t; x0 < n; x0 += 32 * kBatch) {
+    uint4 w[kBatch];
+    int rows[kBatch], cols[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      rows[u] = r;
+      cols[u] = c;
+      r += step_r;
+      c += step_c;
+      if (c >= per) {
+        c -= per;
+        ++r;
+      }
+      w[u] = make_uint4(0, 0, 0, 0);
+      const int x = x0 + 32 * u;
+      if (x < n && rows[u] < tokens) {
+        if (V == 16) {
+          w[u] = *reinterpret_cast<const uint4*>(src + 16 * x);
+        } else {
+          const uint2 y = *reinterpret_cast<const uint2*>(src + 8 * x);
+          w[u].x = y.x;
+          w[u].y = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (x0 + 32 * u >= n) break;
+      if (V == 16) {
+        convert16<CODE>(w[u], chunk_of(to, rows[u], 2 * cols[u]), chunk_of(to, rows[u], 2 * cols[u] + 1));
+      } else {
+        uint4 v;
+        codes_to_half<CODE>(w[u].x, v.x, v.y);
+        codes_to_half<CODE>(w[u].y, v.z, v.w);
+        *reinterpret_cast<uint4*>(chunk_of(to, rows[u], cols[u])) = v;
+      }
+    }
   }
 }
 // The same for d = 16 DS.  Eight lanes take 4 pieces of 16 codes of two
@@ -847,7 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       uint8_t* to = sm + (v ? L::kV : L::kK) + (i & 1) * L::kTileB;
       const int tokens = S.meta[i % kMeta].tokens;
       if (c.d == 16 * DS) convert_tile<CODE, DS>(from, to, tokens, row0, lane);
-      else convert_odd<CODE>(from, to, c.d, tokens, row0, lane);
+      else if (c.d % 16 == 0) convert_odd<CODE, 16>(from, to, c.d, tokens, row0, lane);
+      else convert_odd<CODE, 8>(from, to, c.d, tokens, row0, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
