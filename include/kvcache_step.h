@@ -141,7 +141,9 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  *   least   where n * max_pages * page * Hkv * d * 2, the most bytes of keys and
  *           values that kvcache_attention could have to read, is below this,
  *           the call is kvcache_attention and the groups are not looked at
- *           (sharing adds three short kernels); negative: 320 MB
+ *           (sharing adds three short kernels); negative: where sharing would
+ *           not be faster, by the shape, n, G, Hq and T, if the table were full
+ *           of shared tokens
  *   groups  device int32 [G + 1], groups[0] = 0, not decreasing, groups[G] =
  *           n; anything else is flagged (DROPKV_FLAG_BAD_LENGTH) and nothing
  *           is shared

@@ -56,6 +56,31 @@ bool counts_fit(const kvcache_shape& s, int n, int Hq, int T, int G) {
   return tiles * units < 2147483648.0;
 }
 
+// Cycles that sharing saves, roughly, over all SMs, were the cache's table full of
+// shared tokens.  For 128 of them and a KV head: the shared kernel's tile, once for
+// a group's rows, against kvcache_attention's, for each member and up to 8 rows
+// (three quarters of it for each 8 more; it finds the pages in L2 after the first).
+// Where d is no multiple of 16 the codes come in smaller pieces on both sides.
+double cycles_saved(const kvcache_shape& s, int n, int G, double R) {
+  const double rows = (double)n / G * R;
+  const bool odd = s.d % 16 != 0;
+  const double apart = n * (odd ? 2000.0 : 700.0 + 5 * s.d) * std::max(1.0, 0.75 * std::ceil(R / 8));
+  const double shared = G * (rows > 128 ? 4000 * std::ceil(rows / 256) : odd ? 4000 : 2570);
+  return (double)s.max_pages * s.page / 128 * s.Hkv * (apart - shared);
+}
+// Three more short kernels cost some 35 us (67000 cycles at 1.9 GHz); as tables are
+// longer than what is shared, a third more is asked for (with 67000, 10 x 2-5 behind
+// 2300 to 3600, 16 heads of 128, 3 rows, took 85 us instead of attention's 70).
+// Attention and shared, us:
+//   8, 16 x 16000 tokens in one group, 8 heads of 128       40 and 69   55 and 59
+//   8, 16 x 4000, 32 heads of 96                            47 and 84   47 and 50
+//   64 x 32768, 8 heads of 128                              443         111
+//   10 x 2 behind 18000-28000, 4 heads of 96, 7 rows        78          103
+//   11 x 3 behind 19000-63000, 8 heads of 16, 4 rows        227         302
+//   2 x 4 behind 23000-48000, 16 heads of 80, 40 rows       588         196
+//   10 x 4-7 behind 64000-96000, one head of 112, 6 rows    188         132
+constexpr double kSharingCycles = 90000;
+
 // The workspace of a shared attention (byte offsets); the second half's parts
 // and cuts have the sizes given.
 struct SharedSpace {
@@ -223,16 +248,12 @@ dropkv_status kvcache_shared_attention(const kvcache_shared_attention_call* call
   if ((long long)Hq * T > kMaxSharedRows / n) return DROPKV_ERR_UNSUPPORTED;
   const size_t bytes = (size_t)n * Hq * T * shape.d * 2;
   if (ranges_overlap(call->q, bytes, call->out, bytes)) return DROPKV_ERR_INVALID_ARG;
-  // Sharing pays from some 300 MB of unshared reading on (8 heads of 128
-  // channels, 8 and 16 x 16000 tokens, 266 and 533 MB: attention 40 and 69 us,
-  // shared 55 and 59; 32 heads of 96, 8 and 16 x 4000, 208 and 415 MB: 47 and
-  // 84 against 47 and 50; 64 x 32768 443 against 114).
-  const double most = 2.0 * n * shape.max_pages * shape.page * shape.Hkv * shape.d;
-  if (most < (call->least < 0 ? 320e6 : (double)call->least))
-    return kvcache_attention(call->shape, call->cache, call->layer, call->seqs, n, call->q, Hq, T, 0, 0, call->out,
-                             call->workspace, call->workspace_bytes, call->status, call->stream);
   const int sms = current_sms(nullptr);
   if (sms <= 0) return DROPKV_ERR_CUDA;
+  if (call->least < 0 ? cycles_saved(shape, n, call->G, (double)(Hq / shape.Hkv) * T) < kSharingCycles * sms
+                      : 2.0 * n * shape.max_pages * shape.page * shape.Hkv * shape.d < (double)call->least)
+    return kvcache_attention(call->shape, call->cache, call->layer, call->seqs, n, call->q, Hq, T, 0, 0, call->out,
+                             call->workspace, call->workspace_bytes, call->status, call->stream);
   AttnPlan plan{};
   if (!make_attn_plan(shape, n, Hq, T, 0, 0, sms, &plan) || !counts_fit(shape, n, Hq, T, call->G)) return DROPKV_ERR_UNSUPPORTED;
   const bool by_runs = !plan.team && !plan.solo;

@@ -223,8 +223,9 @@ class PagedCache:
         with the same pages, forks of one sequence for instance: those pages
         are found by their numbers and read once for the whole group.  Where
         the cache's table has no room for `least` bytes of the entries' keys and
-        values (-1: 320 MB, from which on sharing is the faster way) the call
-        is attention(), and the groups are not looked at."""
+        values the call is attention(), and the groups are not looked at; -1:
+        where sharing would not be faster, by the entries to a group, the rows
+        and the cache's shape, if its table were full of shared tokens."""
         n, Hq, T, d = q.shape
         G = groups.shape[0] - 1
         if T > self.T or Hq != self.Hq or G > self.groups:

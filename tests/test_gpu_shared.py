@@ -250,6 +250,24 @@ def test_small_calls_are_attention():
     assert flags_of(c) == B.FLAG_BAD_LENGTH
 
 
+def test_groups_of_one_are_attention():
+    """Where sharing saves nothing the call is attention(), however much there is to read."""
+    n = 8
+    c = PagedCache(n + 1, 2, 64, 40, 128, 8192, 1, "e4m3", Hq=8, T=1, device=DEV, groups=n)
+    seqs = list(range(1, n + 1))
+    put(c, [0], [300], 3)
+    c.fork(ints([0] * n), ints(seqs))
+    put(c, seqs, [1 + 7 * i for i in range(n)], 4)
+    assert c.check() == 0
+    q = queries(n, 8, 1, 64, 5)
+    plain, out = torch.empty_like(q), torch.empty_like(q)
+    c.attention(0, q, plain, seqs=ints(seqs))
+    c.shared_attention(0, q, out.fill_(7.0), ints([1] * (n + 1)), seqs=ints(seqs))     # (not looked at)
+    assert torch.equal(out, plain) and c.check() == 0
+    c.shared_attention(0, q, out, ints([0, n - 1]), seqs=ints(seqs))
+    assert flags_of(c) == B.FLAG_BAD_LENGTH
+
+
 def test_not_a_number_codes_reach_their_rows_only():
     c, seqs, starts = forked([200, 200], [[5, 9], [1, 40]], 2, 2, 64, 32, seed=9)
     q = queries(4, 4, 1, 64, 3)
