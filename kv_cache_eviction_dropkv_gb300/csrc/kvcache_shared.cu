@@ -375,7 +375,8 @@ __device__ __forceinline__ void convert16(const uint4& w, uint8_t* lo, uint8_t* 
 // `tokens` on zero: rows [row0, row0 + 64), by a warp (t: the lane).  V codes at a
 // time, V = 16 where d is a multiple of 16, else 8: the rows lie one behind the
 // other, so the lanes read them as they come, and where a piece belongs is counted
-// along.
+// along.  (Divided out, 8 codes at a time: 10 groups of 4 to 7 sequences behind 64000
+// to 96000 tokens, one head of 112, 186 us instead of 132.)
 template <int CODE, int V>
 __device__ __noinline__ void convert_odd(const uint8_t* from, uint8_t* to, int d, int tokens, int row0, int t) {
   constexpr int kBatch = 4;
