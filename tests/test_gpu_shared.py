@@ -101,6 +101,15 @@ def test_one_group(code, page, d, Hkv, g, T):
     assert c.check() == 0
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [8, 16, 24, 48, 56, 80, 88, 104, 112, 120])
+def test_head_widths(code, d):
+    """Codes in pieces of 8 and 16, in each of the three tile widths; the last tile half full."""
+    c, seqs, starts = forked([3 * 128 + 64 + 5], [[1, 70, 33]], 2, 3, d, 64, code, seed=d)
+    check(c, queries(3, 6, 1, d, 3), seqs, starts)
+    assert c.check() == 0
+
+
 @pytest.mark.parametrize("prefix", [0, 1, 31, 32, 33, 127, 128, 129, 255, 256, 300, 4000])
 def test_prefix_lengths(prefix):
     """Nothing shared, parts of tiles, whole ones; three rows, of which the first may see one token less than a page."""
