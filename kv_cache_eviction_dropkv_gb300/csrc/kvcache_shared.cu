@@ -557,6 +557,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, 
       }
       const bool over = fmaxf(s[0], s[1]) > kMost;
       if (round == 1 || !__any_sync(0xffffffffu, over)) break;
+      // What is loaded, scaled and stored again below (O, the first half of P) may
+      // just have been stored, and loads do not wait for stores by themselves.
+      tmem_wait_st();
       if (h == 0) wait_ld64(v);                            // (what came for the next half row is loaded again)
       ld64(tS + 64 * h, v);
       wait_ld64(v);
@@ -681,6 +684,7 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
                        float o[16];
                        tmem_ld16(tO + 16 * c, o);
                        tmem_wait_ld();
+                       pin16(o);
 #pragma unroll
                        for (int u = 0; u < 16; ++u) o[u] *= factor;
                        tmem_st16(tO + 16 * c, o);
@@ -716,6 +720,7 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
         __syncwarp();
         tmem_ld16(tO + c0, o);
         tmem_wait_ld();
+        pin16(o);
         if (r < s.rows) {
 #pragma unroll
           for (int u = 0; u < 16; u += 4)
