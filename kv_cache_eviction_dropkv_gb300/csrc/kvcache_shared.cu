@@ -284,7 +284,8 @@ constexpr int kConvert = 8, kIssuer = 12, kLoader = 13, kThreads = 32 * 14;
 // is lost of an output is at most 2^-29 of the largest P's for each token.
 constexpr float kLiftLog2 = 4.0f, kPieceLift = 7.0f - kLiftLog2;   // (pieces are told in 2^7)
 constexpr float kMost = 32768.f;                  // most that P of a row and 32 tokens may sum up to (fp16 holds 65504)
-constexpr float kLowLog2 = -60.0f;                // least exponent of the factor of P: below it P is 0 in fp16 anyway
+constexpr float kLowLog2 = -60.0f;                // least exponent of the factor of P
+constexpr float kMostLow = 0x1p-26f;              // the most such a block's P may sum up to: all are 0 in fp16 then
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
 constexpr int kAhead = 6;                         // below 8, the fewest tiles of a batch of descriptions
 constexpr int kMaxStages = 5, kMeta = 16;          // kMeta >= kMaxStages + 4
@@ -508,6 +509,10 @@ __device__ __noinline__ void scale_halves(uint32_t taddr, int columns, float fac
 // row at hand) and the half row is made again from S, which its P has not yet
 // replaced.  follow(factor) lets O follow M, and P of the first half follows
 // too.  A row's first tile always takes that way.
+// A block whose V scale is so far below the others' that e_c would pass under
+// kLowLog2 is made with that instead, so that P does not vanish from l; as its P
+// is then larger than it should be, the references move as soon as any of it
+// would show in fp16.
 template <typename Follow>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, int blocks, float fq, float& m, float& M,
                                              float& l, Follow follow) {
@@ -515,7 +520,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, 
   ld64(tS, v);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    float s[2], e[2];
+    float s[2], e[2], most[2];
     for (int round = 0;; ++round) {
       wait_ld64(v);
       uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull}, f2[2], n2[2];
@@ -523,7 +528,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, 
       for (int b = 0; b < 2; ++b) {
         const int c = 2 * h + b;
         const float f = fmaxf(fq * scales.ks[c], 0x1p-126f);
-        e[b] = fmaxf(scales.lv[c] + m - M + kLiftLog2, kLowLog2);
+        e[b] = scales.lv[c] + m - M + kLiftLog2;
+        most[b] = e[b] < kLowLog2 ? kMostLow : kMost;
+        e[b] = fmaxf(e[b], kLowLog2);
         const float n = c < blocks ? e[b] - m : -INFINITY;   // (no tokens: P = 0)
         f2[b] = f2_pack(f, f);
         n2[b] = f2_pack(n, n);
@@ -555,7 +562,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, 
         const uint64_t a = f2_add(sum2[2 * b], sum2[2 * b + 1]);
         s[b] = f2_lo(a) + f2_hi(a);
       }
-      const bool over = fmaxf(s[0], s[1]) > kMost;
+      const bool over = s[0] > most[0] || s[1] > most[1];
       if (round == 1 || !__any_sync(0xffffffffu, over)) break;
       // What is loaded, scaled and stored again below (O, the first half of P) may
       // just have been stored, and loads do not wait for stores by themselves.

@@ -47,3 +47,53 @@ def test_logits_that_rise_in_every_half_tile(code, d, page, g, T):
     levels(c, pages, 10.0 * (half + 1) + 4.0 * (half % 3), 1)
     check(c, q, seqs, list(range(0, 33, 2)))
     assert c.check() == 0
+
+
+def weighted(c, q, seqs):
+    """Outputs in 64 bits; sum_j p_j |v_j| of each channel; the largest p_j times V scale."""
+    n, Hq, T, d = q.shape
+    out, size = (torch.zeros(n, Hq, T, d, dtype=torch.float64, device=DEV) for _ in range(2))
+    most = torch.zeros(n, Hq, T, 1, dtype=torch.float64, device=DEV)
+    for i, s in enumerate(seqs):
+        L = int(c.length[s])
+        pages = c.table[s, :-(-L // c.page)].long()
+        k, v, scale = ((x.double() * sc[0][pages].double()[..., None, None]).transpose(0, 1).reshape(c.Hkv, -1, x.shape[-1])[:, :L]
+                       for x, sc in ((c.k[0].view(torch.uint8)[pages].view(c.k.dtype), c.k_scale),
+                                     (c.v[0].view(torch.uint8)[pages].view(c.v.dtype), c.v_scale),
+                                     (torch.ones(len(pages), c.Hkv, c.page, 1, device=DEV), c.v_scale)))
+        for t in range(T):
+            x = q[i, :, t].double().reshape(c.Hkv, -1, d) @ k.transpose(-1, -2) / math.sqrt(d)
+            p = torch.softmax(x[..., :L - T + t + 1], -1)
+            out[i, :, t], size[i, :, t] = ((p @ y[:, :L - T + t + 1]).reshape(Hq, d) for y in (v, v.abs()))
+            most[i, :, t] = (p * scale[:, :L - T + t + 1].transpose(-1, -2)).amax(-1).reshape(Hq, 1)
+    return out, size, most
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,page,g,T", [(128, 64, 4, 1), (64, 32, 4, 1), (96, 64, 8, 9)])
+@pytest.mark.parametrize("rise", [20, 35, 50, 60, 70, 100])
+def test_pages_of_tiny_values_behind_one_of_plain_ones(code, d, page, g, T, rise):
+    """V scales 2^0 on the first page and 2^-100 on the others, whose keys are
+    2^rise times as likely: what the first page's tokens weigh in the outputs
+    stands against values 2^100 smaller, so the bound goes by the outputs.
+
+    Bound, W = sum p |v|: 2^-8 of the output (bf16); of W, 2^-11 (P in fp16),
+    2^-12 (base-2 logits up to 2^7 in fp32: three roundings, 2^-24 2^7 ln 2
+    each, and S) and 2^-23 for each of n tokens' additions; what fp16 drops of
+    P, 2^-28 of the row's largest p times V scale for each token, whose code is
+    448 (int8: 127) at most."""
+    c, seqs, _ = forked([1280], [[1 + i % 5 for i in range(32)]], 8, g, d, page, code, T, seed=d)
+    pages = c.table[0, :1280 // page].long()
+    first = int(pages[0])
+    levels(c, pages, [1.0] + [1.0 + rise] * (len(pages) - 1), 1)
+    c.v_scale *= 2.0 ** -100
+    c.v_scale[0, first] *= 2.0 ** 100
+    q = slopes(32, 8 * g, T, d, 3)
+    out = torch.full_like(q, 7.0)
+    c.shared_attention(0, q, out, ints(range(0, 33, 2)), seqs=ints(seqs), least=0)
+    want, size, most = weighted(c, q, seqs)
+    n = int(c.length.max())
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12 + n * 2.0 ** -23) * size + n * 2.0 ** -28 * 448 * most
+    err = (out.double() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    assert c.check() == 0
