@@ -135,7 +135,8 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  * which the tables of all its sequences begin, up to the token that the first
  * query row of each sees, are read once for the whole group; which these are
  * is found on the device, so the results are kvcache_attention's whatever the
- * groups (up to the rounding of another order of summation).  Sequences that
+ * groups (up to roundings: sums in another order, probabilities relative to
+ * another reference).  Sequences that
  * hold less than a full page before their last T tokens take no part in the
  * sharing.
  *   least   where n * max_pages * page * Hkv * d * 2, the most bytes of keys and
@@ -147,8 +148,9 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  *   groups  device int32 [G + 1], groups[0] = 0, not decreasing, groups[G] =
  *           n; anything else is flagged (DROPKV_FLAG_BAD_LENGTH) and nothing
  *           is shared
- * Numerics: probabilities of the shared tokens are off by 2^-11 of themselves
- * or 2^-29 of the row's largest, the rest as kvcache_attention's.  Supported:
+ * Numerics: kvcache_attention's, for the shared tokens too (their probabilities
+ * are off by 2^-11 of themselves, or 2^-32 of the row's largest where that is
+ * more; weighted by the scales of their values).  Supported:
  * what kvcache_attention supports with n * Hq * T <= 2^22, 1 <= G <= n and
  * (max_pages * page / 128 + 1) * (n * Hq * T / 128 + G * Hkv) < 2^31. */
 typedef struct {

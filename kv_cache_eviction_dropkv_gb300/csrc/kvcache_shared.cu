@@ -279,11 +279,16 @@ constexpr int kTile = 128;
 // Warps 0 .. 7: softmax; two for K's codes, two for V's, one that issues, one
 // that loads (128 registers a thread).
 constexpr int kConvert = 8, kIssuer = 12, kLoader = 13, kThreads = 32 * 14;
-// The largest P of fresh references is 2^4: room for logits to rise by some ten
-// before they move again (each move costs a tile's time and a half), and what
-// is lost of an output is at most 2^-29 of the largest P's for each token.
-constexpr float kLiftLog2 = 4.0f, kPieceLift = 7.0f - kLiftLog2;   // (pieces are told in 2^7)
-constexpr float kMost = 32768.f;                  // most that P of a row and 32 tokens may sum up to (fp16 holds 65504)
+// P enters the product times 2^7 and the references are rounded down, so a row's
+// largest P (times its V scale) is 2^7 at least, and what fp16 drops of a token
+// is at most 2^-32 of it, as in kvcache_attention: what is far below the
+// references must not be missing from the outputs while the sum counts it.
+// (Times 2^4, with references rounded up, they move less often, each time for a
+// tile's time and a half: 64 sequences behind 32768 shared tokens 113 instead of
+// 115 us, 16 behind 131072 114 instead of 117; but behind dominant keys 2^20
+// tokens of 2^-27.6 of their weight came out 37 % too large.)
+constexpr float kLiftLog2 = 7.0f;
+constexpr float kMost = 65504.f;                  // most that P of a row and 32 tokens may sum up to: what fp16 holds
 constexpr float kLowLog2 = -60.0f;                // least exponent of the factor of P
 constexpr float kMostLow = 0x1p-26f;              // the most such a block's P may sum up to: all are 0 in fp16 then
 constexpr uint64_t kDrain = 20000000ull;          // 20 ms to drain copies after an abort
@@ -501,12 +506,12 @@ __device__ __noinline__ void scale_halves(uint32_t taddr, int columns, float fac
 
 // A thread's row of a tile: S in its columns of tensor memory becomes P.
 //   x_c = s f_c (base-2 logits; f_c: the row's factor times block c's K scale),
-//   P = 2^(x - m + e_c), e_c = lv_c + m - M + 4,  l += sum of 2^(x - m)
+//   P = 2^(x - m + e_c), e_c = lv_c + m - M + 7,  l += sum of 2^(x - m)
 // m and M are references of the sums and of the outputs (which carry the V
 // scales).  No maximum is looked for: P is made on the references as they are,
 // and only where the sum of a block of 32 shows that some P is too large for
-// fp16 the references move (to whole numbers, at least the maxima of the half
-// row at hand) and the half row is made again from S, which its P has not yet
+// fp16 the references move (to whole numbers, at most 1 below the maxima of the
+// half row at hand) and the half row is made again from S, which its P has not yet
 // replaced.  follow(factor) lets O follow M, and P of the first half follows
 // too.  A row's first tile always takes that way.
 // A block whose V scale is so far below the others' that e_c would pass under
@@ -586,7 +591,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, const Scales& scales, 
           Mt = fmaxf(Mt, x + scales.lv[c]);
         }
       }
-      const float mn = over ? fmaxf(m, ceilf(mt)) : m, Mn = over ? fmaxf(M, ceilf(Mt)) : M;
+      const float mn = over ? fmaxf(m, floorf(mt)) : m, Mn = over ? fmaxf(M, floorf(Mt)) : M;
       l *= m == mn ? 1.f : ex2_approx(m - mn);             // (from nothing: 0 times 0)
       const float factor = M == Mn ? 1.f : ex2_approx(M - Mn);
       m = mn;
@@ -737,7 +742,7 @@ __device__ __forceinline__ void softmax_group(const SharedCall& p, Small& S, uin
       }
       tc_fence_before();
     }
-    if (r < s.rows) p.piece_s[at] = make_float4(m, l, M + kPieceLift, 0.f);
+    if (r < s.rows) p.piece_s[at] = make_float4(m, l, M, 0.f);
     if (!more) return;
     s = next;
     fq = fq_next;

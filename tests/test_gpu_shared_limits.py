@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from kv_cache_eviction_dropkv_gb300 import PagedCache
 from tests.test_gpu_paged import DEV, ints
 from tests.test_gpu_shared import check, forked, queries
 
@@ -97,3 +98,42 @@ def test_pages_of_tiny_values_behind_one_of_plain_ones(code, d, page, g, T, rise
     err = (out.double() - want).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
     assert c.check() == 0
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("Hq", [8, 72])
+@pytest.mark.parametrize("first", [True, False])
+def test_a_flat_tail_behind_dominant_keys(code, Hq, first):
+    """2^20 shared tokens whose weight is 2^-27.6 of two dominant ones' each,
+    0.0025 of the output together, where a CTA has whole units: of 16 rows (the
+    two groups take the tiles in turn, a dominant key each) and of 144.
+
+    All values are 1 but the dominant ones', which are 0.  Bound: the bf16
+    rounding 2^-8 o; the fp32 sums, every addition off by a last place of a sum
+    that only grows: 2^16 products of 16 tokens into an accumulator (2^-23 each
+    if it truncates, 2^-7 o), 2^15 blocks into the sum of weights (2^-24 each,
+    2^-9 o); 2^-10 o for the exponentials' fp32 arguments; the probabilities'
+    fp16 rounding, 2^-32 of the largest for each."""
+    tokens, groups = 1 << 20, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    n = 2 * groups
+    c = PagedCache(n, 1, 8, 9000, 128, tokens // 128, 1, code, Hq=Hq, device=DEV, groups=groups)
+    c.reserve(ints([tokens]))
+    at = [0, 128] if first else [tokens - 129, tokens - 1]
+    k, v = torch.zeros(1, 1, tokens, 8, dtype=torch.bfloat16), torch.ones(1, 1, tokens, 8, dtype=torch.bfloat16)
+    k[..., 1] = 1.0
+    k[0, 0, at, 0], k[0, 0, at, 1] = 26.0, 0.0
+    v[0, 0, at] = 0.0
+    c.store(0, k.to(DEV), v.to(DEV))
+    q = torch.zeros(n, Hq, 1, 8, dtype=torch.bfloat16, device=DEV)
+    q[..., 0], q[..., 1] = 2.125, 1.0625
+    out = torch.zeros_like(q)
+    c.shared_attention(0, q, out, ints(range(0, n + 1, 2)), seqs=ints([0] * n), least=0)
+    assert c.check() == 0
+    pages = c.table[0].long()
+    held, ones = ((x[0].view(torch.uint8)[pages].view(x.dtype).double() * s[0][pages].double()[..., None, None])
+                  .reshape(tokens, 8) for x, s in ((c.k, c.k_scale), (c.v, c.v_scale)))
+    p = torch.softmax(held @ q[0, 0, 0].double() / math.sqrt(8.0), 0)
+    want = float((p @ ones)[0])
+    assert 0.002 < want < 0.003
+    err = float((out.double() - want).abs().max())
+    assert err <= (2.0 ** -8 + 2.0 ** -7 + 2.0 ** -9 + 2.0 ** -10) * want + tokens * 2.0 ** -32 * float(p.max()), (err, want)
