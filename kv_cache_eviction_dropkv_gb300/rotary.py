@@ -114,11 +114,16 @@ class Rotary:
     def apply(self, q, k, q_out, k_out, positions=None, lengths=None, stream=None):
         """q [B, Hq, n, d] and k [B, Hkv, n, d] bf16, of any strides with adjacent
         channels (views of a packed projection, for instance; rows 16-byte
-        aligned), into contiguous q_out and k_out; q or k may be None, and q_out
-        may be q itself where that is contiguous.  positions: int32 [B], row t of
-        sequence b stands at positions[b] + t; int32 [B, n], one for each row;
-        None: row t at t.  Rows from lengths[b] (int32 [B]) on are left as they
-        were.  Problems found on the device are reported by check()."""
+        aligned), into contiguous q_out and k_out; q or k may be None or have no
+        heads, and q_out may be q itself where that is contiguous.  positions:
+        int32 [B], row t of sequence b stands at positions[b] + t; int32 [B, n],
+        one for each row; None: row t at t.  Rows from lengths[b] (int32 [B]) on
+        are left as they were.  Problems found on the device are reported by
+        check()."""
+        if q is not None and q.shape[1] == 0:
+            q = None
+        if k is not None and k.shape[1] == 0:
+            k = None
         if q is None and k is None:
             return
         i, d = self._index, self.d
@@ -138,7 +143,7 @@ class Rotary:
             to_k = B.tensor_address("k_out", k_out, B.bf16, want, i)
         at, kind = B.positions_of(positions, n_seq, n, i)
         to = 0 if lengths is None else B.tensor_address("lengths", lengths, B.int32, (n_seq,), i)
-        if not (n_seq and n and Hq and Hkv):
+        if not (n_seq and n):
             return
         if B.current_device() != i:
             with torch.cuda.device(self.device):
