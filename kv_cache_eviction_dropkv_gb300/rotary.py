@@ -55,7 +55,7 @@ def frequencies(dims: int, base: float = 10000.0, scaling: Optional[dict] = None
             keep = 1.0 - min(1.0, max(0.0, (i - lo) / max(0.001, hi - lo)))
             freq[i] = f / factor * (1 - keep) + f * keep
         amplitude = how.get("amplitude")
-        amplitude = 0.1 * math.log(factor) + 1.0 if amplitude is None else float(amplitude)
+        amplitude = 0.1 * math.log(max(1.0, factor)) + 1.0 if amplitude is None else float(amplitude)
     return freq, amplitude
 
 
@@ -76,7 +76,7 @@ class Rotary:
         that turn more than `fast` times over the original context stay, those
         below `slow` are divided, a ramp over the pairs between, and the
         rotated channels are multiplied by amplitude (default 0.1 ln(factor) +
-        1); "bands" (original=, low=1, high=4): the same with a ramp over the
+        1, or 1 for a factor below 1); "bands" (original=, low=1, high=4): the same with a ramp over the
         turns and no amplitude."""
         self.d, self.dims, self.eps = int(d), int(d if dims is None else dims), float(eps)
         if not 8 <= self.d <= 128 or self.d % 8 or not 0 <= self.dims <= self.d or self.dims % 8:
