@@ -48,9 +48,11 @@ def frequencies(dims: int, base: float = 10000.0, scaling: Optional[dict] = None
     elif kind == "yarn":
         if base <= 1:
             raise ValueError("scaling: yarn needs a base above 1")
+        fast, slow = float(how.get("fast", 32.0)), float(how.get("slow", 1.0))
+        if fast < slow:
+            raise ValueError("scaling: fast must not be below slow")
         edge = lambda turns: dims * math.log(how["original"] / (2 * math.pi * turns)) / (2 * math.log(base))
-        lo = max(0, math.floor(edge(float(how.get("fast", 32.0)))))
-        hi = min(dims - 1, math.ceil(edge(float(how.get("slow", 1.0)))))
+        lo, hi = max(0, math.floor(edge(fast))), min(dims - 1, math.ceil(edge(slow)))
         for i, f in enumerate(freq):
             keep = 1.0 - min(1.0, max(0.0, (i - lo) / max(0.001, hi - lo)))
             freq[i] = f / factor * (1 - keep) + f * keep

@@ -13,3 +13,13 @@ def test_yarn_amplitude(factor, want):
     scaling = dict(kind="yarn", factor=factor, original=4096)
     assert rotary.frequencies(64, 10000.0, scaling)[1] == pytest.approx(want, rel=1e-15)
     assert rotary.frequencies(64, 10000.0, dict(scaling, amplitude=0.75))[1] == 0.75
+
+
+def test_yarn_ramps_the_wrong_way_round_are_refused():
+    """A bound of the slow pairs above that of the fast ones, as "bands" refuses it."""
+    plan = dict(kind="yarn", factor=8.0, original=4096)
+    for bad in (dict(fast=1.0, slow=32.0), dict(slow=33.0), dict(fast=0.5)):
+        with pytest.raises(ValueError):
+            rotary.frequencies(64, 10000.0, {**plan, **bad})
+    for good in (dict(fast=2.0, slow=2.0), dict(fast=None, slow=None), dict(fast=33.0, slow=31.0)):
+        rotary.frequencies(64, 10000.0, {**plan, **good})
