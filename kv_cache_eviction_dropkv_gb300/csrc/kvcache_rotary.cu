@@ -147,11 +147,11 @@ __device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Pairs& 
       for (int o = L / 2; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
       return ss;
     };
-    const float ss = sum_squares(y);
-    float r = rsqrtf(__fmaf_rn(ss, how.inv_d, how.eps));
-    // squares past fp32 (elements above 2^63): once more at 2^-80, where eps is
-    // nothing against them.  (All lanes: the row's own sum decides.)
-    if (__any_sync(0xffffffffu, ss == INFINITY)) {
+    const float mean = __fmaf_rn(sum_squares(y), how.inv_d, how.eps);
+    float r = rsqrtf(mean);
+    // past fp32 (elements above 2^63, or an eps near its end): once more at 2^-80.
+    // (All lanes: the row's own sum decides.)
+    if (__any_sync(0xffffffffu, mean == INFINITY)) {
       const uint64_t down = f2_pack(0x1p-80f, 0x1p-80f);
       Pairs z;
 #pragma unroll
@@ -159,8 +159,8 @@ __device__ __forceinline__ uint4 turn(const uint4& raw, bool norm, const Pairs& 
         z.a[e] = f2_mul(y.a[e], down);
         z.b[e] = f2_mul(y.b[e], down);
       }
-      const float small = sum_squares(z);
-      if (ss == INFINITY) r = __fmul_rn(rsqrtf(__fmul_rn(small, how.inv_d)), 0x1p-80f);
+      const float small = __fmaf_rn(sum_squares(z), how.inv_d, __fmul_rn(__fmul_rn(how.eps, 0x1p-80f), 0x1p-80f));
+      if (mean == INFINITY) r = __fmul_rn(rsqrtf(small), 0x1p-80f);
     }
     const uint64_t r2 = f2_pack(r, r);
 #pragma unroll

@@ -29,3 +29,20 @@ def test_a_tensor_without_heads_leaves_the_other_one():
     plan.apply(q[:, :0], k[:, :0], q[:, :0], k[:, :0])
     plan.apply(q[:, :0], k, None, got := torch.empty_like(k))
     assert torch.equal(got, k_out) and plan.check() == 0
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("x,eps", [(2.0 ** 64, 2.0 ** 127), (2.0 ** 60, 3.4028234e38), (2.0 ** 64, 1e-6), (3.3e38, 1e38),
+                                   (1.0, 3.4028234e38), (2.0 ** -60, 1e-30)])
+def test_norms_where_squares_or_eps_reach_the_end_of_fp32(layout, x, eps):
+    """x / sqrt(mean x^2 + eps) of rows of one magnitude and of rows with a few
+    large elements.  Bound: the tests' of a norm, 2^-8 + 2^-19 of the value, and
+    bf16's smallest half step."""
+    plan = Rotary(64, dims=0, layout=layout, q_norm=torch.ones(64), eps=eps, device=DEV)
+    q = rows(2, 3, 5, 64, 1).sign() * x
+    q[:, 1, :, 9:] *= 2.0 ** -10
+    out = torch.empty_like(q)
+    plan.apply(q, None, out, None)
+    y = q.cpu().double().numpy()
+    want = y / np.sqrt((y * y).mean(-1, keepdims=True) + float(np.float32(eps)))
+    assert np.all(np.abs(out.cpu().double().numpy() - want) <= (2.0 ** -8 + 2.0 ** -19) * np.abs(want) + 2.0 ** -134)
