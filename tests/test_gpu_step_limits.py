@@ -12,6 +12,35 @@ gpu = pytest.mark.gpu
 pytestmark = gpu
 
 
+def within(got, want, off):
+    """got (bf16) is the rounding of a number that is `off` from want at most."""
+    # (fp32 in between is off by half a step of 2^-24 more, for numbers up to 1)
+    lo, hi = (torch.from_numpy((want + s * (off + 2.0 ** -25)).astype(np.float32)).bfloat16() for s in (-1, 1))
+    return bool(((lo <= got) & (got <= hi)).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_sine_and_cosine_are_off_by_a_last_place_of_fp32(layout):
+    """2^-23, at any position.  Pairs (1, 0) become (cos, sin) without another
+    rounding but the last; of 2^23 results some thousands lie within 2^-20 of a
+    border between two bf16 numbers, so that a wrong place shows."""
+    d, n = 128, 1 << 16
+    plan = Rotary(d, base=1000003.0, layout=layout, device=DEV)
+    at = np.random.default_rng(7).integers(-2 ** 31, 2 ** 31, n)
+    at[:4] = -2 ** 31, 2 ** 31 - 1, 0, -1
+    a, b = (slice(0, d // 2), slice(d // 2, d)) if layout == "half" else (slice(0, d, 2), slice(1, d, 2))
+    q = torch.zeros(1, 1, n, d, dtype=torch.bfloat16, device=DEV)
+    q[..., a] = 1.0
+    out = torch.empty_like(q)
+    plan.apply(q, None, out, None, positions=torch.from_numpy(at).to(torch.int32).to(DEV)[None])
+    assert plan.check() == 0
+    turns = at.astype(np.int64).view(np.uint64)[:, None] * plan.turns.cpu().numpy().view(np.uint64)[None]   # (modulo 2^64)
+    angle = 2 * np.pi * (turns.astype(np.float64) * 2.0 ** -64)
+    for got, want in ((out[0, 0][:, a].cpu(), np.cos(angle)), (out[0, 0][:, b].cpu(), np.sin(angle))):
+        assert within(got, want, 2.0 ** -23)
+        assert not within(got, want + 2.0 ** -20, 2.0 ** -23)
+
+
 def test_a_tensor_without_heads_leaves_the_other_one():
     """As in store_rotated(): no heads are no queries, or no keys."""
     plan = Rotary(64, q_norm=weights(64, 1), k_norm=weights(64, 2), device=DEV)
