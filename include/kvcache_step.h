@@ -144,7 +144,8 @@ DROPKV_API dropkv_status kvcache_read(const kvcache_read_call* call);
  *           the call is kvcache_attention and the groups are not looked at
  *           (sharing adds three short kernels); negative: where sharing would
  *           not be faster, by the shape, n, G, Hq and T, if the table were full
- *           of shared tokens
+ *           of shared tokens (lengths are the device's: short prefixes in a
+ *           table for far longer sequences are shared although they need not be)
  *   groups  device int32 [G + 1], groups[0] = 0, not decreasing, groups[G] =
  *           n; anything else is flagged (DROPKV_FLAG_BAD_LENGTH) and nothing
  *           is shared

@@ -1076,8 +1076,11 @@ __device__ __forceinline__ void add4(float4& o, const float4& x, float f) {
 }
 // W > 1: a CTA of W warps joins one row, of up to some 300 pieces, a warp every
 // W-th; else a warp each joins a row (4 to a CTA).  Whole calls with 1, 4 and 8
-// warps a row: 512 rows of 39 pieces 124, 117, 112 us; 1456 rows 90.6, 88.5, 95.2;
-// 2048 rows of 20 pieces 110.7, 114.6, 119.5; 20 rows to an SM 69.8, 76.4, 86.4.
+// warps a row, when P was lifted by 2^4: 512 rows of 39 pieces 124, 117, 112 us;
+// 1456 rows 90.6, 88.5, 95.2; 2048 rows of 20 pieces 110.7, 114.6, 119.5; 20 rows to
+// an SM 69.8, 76.4, 86.4.  The launch bounds leave 40 registers (W > 1) and 64, and
+// the eight loads in flight spill 268 and 116 bytes: 8 to 12 us where the bytes
+// take 4.
 template <int W>
 __global__ void __launch_bounds__(32 * (W > 1 ? W : 4), W > 1 ? 48 / W : 8) final_kernel(const SharedCall p) {
   constexpr bool WHOLE = W > 1;

@@ -70,15 +70,17 @@ double cycles_saved(const kvcache_shape& s, int n, int G, double R) {
 }
 // Three more short kernels cost some 35 us (67000 cycles at 1.9 GHz); as tables are
 // longer than what is shared, a third more is asked for (with 67000, 10 x 2-5 behind
-// 2300 to 3600, 16 heads of 128, 3 rows, took 85 us instead of attention's 70).
-// Attention and shared, us:
-//   8, 16 x 16000 tokens in one group, 8 heads of 128       40 and 69   55 and 59
-//   8, 16 x 4000, 32 heads of 96                            47 and 84   47 and 50
-//   64 x 32768, 8 heads of 128                              443         111
-//   10 x 2 behind 18000-28000, 4 heads of 96, 7 rows        78          103
-//   11 x 3 behind 19000-63000, 8 heads of 16, 4 rows        227         302
-//   2 x 4 behind 23000-48000, 16 heads of 80, 40 rows       588         196
-//   10 x 4-7 behind 64000-96000, one head of 112, 6 rows    188         132
+// 2300 to 3600, 16 heads of 128, 3 rows, would take 81 us instead of attention's 62).
+// Attention and shared, us, with up to 200 tokens of their own:
+//   8, 16 x 16000 tokens in one group, 8 heads of 128       41 and 69   49 and 54
+//   8, 16 x 4000, 32 heads of 96, int8                      47 and 84   47 and 51
+//   64 x 32768, 8 heads of 128                              428         87
+//   10 x 2 behind 18000-28000, 4 heads of 96, 7 rows        68          98
+//   11 x 3 behind 19000-63000, 8 heads of 16, 4 rows        189         247
+//   2 x 4 behind 23000-48000, 16 heads of 80, 40 rows       513         184
+//   10 x 4-7 behind 64000-96000, one head of 112, 6 rows    161         119
+// Short prompts in a long table are where it is wrong: 8 behind 100, 1000, 4000
+// tokens, 8 heads of 128, 512 to 10000 pages of 64: 12, 14, 19     33, 32, 37
 constexpr double kSharingCycles = 90000;
 
 // The workspace of a shared attention (byte offsets); the second half's parts

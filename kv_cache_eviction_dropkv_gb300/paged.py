@@ -40,7 +40,8 @@ class PagedCache:
                  groups: int = 0):
         """pages: pages in the pool; page: tokens per page (32, 64 or 128);
         max_pages: most pages of one sequence (default: all; attention over
-        short sequences is faster with a bound near their length); code: "e4m3" or
+        short sequences is faster with a bound near their length, and
+        shared_attention() takes it for the length of what is shared); code: "e4m3" or
         "int8"; Hq, T: query heads (default: Hkv) and most query rows per
         sequence of an attention() call (they size the workspace), groups: most
         groups of a shared_attention() call (0: there are none)."""
@@ -225,7 +226,11 @@ class PagedCache:
         the cache's table has no room for `least` bytes of the entries' keys and
         values the call is attention(), and the groups are not looked at; -1:
         where sharing would not be faster, by the entries to a group, the rows
-        and the cache's shape, if its table were full of shared tokens."""
+        and the cache's shape, if its table were full of shared tokens.  That
+        is not so in a table that is far longer than the prefixes (one for the
+        whole pool, max_pages' default): short prefixes are shared there although
+        attention() is faster (8 entries behind 1000 tokens, 8 heads of 128: 14
+        instead of 32 us), so call that where prefixes are known to be short."""
         n, Hq, T, d = q.shape
         G = groups.shape[0] - 1
         if T > self.T or Hq != self.Hq or G > self.groups:
