@@ -41,8 +41,8 @@ class PagedCache:
         """pages: pages in the pool; page: tokens per page (32, 64 or 128);
         max_pages: most pages of one sequence (default: all; attention over
         short sequences is faster with a bound near their length, and
-        shared_attention() takes it for the length of what is shared); code: "e4m3" or
-        "int8"; Hq, T: query heads (default: Hkv) and most query rows per
+        shared_attention() takes it for the length of what is shared); code:
+        "e4m3" or "int8"; Hq, T: query heads (default: Hkv) and most query rows per
         sequence of an attention() call (they size the workspace), groups: most
         groups of a shared_attention() call (0: there are none)."""
         if code not in B.CACHE_CODES:

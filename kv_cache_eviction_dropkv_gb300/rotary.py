@@ -78,8 +78,8 @@ class Rotary:
         that turn more than `fast` times over the original context stay, those
         below `slow` are divided, a ramp over the pairs between, and the
         rotated channels are multiplied by amplitude (default 0.1 ln(factor) +
-        1, or 1 for a factor below 1); "bands" (original=, low=1, high=4): the same with a ramp over the
-        turns and no amplitude."""
+        1, or 1 for a factor below 1); "bands" (original=, low=1, high=4): the
+        same with a ramp over the turns and no amplitude."""
         self.d, self.dims, self.eps = int(d), int(d if dims is None else dims), float(eps)
         if not 8 <= self.d <= 128 or self.d % 8 or not 0 <= self.dims <= self.d or self.dims % 8:
             raise ValueError("d is a multiple of 8 up to 128, dims one up to d")
